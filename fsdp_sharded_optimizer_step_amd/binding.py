@@ -21,6 +21,7 @@ ZERO_MAX_ND_FUSED = 128
 GRAD_COMPACT, GRAD_FLAT = 0, 1
 OUT_AG_SLOT, OUT_SHARD = 0, 1
 ACC_OVERWRITE, ACC_EMIT_BF16, ACC_NO_STORE = 1, 2, 4
+ACT8_BLOCK = 128
 
 EXPORTS = ("zero_layout_create", "zero_layout_destroy", "zero_layout_psi", "zero_layout_padded",
            "zero_layout_shard", "zero_layout_n_buckets", "zero_layout_n_d", "zero_layout_rank",
@@ -28,7 +29,10 @@ EXPORTS = ("zero_layout_create", "zero_layout_destroy", "zero_layout_psi", "zero
            "zero_shard_step", "zero_shard_step_ex", "zero_step_scalars", "zero_strerror",
            "zero_gather_params", "zero_reshard", "zero_layout_create_dim0", "zero_layout_kind",
            "zero_shard_step_accumulate", "zero_placement_plan", "zero_shard_step_buckets",
-           "zero_layout_tensor_flat")
+           "zero_layout_tensor_flat", "zero_act8_pack", "zero_act8_unpack",
+           "zero_embedding_lookup", "zero_embedding_grad", "zero_embedding_grad_workspace",
+           "zero_rms_norm", "zero_rms_norm_grad", "zero_rms_norm_grad_workspace",
+           "zero_linear_grad", "zero_linear_grad_workspace")
 
 
 class ZeroError(RuntimeError):
@@ -101,6 +105,23 @@ def load():
     lib.zero_step_scalars.argtypes = [C.POINTER(_AdamW), C.c_int64, C.POINTER(C.c_float)]
     lib.zero_placement_plan.argtypes = [C.c_int32, _i64p, C.POINTER(C.c_double), C.c_int64,
                                         C.c_int32, C.c_int64, _i64p, _i64p]
+    i32, i64, u32, f32 = C.c_int32, C.c_int64, C.c_uint32, C.c_float
+    lib.zero_act8_pack.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+    lib.zero_act8_unpack.argtypes = [vp, vp, i64, i64, vp, i32, i64, vp]
+    lib.zero_embedding_lookup.argtypes = [vp, i32, i64, vp, vp, i32, i64, f32, vp, i64, i32, vp]
+    lib.zero_embedding_grad_workspace.argtypes = [vp, i32, i64, i64]
+    lib.zero_embedding_grad.argtypes = [vp, i32, i64, vp, i32, i64, vp, i64, i32, f32, u32, vp, vp,
+                                        vp, i64, vp]
+    lib.zero_rms_norm.argtypes = [vp, i32, vp, vp, i64, vp, i64, i64, f32, vp, vp, vp, vp, vp, vp]
+    lib.zero_rms_norm_grad_workspace.argtypes = [vp, i32, i64]
+    lib.zero_rms_norm_grad.argtypes = [vp, i32, vp, vp, i64, vp, i64, vp, vp, i64, f32, u32, vp, vp,
+                                       vp, vp, i64, vp]
+    lib.zero_linear_grad_workspace.argtypes = [vp, i32, i32, i64, i64, i64]
+    lib.zero_linear_grad.argtypes = [vp, i32, i32, vp, i64, vp, vp, i64, i64, i64, f32, u32, vp, vp,
+                                     vp, i64, vp]
+    for name in ("zero_embedding_grad_workspace", "zero_rms_norm_grad_workspace",
+                 "zero_linear_grad_workspace"):
+        getattr(lib, name).restype = i64
     lib.zero_strerror.argtypes = [C.c_int]
     lib.zero_strerror.restype = C.c_char_p
     _lib = lib
@@ -393,3 +414,267 @@ def zero_placement_plan(nbytes, traffic, lane_bytes: int, n_lanes: int, align: i
     _check("zero_placement_plan", load().zero_placement_plan(
         n, nb, tr, int(lane_bytes), int(n_lanes), int(align), offs, C.byref(total)))
     return [int(offs[k]) for k in range(n)], int(total.value)
+
+
+# ------------------------------------------------- gradients of a micro-batch
+class _On:
+    """The stream of a call and the device that every tensor of it lies on.
+
+    Used as a context it makes that device the current one (a kernel goes to
+    the device of its stream) and the stream torch's current one, so that a
+    workspace allocated inside belongs to the stream, also under capture."""
+
+    def __init__(self, where, stream, tensors):
+        import torch
+        self.where = where
+        dev = tensors[0].device
+        for t in tensors:
+            if t.device != dev:
+                raise ValueError(f"{where}: tensors on {dev} and {t.device}")
+        if not tensors[0].is_cuda:
+            raise ValueError(f"{where}: needs CUDA tensors")
+        self.device = dev
+        self.stream = torch.cuda.current_stream(dev) if stream is None else stream
+        if self.stream.device != dev:
+            raise ValueError(f"{where}: tensors on {dev}, stream on {self.stream.device}")
+        self.ptr = C.c_void_p(self.stream.cuda_stream)
+        self._plain = stream is None and torch.cuda.current_device() == dev.index
+
+    def __enter__(self):
+        if not self._plain:
+            import torch
+            self._ctx = torch.cuda.stream(self.stream)
+            self._ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if not self._plain:
+            self._ctx.__exit__(*exc)
+
+    def workspace(self, given, nbytes):
+        """(pointer, bytes) of the caller's workspace, or of a new one."""
+        _check(self.where, min(0, nbytes))
+        if given is None:
+            if nbytes == 0:
+                return None, 0
+            import torch
+            given = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            self._keep = given
+        elif not given.is_contiguous() or given.device != self.device:
+            raise ValueError(f"{self.where}: workspace: needs a contiguous tensor on {self.device}")
+        return C.c_void_p(given.data_ptr()), given.numel() * given.element_size()
+
+
+def _of(where, name, t, *dtypes):
+    if t.dtype not in dtypes:
+        raise ValueError(f"{where}: {name}: {t.dtype} is not one of {dtypes}")
+
+
+def _dense(where, name, t, shape, *dtypes):
+    """A contiguous tensor of that shape and one of those types."""
+    _of(where, name, t, *dtypes)
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{where}: {name}: needs a contiguous tensor of shape {tuple(shape)}, "
+                         f"got {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _matrix(where, name, t, rows, cols, *dtypes):
+    """Distance of two rows of a matrix whose rows lie densely."""
+    _of(where, name, t, *dtypes)
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{where}: {name}: needs shape {(rows, cols)}, got {tuple(t.shape)}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{where}: {name}: columns are not adjacent (strides {t.stride()})")
+    if rows <= 1:
+        return max(cols, 1)
+    if t.stride(0) < cols:
+        raise ValueError(f"{where}: {name}: rows overlap (strides {t.stride()})")
+    return max(t.stride(0), 1)
+
+
+def _flat(where, name, t, layout, *dtypes):
+    _of(where, name, t, *dtypes)
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {name}: needs a contiguous tensor")
+    _need(t, f"{where}: {name}", layout.padded)
+
+
+def _types():
+    import torch
+    return torch, (torch.bfloat16, torch.int16, torch.uint16), \
+        (torch.float8_e4m3fn, torch.uint8, torch.int8)
+
+
+def _ptr(t):
+    return None if t is None else C.c_void_p(t.data_ptr())
+
+
+def _numel(where, layout, tensor):
+    if not 0 <= tensor < layout.n_tensors:
+        raise ZeroError(where, ZERO_ERANGE)
+    return layout.numel[tensor]
+
+
+def _grad_args(where, layout, acc, flags, bf16_out):
+    """The tensors among acc and bf16_out that the flags use, checked."""
+    torch, b16, _ = _types()
+    used = []
+    if not (flags & ACC_OVERWRITE and flags & ACC_NO_STORE):
+        if acc is None:
+            raise ValueError(f"{where}: acc is needed with these flags")
+        _flat(where, "acc", acc, layout, torch.float32)
+        used.append(acc)
+    if flags & ACC_EMIT_BF16:
+        if bf16_out is None:
+            raise ValueError(f"{where}: bf16_out is needed with these flags")
+        _flat(where, "bf16_out", bf16_out, layout, *b16)
+        used.append(bf16_out)
+    return used
+
+
+def _codes(where, codes, scales, rows, cols):
+    torch, _, b8 = _types()
+    _dense(where, "codes", codes, (rows, cols), *b8)
+    _dense(where, "scales", scales, (rows, -(-cols // ACT8_BLOCK)), torch.uint8)
+
+
+def zero_act8_pack(x, codes, scales, stream=None):
+    """8-bit codes (rows, cols) and scale bytes (rows, ceil(cols/128)) of x
+    (rows, cols), bfloat16 or float32."""
+    me = "zero_act8_pack"
+    torch, b16, _ = _types()
+    rows, cols = codes.shape if codes.dim() == 2 else (-1, -1)
+    stride = _matrix(me, "x", x, rows, cols, torch.float32, *b16)
+    _codes(me, codes, scales, rows, cols)
+    with _On(me, stream, (x, codes, scales)) as on:
+        _check(me, load().zero_act8_pack(_ptr(x), int(x.dtype == torch.float32), rows, cols, stride,
+                                         _ptr(codes), _ptr(scales), on.ptr))
+
+
+def zero_act8_unpack(codes, scales, out, stream=None):
+    """The values that the codes stand for, into out (rows, cols), bfloat16 or
+    float32."""
+    me = "zero_act8_unpack"
+    torch, b16, _ = _types()
+    rows, cols = codes.shape if codes.dim() == 2 else (-1, -1)
+    stride = _matrix(me, "out", out, rows, cols, torch.float32, *b16)
+    _codes(me, codes, scales, rows, cols)
+    with _On(me, stream, (out, codes, scales)) as on:
+        _check(me, load().zero_act8_unpack(_ptr(codes), _ptr(scales), rows, cols, _ptr(out),
+                                           int(out.dtype == torch.float32), stride, on.ptr))
+
+
+def zero_embedding_lookup(layout: Layout, tensor: int, params, ids, out, scale: float = 1.0,
+                          stream=None):
+    """out[t] = scale * E[ids[t]] for the table `tensor` of the gathered flat
+    buffer `params`; ids: int32 or int64, any shape; out: (ids.numel(), cols),
+    bfloat16 or float32.  A row of zeros where an id is outside the table."""
+    me = "zero_embedding_lookup"
+    torch, b16, _ = _types()
+    n = ids.numel()
+    cols = out.shape[1] if out.dim() == 2 else -1
+    stride = _matrix(me, "out", out, n, cols, torch.float32, *b16)
+    _numel(me, layout, tensor)
+    _dense(me, "ids", ids, ids.shape, torch.int32, torch.int64)
+    _flat(me, "params", params, layout, *b16)
+    with _On(me, stream, (params, ids, out)) as on:
+        _check(me, load().zero_embedding_lookup(
+            layout.handle, tensor, cols, _ptr(params), _ptr(ids), ids.element_size(), n, scale,
+            _ptr(out), stride, int(out.dtype == torch.float32), on.ptr))
+
+
+def zero_embedding_grad(layout: Layout, tensor: int, ids, dy, acc, scale: float = 1.0,
+                        flags: int = 0, bf16_out=None, workspace=None, stream=None):
+    """The table's gradient, scaled, into the flat accumulator `acc` and / or
+    the flat bf16 buffer `bf16_out` as the ACC_ flags say; dy: (ids.numel(),
+    cols), bfloat16 or float32."""
+    me = "zero_embedding_grad"
+    torch, b16, _ = _types()
+    n = ids.numel()
+    cols = dy.shape[1] if dy.dim() == 2 else -1
+    stride = _matrix(me, "dy", dy, n, cols, torch.float32, *b16)
+    _numel(me, layout, tensor)
+    _dense(me, "ids", ids, ids.shape, torch.int32, torch.int64)
+    used = _grad_args(me, layout, acc, flags, bf16_out)
+    lib = load()
+    with _On(me, stream, [ids, dy] + used) as on:
+        ws, ws_bytes = on.workspace(workspace, lib.zero_embedding_grad_workspace(
+            layout.handle, tensor, cols, n))
+        _check(me, lib.zero_embedding_grad(
+            layout.handle, tensor, cols, _ptr(ids), ids.element_size(), n, _ptr(dy), stride,
+            int(dy.dtype == torch.float32), scale, flags, _ptr(acc), _ptr(bf16_out), ws, ws_bytes,
+            on.ptr))
+
+
+def zero_rms_norm(layout: Layout, tensor: int, params, x, res, eps: float, h, rstd, codes, scales,
+                  y=None, stream=None):
+    """h = x + res (res None: x; h may then be None), rstd, and the normed and
+    weighted rows in 8 bits; y: None, or the bf16 values that the codes stand
+    for.  x, res: (rows, cols) bfloat16; cols = the weight's elements."""
+    me = "zero_rms_norm"
+    torch, b16, _ = _types()
+    cols = _numel(me, layout, tensor)
+    rows = rstd.numel()
+    xs = _matrix(me, "x", x, rows, cols, *b16)
+    rs = 0 if res is None else _matrix(me, "res", res, rows, cols, *b16)
+    _dense(me, "rstd", rstd, rstd.shape, torch.float32)
+    for name, t in (("h", h), ("y", y)):
+        if t is not None:
+            _dense(me, name, t, (rows, cols), *b16)
+    _codes(me, codes, scales, rows, cols)
+    _flat(me, "params", params, layout, *b16)
+    with _On(me, stream, [t for t in (params, x, res, h, rstd, codes, scales, y)
+                          if t is not None]) as on:
+        _check(me, load().zero_rms_norm(
+            layout.handle, tensor, _ptr(params), _ptr(x), xs, _ptr(res), rs, rows, eps, _ptr(h),
+            _ptr(rstd), _ptr(codes), _ptr(scales), _ptr(y), on.ptr))
+
+
+def zero_rms_norm_grad(layout: Layout, tensor: int, params, dy, dh, h, rstd, dx, acc,
+                       scale: float = 1.0, flags: int = 0, bf16_out=None, workspace=None,
+                       stream=None):
+    """dx (the gradient of x and of res) from dy and the residual's gradient
+    dh (or None); the weight's gradient, scaled, into `acc` / `bf16_out`."""
+    me = "zero_rms_norm_grad"
+    torch, b16, _ = _types()
+    cols = _numel(me, layout, tensor)
+    rows = rstd.numel()
+    ys = _matrix(me, "dy", dy, rows, cols, *b16)
+    hs = 0 if dh is None else _matrix(me, "dh", dh, rows, cols, *b16)
+    _dense(me, "rstd", rstd, rstd.shape, torch.float32)
+    _dense(me, "h", h, (rows, cols), *b16)
+    _dense(me, "dx", dx, (rows, cols), *b16)
+    _flat(me, "params", params, layout, *b16)
+    used = _grad_args(me, layout, acc, flags, bf16_out)
+    lib = load()
+    with _On(me, stream, [t for t in (params, dy, dh, h, rstd, dx) if t is not None] + used) as on:
+        ws, ws_bytes = on.workspace(workspace, lib.zero_rms_norm_grad_workspace(
+            layout.handle, tensor, rows))
+        _check(me, lib.zero_rms_norm_grad(
+            layout.handle, tensor, _ptr(params), _ptr(dy), ys, _ptr(dh), hs, _ptr(h), _ptr(rstd),
+            rows, scale, flags, _ptr(dx), _ptr(acc), _ptr(bf16_out), ws, ws_bytes, on.ptr))
+
+
+def zero_linear_grad(layout: Layout, tensor: int, dy, codes, scales, acc, scale: float = 1.0,
+                     flags: int = 0, bf16_out=None, transposed: bool = False, workspace=None,
+                     stream=None):
+    """A linear weight's gradient, scaled, into `acc` / `bf16_out`, from the
+    output gradient dy (tokens, out_features) bfloat16 and the input's 8-bit
+    checkpoint (tokens, in_features).  transposed: the weight is kept as
+    (in_features, out_features)."""
+    me = "zero_linear_grad"
+    torch, b16, _ = _types()
+    if dy.dim() != 2 or codes.dim() != 2:
+        raise ValueError(f"{me}: dy and codes need two dimensions")
+    (tokens, o), i = dy.shape, codes.shape[1]
+    stride = _matrix(me, "dy", dy, tokens, o, *b16)
+    _codes(me, codes, scales, tokens, i)
+    _numel(me, layout, tensor)
+    used = _grad_args(me, layout, acc, flags, bf16_out)
+    lib = load()
+    with _On(me, stream, [dy, codes, scales] + used) as on:
+        ws, ws_bytes = on.workspace(workspace, lib.zero_linear_grad_workspace(
+            layout.handle, tensor, int(transposed), o, i, tokens))
+        _check(me, lib.zero_linear_grad(
+            layout.handle, tensor, int(transposed), _ptr(dy), stride, _ptr(codes), _ptr(scales),
+            tokens, o, i, scale, flags, _ptr(acc), _ptr(bf16_out), ws, ws_bytes, on.ptr))

@@ -8,7 +8,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libzero_shard.so")
 SOURCES = ["layout.cpp", "placement.cpp", "shard_step.hip", "pack_accumulate.hip",
-           "gather_reshard.hip"]
+           "gather_reshard.hip", "act8.hip", "embedding.hip", "rms_norm.hip", "linear_grad.hip"]
 
 # Floating point: no contraction into FMA, correctly rounded binary32 divide
 # and square root, subnormals kept (no flush), no fast-math.  Packed fp32

@@ -1,0 +1,556 @@
+// zero_embedding_lookup and zero_embedding_grad.
+//
+// Page "Infra: Data Parallel" (pufanyi.com), section "Zero Redundancy
+// Optimizer (ZeRO)": the updated 16-bit parameters are gathered into one flat
+// buffer before the forward pass, where the lookup reads the table's rows;
+// section "Naive Data Parallelism": without synchronisation a micro-batch's
+// gradients are added to the rank's own sum, which is where the table's
+// gradient goes.
+//
+// lookup: out[t] = scale * E[id_t].  A stream of 2*cols bytes in and out per
+// token with whole rows, so no LDS; a thread takes 8 columns.
+//
+// gradient: dE[v] = sum over the t with id_t = v of dY[t], t ascending, so
+// that the result is the same in every run.  Three launches:
+//   plan   the tokens grouped by id, in ascending order within an id.  The
+//          ids are dealt to slices (slice = id mod S, so that frequent
+//          neighbours fall into different ones); one block per slice reads all
+//          n ids, counts its own and those of lower slices, which gives its
+//          place in the order without talking to other blocks, and places its
+//          tokens in a second reading.  n ids are read from L2 by S blocks:
+//          cheaper at these sizes than the passes of a general sort.
+//   pieces an id with more than kPiece tokens is cut into pieces of kPiece,
+//          summed apart in binary32, so that one frequent token does not keep
+//          one row of threads busy alone
+//   rows   sums an id's few tokens, or its pieces in order, and adds the
+//          scaled sum to the accumulator: once for each distinct id, or for
+//          every row of the table where the flags ask for the whole gradient
+//          (an absent id's is zero).
+#include <algorithm>
+
+#include "tensor_place.hpp"
+
+namespace {
+using namespace zs;
+
+constexpr int kThreads = 256;
+
+template <class T>
+__device__ __forceinline__ int64_t id_at(const void* ids, int64_t t) {
+  return (int64_t)((const T*)ids)[t];
+}
+
+// ------------------------------------------------------------------ lookup
+struct LookupArgs {
+  const uint16_t* params;
+  const void* ids;
+  void* out;
+  int64_t out_stride;
+  Place place;
+  int64_t vocab;
+  int32_t n, cols;
+  FastDiv pieces;     // pieces of 8 columns per row
+  int32_t rows_per_block;
+  float scale;
+};
+
+template <class OUT>
+__device__ __forceinline__ void put8(OUT* p, const float (&x)[8], int n);
+template <>
+__device__ __forceinline__ void put8<uint16_t>(uint16_t* p, const float (&x)[8], int n) {
+  if (n >= 8) {
+    *(u32x4_a2*)p = u32x4{bf16_pack2(x[0], x[1]), bf16_pack2(x[2], x[3]), bf16_pack2(x[4], x[5]),
+                          bf16_pack2(x[6], x[7])};
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) p[k] = (uint16_t)bf16_round(x[k]);
+  }
+}
+template <>
+__device__ __forceinline__ void put8<float>(float* p, const float (&x)[8], int n) {
+  if (n >= 8) {
+    *(f32x4_a4*)p = f32x4{x[0], x[1], x[2], x[3]};
+    *(f32x4_a4*)(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) p[k] = x[k];
+  }
+}
+
+template <class ID, class OUT, bool GAPS>
+__global__ void __launch_bounds__(kThreads) lookup_kernel(const LookupArgs A) {
+  const int64_t t0 = (int64_t)blockIdx.x * A.rows_per_block;
+  const uint32_t units = (uint32_t)A.rows_per_block * A.pieces.d;
+  for (uint32_t u = threadIdx.x; u < units; u += kThreads) {
+    const uint32_t r = fast_div(u, A.pieces);
+    const int32_t c0 = (int32_t)(u - r * A.pieces.d) * 8;
+    const int64_t t = t0 + r;
+    if (t >= A.n) break;
+    const int n = min(8, A.cols - c0);
+    const int64_t id = id_at<ID>(A.ids, t);
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (id >= 0 && id < A.vocab) {
+      const int64_t i = id * A.cols + c0;
+      if (!GAPS && n >= 8) {
+        const u32x4 w = *(const u32x4_a2*)(A.params + place_at<GAPS>(A.place, i));
+        x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
+        x[4] = bf16_lo(w.z); x[5] = bf16_hi(w.z); x[6] = bf16_lo(w.w); x[7] = bf16_hi(w.w);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < n) x[k] = bf16_one(A.params[place_at<GAPS>(A.place, i + k)]);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = A.scale * x[k];
+    }
+    put8<OUT>((OUT*)A.out + t * A.out_stride + c0, x, n);
+  }
+}
+
+// ------------------------------------------------------------------ plan
+// One entry per place in the order.
+struct Entry {
+  int32_t token, row;  // token index, its id
+  int32_t rel, count;  // place among the id's tokens, and how many these are
+};
+static_assert(sizeof(Entry) == 16, "entry");
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWaves = kPlanThreads / 64;
+constexpr int kMaxLocal = 1024;  // ids of one slice: 16 waves x 1024 counters, 64 KiB of LDS
+constexpr int kMinSlices = 256;  // one block per CU
+
+struct PlanArgs {
+  const void* ids;
+  int64_t vocab;
+  int32_t n, local;     // tokens; ids per slice
+  uint32_t slice_bits;  // S = 2^slice_bits slices
+  int32_t* start;       // S*local + 1 places: first place of (slice, id / S)
+  Entry* order;
+};
+
+template <class ID>
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs A) {
+  __shared__ int32_t cnt[kPlanWaves][kMaxLocal];  // counts, later the next free place
+  __shared__ int32_t tot[kMaxLocal];              // an id's tokens
+  __shared__ int32_t first[kMaxLocal];            // its first place
+  __shared__ int32_t wsum[kPlanWaves], wlow[kPlanWaves];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int64_t slice = blockIdx.x;
+  const int64_t mask = ((int64_t)1 << A.slice_bits) - 1;
+  for (int k = tid; k < kPlanWaves * A.local; k += kPlanThreads)
+    cnt[k / A.local][k % A.local] = 0;
+  __syncthreads();
+  // each wave counts its own contiguous part of the tokens
+  const int64_t per = ((int64_t)A.n + kPlanThreads - 1) / kPlanThreads * 64;
+  const int64_t ta = wave * per, tz = min((int64_t)A.n, ta + per);
+  int32_t low = 0;
+#pragma unroll 4
+  for (int64_t t = ta + lane; t < tz; t += 64) {
+    const int64_t id = id_at<ID>(A.ids, t);
+    const bool real = id >= 0 && id < A.vocab;
+    const int64_t s = id & mask;
+    if (real && s < slice) ++low;
+    if (real && s == slice) atomicAdd(&cnt[wave][id >> A.slice_bits], 1);
+  }
+  for (int k = 32; k; k >>= 1) low += __shfl_xor(low, k, 64);
+  if (lane == 0) wlow[wave] = low;
+  __syncthreads();
+  // one id per thread (local <= kMaxLocal = kPlanThreads): its total, then
+  // the running sum over the slice's ids
+  int32_t base = 0;
+  for (int w = 0; w < kPlanWaves; ++w) base += wlow[w];
+  int32_t mine = 0;
+  if (tid < A.local)
+    for (int w = 0; w < kPlanWaves; ++w) mine += cnt[w][tid];
+  int32_t run = mine;
+  for (int k = 1; k < 64; k <<= 1) {
+    const int32_t up = __shfl_up(run, k, 64);
+    if (lane >= k) run += up;
+  }
+  if (lane == 63) wsum[wave] = run;
+  __syncthreads();
+  int32_t before = base;
+  for (int w = 0; w < wave; ++w) before += wsum[w];
+  const int32_t at = before + run - mine;
+  if (tid < A.local) {
+    tot[tid] = mine;
+    first[tid] = at;
+    A.start[slice * A.local + tid] = at;
+    int32_t next = at;
+    for (int w = 0; w < kPlanWaves; ++w) {
+      const int32_t c = cnt[w][tid];
+      cnt[w][tid] = next;
+      next += c;
+    }
+    if (slice == mask && tid == A.local - 1) A.start[(mask + 1) * A.local] = next;
+  }
+  __syncthreads();
+  // second reading: tokens of this slice go to their places, in order (a wave
+  // walks its tokens upwards; equal ids among 64 tokens by lane)
+  for (int64_t t0 = ta; t0 < tz; t0 += 64) {
+    const int64_t t = t0 + lane;
+    int64_t id = -1;
+    if (t < tz) id = id_at<ID>(A.ids, t);
+    const bool own = id >= 0 && id < A.vocab && (id & mask) == slice;
+    uint64_t todo = __ballot(own);
+    const int32_t loc = own ? (int32_t)(id >> A.slice_bits) : -1;
+    while (todo) {
+      const int lead = __ffsll((unsigned long long)todo) - 1;
+      const int32_t l = __shfl(loc, lead, 64);
+      const uint64_t same = __ballot(loc == l);
+      int32_t p0 = 0;
+      if (lane == lead) p0 = atomicAdd(&cnt[wave][l], (int32_t)__popcll(same));
+      p0 = __shfl(p0, lead, 64);
+      if (loc == l) {
+        const int32_t p = p0 + __popcll(same & (((uint64_t)1 << lane) - 1));
+        A.order[p] = Entry{(int32_t)t, (int32_t)id, p - first[l], tot[l]};
+      }
+      todo &= ~same;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ sums
+// Rows summed by one thread without a break; more go to pieces.
+constexpr int kPiece = 64;
+
+struct GradArgs {
+  const void* dy;
+  int64_t dy_stride;
+  const int32_t* start;
+  const Entry* order;
+  float* partial;  // 2 * (n / kPiece + 1) rows of cols
+  GradOut out;
+  int64_t vocab;
+  int32_t n, cols, local;
+  uint32_t slice_bits;
+  FastDiv pieces;  // pieces of 4 columns per row
+  int32_t rows_per_block;
+};
+
+// The partial row of the piece that begins at place p: among the places of a
+// window of kPiece there is at most one first piece of a long id and at most
+// one later piece.
+__device__ __forceinline__ int64_t slot_of(int32_t p, bool first) {
+  return 2 * (int64_t)(p / kPiece) + (first ? 1 : 0);
+}
+
+template <class DY>
+__device__ __forceinline__ f32x4 dy4(const GradArgs& A, int32_t token, int32_t c0, int n) {
+  const DY* p = (const DY*)A.dy + (int64_t)token * A.dy_stride + c0;
+  if (n >= 4) {
+    if constexpr (sizeof(DY) == 2) {
+      const u32x2 w = *(const u32x2_a2*)p;
+      return f32x4{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+    } else {
+      return *(const f32x4_a4*)p;
+    }
+  }
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (k < n) v[k] = sizeof(DY) == 2 ? bf16_one(((const uint16_t*)p)[k]) : ((const float*)p)[k];
+  return v;
+}
+
+// Sum of the tokens at places [p, p + m), ascending.
+template <class DY>
+__device__ __forceinline__ f32x4 sum_places(const GradArgs& A, int32_t p, int32_t m, int32_t c0,
+                                            int n) {
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  int32_t j = 0;
+  for (; j + 4 <= m; j += 4) {
+    f32x4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = dy4<DY>(A, A.order[p + j + u].token, c0, n);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) s += v[u];
+  }
+  for (; j < m; ++j) s += dy4<DY>(A, A.order[p + j].token, c0, n);
+  return s;
+}
+
+// One block per window and kind of piece.
+template <class DY>
+__global__ void __launch_bounds__(kThreads) pieces_kernel(const GradArgs A) {
+  __shared__ int32_t found;
+  const int32_t total = A.start[((int64_t)1 << A.slice_bits) * A.local];
+  const int32_t w0 = (int32_t)(blockIdx.x >> 1) * kPiece;
+  const bool first = (blockIdx.x & 1u) != 0;
+  if (w0 >= total) return;
+  if (threadIdx.x == 0) found = -1;
+  __syncthreads();
+  if (threadIdx.x < kPiece && w0 + (int32_t)threadIdx.x < total) {
+    const Entry e = A.order[w0 + threadIdx.x];
+    if (e.count > kPiece && e.rel % kPiece == 0 && (e.rel == 0) == first)
+      found = w0 + (int32_t)threadIdx.x;
+  }
+  __syncthreads();
+  const int32_t p = found;
+  if (p < 0) return;
+  const Entry e = A.order[p];
+  const int32_t m = min(kPiece, e.count - e.rel);
+  float* to = A.partial + slot_of(p, first) * A.cols;
+  for (int32_t c0 = (int32_t)threadIdx.x * 4; c0 < A.cols; c0 += kThreads * 4) {
+    const int n = min(4, A.cols - c0);
+    const f32x4 s = sum_places<DY>(A, p, m, c0, n);
+    if (n >= 4) {
+      *(f32x4_a4*)(to + c0) = s;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < n) to[c0 + k] = s[k];
+    }
+  }
+}
+
+// DENSE: every row of the table; otherwise one row per distinct id, found at
+// its first place.
+template <class DY, bool GAPS, bool DENSE>
+__global__ void __launch_bounds__(kThreads) rows_kernel(const GradArgs A) {
+  const uint32_t units = (uint32_t)A.rows_per_block * A.pieces.d;
+  const int64_t rows = DENSE ? A.vocab : (int64_t)A.start[((int64_t)1 << A.slice_bits) * A.local];
+  for (int64_t b = blockIdx.x; b * A.rows_per_block < rows; b += gridDim.x) {
+    const int64_t r0 = b * A.rows_per_block;
+    for (uint32_t u = threadIdx.x; u < units; u += kThreads) {
+      const uint32_t r = fast_div(u, A.pieces);
+      const int32_t c0 = (int32_t)(u - r * A.pieces.d) * 4;
+      const int64_t x = r0 + r;
+      if (x >= rows) break;
+      int64_t v;
+      int32_t p, count;
+      if constexpr (DENSE) {
+        const int64_t mask = ((int64_t)1 << A.slice_bits) - 1;
+        const int32_t* s = A.start + (x & mask) * A.local + (x >> A.slice_bits);
+        v = x;
+        p = s[0];
+        count = s[1] - p;
+      } else {
+        const Entry e = A.order[x];
+        if (e.rel != 0) continue;
+        v = e.row;
+        p = (int32_t)x;
+        count = e.count;
+      }
+      const int n = min(4, A.cols - c0);
+      f32x4 s = {0.f, 0.f, 0.f, 0.f};
+      if (count <= kPiece) {
+        s = sum_places<DY>(A, p, count, c0, n);
+      } else {
+        for (int32_t j = 0; j < count; j += kPiece) {
+          const float* q = A.partial + slot_of(p + j, j == 0) * A.cols + c0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < n) s[k] += q[k];
+        }
+      }
+      const int64_t i = v * A.cols + c0;
+      if (!GAPS && n >= 4) {
+        grad_store4(A.out, place_at<GAPS>(A.out.place, i), s);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < n) grad_store(A.out, place_at<GAPS>(A.out.place, i + k), s[k]);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host
+struct Plan {
+  uint32_t slice_bits;
+  int64_t slices, local;
+  int64_t start_bytes, order_bytes, partial_bytes, bytes;
+};
+int64_t up16(int64_t n) { return (n + 15) & ~(int64_t)15; }
+
+Plan make_plan(int64_t vocab, int64_t cols, int64_t n) {
+  Plan p;
+  p.slice_bits = 8;
+  while (((int64_t)kMaxLocal << p.slice_bits) < vocab) ++p.slice_bits;
+  p.slices = (int64_t)1 << p.slice_bits;
+  p.local = std::max<int64_t>(1, (vocab + p.slices - 1) / p.slices);
+  p.start_bytes = up16((p.slices * p.local + 1) * 4);
+  p.order_bytes = n * (int64_t)sizeof(Entry);
+  p.partial_bytes = 2 * (n / kPiece + 1) * cols * 4;
+  p.bytes = p.start_bytes + p.order_bytes + p.partial_bytes;
+  return p;
+}
+static_assert(kMinSlices == 1 << 8, "slice_bits starts at 8");
+
+int shape_ok(const zero_layout* L, int32_t tensor, int64_t cols, int64_t n) {
+  if (!L || cols < 1 || n < 0) return ZERO_EINVAL;
+  if (!tensor_ok(L, tensor)) return ZERO_ERANGE;
+  const int64_t numel = L->numel[(size_t)tensor];
+  if (numel % cols != 0) return ZERO_EINVAL;
+  if (cols > ZERO_MAX_COLS || n > ZERO_MAX_ROWS || numel / cols > ZERO_MAX_ROWS) return ZERO_ERANGE;
+  return ZERO_OK;
+}
+
+// Rows of a block: about 4 units per thread, 1 row at least.
+int32_t rows_per_block(int64_t units_per_row) {
+  return (int32_t)std::max<int64_t>(1, 4 * kThreads / std::max<int64_t>(1, units_per_row));
+}
+
+template <class ID, class OUT, bool GAPS>
+int launch_lookup(const LookupArgs& A, hipStream_t s) {
+  const int64_t blocks = ((int64_t)A.n + A.rows_per_block - 1) / A.rows_per_block;
+  // the dispatch grid counts work-items in 32 bits
+  constexpr int64_t kMaxBlocks = (int64_t)1 << 20;
+  LookupArgs B = A;
+  for (int64_t b0 = 0; b0 < blocks; b0 += kMaxBlocks) {
+    const int64_t t0 = b0 * A.rows_per_block;
+    B.ids = (const ID*)A.ids + t0;
+    B.out = (OUT*)A.out + t0 * A.out_stride;
+    B.n = (int32_t)(A.n - t0);
+    hipLaunchKernelGGL((lookup_kernel<ID, OUT, GAPS>), dim3((unsigned)std::min(kMaxBlocks, blocks - b0)),
+                       dim3(kThreads), 0, s, B);
+    const int rc = launched();
+    if (rc != ZERO_OK) return rc;
+  }
+  return ZERO_OK;
+}
+template <class ID, class OUT>
+int launch_lookup(const LookupArgs& A, hipStream_t s) {
+  return A.place.gap ? launch_lookup<ID, OUT, true>(A, s) : launch_lookup<ID, OUT, false>(A, s);
+}
+
+template <class DY, bool GAPS, bool DENSE>
+int launch_rows(const GradArgs& A, hipStream_t s) {
+  const int64_t rows = DENSE ? A.vocab : (int64_t)A.n;
+  const int64_t blocks = (rows + A.rows_per_block - 1) / A.rows_per_block;
+  hipLaunchKernelGGL((rows_kernel<DY, GAPS, DENSE>),
+                     dim3((unsigned)std::min<int64_t>(blocks, 1 << 20)), dim3(kThreads), 0, s, A);
+  return launched();
+}
+
+template <class DY>
+int launch_grad(const GradArgs& A, bool dense, hipStream_t s) {
+  if (A.n > kPiece) {
+    hipLaunchKernelGGL(pieces_kernel<DY>, dim3(2 * (unsigned)((A.n + kPiece - 1) / kPiece)),
+                       dim3(kThreads), 0, s, A);
+    const int rc = launched();
+    if (rc != ZERO_OK) return rc;
+  }
+  const bool gaps = A.out.place.gap != 0;
+  if (dense) return gaps ? launch_rows<DY, true, true>(A, s) : launch_rows<DY, false, true>(A, s);
+  return gaps ? launch_rows<DY, true, false>(A, s) : launch_rows<DY, false, false>(A, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+int zero_embedding_lookup(const zero_layout* L, int32_t tensor, int64_t cols,
+                          const uint16_t* params_flat, const void* ids, int32_t id_bytes,
+                          int64_t n_ids, float scale, void* out, int64_t out_stride,
+                          int32_t out_dtype, hipStream_t stream) {
+  const int rc = shape_ok(L, tensor, cols, n_ids);
+  if (rc != ZERO_OK) return rc;
+  if ((id_bytes != 4 && id_bytes != 8) || (out_dtype != ZERO_DTYPE_BF16 && out_dtype != ZERO_DTYPE_F32))
+    return ZERO_EINVAL;
+  if (!(scale - scale == 0.0f)) return ZERO_EINVAL;
+  if (n_ids == 0) return ZERO_OK;
+  const int64_t numel = L->numel[(size_t)tensor];
+  if (!ids || !out || (numel > 0 && !params_flat) || out_stride < cols) return ZERO_EINVAL;
+  if (out_stride > ZERO_MAX_STRIDE) return ZERO_ERANGE;
+  LookupArgs A;
+  int64_t lo, hi;
+  A.place = make_place(L, tensor, &lo, &hi);
+  const Bytes outs[] = {rows_of(out, n_ids, cols, out_stride, out_dtype == ZERO_DTYPE_F32 ? 4 : 2)};
+  const Bytes ins[] = {Bytes{params_flat ? params_flat + lo : nullptr, 2 * (hi - lo)},
+                       Bytes{ids, n_ids * id_bytes}};
+  if (any_overlap(outs, ins)) return ZERO_EOVERLAP;
+  if (hip_error_pending()) return ZERO_EHIP;
+  A.params = params_flat;
+  A.ids = ids;
+  A.out = out;
+  A.out_stride = out_stride;
+  A.vocab = numel / cols;
+  A.n = (int32_t)n_ids;
+  A.cols = (int32_t)cols;
+  A.pieces = make_fast_div((uint32_t)((cols + 7) / 8));
+  A.rows_per_block = rows_per_block(A.pieces.d);
+  A.scale = scale;
+  if (id_bytes == 4)
+    return out_dtype == ZERO_DTYPE_F32 ? launch_lookup<int32_t, float>(A, stream)
+                                       : launch_lookup<int32_t, uint16_t>(A, stream);
+  return out_dtype == ZERO_DTYPE_F32 ? launch_lookup<int64_t, float>(A, stream)
+                                     : launch_lookup<int64_t, uint16_t>(A, stream);
+}
+
+int64_t zero_embedding_grad_workspace(const zero_layout* L, int32_t tensor, int64_t cols,
+                                      int64_t n_ids) {
+  const int rc = shape_ok(L, tensor, cols, n_ids);
+  if (rc != ZERO_OK) return rc;
+  return make_plan(L->numel[(size_t)tensor] / cols, cols, n_ids).bytes;
+}
+
+int zero_embedding_grad(const zero_layout* L, int32_t tensor, int64_t cols, const void* ids,
+                        int32_t id_bytes, int64_t n_ids, const void* dy, int64_t dy_stride,
+                        int32_t dy_dtype, float scale, uint32_t flags, float* acc_flat,
+                        uint16_t* bf16_flat, void* workspace, int64_t workspace_bytes,
+                        hipStream_t stream) {
+  int rc = shape_ok(L, tensor, cols, n_ids);
+  if (rc != ZERO_OK) return rc;
+  if ((id_bytes != 4 && id_bytes != 8) || (dy_dtype != ZERO_DTYPE_BF16 && dy_dtype != ZERO_DTYPE_F32))
+    return ZERO_EINVAL;
+  const int64_t numel = L->numel[(size_t)tensor];
+  rc = grad_out_ok(flags, scale, acc_flat, bf16_flat, numel);
+  if (rc != ZERO_OK) return rc;
+  const bool dense = (flags & (ZERO_ACC_OVERWRITE | ZERO_ACC_EMIT_BF16)) != 0;
+  if (numel == 0 || (n_ids == 0 && !dense)) return ZERO_OK;
+  if (n_ids > 0 && (!ids || !dy || dy_stride < cols)) return ZERO_EINVAL;
+  if (dy_stride > ZERO_MAX_STRIDE) return ZERO_ERANGE;
+  const Plan p = make_plan(numel / cols, cols, n_ids);
+  if (!workspace || workspace_bytes < p.bytes || ((uintptr_t)workspace & 15u)) return ZERO_EINVAL;
+  GradArgs A;
+  int64_t lo, hi;
+  A.out.place = make_place(L, tensor, &lo, &hi);
+  const Bytes outs[] = {Bytes{acc_used(flags) ? acc_flat + lo : nullptr, 4 * (hi - lo)},
+                        Bytes{(flags & ZERO_ACC_EMIT_BF16) ? bf16_flat + lo : nullptr, 2 * (hi - lo)},
+                        Bytes{workspace, p.bytes}};
+  const Bytes ins[] = {Bytes{ids, n_ids * id_bytes},
+                       rows_of(dy, n_ids, cols, dy_stride, dy_dtype == ZERO_DTYPE_F32 ? 4 : 2)};
+  if (any_overlap(outs, ins)) return ZERO_EOVERLAP;
+  if (hip_error_pending()) return ZERO_EHIP;
+
+  PlanArgs P;
+  P.ids = ids;
+  P.vocab = numel / cols;
+  P.n = (int32_t)n_ids;
+  P.local = (int32_t)p.local;
+  P.slice_bits = p.slice_bits;
+  P.start = (int32_t*)workspace;
+  P.order = (Entry*)((char*)workspace + p.start_bytes);
+  if (id_bytes == 4)
+    hipLaunchKernelGGL(plan_kernel<int32_t>, dim3((unsigned)p.slices), dim3(kPlanThreads), 0, stream, P);
+  else
+    hipLaunchKernelGGL(plan_kernel<int64_t>, dim3((unsigned)p.slices), dim3(kPlanThreads), 0, stream, P);
+  rc = launched();
+  if (rc != ZERO_OK) return rc;
+
+  A.dy = dy;
+  A.dy_stride = dy_stride;
+  A.start = P.start;
+  A.order = P.order;
+  A.partial = (float*)((char*)workspace + p.start_bytes + p.order_bytes);
+  A.out.acc = acc_flat;
+  A.out.out = bf16_flat;
+  A.out.scale = scale;
+  A.out.flags = flags;
+  A.vocab = P.vocab;
+  A.n = P.n;
+  A.cols = (int32_t)cols;
+  A.local = P.local;
+  A.slice_bits = P.slice_bits;
+  A.pieces = make_fast_div((uint32_t)((cols + 3) / 4));
+  A.rows_per_block = rows_per_block(A.pieces.d);
+  return dy_dtype == ZERO_DTYPE_F32 ? launch_grad<float>(A, dense, stream)
+                                    : launch_grad<uint16_t>(A, dense, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,437 @@
+// zero_rms_norm and zero_rms_norm_grad.
+//
+// Page "Infra: Data Parallel" (pufanyi.com), section "Zero Redundancy
+// Optimizer (ZeRO)": the norm's weight is read from the flat buffer of
+// gathered parameters; section "Naive Data Parallelism": its gradient is
+// added to the rank's sum over micro-batches.
+//
+//   forward   h = bf16(x + r);  R = 1 / sqrt(mean(h^2) + eps);  y = act8(h*R*w)
+//   backward  g = dy*w;  c = mean(g*h) * R^2;  dx = bf16(dh + R*(g - c*h))
+//             dw = sum over rows of dy*h*R
+// (the rounding of y to 8 bits is passed straight through).  Everything
+// between the loads and the stores is binary32.
+//
+// Both are HBM streams: each row is read once and stays in registers between
+// its statistics and its output, 8 consecutive columns per lane and piece; 16
+// lanes of a DPP row hold one block of 128 columns of the 8-bit output.  A
+// row takes 64 to 1024 threads, so that a thread keeps at most 32 columns.
+// The weight's gradient is summed over a fixed number of row groups in
+// registers, and over the groups, in order, by a second launch: the same sum
+// in every run.
+#include <algorithm>
+
+#include "act8.hpp"
+
+namespace {
+using namespace zs;
+
+constexpr int kMaxNormCols = ZERO_MAX_NORM_COLS;
+
+// 8 bf16 values, as loaded.
+struct Piece8 {
+  u32x4 w;
+};
+__device__ __forceinline__ Piece8 load8(const uint16_t* p, int n) {
+  if (n >= 8) return Piece8{*(const u32x4_a2*)p};
+  u32x4 w = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (k < n) w[k >> 1] |= (uint32_t)p[k] << (16 * (k & 1));
+  return Piece8{w};
+}
+__device__ __forceinline__ void store8(uint16_t* p, u32x4 w, int n) {
+  if (n >= 8) {
+    *(u32x4_a2*)p = w;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) p[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+  }
+}
+__device__ __forceinline__ float at8(const Piece8& p, int k) {
+  return (k & 1) ? bf16_hi(p.w[k >> 1]) : bf16_lo(p.w[k >> 1]);
+}
+__device__ __forceinline__ u32x4 round8(const float (&x)[8]) {
+  return u32x4{bf16_pack2(x[0], x[1]), bf16_pack2(x[2], x[3]), bf16_pack2(x[4], x[5]),
+               bf16_pack2(x[6], x[7])};
+}
+template <bool GAPS>
+__device__ __forceinline__ Piece8 weight8(const uint16_t* params, const Place& pl, int c0, int n) {
+  if (!GAPS) return load8(params + pl.x0 + c0, n);
+  u32x4 w = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (k < n) w[k >> 1] |= (uint32_t)params[place_at<GAPS>(pl, c0 + k)] << (16 * (k & 1));
+  return Piece8{w};
+}
+
+// Sum over the NT threads of a row; `slot`: NT/64 floats of LDS of this row,
+// not read by anyone else until the next barrier.
+template <int NT>
+__device__ __forceinline__ float row_sum(float x, float* slot) {
+#pragma unroll
+  for (int k = 32; k; k >>= 1) x += __shfl_xor(x, k, 64);
+  if constexpr (NT > 64) {
+    const int w = (threadIdx.x % NT) >> 6;
+    if ((threadIdx.x & 63) == 0) slot[w] = x;
+    __syncthreads();
+    x = 0.f;
+#pragma unroll
+    for (int k = 0; k < NT / 64; ++k) x += slot[k];
+  }
+  return x;
+}
+
+// Threads of a block for a row of NT threads: rows of one wave share a block.
+template <int NT>
+constexpr int kBlock = NT < 256 ? 256 : NT;
+
+struct NormArgs {
+  const uint16_t *params, *x, *res;
+  int64_t x_stride, res_stride;
+  Place place;
+  uint16_t *h, *y;
+  float* rstd;
+  uint8_t *codes, *scales;
+  int64_t rows;
+  int32_t cols, nb;
+  float eps;
+};
+
+template <int NT, int NP, bool GAPS>
+__global__ void __launch_bounds__(kBlock<NT>) norm_kernel(const NormArgs A) {
+  constexpr int kRows = kBlock<NT> / NT;
+  __shared__ float red[2][kBlock<NT> / 64];
+  const int tid = threadIdx.x % NT, sub = threadIdx.x / NT;
+  Piece8 w[NP];
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    const int c0 = (k * NT + tid) * 8;
+    w[k] = weight8<GAPS>(A.params, A.place, c0, A.cols - c0);
+  }
+  int turn = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < A.rows; r0 += (int64_t)gridDim.x * kRows) {
+    const int64_t r = r0 + sub;
+    const bool live = r < A.rows;
+    Piece8 h[NP];
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int c0 = (k * NT + tid) * 8, n = live ? A.cols - c0 : 0;
+      h[k] = load8(A.x + r * A.x_stride + c0, n);
+      if (A.res) {
+        const Piece8 b = load8(A.res + r * A.res_stride + c0, n);
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = at8(h[k], j) + at8(b, j);
+        h[k].w = round8(v);
+      }
+      if (A.h) store8(A.h + r * A.cols + c0, h[k].w, n);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss += at8(h[k], j) * at8(h[k], j);
+    }
+    // two slots in turn: a wave may write the next row's sum while another
+    // still reads this one's
+    ss = row_sum<NT>(ss, &red[turn][0]);
+    turn ^= 1;
+    const float rstd = 1.0f / __builtin_sqrtf(ss / (float)A.cols + A.eps);
+    if (live && tid == 0) A.rstd[r] = rstd;
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int c0 = (k * NT + tid) * 8, n = live ? A.cols - c0 : 0;
+      float v[8];
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = at8(h[k], j) * rstd * at8(w[k], j);
+        m = max(m, j < n ? finite_mag(v[j]) : 0u);
+      }
+      const uint32_t e = act8_byte(max16(m));
+      const float inv = act8_inv(e);
+      const u32x2 q = {act8_pack4(v, inv), act8_pack4(v + 4, inv)};
+      uint8_t* qp = A.codes + r * A.cols + c0;
+      if (n >= 8) {
+        *(u32x2_a1*)qp = q;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < n) qp[j] = (uint8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+      }
+      if ((tid & 15) == 0 && n > 0) A.scales[r * A.nb + (c0 >> 7)] = (uint8_t)e;
+      if (A.y) {
+        const float s = act8_scale(e);
+        const u32x2 a = act8_bf16x4(q.x, s), b = act8_bf16x4(q.y, s);
+        store8(A.y + r * A.cols + c0, u32x4{a.x, a.y, b.x, b.y}, n);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ backward
+struct NormGradArgs {
+  const uint16_t *params, *dy, *dh, *h;
+  int64_t dy_stride, dh_stride;
+  Place place;
+  const float* rstd;
+  uint16_t* dx;
+  float* partial;  // groups x cols
+  int64_t rows, rows_per_group;
+  int32_t cols;
+};
+
+// One block per group of consecutive rows.
+template <int NT, int NP, bool GAPS>
+__global__ void __launch_bounds__(NT) norm_grad_kernel(const NormGradArgs A) {
+  __shared__ float red[2][NT / 64];
+  const int tid = threadIdx.x;
+  Piece8 w[NP];
+  float dw[NP][8];
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    const int c0 = (k * NT + tid) * 8;
+    w[k] = weight8<GAPS>(A.params, A.place, c0, A.cols - c0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[k][j] = 0.f;
+  }
+  const int64_t ra = (int64_t)blockIdx.x * A.rows_per_group;
+  const int64_t rz = min(A.rows, ra + A.rows_per_group);
+  int turn = 0;
+  for (int64_t r = ra; r < rz; ++r) {
+    Piece8 dy[NP], h[NP], dh[NP];
+    const float R = A.rstd[r];
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int c0 = (k * NT + tid) * 8, n = A.cols - c0;
+      dy[k] = load8(A.dy + r * A.dy_stride + c0, n);
+      h[k] = load8(A.h + r * A.cols + c0, n);
+      if (A.dh) dh[k] = load8(A.dh + r * A.dh_stride + c0, n);
+    }
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = at8(dy[k], j), x = at8(h[k], j);
+        s += d * at8(w[k], j) * x;
+        dw[k][j] += d * x * R;
+      }
+    }
+    s = row_sum<NT>(s, &red[turn][0]);
+    turn ^= 1;
+    const float c = s / (float)A.cols * R * R;
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int c0 = (k * NT + tid) * 8, n = A.cols - c0;
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float g = at8(dy[k], j) * at8(w[k], j);
+        const float d = R * (g - c * at8(h[k], j));
+        v[j] = A.dh ? at8(dh[k], j) + d : d;
+      }
+      store8(A.dx + r * A.cols + c0, round8(v), n);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    const int c0 = (k * NT + tid) * 8, n = A.cols - c0;
+    float* p = A.partial + (int64_t)blockIdx.x * A.cols + c0;
+    if (n >= 8) {
+      *(f32x4_a4*)p = f32x4{dw[k][0], dw[k][1], dw[k][2], dw[k][3]};
+      *(f32x4_a4*)(p + 4) = f32x4{dw[k][4], dw[k][5], dw[k][6], dw[k][7]};
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) p[j] = dw[k][j];
+    }
+  }
+}
+
+// Sum over the groups: 32 columns per block, 32 threads per column, each
+// taking every 32nd group in order; then the 32 sums in order.
+constexpr int kSumCols = 32, kSumWays = 32;
+template <bool GAPS>
+__global__ void __launch_bounds__(kSumCols* kSumWays)
+    norm_sum_kernel(const float* partial, int32_t groups, int32_t cols, const GradOut out) {
+  __shared__ float part[kSumWays][kSumCols + 1];
+  const int c = threadIdx.x % kSumCols, way = threadIdx.x / kSumCols;
+  const int32_t col = (int32_t)blockIdx.x * kSumCols + c;
+  float s = 0.f;
+  if (col < cols) {
+#pragma unroll 4
+    for (int32_t g = way; g < groups; g += kSumWays) s += partial[(int64_t)g * cols + col];
+  }
+  part[way][c] = s;
+  __syncthreads();
+  if (way == 0 && col < cols) {
+    float t = 0.f;
+#pragma unroll
+    for (int k = 0; k < kSumWays; ++k) t += part[k][c];
+    grad_store(out, place_at<GAPS>(out.place, col), t);
+  }
+}
+
+// ------------------------------------------------------------------ host
+// Row groups of the weight's gradient: a function of the shape alone, so the
+// order of the sum is too.
+constexpr int64_t kMaxGroups = 512;
+int64_t rows_per_group(int64_t rows) {
+  return std::max<int64_t>(4, (rows + kMaxGroups - 1) / kMaxGroups);
+}
+int64_t groups_of(int64_t rows) {
+  return rows == 0 ? 0 : (rows + rows_per_group(rows) - 1) / rows_per_group(rows);
+}
+
+int shape_ok(const zero_layout* L, int32_t tensor, int64_t rows) {
+  if (!L || rows < 0) return ZERO_EINVAL;
+  if (!tensor_ok(L, tensor)) return ZERO_ERANGE;
+  const int64_t cols = L->numel[(size_t)tensor];
+  if (cols > kMaxNormCols || rows > ZERO_MAX_ROWS) return ZERO_ERANGE;
+  return ZERO_OK;
+}
+
+template <int NT, int NP>
+int launch_norm(const NormArgs& A, hipStream_t s) {
+  constexpr int kRows = kBlock<NT> / NT;
+  const unsigned grid = (unsigned)std::min<int64_t>((A.rows + kRows - 1) / kRows, 1 << 14);
+  if (A.place.gap)
+    hipLaunchKernelGGL((norm_kernel<NT, NP, true>), dim3(grid), dim3(kBlock<NT>), 0, s, A);
+  else
+    hipLaunchKernelGGL((norm_kernel<NT, NP, false>), dim3(grid), dim3(kBlock<NT>), 0, s, A);
+  return launched();
+}
+template <int NT, int NP>
+int launch_norm_grad(const NormGradArgs& A, int64_t groups, hipStream_t s) {
+  if (A.place.gap)
+    hipLaunchKernelGGL((norm_grad_kernel<NT, NP, true>), dim3((unsigned)groups), dim3(NT), 0, s, A);
+  else
+    hipLaunchKernelGGL((norm_grad_kernel<NT, NP, false>), dim3((unsigned)groups), dim3(NT), 0, s, A);
+  return launched();
+}
+
+}  // namespace
+
+extern "C" {
+
+int zero_rms_norm(const zero_layout* L, int32_t tensor, const uint16_t* params_flat,
+                  const uint16_t* x, int64_t x_stride, const uint16_t* res, int64_t res_stride,
+                  int64_t rows, float eps, uint16_t* h, float* rstd, uint8_t* codes,
+                  uint8_t* scales, uint16_t* y, hipStream_t stream) {
+  const int rc = shape_ok(L, tensor, rows);
+  if (rc != ZERO_OK) return rc;
+  if (!(eps >= 0.0f) || !(eps - eps == 0.0f)) return ZERO_EINVAL;
+  const int64_t cols = L->numel[(size_t)tensor];
+  if (rows == 0 || cols == 0) return ZERO_OK;
+  if (!params_flat || !x || !rstd || !codes || !scales || (res && !h)) return ZERO_EINVAL;
+  if (x_stride < cols || (res && res_stride < cols)) return ZERO_EINVAL;
+  if (x_stride > ZERO_MAX_STRIDE || (res && res_stride > ZERO_MAX_STRIDE)) return ZERO_ERANGE;
+  NormArgs A;
+  int64_t lo, hi;
+  A.place = make_place(L, tensor, &lo, &hi);
+  const int64_t nb = (cols + kAct8Block - 1) / kAct8Block;
+  const Bytes outs[] = {Bytes{h, 2 * rows * cols}, Bytes{y, 2 * rows * cols}, Bytes{rstd, 4 * rows},
+                        Bytes{codes, rows * cols}, Bytes{scales, rows * nb}};
+  const Bytes ins[] = {Bytes{params_flat + lo, 2 * (hi - lo)}, rows_of(x, rows, cols, x_stride, 2),
+                       rows_of(res, rows, cols, res_stride, 2)};
+  if (any_overlap(outs, ins)) return ZERO_EOVERLAP;
+  if (hip_error_pending()) return ZERO_EHIP;
+  A.params = params_flat;
+  A.x = x;
+  A.res = res;
+  A.x_stride = x_stride;
+  A.res_stride = res_stride;
+  A.h = h;
+  A.y = y;
+  A.rstd = rstd;
+  A.codes = codes;
+  A.scales = scales;
+  A.rows = rows;
+  A.cols = (int32_t)cols;
+  A.nb = (int32_t)nb;
+  A.eps = eps;
+  if (cols <= 512) return launch_norm<64, 1>(A, stream);
+  if (cols <= 1024) return launch_norm<64, 2>(A, stream);
+  if (cols <= 2048) return launch_norm<256, 1>(A, stream);
+  if (cols <= 4096) return launch_norm<256, 2>(A, stream);
+  if (cols <= 8192) return launch_norm<256, 4>(A, stream);
+  if (cols <= 16384) return launch_norm<512, 4>(A, stream);
+  return launch_norm<1024, 4>(A, stream);
+}
+
+int64_t zero_rms_norm_grad_workspace(const zero_layout* L, int32_t tensor, int64_t rows) {
+  const int rc = shape_ok(L, tensor, rows);
+  if (rc != ZERO_OK) return rc;
+  return groups_of(rows) * L->numel[(size_t)tensor] * 4;
+}
+
+int zero_rms_norm_grad(const zero_layout* L, int32_t tensor, const uint16_t* params_flat,
+                       const uint16_t* dy, int64_t dy_stride, const uint16_t* dh,
+                       int64_t dh_stride, const uint16_t* h, const float* rstd, int64_t rows,
+                       float scale, uint32_t flags, uint16_t* dx, float* acc_flat,
+                       uint16_t* bf16_flat, void* workspace, int64_t workspace_bytes,
+                       hipStream_t stream) {
+  int rc = shape_ok(L, tensor, rows);
+  if (rc != ZERO_OK) return rc;
+  const int64_t cols = L->numel[(size_t)tensor];
+  rc = grad_out_ok(flags, scale, acc_flat, bf16_flat, cols);
+  if (rc != ZERO_OK) return rc;
+  // without rows the gradient is zero, which changes something only where
+  // the flags ask for an overwrite or an emission
+  if (cols == 0 || (rows == 0 && !(flags & (ZERO_ACC_OVERWRITE | ZERO_ACC_EMIT_BF16)))) return ZERO_OK;
+  const int64_t groups = groups_of(rows), need = groups * cols * 4;
+  if (rows > 0) {
+    if (!params_flat || !dy || !h || !rstd || !dx || !workspace) return ZERO_EINVAL;
+    if (dy_stride < cols || (dh && dh_stride < cols)) return ZERO_EINVAL;
+    if (dy_stride > ZERO_MAX_STRIDE || (dh && dh_stride > ZERO_MAX_STRIDE)) return ZERO_ERANGE;
+    if (workspace_bytes < need || ((uintptr_t)workspace & 15u)) return ZERO_EINVAL;
+  }
+  NormGradArgs A;
+  GradOut out;
+  int64_t lo, hi;
+  out.place = A.place = make_place(L, tensor, &lo, &hi);
+  const Bytes outs[] = {Bytes{dx, 2 * rows * cols},
+                        Bytes{acc_used(flags) ? acc_flat + lo : nullptr, 4 * (hi - lo)},
+                        Bytes{(flags & ZERO_ACC_EMIT_BF16) ? bf16_flat + lo : nullptr, 2 * (hi - lo)},
+                        Bytes{workspace, need}};
+  const Bytes ins[] = {Bytes{params_flat ? params_flat + lo : nullptr, 2 * (hi - lo)},
+                       rows_of(dy, rows, cols, dy_stride, 2), rows_of(dh, rows, cols, dh_stride, 2),
+                       Bytes{h, 2 * rows * cols}, Bytes{rstd, 4 * rows}};
+  if (any_overlap(outs, ins)) return ZERO_EOVERLAP;
+  if (hip_error_pending()) return ZERO_EHIP;
+  if (rows > 0) {
+    A.params = params_flat;
+    A.dy = dy;
+    A.dh = dh;
+    A.h = h;
+    A.dy_stride = dy_stride;
+    A.dh_stride = dh_stride;
+    A.rstd = rstd;
+    A.dx = dx;
+    A.partial = (float*)workspace;
+    A.rows = rows;
+    A.rows_per_group = rows_per_group(rows);
+    A.cols = (int32_t)cols;
+    if (cols <= 512) rc = launch_norm_grad<64, 1>(A, groups, stream);
+    else if (cols <= 1024) rc = launch_norm_grad<128, 1>(A, groups, stream);
+    else if (cols <= 2048) rc = launch_norm_grad<256, 1>(A, groups, stream);
+    else if (cols <= 4096) rc = launch_norm_grad<256, 2>(A, groups, stream);
+    else if (cols <= 8192) rc = launch_norm_grad<512, 2>(A, groups, stream);
+    else if (cols <= 16384) rc = launch_norm_grad<1024, 2>(A, groups, stream);
+    else rc = launch_norm_grad<1024, 4>(A, groups, stream);
+    if (rc != ZERO_OK) return rc;
+  }
+  out.acc = acc_flat;
+  out.out = bf16_flat;
+  out.scale = scale;
+  out.flags = flags;
+  const unsigned grid = (unsigned)((cols + kSumCols - 1) / kSumCols);
+  if (out.place.gap)
+    hipLaunchKernelGGL(norm_sum_kernel<true>, dim3(grid), dim3(kSumCols * kSumWays), 0, stream,
+                       (const float*)workspace, (int32_t)groups, (int32_t)cols, out);
+  else
+    hipLaunchKernelGGL(norm_sum_kernel<false>, dim3(grid), dim3(kSumCols * kSumWays), 0, stream,
+                       (const float*)workspace, (int32_t)groups, (int32_t)cols, out);
+  return launched();
+}
+
+}  // extern "C"

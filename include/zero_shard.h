@@ -426,6 +426,140 @@ int zero_placement_plan(int32_t n, const int64_t* nbytes, const double* traffic,
  * {s, rho, a_wd, B1, C1, B2, C2, E}.  Errors: ZERO_EINVAL. */
 int zero_step_scalars(const zero_adamw* hp, int64_t t, float out[8]);
 
+/* ------------------------------------------------ gradients of a micro-batch
+ * ("Naive Data Parallelism": without synchronisation the gradients of a
+ * micro-batch are added to the rank's own sum, each scaled by 1/n_micro;
+ * "Zero Redundancy Optimizer (ZeRO)": the updated 16-bit parameters are
+ * gathered before the forward pass.)
+ *
+ * The calls below stand on both sides of the step: they read parameters out
+ * of the gathered flat buffer (P bf16 values, the All-Gather output) and put
+ * parameter gradients into the rank's flat accumulator (P floats), so that a
+ * table's, a norm's or a linear weight's gradient needs no tensor of its own,
+ * no zero_bucket_pack and no zero_grad_accumulate.  `tensor` is the
+ * parameter's index in the layout; its elements are found at their flat
+ * positions (zero_layout_tensor_flat), also where bucket padding falls inside
+ * the tensor.  Nothing else of a flat buffer is read or written, padding
+ * included.
+ *
+ * Gradients take `scale` and the flags of zero_grad_accumulate: for every
+ * element g of the tensor's gradient (summed in binary32),
+ *   a = OVERWRITE ? scale*g : acc + scale*g   (product, sum: one rounding each)
+ * then acc = a unless NO_STORE, and bf16_flat = bf16(a) if EMIT_BF16.
+ * acc_flat_dev may be NULL only with OVERWRITE|NO_STORE, bf16_flat_dev unless
+ * EMIT_BF16.
+ *
+ * Matrices are rows of consecutive columns; a stride is the distance of two
+ * rows in elements (at least the number of columns); matrices without a
+ * stride argument are dense.  Any alignment is accepted.  No outputs may
+ * overlap each other or an input; in particular nothing works in place.
+ * A workspace (16-byte aligned, of the bytes that the call's _workspace
+ * function gives for the same sizes) holds intermediate sums: its contents
+ * before and after a call mean nothing, and two calls that may run at the
+ * same time (or two captured graphs that may be replayed at the same time)
+ * need a workspace each.  The _workspace functions run on the host only and
+ * return bytes, or a negative status.
+ *
+ * Sums have a fixed order: the same call gives the same bits every time.
+ * Common errors: ZERO_EINVAL (null pointer, negative size, sizes that do not
+ * multiply to the tensor's element count, a stride below the row's length,
+ * bad enum or flag, scale not finite, workspace too small or misaligned),
+ * ZERO_ERANGE (tensor index; more than ZERO_MAX_ROWS rows, ZERO_MAX_COLS
+ * columns or a stride above ZERO_MAX_STRIDE), ZERO_EOVERLAP, ZERO_EHIP. */
+#define ZERO_MAX_ROWS (1 << 30)
+#define ZERO_MAX_COLS (1 << 24)
+#define ZERO_MAX_STRIDE (1 << 24)
+
+/* Activations in 8 bits (checkpoints for the backward pass).
+ *
+ * codes: rows x cols bytes, e4m3 (OCP: largest value 448, a NaN, no
+ * infinities).  scales: rows x ceil(cols / ZERO_ACT8_BLOCK) bytes e, one for
+ * each block of 128 columns of a row (the last block may be shorter); a code
+ * c of the block stands for the value c * 2^(e-127).
+ *
+ * pack: with a = m*2^k (1 <= m < 2) the largest finite magnitude of the
+ * block, e = max(10, 127 + k - 8 + (m > 1.75 ? 1 : 0)); a block without one
+ * has e = 10.  A code is x * 2^(127-e) rounded to nearest, ties to even: no
+ * finite value saturates.  Infinities and NaN become NaN codes and leave
+ * their block's other values as they are.
+ * unpack: the values, in bf16 or binary32, exactly (e of 10 to 247, as pack
+ * writes them; other bytes give unspecified values).  The one value beyond
+ * both types' range is 2^128, which magnitudes from 1.9375 * 2^127 round to:
+ * it reads back as infinity.
+ *
+ * dtype: ZERO_DTYPE_BF16 or ZERO_DTYPE_F32, the type of x / out.  Moves 3 or
+ * 5 bytes per element. */
+#define ZERO_ACT8_BLOCK 128
+int zero_act8_pack(const void* x_dev, int32_t dtype, int64_t rows, int64_t cols, int64_t x_stride,
+                   uint8_t* codes_dev, uint8_t* scales_dev, hipStream_t stream);
+int zero_act8_unpack(const uint8_t* codes_dev, const uint8_t* scales_dev, int64_t rows,
+                     int64_t cols, void* out_dev, int32_t dtype, int64_t out_stride,
+                     hipStream_t stream);
+
+/* Embedding.  The tensor is a table of numel / cols rows of cols elements.
+ * ids: n_ids token ids of id_bytes (4 or 8) bytes each, signed.  An id
+ * outside [0, numel / cols) marks a place without a token.
+ *
+ * lookup: out[t] = scale * E[id_t] in binary32, rounded to out_dtype; a row of
+ * zeros for a place without a token.
+ * grad: dE[v] = sum over t with id_t = v, t ascending, of dY[t]: in pieces of
+ * 64 tokens, then over the pieces.  Places without a token add nothing.  With
+ * flags 0 only the rows of ids that occur are touched; OVERWRITE and
+ * EMIT_BF16 cover every row of the table, absent ids having a zero gradient. */
+int zero_embedding_lookup(const zero_layout* layout, int32_t tensor, int64_t cols,
+                          const uint16_t* params_flat_dev, const void* ids_dev, int32_t id_bytes,
+                          int64_t n_ids, float scale, void* out_dev, int64_t out_stride,
+                          int32_t out_dtype, hipStream_t stream);
+int64_t zero_embedding_grad_workspace(const zero_layout* layout, int32_t tensor, int64_t cols,
+                                      int64_t n_ids);
+int zero_embedding_grad(const zero_layout* layout, int32_t tensor, int64_t cols,
+                        const void* ids_dev, int32_t id_bytes, int64_t n_ids, const void* dy_dev,
+                        int64_t dy_stride, int32_t dy_dtype, float scale, uint32_t flags,
+                        float* acc_flat_dev, uint16_t* bf16_flat_dev, void* workspace_dev,
+                        int64_t workspace_bytes, hipStream_t stream);
+
+/* Root-mean-square norm.  The tensor is the weight w of cols = numel elements
+ * (at most ZERO_MAX_NORM_COLS, else ZERO_ERANGE).
+ *
+ * forward, for every row: h = bf16(x + res) (res NULL: h = x),
+ *   rstd = 1 / sqrt(mean(h^2) + eps), and h * rstd * w in the 8-bit format of
+ *   zero_act8_pack.  h_dev: the new residual (may be NULL if res is);
+ *   y_dev: NULL, or the bf16 values that the codes stand for, so that the
+ *   forward product reads exactly what the backward product will.
+ * grad, for every row, with g = dy * w:
+ *   dx = bf16(dh + rstd * (g - h * rstd^2 * mean(g * h)))   (dh NULL: 0)
+ *   which is the gradient of both x and res; the weight's gradient is the sum
+ *   over the rows of dy * h * rstd.  The rounding to 8 bits counts as the
+ *   identity.  h_dev is the forward pass's h (x where there was none). */
+#define ZERO_MAX_NORM_COLS 32768
+int zero_rms_norm(const zero_layout* layout, int32_t tensor, const uint16_t* params_flat_dev,
+                  const uint16_t* x_dev, int64_t x_stride, const uint16_t* res_dev,
+                  int64_t res_stride, int64_t rows, float eps, uint16_t* h_dev, float* rstd_dev,
+                  uint8_t* codes_dev, uint8_t* scales_dev, uint16_t* y_dev, hipStream_t stream);
+int64_t zero_rms_norm_grad_workspace(const zero_layout* layout, int32_t tensor, int64_t rows);
+int zero_rms_norm_grad(const zero_layout* layout, int32_t tensor, const uint16_t* params_flat_dev,
+                       const uint16_t* dy_dev, int64_t dy_stride, const uint16_t* dh_dev,
+                       int64_t dh_stride, const uint16_t* h_dev, const float* rstd_dev,
+                       int64_t rows, float scale, uint32_t flags, uint16_t* dx_dev,
+                       float* acc_flat_dev, uint16_t* bf16_flat_dev, void* workspace_dev,
+                       int64_t workspace_bytes, hipStream_t stream);
+
+/* A linear weight's gradient from an 8-bit checkpoint of the layer's input.
+ *
+ * dW[o, i] = sum over tokens t of dY[t, o] * X[t, i]; the tensor holds
+ * (out_features, in_features), or with transposed = 1 (in_features,
+ * out_features).  dY: bf16.  X: codes and scales of zero_act8_pack or
+ * zero_rms_norm, tokens x in_features.  Products are exact, sums binary32 in
+ * the matrix cores (their order depends on the sizes alone). */
+int64_t zero_linear_grad_workspace(const zero_layout* layout, int32_t tensor, int32_t transposed,
+                                   int64_t out_features, int64_t in_features, int64_t tokens);
+int zero_linear_grad(const zero_layout* layout, int32_t tensor, int32_t transposed,
+                     const uint16_t* dy_dev, int64_t dy_stride, const uint8_t* codes_dev,
+                     const uint8_t* scales_dev, int64_t tokens, int64_t out_features,
+                     int64_t in_features, float scale, uint32_t flags, float* acc_flat_dev,
+                     uint16_t* bf16_flat_dev, void* workspace_dev, int64_t workspace_bytes,
+                     hipStream_t stream);
+
 /* Static description of a status code. */
 const char* zero_strerror(int status);
 
