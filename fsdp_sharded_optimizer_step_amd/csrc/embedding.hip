@@ -121,6 +121,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kMaxLocal = 1024;  // ids of one slice: 16 waves x 1024 counters, 64 KiB of LDS
 constexpr int kMinSlices = 256;  // one block per CU
+constexpr int kBatch = 16;
 
 struct PlanArgs {
   const void* ids;
@@ -140,20 +141,31 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs A) {
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int64_t slice = blockIdx.x;
   const int64_t mask = ((int64_t)1 << A.slice_bits) - 1;
-  for (int k = tid; k < kPlanWaves * A.local; k += kPlanThreads)
-    cnt[k / A.local][k % A.local] = 0;
+  if (tid < A.local)
+    for (int w = 0; w < kPlanWaves; ++w) cnt[w][tid] = 0;
   __syncthreads();
   // each wave counts its own contiguous part of the tokens
   const int64_t per = ((int64_t)A.n + kPlanThreads - 1) / kPlanThreads * 64;
   const int64_t ta = wave * per, tz = min((int64_t)A.n, ta + per);
+  // (kBatch loads at a time: the readings are bound by their latency)
   int32_t low = 0;
-#pragma unroll 4
-  for (int64_t t = ta + lane; t < tz; t += 64) {
-    const int64_t id = id_at<ID>(A.ids, t);
-    const bool real = id >= 0 && id < A.vocab;
-    const int64_t s = id & mask;
-    if (real && s < slice) ++low;
-    if (real && s == slice) atomicAdd(&cnt[wave][id >> A.slice_bits], 1);
+  int64_t id[kBatch];
+  auto read = [&](int64_t t0) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int64_t t = t0 + k * 64 + lane;
+      id[k] = t < tz ? id_at<ID>(A.ids, t) : -1;
+    }
+  };
+  for (int64_t t0 = ta; t0 < tz; t0 += 64 * kBatch) {
+    read(t0);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const bool real = id[k] >= 0 && id[k] < A.vocab;
+      const int64_t s = id[k] & mask;
+      if (real && s < slice) ++low;
+      if (real && s == slice) atomicAdd(&cnt[wave][id[k] >> A.slice_bits], 1);
+    }
   }
   for (int k = 32; k; k >>= 1) low += __shfl_xor(low, k, 64);
   if (lane == 0) wlow[wave] = low;
@@ -190,32 +202,37 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs A) {
   __syncthreads();
   // second reading: tokens of this slice go to their places, in order (a wave
   // walks its tokens upwards; equal ids among 64 tokens by lane)
-  for (int64_t t0 = ta; t0 < tz; t0 += 64) {
-    const int64_t t = t0 + lane;
-    int64_t id = -1;
-    if (t < tz) id = id_at<ID>(A.ids, t);
-    const bool own = id >= 0 && id < A.vocab && (id & mask) == slice;
-    uint64_t todo = __ballot(own);
-    const int32_t loc = own ? (int32_t)(id >> A.slice_bits) : -1;
-    while (todo) {
-      const int lead = __ffsll((unsigned long long)todo) - 1;
-      const int32_t l = __shfl(loc, lead, 64);
-      const uint64_t same = __ballot(loc == l);
-      int32_t p0 = 0;
-      if (lane == lead) p0 = atomicAdd(&cnt[wave][l], (int32_t)__popcll(same));
-      p0 = __shfl(p0, lead, 64);
-      if (loc == l) {
-        const int32_t p = p0 + __popcll(same & (((uint64_t)1 << lane) - 1));
-        A.order[p] = Entry{(int32_t)t, (int32_t)id, p - first[l], tot[l]};
+  for (int64_t t0 = ta; t0 < tz; t0 += 64 * kBatch) {
+    if (tz - ta > 64 * kBatch) read(t0);  // one batch: still in registers
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const bool own = id[k] >= 0 && id[k] < A.vocab && (id[k] & mask) == slice;
+      const int32_t loc = own ? (int32_t)(id[k] >> A.slice_bits) : -1;
+      uint64_t todo = __ballot(own);
+      while (todo) {
+        const int lead = __ffsll((unsigned long long)todo) - 1;
+        const int32_t l = __builtin_amdgcn_readlane(loc, lead);
+        const uint64_t same = __ballot(loc == l);
+        int32_t p0 = 0;
+        if (lane == lead) p0 = atomicAdd(&cnt[wave][l], (int32_t)__popcll(same));
+        p0 = __builtin_amdgcn_readlane(p0, lead);
+        if (loc == l) {
+          const int32_t p = p0 + __popcll(same & (((uint64_t)1 << lane) - 1));
+          A.order[p] = Entry{(int32_t)(t0 + k * 64 + lane), (int32_t)id[k], p - first[l], tot[l]};
+        }
+        todo &= ~same;
       }
-      todo &= ~same;
     }
   }
 }
 
 // ------------------------------------------------------------------ sums
-// Rows summed by one thread without a break; more go to pieces.
-constexpr int kPiece = 64;
+// Tokens summed by one thread without a break; more go to pieces.
+#ifndef PIECE
+#define PIECE 16
+#endif
+constexpr int kPiece = PIECE;
+static_assert(kPiece <= 64, "a window fits a wave");
 
 struct GradArgs {
   const void* dy;
@@ -229,6 +246,9 @@ struct GradArgs {
   uint32_t slice_bits;
   FastDiv pieces;  // pieces of 4 columns per row
   int32_t rows_per_block;
+  uint32_t piece_blocks;
+  FastDiv chunks;       // blocks of a row (or of rows_per_block rows)
+  uint32_t row_blocks;  // groups of rows that the grid covers at once
 };
 
 // The partial row of the piece that begins at place p: among the places of a
@@ -243,7 +263,7 @@ __device__ __forceinline__ f32x4 dy4(const GradArgs& A, int32_t token, int32_t c
   const DY* p = (const DY*)A.dy + (int64_t)token * A.dy_stride + c0;
   if (n >= 4) {
     if constexpr (sizeof(DY) == 2) {
-      const u32x2 w = *(const u32x2_a2*)p;
+      const u32x2 w = __builtin_nontemporal_load((const u32x2_a2*)p);
       return f32x4{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
     } else {
       return *(const f32x4_a4*)p;
@@ -256,106 +276,188 @@ __device__ __forceinline__ f32x4 dy4(const GradArgs& A, int32_t token, int32_t c
   return v;
 }
 
-// Sum of the tokens at places [p, p + m), ascending.
+// s and the tokens at places [p, p + m), ascending; m >= 1.
 template <class DY>
-__device__ __forceinline__ f32x4 sum_places(const GradArgs& A, int32_t p, int32_t m, int32_t c0,
-                                            int n) {
-  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+__device__ __forceinline__ f32x4 sum_places(const GradArgs& A, f32x4 s, int32_t p, int32_t m,
+                                            int32_t c0, int n) {
   int32_t j = 0;
-  for (; j + 4 <= m; j += 4) {
+  for (; j + 8 <= m; j += 8) {
+    f32x4 v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = dy4<DY>(A, A.order[p + j + u].token, c0, n);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s += v[u];
+  }
+  if (m - j == 1) return s + dy4<DY>(A, A.order[p + j].token, c0, n);
+  for (; j < m; j += 4) {
     f32x4 v[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = dy4<DY>(A, A.order[p + j + u].token, c0, n);
+    for (int u = 0; u < 4; ++u) v[u] = dy4<DY>(A, A.order[p + min(j + u, m - 1)].token, c0, n);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) s += v[u];
+    for (int u = 0; u < 4; ++u)
+      if (j + u < m) s += v[u];
   }
-  for (; j < m; ++j) s += dy4<DY>(A, A.order[p + j].token, c0, n);
   return s;
 }
 
-// One block per window and kind of piece.
-template <class DY>
-__global__ void __launch_bounds__(kThreads) pieces_kernel(const GradArgs A) {
-  __shared__ int32_t found;
-  const int32_t total = A.start[((int64_t)1 << A.slice_bits) * A.local];
-  const int32_t w0 = (int32_t)(blockIdx.x >> 1) * kPiece;
-  const bool first = (blockIdx.x & 1u) != 0;
-  if (w0 >= total) return;
-  if (threadIdx.x == 0) found = -1;
-  __syncthreads();
-  if (threadIdx.x < kPiece && w0 + (int32_t)threadIdx.x < total) {
-    const Entry e = A.order[w0 + threadIdx.x];
-    if (e.count > kPiece && e.rel % kPiece == 0 && (e.rel == 0) == first)
-      found = w0 + (int32_t)threadIdx.x;
-  }
-  __syncthreads();
-  const int32_t p = found;
-  if (p < 0) return;
-  const Entry e = A.order[p];
-  const int32_t m = min(kPiece, e.count - e.rel);
-  float* to = A.partial + slot_of(p, first) * A.cols;
-  for (int32_t c0 = (int32_t)threadIdx.x * 4; c0 < A.cols; c0 += kThreads * 4) {
-    const int n = min(4, A.cols - c0);
-    const f32x4 s = sum_places<DY>(A, p, m, c0, n);
-    if (n >= 4) {
-      *(f32x4_a4*)(to + c0) = s;
-    } else {
+// Columns [c0, c0 + n) of row v, n <= 4.
+template <bool GAPS>
+__device__ __forceinline__ void row_out(const GradArgs& A, int64_t v, int32_t c0, int n, f32x4 s) {
+  const int64_t i = v * A.cols + c0;
+  if (!GAPS && n >= 4) {
+    grad_store4(A.out, place_at<GAPS>(A.out.place, i), s);
+  } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (k < n) to[c0 + k] = s[k];
+    for (int k = 0; k < 4; ++k)
+      if (k < n) grad_store(A.out, place_at<GAPS>(A.out.place, i + k), s[k]);
+  }
+}
+
+__device__ __forceinline__ void piece_out(const GradArgs& A, int32_t p, bool first, int32_t c0,
+                                          int n, f32x4 s) {
+  float* to = A.partial + slot_of(p, first) * A.cols + c0;
+  if (n >= 4) {
+    *(f32x4_a4*)to = s;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < n) to[k] = s[k];
+  }
+}
+
+// The first place of the window from w0 that begins a piece of a long id: the
+// id's first piece, or a later one.  -1: none.  For a whole wave.
+__device__ __forceinline__ int32_t piece_in_window(const GradArgs& A, int32_t total, int32_t w0,
+                                                   bool first) {
+  const int lane = threadIdx.x & 63;
+  bool here = false;
+  if (lane < kPiece && w0 + lane < total) {
+    const Entry e = A.order[w0 + lane];
+    here = e.count > kPiece && e.rel % kPiece == 0 && (e.rel == 0) == first;
+  }
+  const uint64_t found = __ballot(here);
+  return found ? w0 + __ffsll((unsigned long long)found) - 1 : -1;
+}
+
+// One row per distinct id or piece, found at its first place.  A thread takes
+// up to kUnits groups of 4 columns, kThreads apart.  Nearly every id of a
+// batch occurs once, so the row's accumulator and its first token are
+// requested together, before any of the sum.
+#ifndef UNITS
+#define UNITS 1
+#endif
+constexpr int kUnits = UNITS;
+template <class DY, bool GAPS>
+__global__ void __launch_bounds__(kThreads) places_kernel(const GradArgs A) {
+  const int32_t total = A.start[((int64_t)1 << A.slice_bits) * A.local];
+  const uint32_t units = (uint32_t)A.rows_per_block * A.pieces.d;
+  // a row's blocks follow each other
+  const uint32_t bx = fast_div(blockIdx.x, A.chunks);
+  const uint32_t u0 = (blockIdx.x - bx * A.chunks.d) * (kThreads * kUnits) + threadIdx.x;
+  for (int64_t x0 = (int64_t)bx * A.rows_per_block; x0 < total;
+       x0 += (int64_t)A.row_blocks * A.rows_per_block) {
+    int32_t c0[kUnits];
+    int64_t x[kUnits], at[kUnits];
+    Entry e[kUnits];
+    f32x4 base[kUnits], s[kUnits];
+    bool on[kUnits];
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      const uint32_t u = u0 + k * kThreads;
+      const uint32_t r = fast_div(u, A.pieces);
+      c0[k] = (int32_t)(u - r * A.pieces.d) * 4;
+      x[k] = x0 + r;
+      on[k] = u < units && x[k] < total;
+      if (on[k]) e[k] = A.order[x[k]];
+      on[k] = on[k] && e[k].rel % kPiece == 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      if (!on[k]) continue;
+      const int n = min(4, A.cols - c0[k]);
+      at[k] = GAPS ? 0 : place_at<false>(A.out.place, (int64_t)e[k].row * A.cols + c0[k]);
+      if (!GAPS && n >= 4 && e[k].count <= kPiece) base[k] = grad_load4(A.out, at[k]);
+      s[k] = dy4<DY>(A, e[k].token, c0[k], n);
+    }
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      if (!on[k]) continue;
+      const int n = min(4, A.cols - c0[k]);
+      const int32_t m = min(kPiece, e[k].count - e[k].rel);
+      if (m > 1) s[k] = sum_places<DY>(A, s[k], (int32_t)x[k] + 1, m - 1, c0[k], n);
+      if (e[k].count > kPiece)
+        piece_out(A, (int32_t)x[k], e[k].rel == 0, c0[k], n, s[k]);
+      else if (!GAPS && n >= 4)
+        grad_store4(A.out, at[k], s[k], base[k]);
+      else
+        row_out<GAPS>(A, e[k].row, c0[k], n, s[k]);
     }
   }
 }
 
-// DENSE: every row of the table; otherwise one row per distinct id, found at
-// its first place.
-template <class DY, bool GAPS, bool DENSE>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const GradArgs A) {
+// Every row of the table but those of long ids, whose pieces the first
+// piece_blocks blocks sum.
+template <class DY, bool GAPS>
+__global__ void __launch_bounds__(kThreads) table_kernel(const GradArgs A) {
+  if (blockIdx.x < A.piece_blocks) {
+    const int32_t total = A.start[((int64_t)1 << A.slice_bits) * A.local];
+    for (int64_t b = blockIdx.x; (b >> 1) * kPiece < total; b += A.piece_blocks) {
+      const bool first = (b & 1) != 0;
+      const int32_t p = piece_in_window(A, total, (int32_t)(b >> 1) * kPiece, first);
+      if (p < 0) continue;
+      const Entry e = A.order[p];
+      for (int32_t c0 = (int32_t)threadIdx.x * 4; c0 < A.cols; c0 += kThreads * 4) {
+        const int n = min(4, A.cols - c0);
+        piece_out(A, p, first, c0, n, sum_places<DY>(A, f32x4{0.f, 0.f, 0.f, 0.f}, p,
+                                               min(kPiece, e.count - e.rel), c0, n));
+      }
+    }
+    return;
+  }
   const uint32_t units = (uint32_t)A.rows_per_block * A.pieces.d;
-  const int64_t rows = DENSE ? A.vocab : (int64_t)A.start[((int64_t)1 << A.slice_bits) * A.local];
-  for (int64_t b = blockIdx.x; b * A.rows_per_block < rows; b += gridDim.x) {
-    const int64_t r0 = b * A.rows_per_block;
+  const int64_t mask = ((int64_t)1 << A.slice_bits) - 1;
+  for (int64_t b = blockIdx.x - A.piece_blocks; b * A.rows_per_block < A.vocab;
+       b += gridDim.x - A.piece_blocks) {
     for (uint32_t u = threadIdx.x; u < units; u += kThreads) {
       const uint32_t r = fast_div(u, A.pieces);
       const int32_t c0 = (int32_t)(u - r * A.pieces.d) * 4;
-      const int64_t x = r0 + r;
-      if (x >= rows) break;
-      int64_t v;
-      int32_t p, count;
-      if constexpr (DENSE) {
-        const int64_t mask = ((int64_t)1 << A.slice_bits) - 1;
-        const int32_t* s = A.start + (x & mask) * A.local + (x >> A.slice_bits);
-        v = x;
-        p = s[0];
-        count = s[1] - p;
-      } else {
-        const Entry e = A.order[x];
-        if (e.rel != 0) continue;
-        v = e.row;
-        p = (int32_t)x;
-        count = e.count;
-      }
+      const int64_t v = b * A.rows_per_block + r;
+      if (v >= A.vocab) break;
+      const int32_t* at = A.start + (v & mask) * A.local + (v >> A.slice_bits);
+      const int32_t p = at[0], count = at[1] - p;
+      if (count > kPiece) continue;
       const int n = min(4, A.cols - c0);
       f32x4 s = {0.f, 0.f, 0.f, 0.f};
-      if (count <= kPiece) {
-        s = sum_places<DY>(A, p, count, c0, n);
-      } else {
-        for (int32_t j = 0; j < count; j += kPiece) {
-          const float* q = A.partial + slot_of(p + j, j == 0) * A.cols + c0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < n) s[k] += q[k];
-        }
-      }
-      const int64_t i = v * A.cols + c0;
-      if (!GAPS && n >= 4) {
-        grad_store4(A.out, place_at<GAPS>(A.out.place, i), s);
+      if (count > 0) s = sum_places<DY>(A, s, p, count, c0, n);
+      row_out<GAPS>(A, v, c0, n, s);
+    }
+  }
+}
+
+// The rows of long ids from their pieces, in order; the grid's second side
+// covers the columns.
+template <bool GAPS>
+__global__ void __launch_bounds__(kThreads) join_kernel(const GradArgs A) {
+  const int32_t total = A.start[((int64_t)1 << A.slice_bits) * A.local];
+  const int32_t c0 = (int32_t)(blockIdx.y * kThreads + threadIdx.x) * 4;
+  const int n = min(4, A.cols - c0);
+  for (int64_t w = blockIdx.x; w * kPiece < total; w += gridDim.x) {
+    const int32_t p = piece_in_window(A, total, (int32_t)w * kPiece, true);
+    if (p < 0 || n <= 0) continue;
+    const Entry e = A.order[p];
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int32_t j = 0; j < e.count; j += kPiece) {
+      const float* q = A.partial + slot_of(p + j, j == 0) * A.cols + c0;
+      if (n >= 4) {
+        s += *(const f32x4_a4*)q;
       } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (k < n) grad_store(A.out, place_at<GAPS>(A.out.place, i + k), s[k]);
+          if (k < n) s[k] += q[k];
       }
     }
+    row_out<GAPS>(A, e.row, c0, n, s);
   }
 }
 
@@ -418,26 +520,37 @@ int launch_lookup(const LookupArgs& A, hipStream_t s) {
   return A.place.gap ? launch_lookup<ID, OUT, true>(A, s) : launch_lookup<ID, OUT, false>(A, s);
 }
 
-template <class DY, bool GAPS, bool DENSE>
-int launch_rows(const GradArgs& A, hipStream_t s) {
-  const int64_t rows = DENSE ? A.vocab : (int64_t)A.n;
-  const int64_t blocks = (rows + A.rows_per_block - 1) / A.rows_per_block;
-  hipLaunchKernelGGL((rows_kernel<DY, GAPS, DENSE>),
-                     dim3((unsigned)std::min<int64_t>(blocks, 1 << 20)), dim3(kThreads), 0, s, A);
+template <class DY, bool GAPS>
+int launch_sums(const GradArgs& B, bool dense, hipStream_t s) {
+  GradArgs A = B;
+  const int64_t windows = (A.n + kPiece - 1) / kPiece;
+  const bool pieces = A.n > kPiece;
+  if (dense) {
+    A.piece_blocks = pieces ? (unsigned)std::min<int64_t>(2 * windows, 1 << 12) : 0u;
+    const int64_t blocks = (A.vocab + A.rows_per_block - 1) / A.rows_per_block;
+    hipLaunchKernelGGL((table_kernel<DY, GAPS>),
+                       dim3(A.piece_blocks + (unsigned)std::min<int64_t>(blocks, 1 << 20)),
+                       dim3(kThreads), 0, s, A);
+  } else {
+    const int64_t blocks = (A.n + A.rows_per_block - 1) / A.rows_per_block;
+    const int64_t units = (int64_t)A.rows_per_block * A.pieces.d;
+    A.chunks = make_fast_div((uint32_t)((units + kThreads * kUnits - 1) / (kThreads * kUnits)));
+    A.row_blocks = (uint32_t)std::min<int64_t>(blocks, std::max<int64_t>(1, (1 << 22) / A.chunks.d));
+    hipLaunchKernelGGL((places_kernel<DY, GAPS>), dim3(A.row_blocks * A.chunks.d), dim3(kThreads), 0,
+                       s, A);
+  }
+  const int rc = launched();
+  if (rc != ZERO_OK || !pieces) return rc;
+  hipLaunchKernelGGL(join_kernel<GAPS>,
+                     dim3((unsigned)std::min<int64_t>(windows, 1 << 16),
+                          (A.pieces.d + kThreads - 1) / kThreads),
+                     dim3(kThreads), 0, s, A);
   return launched();
 }
 
 template <class DY>
 int launch_grad(const GradArgs& A, bool dense, hipStream_t s) {
-  if (A.n > kPiece) {
-    hipLaunchKernelGGL(pieces_kernel<DY>, dim3(2 * (unsigned)((A.n + kPiece - 1) / kPiece)),
-                       dim3(kThreads), 0, s, A);
-    const int rc = launched();
-    if (rc != ZERO_OK) return rc;
-  }
-  const bool gaps = A.out.place.gap != 0;
-  if (dense) return gaps ? launch_rows<DY, true, true>(A, s) : launch_rows<DY, false, true>(A, s);
-  return gaps ? launch_rows<DY, true, false>(A, s) : launch_rows<DY, false, false>(A, s);
+  return A.out.place.gap ? launch_sums<DY, true>(A, dense, s) : launch_sums<DY, false>(A, dense, s);
 }
 
 }  // namespace

@@ -28,53 +28,76 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kThreads = 256;            // 4 waves, two by two over the tile
-constexpr int kStep = 64;                // tokens of one LDS tile
-constexpr int kPanelBytes = kStep * 64 + 64;  // 64 bytes apart: writes of one token row spread over the banks
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+
+constexpr int kThreads = 256;  // 4 waves, two by two over the tile
+constexpr int kStep = 64;      // tokens of one LDS tile
+// A panel: 64 tokens of 32 columns in bf16, 64 bytes to a token.  Panels lie
+// 64 bytes further apart than they are long, so that the writes of one token
+// row, which go to as many panels as the tile is wide, spread over the banks.
+constexpr int kPanelBytes = kStep * 64 + 64;
 
 struct Args {
   const uint16_t* dy;
   int64_t dy_stride;
   const uint8_t* codes;
   const uint8_t* scales;
-  int64_t tokens, tokens_per_split;
+  int64_t tokens;
   int32_t O, I, nb;
-  int32_t rows, cols;           // of the gradient: (O, I), or (I, O) when transposed
+  int32_t rows, cols;  // of the gradient: (O, I), or (I, O) when transposed
   int32_t row_tiles, col_tiles;
-  int32_t splits;
-  float* partial;               // splits x rows x cols where the result does not go out directly
+  int32_t whole;       // tiles that one block sums over all tokens
+  int32_t splits;      // blocks of each further tile
+  int64_t tokens_per_split;
+  int32_t fast;        // columns come in whole chunks
+  int32_t direct;      // whole tiles go straight to the gradient (else: like split ones)
+  float* partial;      // per split and further tile, a tile of binary32 sums
   GradOut out;
 };
 
-// Chunks of dY: 8 columns of one token; of X: 16 columns.
+// One thread's part of a tile of TC columns and kStep tokens: chunks of 8
+// columns of dY or 16 of X (16 bytes each).  `fast` loads take whole chunks
+// of whole steps; a chunk past the last column is read from the last one (its
+// sums are not stored).  fill() checks every element and goes to LDS at once.
 template <int TC>
 struct DyTile {
   static constexpr int kPerRow = TC / 8, kRows = kThreads / kPerRow, kN = kStep / kRows;
   u32x4 v[kN];
-  __device__ __forceinline__ void load(const Args& A, int64_t t0, int64_t tz, int32_t c0) {
-    const int col = c0 + (threadIdx.x % kPerRow) * 8;
+  static __device__ __forceinline__ int col() { return (threadIdx.x % kPerRow) * 8; }
+  static __device__ __forceinline__ int row() { return threadIdx.x / kPerRow; }
+  static __device__ __forceinline__ uint32_t fast_offset(const Args& A, int32_t c0) {
+    return (uint32_t)(row() * A.dy_stride + min(c0 + col(), A.O - 8)) * 2u;
+  }
+  __device__ __forceinline__ void fast(const Args& A, int64_t t0, uint32_t off) {
+    const char* p = (const char*)(A.dy + t0 * A.dy_stride);
 #pragma unroll
+    for (int k = 0; k < kN; ++k) v[k] = *(const u32x4_a2*)(p + (int64_t)k * kRows * 2 * A.dy_stride + off);
+  }
+  static __device__ __forceinline__ void fill(const Args& A, int64_t t0, int64_t tz, int32_t c0,
+                                              lds_char* lds) {
+    const int c = c0 + col();
+    lds_char* to = lds + (col() >> 5) * kPanelBytes + row() * 64 + (col() & 31) * 2;
+#pragma unroll 1
     for (int k = 0; k < kN; ++k) {
-      const int64_t t = t0 + k * kRows + threadIdx.x / kPerRow;
-      const uint16_t* p = A.dy + t * A.dy_stride + col;
-      const int n = t < tz ? A.O - col : 0;
-      v[k] = u32x4{0u, 0u, 0u, 0u};
+      const int64_t t = t0 + k * kRows + row();
+      const uint16_t* p = A.dy + t * A.dy_stride + c;
+      const int n = t < tz ? A.O - c : 0;
+      u32x4 w = {0u, 0u, 0u, 0u};
       if (n >= 8) {
-        v[k] = *(const u32x4_a2*)p;
+        w = *(const u32x4_a2*)p;
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (j < n) v[k][j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+          if (j < n) w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
       }
+      *(lds_u32x4*)(to + k * kRows * 64) = w;
     }
   }
-  __device__ __forceinline__ void store(char* lds) const {
-    const int c = (threadIdx.x % kPerRow) * 8;
+  __device__ __forceinline__ void store(lds_char* lds) const {
+    lds_char* p = lds + (col() >> 5) * kPanelBytes + row() * 64 + (col() & 31) * 2;
 #pragma unroll
-    for (int k = 0; k < kN; ++k) {
-      const int t = k * kRows + threadIdx.x / kPerRow;
-      *(u32x4*)(lds + (c >> 5) * kPanelBytes + t * 64 + (c & 31) * 2) = v[k];
-    }
+    for (int k = 0; k < kN; ++k) *(lds_u32x4*)(p + k * kRows * 64) = v[k];
   }
 };
 
@@ -83,43 +106,62 @@ struct XTile {
   static constexpr int kPerRow = TC / 16, kRows = kThreads / kPerRow, kN = kStep / kRows;
   u32x4 v[kN];
   uint32_t e[kN];
-  __device__ __forceinline__ void load(const Args& A, int64_t t0, int64_t tz, int32_t c0) {
-    const int col = c0 + (threadIdx.x % kPerRow) * 16;
+  static __device__ __forceinline__ int col() { return (threadIdx.x % kPerRow) * 16; }
+  static __device__ __forceinline__ int row() { return threadIdx.x / kPerRow; }
+  static __device__ __forceinline__ uint32_t fast_offset(const Args& A, int32_t c0) {
+    return (uint32_t)(row() * A.I + min(c0 + col(), A.I - 16));
+  }
+  static __device__ __forceinline__ uint32_t fast_scale_offset(const Args& A, int32_t c0) {
+    return (uint32_t)(row() * A.nb + (min(c0 + col(), A.I - 16) >> 7));
+  }
+  __device__ __forceinline__ void fast(const Args& A, int64_t t0, uint32_t off, uint32_t soff) {
+    const char* p = (const char*)(A.codes + t0 * A.I);
+    const uint8_t* s = A.scales + t0 * A.nb;
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
-      const int64_t t = t0 + k * kRows + threadIdx.x / kPerRow;
-      const uint8_t* p = A.codes + t * A.I + col;
-      const int n = t < tz ? A.I - col : 0;
-      v[k] = u32x4{0u, 0u, 0u, 0u};
-      e[k] = 127u;
-      if (n > 0) e[k] = A.scales[t * A.nb + (col >> 7)];
+      v[k] = *(const u32x4_a1*)(p + (int64_t)k * kRows * A.I + off);
+      e[k] = *(s + (int64_t)k * kRows * A.nb + soff);
+    }
+  }
+  static __device__ __forceinline__ void put(lds_char* to, const u32x4& v, uint32_t byte) {
+    const float s = act8_scale(byte);
+    const u32x2 a = act8_bf16x4(v.x, s), b = act8_bf16x4(v.y, s);
+    const u32x2 d = act8_bf16x4(v.z, s), f = act8_bf16x4(v.w, s);
+    *(lds_u32x4*)to = u32x4{a.x, a.y, b.x, b.y};
+    *(lds_u32x4*)(to + 16) = u32x4{d.x, d.y, f.x, f.y};
+  }
+  static __device__ __forceinline__ void fill(const Args& A, int64_t t0, int64_t tz, int32_t c0,
+                                              lds_char* lds) {
+    const int c = c0 + col();
+    lds_char* to = lds + (col() >> 5) * kPanelBytes + row() * 64 + (col() & 31) * 2;
+#pragma unroll 1
+    for (int k = 0; k < kN; ++k) {
+      const int64_t t = t0 + k * kRows + row();
+      const uint8_t* p = A.codes + t * A.I + c;
+      const int n = t < tz ? A.I - c : 0;
+      u32x4 w = {0u, 0u, 0u, 0u};
+      uint32_t b = 127u;
+      if (n > 0) b = A.scales[t * A.nb + (c >> 7)];
       if (n >= 16) {
-        v[k] = *(const u32x4_a1*)p;
+        w = *(const u32x4_a1*)p;
       } else {
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          if (j < n) v[k][j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
+          if (j < n) w[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
       }
+      put(to + k * kRows * 64, w, b);
     }
   }
-  __device__ __forceinline__ void store(char* lds) const {
-    const int c = (threadIdx.x % kPerRow) * 16;
+  __device__ __forceinline__ void store(lds_char* lds) const {
+    lds_char* p = lds + (col() >> 5) * kPanelBytes + row() * 64 + (col() & 31) * 2;
 #pragma unroll
-    for (int k = 0; k < kN; ++k) {
-      const int t = k * kRows + threadIdx.x / kPerRow;
-      char* p = lds + (c >> 5) * kPanelBytes + t * 64 + (c & 31) * 2;
-      const float s = act8_scale(e[k]);
-      const u32x2 a = act8_bf16x4(v[k].x, s), b = act8_bf16x4(v[k].y, s);
-      const u32x2 d = act8_bf16x4(v[k].z, s), f = act8_bf16x4(v[k].w, s);
-      *(u32x4*)p = u32x4{a.x, a.y, b.x, b.y};
-      *(u32x4*)(p + 16) = u32x4{d.x, d.y, f.x, f.y};
-    }
+    for (int k = 0; k < kN; ++k) put(p + k * kRows * 64, v[k], e[k]);
   }
 };
 
 // 32 columns x 16 tokens of a panel as a matrix operand: lane l holds column
 // l % 32, tokens 4*(l / 32) + {0..3, 8..11}.
-__device__ __forceinline__ bf16x8 frag(const char* panel) {
+__device__ __forceinline__ bf16x8 frag(const lds_char* panel) {
   typedef __attribute__((address_space(3))) s16x4 lds_t;
   const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)panel);
   const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(panel + 512));
@@ -130,16 +172,48 @@ __device__ __forceinline__ int frag_offset() {
   return ((i >> 2) + 4 * (g >> 1)) * 64 + (g & 1) * 32 + (i & 3) * 8;
 }
 
+// Tile number to place: groups of 8 rows of tiles, column by column within a
+// group, so that tiles worked on together share their operands in the L2.
+__device__ __forceinline__ void tile_at(const Args& A, int32_t tile, int32_t& r, int32_t& c) {
+  const int32_t per = 8 * A.col_tiles, g = tile / per, in = tile - g * per;
+  const int32_t h = min(8, A.row_tiles - g * 8);
+  c = in / h;
+  r = g * 8 + in - c * h;
+}
+
 // W: 32-column panels of a wave along each side; the block's tile is 2W
 // panels wide and high.  TR: rows of the gradient are X's columns.
+//
+// Two LDS buffers.  While the matrix cores work on one step, the next one's
+// chunks are converted and written to the other buffer and those of the step
+// after that are requested; fragments are read a sixteenth of tokens ahead.
+// One barrier a step, before its last sixteenth, whose fragments are already
+// in registers.
 template <int W, bool TR>
-__global__ void __launch_bounds__(kThreads) grad_kernel(const Args A) {
+__global__ void __launch_bounds__(kThreads, 1) grad_kernel(const Args A) {
   constexpr int kSide = 64 * W;
-  __shared__ __align__(16) char lds[2][2 * W * kPanelBytes];  // rows' operand, columns' operand
-  const int tile = blockIdx.x;
-  const int32_t r0 = (tile / A.col_tiles) * kSide, c0 = (tile % A.col_tiles) * kSide;
-  const int64_t ta = (int64_t)blockIdx.y * A.tokens_per_split;
-  const int64_t tz = min(A.tokens, ta + A.tokens_per_split);
+  constexpr int kOperand = 2 * W * kPanelBytes, kBuffer = 2 * kOperand;
+  __shared__ __align__(16) char shared[2 * kBuffer];
+  lds_char* lds = (lds_char*)shared;
+
+  // whole tiles first, dealt to the XCDs (block b runs on XCD b % 8) in runs
+  int32_t tile, split = 0;
+  int64_t ta = 0, tz = A.tokens;
+  if ((int32_t)blockIdx.x < A.whole) {
+    tile = (A.whole & 7) ? (int32_t)blockIdx.x
+                         : (int32_t)(blockIdx.x & 7) * (A.whole >> 3) + (int32_t)(blockIdx.x >> 3);
+  } else {
+    const int32_t x = (int32_t)blockIdx.x - A.whole;
+    split = x % A.splits;
+    tile = A.whole + x / A.splits;
+    ta = split * A.tokens_per_split;
+    tz = min(A.tokens, ta + A.tokens_per_split);
+  }
+  int32_t r0, c0;
+  tile_at(A, tile, r0, c0);
+  r0 *= kSide;
+  c0 *= kSide;
+
   const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1, lane = threadIdx.x & 63;
   f32x16 acc[W][W];
 #pragma unroll
@@ -151,101 +225,192 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const Args A) {
 
   DyTile<kSide> dy;
   XTile<kSide> x;
-  const char* fa = lds[0] + wm * W * kPanelBytes + frag_offset();
-  const char* fb = lds[1] + wn * W * kPanelBytes + frag_offset();
-  for (int64_t t = ta; t < tz; t += kStep) {
-    dy.load(A, t, tz, TR ? c0 : r0);
-    x.load(A, t, tz, TR ? r0 : c0);
-    __syncthreads();
-    dy.store(lds[TR ? 1 : 0]);
-    x.store(lds[TR ? 0 : 1]);
-    __syncthreads();
+  const int32_t dy_c = TR ? c0 : r0, x_c = TR ? r0 : c0;
+  const uint32_t dy_off = dy.fast_offset(A, dy_c), x_off = x.fast_offset(A, x_c),
+                 s_off = x.fast_scale_offset(A, x_c);
+  lds_char* const dy_lds = lds + (TR ? kOperand : 0);
+  lds_char* const x_lds = lds + (TR ? 0 : kOperand);
+  const lds_char* const fa = lds + wm * W * kPanelBytes + frag_offset();
+  const lds_char* const fb = lds + kOperand + wn * W * kPanelBytes + frag_offset();
+
+  const int64_t steps = (tz - ta + kStep - 1) / kStep;
+  const int64_t full = A.fast ? (tz - ta) / kStep : 0;  // steps that fast loads can take
+  auto load = [&](int64_t k) {
+    dy.fast(A, ta + k * kStep, dy_off);
+    x.fast(A, ta + k * kStep, x_off, s_off);
+  };
+  auto fill = [&](int64_t k, int buf) {
+    dy.fill(A, ta + k * kStep, tz, dy_c, dy_lds + buf * kBuffer);
+    x.fill(A, ta + k * kStep, tz, x_c, x_lds + buf * kBuffer);
+  };
+  bf16x8 a[2][W], b[2][W];
+  auto read = [&](int to, int buf, int s) {
 #pragma unroll
-    for (int s = 0; s < kStep / 16; ++s) {
-      bf16x8 a[W], b[W];
-#pragma unroll
-      for (int k = 0; k < W; ++k) {
-        a[k] = frag(fa + k * kPanelBytes + s * 1024);
-        b[k] = frag(fb + k * kPanelBytes + s * 1024);
-      }
-#pragma unroll
-      for (int m = 0; m < W; ++m)
-#pragma unroll
-        for (int n = 0; n < W; ++n)
-          acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[m], b[n], acc[m][n], 0, 0, 0);
+    for (int k = 0; k < W; ++k) {
+      a[to][k] = frag(fa + buf * kBuffer + k * kPanelBytes + s * 1024);
+      b[to][k] = frag(fb + buf * kBuffer + k * kPanelBytes + s * 1024);
     }
-  }
-  // lane l, register k: row 8*(k/4) + 4*(l/32) + k%4, column l%32
-#pragma unroll
-  for (int n = 0; n < W; ++n) {
-    const int32_t c = c0 + (wn * W + n) * 32 + (lane & 31);
-    if (c >= A.cols) continue;
+  };
+  auto multiply = [&](int from) {
 #pragma unroll
     for (int m = 0; m < W; ++m)
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int32_t r = r0 + (wm * W + m) * 32 + 8 * (k >> 2) + 4 * (lane >> 5) + (k & 3);
-        if (r >= A.rows) continue;
-        const int64_t i = (int64_t)r * A.cols + c;
-        if (A.partial)
-          A.partial[(int64_t)blockIdx.y * A.rows * A.cols + i] = acc[m][n][k];
-        else
-          grad_store(A.out, A.out.place.x0 + i, acc[m][n][k]);
-      }
+      for (int n = 0; n < W; ++n)
+        acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[from][m], b[from][n], acc[m][n], 0, 0, 0);
+  };
+  auto store = [&](int buf) {
+    dy.store(dy_lds + buf * kBuffer);
+    x.store(x_lds + buf * kBuffer);
+  };
+
+  if (steps > 0) {
+    if (full > 0) {
+      load(0);
+      store(0);
+    } else {
+      fill(0, 0);
+    }
+    if (full > 1) load(1);
+    __syncthreads();
+    read(0, 0, 0);
+    int64_t k = 0;
+    int buf = 0;
+    for (; k + 2 < full; ++k) {
+      read(1, buf, 1);
+      multiply(0);
+      read(0, buf, 2);
+      multiply(1);
+      read(1, buf, 3);
+      store(buf ^ 1);
+      load(k + 2);
+      multiply(0);
+      __syncthreads();
+      buf ^= 1;
+      read(0, buf, 0);
+      multiply(1);
+    }
+    // the last full steps, and those that need checks
+    for (; k < steps; ++k) {
+      read(1, buf, 1);
+      multiply(0);
+      read(0, buf, 2);
+      multiply(1);
+      read(1, buf, 3);
+      multiply(0);
+      if (k + 1 < full)
+        store(buf ^ 1);
+      else if (k + 1 < steps)
+        fill(k + 1, buf ^ 1);
+      __syncthreads();
+      buf ^= 1;
+      if (k + 1 < steps) read(0, buf, 0);
+      multiply(1);
+    }
   }
+
+  // lane l, register k: row 8*(k/4) + 4*(l/32) + k%4, column l%32
+  if (A.direct && tile < A.whole) {
+#pragma unroll
+    for (int n = 0; n < W; ++n) {
+      const int32_t c = c0 + (wn * W + n) * 32 + (lane & 31);
+      if (c >= A.cols) continue;
+#pragma unroll
+      for (int m = 0; m < W; ++m)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int32_t r = r0 + (wm * W + m) * 32 + 8 * (k >> 2) + 4 * (lane >> 5) + (k & 3);
+          if (r >= A.rows) continue;
+          grad_store(A.out, A.out.place.x0 + (int64_t)r * A.cols + c, acc[m][n][k]);
+        }
+    }
+    return;
+  }
+  // a tile of the workspace, rows of kSide columns
+  const int64_t slot = A.direct ? (int64_t)(tile - A.whole) * A.splits + split : tile < A.whole
+      ? tile : A.whole + (int64_t)(tile - A.whole) * A.splits + split;
+  float* const to = A.partial + slot * kSide * kSide;
+#pragma unroll
+  for (int n = 0; n < W; ++n)
+#pragma unroll
+    for (int m = 0; m < W; ++m)
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        to[((wm * W + m) * 32 + 8 * (k >> 2) + 4 * (lane >> 5) + (k & 3)) * kSide +
+           (wn * W + n) * 32 + (lane & 31)] = acc[m][n][k];
 }
 
-// Adds up the splits, in order, and hands the sum on.
-template <bool GAPS>
-__global__ void __launch_bounds__(kThreads)
-    sum_kernel(const float* partial, int32_t splits, int64_t numel, const GradOut out) {
-  const int64_t T = (int64_t)gridDim.x * kThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i * 4 < numel; i += T) {
-    const int64_t e = i * 4;
-    const int n = (int)min((int64_t)4, numel - e);
+// Adds up a tile's splits, in order, and hands the sum on: blocks over the
+// tiles from `first`, kSumParts to a tile.
+constexpr int kSumParts = 16;
+template <int SIDE, bool GAPS>
+__global__ void __launch_bounds__(kThreads) sum_kernel(const Args A, int32_t first) {
+  const int32_t tile = first + (int32_t)(blockIdx.x / kSumParts);
+  const int32_t part = blockIdx.x % kSumParts;
+  int32_t r0, c0;
+  tile_at(A, tile, r0, c0);
+  r0 *= SIDE;
+  c0 *= SIDE;
+  const int32_t n_splits = tile < A.whole ? 1 : A.splits;
+  const int64_t slot = A.direct ? (int64_t)(tile - A.whole) * A.splits : tile < A.whole
+      ? tile : A.whole + (int64_t)(tile - A.whole) * A.splits;
+  const float* from = A.partial + slot * SIDE * SIDE;
+  constexpr int kPart = SIDE * SIDE / 4 / kSumParts;  // groups of 4 columns
+  for (int g = part * kPart + threadIdx.x; g < (part + 1) * kPart; g += kThreads) {
+    const int32_t r = r0 + g / (SIDE / 4), c = c0 + (g % (SIDE / 4)) * 4;
+    const int n = min(4, A.cols - c);
+    if (r >= A.rows || n <= 0) continue;
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < splits; ++k) {
-      const float* p = partial + (int64_t)k * numel + e;
-      if (n >= 4) {
-        s += *(const f32x4_a4*)p;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < n) s[j] += p[j];
-      }
-    }
+    for (int k = 0; k < n_splits; ++k) s += *(const f32x4*)(from + (int64_t)k * SIDE * SIDE + g * 4);
+    const int64_t e = (int64_t)r * A.cols + c;
     if (!GAPS && n >= 4) {
-      grad_store4(out, place_at<GAPS>(out.place, e), s);
+      grad_store4(A.out, place_at<GAPS>(A.out.place, e), s);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (j < n) grad_store(out, place_at<GAPS>(out.place, e + j), s[j]);
+        if (j < n) grad_store(A.out, place_at<GAPS>(A.out.place, e + j), s[j]);
     }
   }
 }
 
 // ------------------------------------------------------------------ host
 struct Plan {
-  int64_t row_tiles, col_tiles, splits, tokens_per_split, bytes;
+  int64_t side, row_tiles, col_tiles, whole, further, splits, tokens_per_split, slots, bytes;
+  bool direct;
 };
 
-// Tiles of 128 x 128.  Fewer tiles than the chip takes at once (256 CUs, two
-// blocks each) leave the sum over tokens to several blocks, 256 tokens each
-// at least.  Where padding falls inside the tensor the result goes through
-// the workspace too, and the sum places it.
+// Tiles that fill the chip's 256 CUs are summed by one block each; the rest of
+// the tiles, fewer than 256, share the CUs, each tile's tokens being split
+// over as many blocks as there is room for, kMinSplit tokens each at least.
+// Where padding falls inside the tensor every tile goes through the
+// workspace, and the sum places it.
+constexpr int64_t kCus = 256, kMinSplit = 256;
+#ifndef SIDE
+#define SIDE 256
+#endif
 Plan make_plan(const zero_layout* L, int32_t tensor, int64_t rows, int64_t cols, int64_t tokens) {
   int64_t lo, hi;
-  const bool gaps = make_place(L, tensor, &lo, &hi).gap != 0;
   Plan p;
-  p.row_tiles = (rows + 127) / 128;
-  p.col_tiles = (cols + 127) / 128;
-  const int64_t tiles = std::max<int64_t>(1, p.row_tiles * p.col_tiles);
-  const int64_t most = std::max<int64_t>(1, (tokens + 255) / 256);
-  p.splits = std::max<int64_t>(1, std::min<int64_t>({most, 512 / tiles, 32}));
-  p.tokens_per_split = (tokens + p.splits * kStep - 1) / (p.splits * kStep) * kStep;
-  if (p.tokens_per_split == 0) p.tokens_per_split = kStep;
-  p.splits = std::max<int64_t>(1, (tokens + p.tokens_per_split - 1) / p.tokens_per_split);
-  p.bytes = p.splits > 1 || gaps ? p.splits * rows * cols * 4 : 0;
+  p.direct = make_place(L, tensor, &lo, &hi).gap == 0;
+  p.side = SIDE;
+  p.row_tiles = (rows + p.side - 1) / p.side;
+  p.col_tiles = (cols + p.side - 1) / p.side;
+  const int64_t tiles = p.row_tiles * p.col_tiles;
+  p.whole = tiles / kCus * kCus;
+  p.further = tiles - p.whole;
+  p.splits = 1;
+  p.tokens_per_split = std::max<int64_t>(tokens, 1);
+  if (p.further > 0) {
+    const int64_t most = std::max<int64_t>(1, tokens / kMinSplit);
+    p.splits = std::max<int64_t>(1, std::min(most, kCus / p.further));
+    p.tokens_per_split = std::max<int64_t>(1, (tokens + p.splits * kStep - 1) / (p.splits * kStep)) * kStep;
+    p.splits = std::max<int64_t>(1, (tokens + p.tokens_per_split - 1) / p.tokens_per_split);
+    if (p.splits == 1) {  // nothing to split
+      p.whole = tiles;
+      p.further = 0;
+    }
+  }
+  p.slots = (p.direct ? 0 : p.whole) + p.further * p.splits;
+  p.bytes = p.slots * p.side * p.side * 4;
   return p;
 }
 
@@ -255,6 +420,22 @@ int shape_ok(const zero_layout* L, int32_t tensor, int64_t O, int64_t I, int64_t
   if (O > ZERO_MAX_COLS || I > ZERO_MAX_COLS || tokens > ZERO_MAX_ROWS) return ZERO_ERANGE;
   if (O * I != L->numel[(size_t)tensor]) return ZERO_EINVAL;
   return ZERO_OK;
+}
+
+template <int W, bool TR>
+int launch(const Args& A, const Plan& p, hipStream_t s) {
+  constexpr int kSide = 64 * W;
+  hipLaunchKernelGGL((grad_kernel<W, TR>), dim3((unsigned)(p.whole + p.further * p.splits)),
+                     dim3(kThreads), 0, s, A);
+  const int rc = launched();
+  if (rc != ZERO_OK || p.slots == 0) return rc;
+  const int32_t first = p.direct ? (int32_t)p.whole : 0;
+  const unsigned grid = (unsigned)((p.whole + p.further - first) * kSumParts);
+  if (A.out.place.gap)
+    hipLaunchKernelGGL((sum_kernel<kSide, true>), dim3(grid), dim3(kThreads), 0, s, A, first);
+  else
+    hipLaunchKernelGGL((sum_kernel<kSide, false>), dim3(grid), dim3(kThreads), 0, s, A, first);
+  return launched();
 }
 
 }  // namespace
@@ -290,7 +471,8 @@ int zero_linear_grad(const zero_layout* L, int32_t tensor, int32_t transposed, c
   const Plan p = make_plan(L, tensor, rows, cols, tokens);
   if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes || ((uintptr_t)workspace & 15u)))
     return ZERO_EINVAL;
-  if (p.row_tiles * p.col_tiles > ((int64_t)1 << 23)) return ZERO_ERANGE;
+  // the dispatch grid counts work-items in 32 bits
+  if (p.row_tiles * p.col_tiles > ((int64_t)1 << 18)) return ZERO_ERANGE;
   Args A;
   int64_t lo, hi;
   A.out.place = make_place(L, tensor, &lo, &hi);
@@ -308,6 +490,9 @@ int zero_linear_grad(const zero_layout* L, int32_t tensor, int32_t transposed, c
   A.scales = scales;
   A.tokens = tokens;
   A.tokens_per_split = p.tokens_per_split;
+  A.whole = (int32_t)p.whole;
+  A.fast = O % 8 == 0 && I % 16 == 0;
+  A.direct = p.direct;
   A.O = (int32_t)O;
   A.I = (int32_t)I;
   A.nb = (int32_t)nb;
@@ -321,21 +506,9 @@ int zero_linear_grad(const zero_layout* L, int32_t tensor, int32_t transposed, c
   A.out.out = bf16_flat;
   A.out.scale = scale;
   A.out.flags = flags;
-  const dim3 grid((unsigned)(p.row_tiles * p.col_tiles), (unsigned)p.splits);
-  if (transposed)
-    hipLaunchKernelGGL((grad_kernel<2, true>), grid, dim3(kThreads), 0, stream, A);
-  else
-    hipLaunchKernelGGL((grad_kernel<2, false>), grid, dim3(kThreads), 0, stream, A);
-  rc = launched();
-  if (rc != ZERO_OK || !A.partial) return rc;
-  const unsigned sgrid = (unsigned)std::min<int64_t>((numel / 4 + kThreads) / kThreads, 1 << 14);
-  if (A.out.place.gap)
-    hipLaunchKernelGGL(sum_kernel<true>, dim3(sgrid), dim3(kThreads), 0, stream, A.partial,
-                       A.splits, numel, A.out);
-  else
-    hipLaunchKernelGGL(sum_kernel<false>, dim3(sgrid), dim3(kThreads), 0, stream, A.partial,
-                       A.splits, numel, A.out);
-  return launched();
+  const int rc2 = p.side == 256 ? (transposed ? launch<4, true>(A, p, stream) : launch<4, false>(A, p, stream))
+                                : (transposed ? launch<2, true>(A, p, stream) : launch<2, false>(A, p, stream));
+  return rc2;
 }
 
 }  // extern "C"

@@ -24,6 +24,14 @@ typedef u32x4 u32x4_a1 __attribute__((aligned(1)));
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
 
+// Streamed once: non-temporal.
+__device__ __forceinline__ f32x4 ld4_stream(const float* p) {
+  return __builtin_nontemporal_load((const f32x4_a4*)p);
+}
+__device__ __forceinline__ void st4_stream(float* p, f32x4 v) {
+  __builtin_nontemporal_store(v, (f32x4_a4*)p);
+}
+
 // Element i of the tensor lies at flat position x0 + i where no padding falls
 // inside the tensor (gap == 0, x0 a flat position), otherwise at
 // x + (x / cap) * gap with x = x0 + i its stream position.
@@ -57,16 +65,20 @@ __device__ __forceinline__ void grad_store(const GradOut& o, int64_t p, float g)
   if (o.flags & ZERO_ACC_EMIT_BF16) o.out[p] = (uint16_t)bf16_round(a);
 }
 
-// Four consecutive flat positions.
-__device__ __forceinline__ void grad_store4(const GradOut& o, int64_t p, f32x4 g) {
+// Four consecutive flat positions; `b`: what the accumulator holds there,
+// which a kernel may have loaded early (grad_load4).
+__device__ __forceinline__ f32x4 grad_load4(const GradOut& o, int64_t p) {
+  return (o.flags & ZERO_ACC_OVERWRITE) ? f32x4{0.f, 0.f, 0.f, 0.f} : ld4_stream(o.acc + p);
+}
+__device__ __forceinline__ void grad_store4(const GradOut& o, int64_t p, f32x4 g, f32x4 b) {
   f32x4 a = {o.scale * g.x, o.scale * g.y, o.scale * g.z, o.scale * g.w};
-  if (!(o.flags & ZERO_ACC_OVERWRITE)) {
-    const f32x4 b = *(const f32x4_a4*)(o.acc + p);
-    a = f32x4{b.x + a.x, b.y + a.y, b.z + a.z, b.w + a.w};
-  }
-  if (!(o.flags & ZERO_ACC_NO_STORE)) *(f32x4_a4*)(o.acc + p) = a;
+  if (!(o.flags & ZERO_ACC_OVERWRITE)) a = f32x4{b.x + a.x, b.y + a.y, b.z + a.z, b.w + a.w};
+  if (!(o.flags & ZERO_ACC_NO_STORE)) st4_stream(o.acc + p, a);
   if (o.flags & ZERO_ACC_EMIT_BF16)
     *(u32x2_a2*)(o.out + p) = u32x2{bf16_pack2(a.x, a.y), bf16_pack2(a.z, a.w)};
+}
+__device__ __forceinline__ void grad_store4(const GradOut& o, int64_t p, f32x4 g) {
+  grad_store4(o, p, g, grad_load4(o, p));
 }
 
 // Exact division of n < 2^31 by d in [1, 2^31): with s = ceil(log2 d) and
