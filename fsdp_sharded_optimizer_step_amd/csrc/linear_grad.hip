@@ -69,10 +69,13 @@ struct DyTile {
   static __device__ __forceinline__ uint32_t fast_offset(const Args& A, int32_t c0) {
     return (uint32_t)(row() * A.dy_stride + min(c0 + col(), A.O - 8)) * 2u;
   }
+  __device__ __forceinline__ void fast1(const Args& A, int64_t t0, uint32_t off, int k) {
+    const char* p = (const char*)(A.dy + (t0 + k * kRows) * A.dy_stride);
+    v[k] = *(const u32x4_a2*)(p + off);
+  }
   __device__ __forceinline__ void fast(const Args& A, int64_t t0, uint32_t off) {
-    const char* p = (const char*)(A.dy + t0 * A.dy_stride);
 #pragma unroll
-    for (int k = 0; k < kN; ++k) v[k] = *(const u32x4_a2*)(p + (int64_t)k * kRows * 2 * A.dy_stride + off);
+    for (int k = 0; k < kN; ++k) fast1(A, t0, off, k);
   }
   static __device__ __forceinline__ void fill(const Args& A, int64_t t0, int64_t tz, int32_t c0,
                                               lds_char* lds) {
@@ -94,10 +97,12 @@ struct DyTile {
       *(lds_u32x4*)(to + k * kRows * 64) = w;
     }
   }
+  __device__ __forceinline__ void store1(lds_char* lds, int k) const {
+    *(lds_u32x4*)(lds + (col() >> 5) * kPanelBytes + (k * kRows + row()) * 64 + (col() & 31) * 2) = v[k];
+  }
   __device__ __forceinline__ void store(lds_char* lds) const {
-    lds_char* p = lds + (col() >> 5) * kPanelBytes + row() * 64 + (col() & 31) * 2;
 #pragma unroll
-    for (int k = 0; k < kN; ++k) *(lds_u32x4*)(p + k * kRows * 64) = v[k];
+    for (int k = 0; k < kN; ++k) store1(lds, k);
   }
 };
 
@@ -114,14 +119,16 @@ struct XTile {
   static __device__ __forceinline__ uint32_t fast_scale_offset(const Args& A, int32_t c0) {
     return (uint32_t)(row() * A.nb + (min(c0 + col(), A.I - 16) >> 7));
   }
+  __device__ __forceinline__ void fast1(const Args& A, int64_t t0, uint32_t off, uint32_t soff,
+                                        int k) {
+    const uint8_t* p = A.codes + (t0 + k * kRows) * A.I;
+    const uint8_t* s = A.scales + (t0 + k * kRows) * A.nb;
+    v[k] = *(const u32x4_a1*)(p + off);
+    e[k] = s[soff];
+  }
   __device__ __forceinline__ void fast(const Args& A, int64_t t0, uint32_t off, uint32_t soff) {
-    const char* p = (const char*)(A.codes + t0 * A.I);
-    const uint8_t* s = A.scales + t0 * A.nb;
 #pragma unroll
-    for (int k = 0; k < kN; ++k) {
-      v[k] = *(const u32x4_a1*)(p + (int64_t)k * kRows * A.I + off);
-      e[k] = *(s + (int64_t)k * kRows * A.nb + soff);
-    }
+    for (int k = 0; k < kN; ++k) fast1(A, t0, off, soff, k);
   }
   static __device__ __forceinline__ void put(lds_char* to, const u32x4& v, uint32_t byte) {
     const float s = act8_scale(byte);
@@ -152,10 +159,12 @@ struct XTile {
       put(to + k * kRows * 64, w, b);
     }
   }
+  __device__ __forceinline__ void store1(lds_char* lds, int k) const {
+    put(lds + (col() >> 5) * kPanelBytes + (k * kRows + row()) * 64 + (col() & 31) * 2, v[k], e[k]);
+  }
   __device__ __forceinline__ void store(lds_char* lds) const {
-    lds_char* p = lds + (col() >> 5) * kPanelBytes + row() * 64 + (col() & 31) * 2;
 #pragma unroll
-    for (int k = 0; k < kN; ++k) put(p + k * kRows * 64, v[k], e[k]);
+    for (int k = 0; k < kN; ++k) store1(lds, k);
   }
 };
 
@@ -170,6 +179,25 @@ __device__ __forceinline__ bf16x8 frag(const lds_char* panel) {
 __device__ __forceinline__ int frag_offset() {
   const int l = threadIdx.x & 63, g = l >> 4, i = l & 15;
   return ((i >> 2) + 4 * (g >> 1)) * 64 + (g & 1) * 32 + (i & 3) * 8;
+}
+
+// Instruction order of a stretch of MF matrix instructions: the LDS reads (DR)
+// beside the first half of them, so that the next stretch finds its
+// fragments, LDS writes (DW) and global loads (GL) beside the second half.
+template <int MF, int DR, int DW, int GL>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int k = 0; k < MF / 2; ++k) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 2 * DR / MF, 0);
+  }
+#pragma unroll
+  for (int k = 0; k < MF / 2; ++k) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (DW > 0) __builtin_amdgcn_sched_group_barrier(0x200, 2 * DW / MF, 0);
+    if constexpr (GL > 0) __builtin_amdgcn_sched_group_barrier(0x020, 2 * GL / MF, 0);
+  }
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 // Tile number to place: groups of 8 rows of tiles, column by column within a
@@ -223,11 +251,12 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const Args A) {
 #pragma unroll
       for (int k = 0; k < 16; ++k) acc[a][b][k] = 0.f;
 
-  DyTile<kSide> dy;
-  XTile<kSide> x;
+  DyTile<kSide> dy[2];
+  XTile<kSide> x[2];
   const int32_t dy_c = TR ? c0 : r0, x_c = TR ? r0 : c0;
-  const uint32_t dy_off = dy.fast_offset(A, dy_c), x_off = x.fast_offset(A, x_c),
-                 s_off = x.fast_scale_offset(A, x_c);
+  const uint32_t dy_off = DyTile<kSide>::fast_offset(A, dy_c),
+                 x_off = XTile<kSide>::fast_offset(A, x_c),
+                 s_off = XTile<kSide>::fast_scale_offset(A, x_c);
   lds_char* const dy_lds = lds + (TR ? kOperand : 0);
   lds_char* const x_lds = lds + (TR ? 0 : kOperand);
   const lds_char* const fa = lds + wm * W * kPanelBytes + frag_offset();
@@ -235,21 +264,25 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const Args A) {
 
   const int64_t steps = (tz - ta + kStep - 1) / kStep;
   const int64_t full = A.fast ? (tz - ta) / kStep : 0;  // steps that fast loads can take
-  auto load = [&](int64_t k) {
-    dy.fast(A, ta + k * kStep, dy_off);
-    x.fast(A, ta + k * kStep, x_off, s_off);
+  // full step k waits in set k % 2 of the registers
+  auto load = [&](int64_t k, int set) {
+    dy[set].fast(A, ta + k * kStep, dy_off);
+    x[set].fast(A, ta + k * kStep, x_off, s_off);
   };
   auto fill = [&](int64_t k, int buf) {
-    dy.fill(A, ta + k * kStep, tz, dy_c, dy_lds + buf * kBuffer);
-    x.fill(A, ta + k * kStep, tz, x_c, x_lds + buf * kBuffer);
+    DyTile<kSide>::fill(A, ta + k * kStep, tz, dy_c, dy_lds + buf * kBuffer);
+    XTile<kSide>::fill(A, ta + k * kStep, tz, x_c, x_lds + buf * kBuffer);
   };
   bf16x8 a[2][W], b[2][W];
+  auto read1 = [&](int to, int buf, int s, int q) {
+    if (q & 1)
+      b[to][q >> 1] = frag(fb + buf * kBuffer + (q >> 1) * kPanelBytes + s * 1024);
+    else
+      a[to][q >> 1] = frag(fa + buf * kBuffer + (q >> 1) * kPanelBytes + s * 1024);
+  };
   auto read = [&](int to, int buf, int s) {
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
-      a[to][k] = frag(fa + buf * kBuffer + k * kPanelBytes + s * 1024);
-      b[to][k] = frag(fb + buf * kBuffer + k * kPanelBytes + s * 1024);
-    }
+    for (int q = 0; q < 2 * W; ++q) read1(to, buf, s, q);
   };
   auto multiply = [&](int from) {
 #pragma unroll
@@ -258,71 +291,126 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const Args A) {
       for (int n = 0; n < W; ++n)
         acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[from][m], b[from][n], acc[m][n], 0, 0, 0);
   };
-  auto store = [&](int buf) {
-    dy.store(dy_lds + buf * kBuffer);
-    x.store(x_lds + buf * kBuffer);
+  auto store = [&](int set, int buf) {
+    dy[set].store(dy_lds + buf * kBuffer);
+    x[set].store(x_lds + buf * kBuffer);
+  };
+  // Step k, in buffer `buf`: its products; step k + 1 goes from the registers
+  // to the other buffer, step k + 3 is requested into the same registers.
+  auto step = [&](int64_t k, int buf) {
+    constexpr int kM = W * W, kR = 4 * W, kX = XTile<kSide>::kN, kDy = DyTile<kSide>::kN;
+    const int set = buf ^ 1;
+    read(1, buf, 1);
+    x[set].store(x_lds + (buf ^ 1) * kBuffer);
+    x[set].fast(A, ta + (k + 3) * kStep, x_off, s_off);
+    multiply(0);
+    interleave<kM, kR, 2 * kX, 2 * kX>();
+    read(0, buf, 2);
+    dy[set].store(dy_lds + (buf ^ 1) * kBuffer);
+    dy[set].fast(A, ta + (k + 3) * kStep, dy_off);
+    multiply(1);
+    interleave<kM, kR, kDy, kDy>();
+    read(1, buf, 3);
+    multiply(0);
+    interleave<kM, kR, 0, 0>();
+    __syncthreads();
+    read(0, buf ^ 1, 0);
+    multiply(1);
+    interleave<kM, kR, 0, 0>();
   };
 
   if (steps > 0) {
     if (full > 0) {
-      load(0);
-      store(0);
+      load(0, 0);
+      store(0, 0);
     } else {
       fill(0, 0);
     }
-    if (full > 1) load(1);
+    if (full > 1) load(1, 1);
+    if (full > 2) load(2, 0);
     __syncthreads();
     read(0, 0, 0);
     int64_t k = 0;
-    int buf = 0;
-    for (; k + 2 < full; ++k) {
-      read(1, buf, 1);
-      multiply(0);
-      read(0, buf, 2);
-      multiply(1);
-      read(1, buf, 3);
-      store(buf ^ 1);
-      load(k + 2);
-      multiply(0);
-      __syncthreads();
-      buf ^= 1;
-      read(0, buf, 0);
-      multiply(1);
+    for (; k + 4 < full; k += 2) {
+      step(k, 0);
+      step(k + 1, 1);
     }
     // the last full steps, and those that need checks
     for (; k < steps; ++k) {
+      const int buf = (int)(k & 1);
       read(1, buf, 1);
       multiply(0);
       read(0, buf, 2);
       multiply(1);
       read(1, buf, 3);
       multiply(0);
-      if (k + 1 < full)
-        store(buf ^ 1);
-      else if (k + 1 < steps)
+      if (k + 1 < full) {
+        if (buf)
+          store(0, 0);
+        else
+          store(1, 1);
+        if (k + 3 < full) {
+          if (buf)
+            load(k + 3, 0);
+          else
+            load(k + 3, 1);
+        }
+      } else if (k + 1 < steps) {
         fill(k + 1, buf ^ 1);
+      }
       __syncthreads();
-      buf ^= 1;
-      if (k + 1 < steps) read(0, buf, 0);
+      if (k + 1 < steps) read(0, buf ^ 1, 0);
       multiply(1);
     }
   }
 
   // lane l, register k: row 8*(k/4) + 4*(l/32) + k%4, column l%32
   if (A.direct && tile < A.whole) {
+    // Two 32 x 32 blocks at a time, every load before the first store: one
+    // wait for memory per 32 values (with a wait for each value this part
+    // took a quarter of the kernel's time).
+    const uint32_t lane_off = (uint32_t)(4 * (lane >> 5)) * (uint32_t)A.cols + (lane & 31);
+    const bool add = !(A.out.flags & ZERO_ACC_OVERWRITE);
+    const bool keep = !(A.out.flags & ZERO_ACC_NO_STORE), emit = A.out.flags & ZERO_ACC_EMIT_BF16;
 #pragma unroll
-    for (int n = 0; n < W; ++n) {
-      const int32_t c = c0 + (wn * W + n) * 32 + (lane & 31);
-      if (c >= A.cols) continue;
+    for (int m = 0; m < W; ++m)
 #pragma unroll
-      for (int m = 0; m < W; ++m)
+      for (int n0 = 0; n0 < W; n0 += 2) {
+        const int32_t rb = r0 + (wm * W + m) * 32, cb = c0 + (wn * W + n0) * 32;
+        const int64_t at = A.out.place.x0 + (int64_t)rb * A.cols + cb;
+        float* const p = A.out.acc + at;
+        uint16_t* const q = A.out.out + at;
+        const int32_t row_left = A.rows - rb - 4 * (lane >> 5), col_left = A.cols - cb - (lane & 31);
+        float v[2][16];
+        if (add) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int32_t r = r0 + (wm * W + m) * 32 + 8 * (k >> 2) + 4 * (lane >> 5) + (k & 3);
-          if (r >= A.rows) continue;
-          grad_store(A.out, A.out.place.x0 + (int64_t)r * A.cols + c, acc[m][n][k]);
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int32_t r = 8 * (k >> 2) + (k & 3);
+              if (r < row_left && n * 32 < col_left)
+                v[n][k] = __builtin_nontemporal_load(p + (int64_t)r * A.cols + n * 32 + lane_off);
+            }
         }
-    }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float g = A.out.scale * acc[m][n0 + n][k];
+            v[n][k] = add ? v[n][k] + g : g;
+          }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int32_t r = 8 * (k >> 2) + (k & 3);
+            if (r < row_left && n * 32 < col_left) {
+              const int64_t o = (int64_t)r * A.cols + n * 32;
+              if (keep) __builtin_nontemporal_store(v[n][k], p + o + lane_off);
+              if (emit) q[o + lane_off] = (uint16_t)bf16_round(v[n][k]);
+            }
+          }
+      }
     return;
   }
   // a tile of the workspace, rows of kSide columns
@@ -384,14 +472,14 @@ struct Plan {
 // Where padding falls inside the tensor every tile goes through the
 // workspace, and the sum places it.
 constexpr int64_t kCus = 256, kMinSplit = 256;
-#ifndef SIDE
-#define SIDE 256
+#ifndef TILE_SIDE
+#define TILE_SIDE 256
 #endif
 Plan make_plan(const zero_layout* L, int32_t tensor, int64_t rows, int64_t cols, int64_t tokens) {
   int64_t lo, hi;
   Plan p;
   p.direct = make_place(L, tensor, &lo, &hi).gap == 0;
-  p.side = SIDE;
+  p.side = TILE_SIDE;
   p.row_tiles = (rows + p.side - 1) / p.side;
   p.col_tiles = (cols + p.side - 1) / p.side;
   const int64_t tiles = p.row_tiles * p.col_tiles;
