@@ -31,12 +31,25 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 
-constexpr int kThreads = 256;  // 4 waves, two by two over the tile
-constexpr int kStep = 64;      // tokens of one LDS tile
-// A panel: 64 tokens of 32 columns in bf16, 64 bytes to a token.  Panels lie
-// 64 bytes further apart than they are long, so that the writes of one token
-// row, which go to as many panels as the tile is wide, spread over the banks.
-constexpr int kPanelBytes = kStep * 64 + 64;
+// The shape of a block: G groups of 4 waves; the waves of a group lie two by
+// two over the tile, W panels of 32 columns along each side of a wave, and
+// each group sums 64 of the 64*G tokens of an LDS tile.
+template <int W_, int G_>
+struct Shape {
+  static constexpr int W = W_, G = G_;
+  static constexpr int kSide = 64 * W;
+  static constexpr int kThreads = 256 * G;
+  static constexpr int kStep = 64 * G;  // tokens of one LDS tile
+  // A panel: kStep tokens of 32 columns in bf16, 64 bytes to a token.  Panels
+  // lie 64 bytes further apart than they are long, so that the writes of one
+  // token row, which go to as many panels as the tile is wide, spread over
+  // the banks.
+  static constexpr int kPanelBytes = kStep * 64 + 64;
+  static constexpr int kOperand = 2 * W * kPanelBytes, kBuffer = 2 * kOperand;
+};
+typedef Shape<4, 1> Large;
+typedef Shape<2, 2> Small;
+constexpr int kSumThreads = 256;
 
 struct Args {
   const uint16_t* dy;
@@ -56,13 +69,13 @@ struct Args {
   GradOut out;
 };
 
-// One thread's part of a tile of TC columns and kStep tokens: chunks of 8
+// One thread's part of a tile of kSide columns and kStep tokens: chunks of 8
 // columns of dY or 16 of X (16 bytes each).  `fast` loads take whole chunks
 // of whole steps; a chunk past the last column is read from the last one (its
 // sums are not stored).  fill() checks every element and goes to LDS at once.
-template <int TC>
+template <class S>
 struct DyTile {
-  static constexpr int kPerRow = TC / 8, kRows = kThreads / kPerRow, kN = kStep / kRows;
+  static constexpr int kPerRow = S::kSide / 8, kRows = S::kThreads / kPerRow, kN = S::kStep / kRows;
   u32x4 v[kN];
   static __device__ __forceinline__ int col() { return (threadIdx.x % kPerRow) * 8; }
   static __device__ __forceinline__ int row() { return threadIdx.x / kPerRow; }
@@ -80,7 +93,7 @@ struct DyTile {
   static __device__ __forceinline__ void fill(const Args& A, int64_t t0, int64_t tz, int32_t c0,
                                               lds_char* lds) {
     const int c = c0 + col();
-    lds_char* to = lds + (col() >> 5) * kPanelBytes + row() * 64 + (col() & 31) * 2;
+    lds_char* to = lds + (col() >> 5) * S::kPanelBytes + row() * 64 + (col() & 31) * 2;
 #pragma unroll 1
     for (int k = 0; k < kN; ++k) {
       const int64_t t = t0 + k * kRows + row();
@@ -98,7 +111,7 @@ struct DyTile {
     }
   }
   __device__ __forceinline__ void store1(lds_char* lds, int k) const {
-    *(lds_u32x4*)(lds + (col() >> 5) * kPanelBytes + (k * kRows + row()) * 64 + (col() & 31) * 2) = v[k];
+    *(lds_u32x4*)(lds + (col() >> 5) * S::kPanelBytes + (k * kRows + row()) * 64 + (col() & 31) * 2) = v[k];
   }
   __device__ __forceinline__ void store(lds_char* lds) const {
 #pragma unroll
@@ -106,9 +119,9 @@ struct DyTile {
   }
 };
 
-template <int TC>
+template <class S>
 struct XTile {
-  static constexpr int kPerRow = TC / 16, kRows = kThreads / kPerRow, kN = kStep / kRows;
+  static constexpr int kPerRow = S::kSide / 16, kRows = S::kThreads / kPerRow, kN = S::kStep / kRows;
   u32x4 v[kN];
   uint32_t e[kN];
   static __device__ __forceinline__ int col() { return (threadIdx.x % kPerRow) * 16; }
@@ -130,17 +143,23 @@ struct XTile {
 #pragma unroll
     for (int k = 0; k < kN; ++k) fast1(A, t0, off, soff, k);
   }
+  // A chunk's 32 bytes go to LDS as two writes.  Eight lanes write at a time,
+  // to four panels, of which those two apart share their banks: the lanes of
+  // the further two write their second half first.
   static __device__ __forceinline__ void put(lds_char* to, const u32x4& v, uint32_t byte) {
+    const bool swap = (col() >> 6) & 1;
     const float s = act8_scale(byte);
-    const u32x2 a = act8_bf16x4(v.x, s), b = act8_bf16x4(v.y, s);
-    const u32x2 d = act8_bf16x4(v.z, s), f = act8_bf16x4(v.w, s);
-    *(lds_u32x4*)to = u32x4{a.x, a.y, b.x, b.y};
-    *(lds_u32x4*)(to + 16) = u32x4{d.x, d.y, f.x, f.y};
+    const u32x2 first = swap ? u32x2{v.z, v.w} : u32x2{v.x, v.y};
+    const u32x2 second = swap ? u32x2{v.x, v.y} : u32x2{v.z, v.w};
+    const u32x2 a = act8_bf16x4(first.x, s), b = act8_bf16x4(first.y, s);
+    const u32x2 d = act8_bf16x4(second.x, s), f = act8_bf16x4(second.y, s);
+    *(lds_u32x4*)(to + (swap ? 16 : 0)) = u32x4{a.x, a.y, b.x, b.y};
+    *(lds_u32x4*)(to + (swap ? 0 : 16)) = u32x4{d.x, d.y, f.x, f.y};
   }
   static __device__ __forceinline__ void fill(const Args& A, int64_t t0, int64_t tz, int32_t c0,
                                               lds_char* lds) {
     const int c = c0 + col();
-    lds_char* to = lds + (col() >> 5) * kPanelBytes + row() * 64 + (col() & 31) * 2;
+    lds_char* to = lds + (col() >> 5) * S::kPanelBytes + row() * 64 + (col() & 31) * 2;
 #pragma unroll 1
     for (int k = 0; k < kN; ++k) {
       const int64_t t = t0 + k * kRows + row();
@@ -160,7 +179,7 @@ struct XTile {
     }
   }
   __device__ __forceinline__ void store1(lds_char* lds, int k) const {
-    put(lds + (col() >> 5) * kPanelBytes + (k * kRows + row()) * 64 + (col() & 31) * 2, v[k], e[k]);
+    put(lds + (col() >> 5) * S::kPanelBytes + (k * kRows + row()) * 64 + (col() & 31) * 2, v[k], e[k]);
   }
   __device__ __forceinline__ void store(lds_char* lds) const {
 #pragma unroll
@@ -209,18 +228,23 @@ __device__ __forceinline__ void tile_at(const Args& A, int32_t tile, int32_t& r,
   r = g * 8 + in - c * h;
 }
 
-// W: 32-column panels of a wave along each side; the block's tile is 2W
-// panels wide and high.  TR: rows of the gradient are X's columns.
+// The workspace's tiles: those that do not go out directly.
+__device__ __forceinline__ int64_t slot_of(const Args& A, int32_t tile, int32_t split) {
+  const int64_t kept = A.direct ? 0 : A.whole;
+  return tile < A.whole ? tile : kept + (int64_t)(tile - A.whole) * A.splits + split;
+}
+
+// TR: rows of the gradient are X's columns.
 //
 // Two LDS buffers.  While the matrix cores work on one step, the next one's
 // chunks are converted and written to the other buffer and those of the step
 // after that are requested; fragments are read a sixteenth of tokens ahead.
 // One barrier a step, before its last sixteenth, whose fragments are already
 // in registers.
-template <int W, bool TR>
-__global__ void __launch_bounds__(kThreads, 1) grad_kernel(const Args A) {
-  constexpr int kSide = 64 * W;
-  constexpr int kOperand = 2 * W * kPanelBytes, kBuffer = 2 * kOperand;
+template <class S, bool TR>
+__global__ void __launch_bounds__(S::kThreads, 1) grad_kernel(const Args A) {
+  constexpr int W = S::W, G = S::G, kSide = S::kSide, kStep = S::kStep;
+  constexpr int kPanelBytes = S::kPanelBytes, kOperand = S::kOperand, kBuffer = S::kBuffer;
   __shared__ __align__(16) char shared[2 * kBuffer];
   lds_char* lds = (lds_char*)shared;
 
@@ -242,7 +266,8 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const Args A) {
   r0 *= kSide;
   c0 *= kSide;
 
-  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1, lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6, wm = (wave >> 1) & 1, wn = wave & 1, group = wave >> 2;
+  const int lane = threadIdx.x & 63;
   f32x16 acc[W][W];
 #pragma unroll
   for (int a = 0; a < W; ++a)
@@ -251,16 +276,17 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const Args A) {
 #pragma unroll
       for (int k = 0; k < 16; ++k) acc[a][b][k] = 0.f;
 
-  DyTile<kSide> dy[2];
-  XTile<kSide> x[2];
+  DyTile<S> dy[2];
+  XTile<S> x[2];
   const int32_t dy_c = TR ? c0 : r0, x_c = TR ? r0 : c0;
-  const uint32_t dy_off = DyTile<kSide>::fast_offset(A, dy_c),
-                 x_off = XTile<kSide>::fast_offset(A, x_c),
-                 s_off = XTile<kSide>::fast_scale_offset(A, x_c);
+  const uint32_t dy_off = DyTile<S>::fast_offset(A, dy_c),
+                 x_off = XTile<S>::fast_offset(A, x_c),
+                 s_off = XTile<S>::fast_scale_offset(A, x_c);
   lds_char* const dy_lds = lds + (TR ? kOperand : 0);
   lds_char* const x_lds = lds + (TR ? 0 : kOperand);
-  const lds_char* const fa = lds + wm * W * kPanelBytes + frag_offset();
-  const lds_char* const fb = lds + kOperand + wn * W * kPanelBytes + frag_offset();
+  // a group's 64 tokens: 4096 bytes of a panel
+  const lds_char* const fa = lds + wm * W * kPanelBytes + group * 4096 + frag_offset();
+  const lds_char* const fb = lds + kOperand + wn * W * kPanelBytes + group * 4096 + frag_offset();
 
   const int64_t steps = (tz - ta + kStep - 1) / kStep;
   const int64_t full = A.fast ? (tz - ta) / kStep : 0;  // steps that fast loads can take
@@ -270,8 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const Args A) {
     x[set].fast(A, ta + k * kStep, x_off, s_off);
   };
   auto fill = [&](int64_t k, int buf) {
-    DyTile<kSide>::fill(A, ta + k * kStep, tz, dy_c, dy_lds + buf * kBuffer);
-    XTile<kSide>::fill(A, ta + k * kStep, tz, x_c, x_lds + buf * kBuffer);
+    DyTile<S>::fill(A, ta + k * kStep, tz, dy_c, dy_lds + buf * kBuffer);
+    XTile<S>::fill(A, ta + k * kStep, tz, x_c, x_lds + buf * kBuffer);
   };
   bf16x8 a[2][W], b[2][W];
   auto read1 = [&](int to, int buf, int s, int q) {
@@ -298,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const Args A) {
   // Step k, in buffer `buf`: its products; step k + 1 goes from the registers
   // to the other buffer, step k + 3 is requested into the same registers.
   auto step = [&](int64_t k, int buf) {
-    constexpr int kM = W * W, kR = 4 * W, kX = XTile<kSide>::kN, kDy = DyTile<kSide>::kN;
+    constexpr int kM = W * W, kR = 4 * W, kX = XTile<S>::kN, kDy = DyTile<S>::kN;
     const int set = buf ^ 1;
     read(1, buf, 1);
     x[set].store(x_lds + (buf ^ 1) * kBuffer);
@@ -364,6 +390,41 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const Args A) {
     }
   }
 
+  // Two groups: each keeps one half of its rows of blocks and gets the other
+  // group's sums of it through LDS.
+  constexpr int kMine = W / G;  // rows of blocks of a wave
+  const int m0 = group * kMine;
+  if constexpr (G == 2) {
+    typedef __attribute__((address_space(3))) float lds_float;
+    lds_float* const box = (lds_float*)lds + (threadIdx.x & 255);
+    constexpr int kHalf = kMine * W * 16 * 256;  // what one group sends
+    static_assert(2 * kHalf * 4 <= 2 * kBuffer, "both fit the buffers");
+    __syncthreads();
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+      if (group == g) {
+#pragma unroll
+        for (int m = 0; m < kMine; ++m)
+#pragma unroll
+          for (int n = 0; n < W; ++n)
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              box[g * kHalf + ((m * W + n) * 16 + k) * 256] = acc[(1 - g) * kMine + m][n][k];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+      if (group == g) {
+#pragma unroll
+        for (int m = 0; m < kMine; ++m)
+#pragma unroll
+          for (int n = 0; n < W; ++n)
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              acc[m][n][k] = acc[g * kMine + m][n][k] + box[(1 - g) * kHalf + ((m * W + n) * 16 + k) * 256];
+      }
+  }
+
   // lane l, register k: row 8*(k/4) + 4*(l/32) + k%4, column l%32
   if (A.direct && tile < A.whole) {
     // Two 32 x 32 blocks at a time, every load before the first store: one
@@ -373,10 +434,10 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const Args A) {
     const bool add = !(A.out.flags & ZERO_ACC_OVERWRITE);
     const bool keep = !(A.out.flags & ZERO_ACC_NO_STORE), emit = A.out.flags & ZERO_ACC_EMIT_BF16;
 #pragma unroll
-    for (int m = 0; m < W; ++m)
+    for (int m = 0; m < kMine; ++m)
 #pragma unroll
       for (int n0 = 0; n0 < W; n0 += 2) {
-        const int32_t rb = r0 + (wm * W + m) * 32, cb = c0 + (wn * W + n0) * 32;
+        const int32_t rb = r0 + (wm * W + m0 + m) * 32, cb = c0 + (wn * W + n0) * 32;
         const int64_t at = A.out.place.x0 + (int64_t)rb * A.cols + cb;
         float* const p = A.out.acc + at;
         uint16_t* const q = A.out.out + at;
@@ -414,40 +475,36 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const Args A) {
     return;
   }
   // a tile of the workspace, rows of kSide columns
-  const int64_t slot = A.direct ? (int64_t)(tile - A.whole) * A.splits + split : tile < A.whole
-      ? tile : A.whole + (int64_t)(tile - A.whole) * A.splits + split;
-  float* const to = A.partial + slot * kSide * kSide;
+  float* const to = A.partial + slot_of(A, tile, split) * kSide * kSide + 4 * (lane >> 5) * kSide + (lane & 31);
 #pragma unroll
-  for (int n = 0; n < W; ++n)
+  for (int m = 0; m < kMine; ++m)
 #pragma unroll
-    for (int m = 0; m < W; ++m)
+    for (int n = 0; n < W; ++n)
 #pragma unroll
       for (int k = 0; k < 16; ++k)
-        to[((wm * W + m) * 32 + 8 * (k >> 2) + 4 * (lane >> 5) + (k & 3)) * kSide +
-           (wn * W + n) * 32 + (lane & 31)] = acc[m][n][k];
+        to[((wm * W + m0 + m) * 32 + 8 * (k >> 2) + (k & 3)) * kSide + (wn * W + n) * 32] = acc[m][n][k];
 }
 
 // Adds up a tile's splits, in order, and hands the sum on: blocks over the
-// tiles from `first`, kSumParts to a tile.
-constexpr int kSumParts = 16;
+// tiles from `first`, `parts` to a tile.
 template <int SIDE, bool GAPS>
-__global__ void __launch_bounds__(kThreads) sum_kernel(const Args A, int32_t first) {
-  const int32_t tile = first + (int32_t)(blockIdx.x / kSumParts);
-  const int32_t part = blockIdx.x % kSumParts;
+__global__ void __launch_bounds__(kSumThreads) sum_kernel(const Args A, int32_t first,
+                                                          int32_t parts) {
+  const int32_t tile = first + (int32_t)blockIdx.x / parts;
+  const int32_t part = (int32_t)blockIdx.x % parts;
   int32_t r0, c0;
   tile_at(A, tile, r0, c0);
   r0 *= SIDE;
   c0 *= SIDE;
   const int32_t n_splits = tile < A.whole ? 1 : A.splits;
-  const int64_t slot = A.direct ? (int64_t)(tile - A.whole) * A.splits : tile < A.whole
-      ? tile : A.whole + (int64_t)(tile - A.whole) * A.splits;
-  const float* from = A.partial + slot * SIDE * SIDE;
-  constexpr int kPart = SIDE * SIDE / 4 / kSumParts;  // groups of 4 columns
-  for (int g = part * kPart + threadIdx.x; g < (part + 1) * kPart; g += kThreads) {
+  const float* from = A.partial + slot_of(A, tile, 0) * SIDE * SIDE;
+  const int per = SIDE * SIDE / 4 / parts;  // groups of 4 columns
+  for (int g = part * per + threadIdx.x; g < (part + 1) * per; g += kSumThreads) {
     const int32_t r = r0 + g / (SIDE / 4), c = c0 + (g % (SIDE / 4)) * 4;
     const int n = min(4, A.cols - c);
     if (r >= A.rows || n <= 0) continue;
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
     for (int k = 0; k < n_splits; ++k) s += *(const f32x4*)(from + (int64_t)k * SIDE * SIDE + g * 4);
     const int64_t e = (int64_t)r * A.cols + c;
     if (!GAPS && n >= 4) {
@@ -463,6 +520,7 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const Args A, int32_t fir
 // ------------------------------------------------------------------ host
 struct Plan {
   int64_t side, row_tiles, col_tiles, whole, further, splits, tokens_per_split, slots, bytes;
+  double us;
   bool direct;
 };
 
@@ -471,15 +529,13 @@ struct Plan {
 // over as many blocks as there is room for, kMinSplit tokens each at least.
 // Where padding falls inside the tensor every tile goes through the
 // workspace, and the sum places it.
-constexpr int64_t kCus = 256, kMinSplit = 256;
-#ifndef TILE_SIDE
-#define TILE_SIDE 256
-#endif
-Plan make_plan(const zero_layout* L, int32_t tensor, int64_t rows, int64_t cols, int64_t tokens) {
-  int64_t lo, hi;
+constexpr int64_t kCus = 256, kMinSplit = 256, kGrain = 128, kMaxSplits = 32;
+
+template <class S>
+Plan plan_for(bool direct, int64_t rows, int64_t cols, int64_t tokens) {
   Plan p;
-  p.direct = make_place(L, tensor, &lo, &hi).gap == 0;
-  p.side = TILE_SIDE;
+  p.direct = direct;
+  p.side = S::kSide;
   p.row_tiles = (rows + p.side - 1) / p.side;
   p.col_tiles = (cols + p.side - 1) / p.side;
   const int64_t tiles = p.row_tiles * p.col_tiles;
@@ -489,8 +545,8 @@ Plan make_plan(const zero_layout* L, int32_t tensor, int64_t rows, int64_t cols,
   p.tokens_per_split = std::max<int64_t>(tokens, 1);
   if (p.further > 0) {
     const int64_t most = std::max<int64_t>(1, tokens / kMinSplit);
-    p.splits = std::max<int64_t>(1, std::min(most, kCus / p.further));
-    p.tokens_per_split = std::max<int64_t>(1, (tokens + p.splits * kStep - 1) / (p.splits * kStep)) * kStep;
+    p.splits = std::max<int64_t>(1, std::min({most, kCus / p.further, kMaxSplits}));
+    p.tokens_per_split = std::max<int64_t>(1, (tokens + p.splits * kGrain - 1) / (p.splits * kGrain)) * kGrain;
     p.splits = std::max<int64_t>(1, (tokens + p.tokens_per_split - 1) / p.tokens_per_split);
     if (p.splits == 1) {  // nothing to split
       p.whole = tiles;
@@ -499,7 +555,32 @@ Plan make_plan(const zero_layout* L, int32_t tensor, int64_t rows, int64_t cols,
   }
   p.slots = (p.direct ? 0 : p.whole) + p.further * p.splits;
   p.bytes = p.slots * p.side * p.side * 4;
+  // Time in us, from what one block was measured to take: a step of an LDS
+  // tile, and 8 bytes for each accumulator or workspace element at 4.7 TB/s.
+  const double step = S::kSide == 256 ? 1.53 : 1.02;
+  const double tile_io = (double)(p.side * p.side) * 8 / 4.7e6;
+  const auto steps = [](int64_t t) { return (double)((t + S::kStep - 1) / S::kStep); };
+  const double rounds = (double)((p.whole + kCus - 1) / kCus);
+  p.us = rounds * (steps(tokens) * step + kCus * tile_io);
+  if (p.further > 0)
+    p.us += steps(p.tokens_per_split) * step + (double)(p.further * (p.splits + 1)) * tile_io + 4;
   return p;
+}
+
+// The larger tile does twice the products per byte of LDS, the smaller one
+// leaves fewer CUs idle and fewer sums to the workspace.  Measured, 256 against
+// 128 columns (us): 8192 tokens, 4096 x 4096: 235, 302; 16384 tokens, 1024 x
+// 4096: 135, 151; 4000 tokens, 1024 x 4096: 61, 48; 4096 tokens, 2048 x 2048:
+// 59, 46; 1024 tokens, 768 x 768: 28, 17.  The estimate tells them apart.
+Plan make_plan(const zero_layout* L, int32_t tensor, int64_t rows, int64_t cols, int64_t tokens) {
+  int64_t lo, hi;
+  const bool direct = make_place(L, tensor, &lo, &hi).gap == 0;
+  const Plan a = plan_for<Large>(direct, rows, cols, tokens);
+  const Plan b = plan_for<Small>(direct, rows, cols, tokens);
+#ifdef TILE_SIDE
+  return TILE_SIDE == 256 ? a : b;
+#endif
+  return a.us <= b.us ? a : b;
 }
 
 int shape_ok(const zero_layout* L, int32_t tensor, int64_t O, int64_t I, int64_t tokens) {
@@ -510,20 +591,29 @@ int shape_ok(const zero_layout* L, int32_t tensor, int64_t O, int64_t I, int64_t
   return ZERO_OK;
 }
 
-template <int W, bool TR>
+template <class S, bool TR>
 int launch(const Args& A, const Plan& p, hipStream_t s) {
-  constexpr int kSide = 64 * W;
-  hipLaunchKernelGGL((grad_kernel<W, TR>), dim3((unsigned)(p.whole + p.further * p.splits)),
-                     dim3(kThreads), 0, s, A);
+  hipLaunchKernelGGL((grad_kernel<S, TR>), dim3((unsigned)(p.whole + p.further * p.splits)),
+                     dim3(S::kThreads), 0, s, A);
   const int rc = launched();
   if (rc != ZERO_OK || p.slots == 0) return rc;
   const int32_t first = p.direct ? (int32_t)p.whole : 0;
-  const unsigned grid = (unsigned)((p.whole + p.further - first) * kSumParts);
+  // about 2048 blocks, a power of two for each tile, 4 KB of sums each at least
+  const int64_t n = p.whole + p.further - first;
+  int32_t parts = S::kSide * S::kSide / 1024;
+  while (parts > 1 && parts * n > 2048) parts >>= 1;
+  const unsigned grid = (unsigned)(n * parts);
   if (A.out.place.gap)
-    hipLaunchKernelGGL((sum_kernel<kSide, true>), dim3(grid), dim3(kThreads), 0, s, A, first);
+    hipLaunchKernelGGL((sum_kernel<S::kSide, true>), dim3(grid), dim3(kSumThreads), 0, s, A, first,
+                       parts);
   else
-    hipLaunchKernelGGL((sum_kernel<kSide, false>), dim3(grid), dim3(kThreads), 0, s, A, first);
+    hipLaunchKernelGGL((sum_kernel<S::kSide, false>), dim3(grid), dim3(kSumThreads), 0, s, A, first,
+                       parts);
   return launched();
+}
+template <class S>
+int launch(const Args& A, const Plan& p, bool tr, hipStream_t s) {
+  return tr ? launch<S, true>(A, p, s) : launch<S, false>(A, p, s);
 }
 
 }  // namespace
@@ -559,7 +649,7 @@ int zero_linear_grad(const zero_layout* L, int32_t tensor, int32_t transposed, c
   const Plan p = make_plan(L, tensor, rows, cols, tokens);
   if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes || ((uintptr_t)workspace & 15u)))
     return ZERO_EINVAL;
-  // the dispatch grid counts work-items in 32 bits
+  // the dispatch grids count work-items in 32 bits
   if (p.row_tiles * p.col_tiles > ((int64_t)1 << 18)) return ZERO_ERANGE;
   Args A;
   int64_t lo, hi;
@@ -594,9 +684,8 @@ int zero_linear_grad(const zero_layout* L, int32_t tensor, int32_t transposed, c
   A.out.out = bf16_flat;
   A.out.scale = scale;
   A.out.flags = flags;
-  const int rc2 = p.side == 256 ? (transposed ? launch<4, true>(A, p, stream) : launch<4, false>(A, p, stream))
-                                : (transposed ? launch<2, true>(A, p, stream) : launch<2, false>(A, p, stream));
-  return rc2;
+  return p.side == Large::kSide ? launch<Large>(A, p, transposed != 0, stream)
+                                : launch<Small>(A, p, transposed != 0, stream);
 }
 
 }  // extern "C"
