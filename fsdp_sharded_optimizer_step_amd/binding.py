@@ -171,6 +171,7 @@ class Layout:
         self._h = h
         self.n_tensors = len(numel)
         self.numel = [int(n) for n in numel]
+        self.flat_len = lib.zero_layout_padded(h)
 
     @property
     def handle(self):
@@ -417,96 +418,106 @@ def zero_placement_plan(nbytes, traffic, lane_bytes: int, n_lanes: int, align: i
 
 
 # ------------------------------------------------- gradients of a micro-batch
-class _On:
-    """The stream of a call and the device that every tensor of it lies on.
+# These calls are short (some microseconds of GPU time on small batches), so the
+# wrappers check with as few Python steps as they can.
+_kinds = None
 
-    Used as a context it makes that device the current one (a kernel goes to
-    the device of its stream) and the stream torch's current one, so that a
-    workspace allocated inside belongs to the stream, also under capture."""
 
-    def __init__(self, where, stream, tensors):
+def _types():
+    """torch, and the types of bf16 buffers, of 8-bit codes, of ids, of
+    matrices that may be bf16 or binary32, and binary32 alone."""
+    global _kinds
+    if _kinds is None:
         import torch
-        self.where = where
-        dev = tensors[0].device
-        for t in tensors:
-            if t.device != dev:
-                raise ValueError(f"{where}: tensors on {dev} and {t.device}")
-        if not tensors[0].is_cuda:
-            raise ValueError(f"{where}: needs CUDA tensors")
-        self.device = dev
-        self.stream = torch.cuda.current_stream(dev) if stream is None else stream
-        if self.stream.device != dev:
-            raise ValueError(f"{where}: tensors on {dev}, stream on {self.stream.device}")
-        self.ptr = C.c_void_p(self.stream.cuda_stream)
-        self._plain = stream is None and torch.cuda.current_device() == dev.index
-
-    def __enter__(self):
-        if not self._plain:
-            import torch
-            self._ctx = torch.cuda.stream(self.stream)
-            self._ctx.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if not self._plain:
-            self._ctx.__exit__(*exc)
-
-    def workspace(self, given, nbytes):
-        """(pointer, bytes) of the caller's workspace, or of a new one."""
-        _check(self.where, min(0, nbytes))
-        if given is None:
-            if nbytes == 0:
-                return None, 0
-            import torch
-            given = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-            self._keep = given
-        elif not given.is_contiguous() or given.device != self.device:
-            raise ValueError(f"{self.where}: workspace: needs a contiguous tensor on {self.device}")
-        return C.c_void_p(given.data_ptr()), given.numel() * given.element_size()
+        b16 = frozenset((torch.bfloat16, torch.int16, torch.uint16))
+        _kinds = (torch, b16, frozenset((torch.float8_e4m3fn, torch.uint8, torch.int8)),
+                  frozenset((torch.int32, torch.int64)), b16 | {torch.float32},
+                  frozenset((torch.float32,)))
+    return _kinds
 
 
-def _of(where, name, t, *dtypes):
-    if t.dtype not in dtypes:
-        raise ValueError(f"{where}: {name}: {t.dtype} is not one of {dtypes}")
+def _enqueue(where, stream, tensors, call):
+    """call(stream pointer, device) with the tensors' device current, after a
+    check that they and the stream share it.  Given a stream, it is torch's
+    current one during the call, so that a workspace allocated inside belongs
+    to it, also under capture."""
+    torch = _types()[0]
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError(f"{where}: tensors on {tensors[0].device} and {t.device}")
+    if dev < 0:
+        raise ValueError(f"{where}: needs CUDA tensors")
+    if stream is None and torch._C._cuda_getDevice() == dev:
+        rc = call(torch._C._cuda_getCurrentRawStream(dev), tensors[0].device)
+    else:
+        s = torch.cuda.current_stream(dev) if stream is None else stream
+        if s.device.index != dev:
+            raise ValueError(f"{where}: tensors on {tensors[0].device}, stream on {s.device}")
+        with torch.cuda.stream(s):
+            rc = call(s.cuda_stream, tensors[0].device)
+    if rc != ZERO_OK:
+        raise ZeroError(where, rc)
 
 
-def _dense(where, name, t, shape, *dtypes):
+def _workspace(where, given, nbytes, device):
+    """The caller's workspace, or a new one of nbytes (a negative status
+    raises)."""
+    if nbytes < 0:
+        raise ZeroError(where, nbytes)
+    if given is None:
+        torch = _types()[0]
+        return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    if not given.is_contiguous() or given.device != device:
+        raise ValueError(f"{where}: workspace: needs a contiguous tensor on {device}")
+    return given
+
+
+def _bad_type(where, name, t, types):
+    return ValueError(f"{where}: {name}: {t.dtype} is not one of "
+                      f"{sorted(str(k) for k in types)}")
+
+
+def _dense(where, name, t, shape, types):
     """A contiguous tensor of that shape and one of those types."""
-    _of(where, name, t, *dtypes)
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype not in types:
+        raise _bad_type(where, name, t, types)
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{where}: {name}: needs a contiguous tensor of shape {tuple(shape)}, "
                          f"got {tuple(t.shape)} with strides {t.stride()}")
 
 
-def _matrix(where, name, t, rows, cols, *dtypes):
+def _matrix(where, name, t, rows, cols, types):
     """Distance of two rows of a matrix whose rows lie densely."""
-    _of(where, name, t, *dtypes)
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.dtype not in types:
+        raise _bad_type(where, name, t, types)
+    if t.shape != (rows, cols):
         raise ValueError(f"{where}: {name}: needs shape {(rows, cols)}, got {tuple(t.shape)}")
-    if cols > 1 and t.stride(1) != 1:
+    s0, s1 = t.stride()
+    if cols > 1 and s1 != 1:
         raise ValueError(f"{where}: {name}: columns are not adjacent (strides {t.stride()})")
     if rows <= 1:
         return max(cols, 1)
-    if t.stride(0) < cols:
+    if s0 < cols:
         raise ValueError(f"{where}: {name}: rows overlap (strides {t.stride()})")
-    return max(t.stride(0), 1)
+    return max(s0, 1)
 
 
-def _flat(where, name, t, layout, *dtypes):
-    _of(where, name, t, *dtypes)
+def _flat(where, name, t, layout, types):
+    if t.dtype not in types:
+        raise _bad_type(where, name, t, types)
     if not t.is_contiguous():
         raise ValueError(f"{where}: {name}: needs a contiguous tensor")
-    _need(t, f"{where}: {name}", layout.padded)
-
-
-def _types():
-    import torch
-    return torch, (torch.bfloat16, torch.int16, torch.uint16), \
-        (torch.float8_e4m3fn, torch.uint8, torch.int8)
+    if t.numel() < layout.flat_len:
+        _need(t, f"{where}: {name}", layout.flat_len)
 
 
 def _ptr(t):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+def _size(t):
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 def _numel(where, layout, tensor):
@@ -517,51 +528,51 @@ def _numel(where, layout, tensor):
 
 def _grad_args(where, layout, acc, flags, bf16_out):
     """The tensors among acc and bf16_out that the flags use, checked."""
-    torch, b16, _ = _types()
+    _, b16, _, _, _, f32 = _types()
     used = []
     if not (flags & ACC_OVERWRITE and flags & ACC_NO_STORE):
         if acc is None:
             raise ValueError(f"{where}: acc is needed with these flags")
-        _flat(where, "acc", acc, layout, torch.float32)
+        _flat(where, "acc", acc, layout, f32)
         used.append(acc)
     if flags & ACC_EMIT_BF16:
         if bf16_out is None:
             raise ValueError(f"{where}: bf16_out is needed with these flags")
-        _flat(where, "bf16_out", bf16_out, layout, *b16)
+        _flat(where, "bf16_out", bf16_out, layout, b16)
         used.append(bf16_out)
     return used
 
 
 def _codes(where, codes, scales, rows, cols):
-    torch, _, b8 = _types()
-    _dense(where, "codes", codes, (rows, cols), *b8)
-    _dense(where, "scales", scales, (rows, -(-cols // ACT8_BLOCK)), torch.uint8)
+    torch, _, b8, _, _, _ = _types()
+    _dense(where, "codes", codes, (rows, cols), b8)
+    _dense(where, "scales", scales, (rows, -(-cols // ACT8_BLOCK)), (torch.uint8,))
 
 
 def zero_act8_pack(x, codes, scales, stream=None):
     """8-bit codes (rows, cols) and scale bytes (rows, ceil(cols/128)) of x
     (rows, cols), bfloat16 or float32."""
     me = "zero_act8_pack"
-    torch, b16, _ = _types()
+    torch, _, _, _, real, _ = _types()
     rows, cols = codes.shape if codes.dim() == 2 else (-1, -1)
-    stride = _matrix(me, "x", x, rows, cols, torch.float32, *b16)
+    stride = _matrix(me, "x", x, rows, cols, real)
     _codes(me, codes, scales, rows, cols)
-    with _On(me, stream, (x, codes, scales)) as on:
-        _check(me, load().zero_act8_pack(_ptr(x), int(x.dtype == torch.float32), rows, cols, stride,
-                                         _ptr(codes), _ptr(scales), on.ptr))
+    _enqueue(me, stream, (x, codes, scales), lambda s, _: load().zero_act8_pack(
+        x.data_ptr(), int(x.dtype == torch.float32), rows, cols, stride, codes.data_ptr(),
+        scales.data_ptr(), s))
 
 
 def zero_act8_unpack(codes, scales, out, stream=None):
     """The values that the codes stand for, into out (rows, cols), bfloat16 or
     float32."""
     me = "zero_act8_unpack"
-    torch, b16, _ = _types()
+    torch, _, _, _, real, _ = _types()
     rows, cols = codes.shape if codes.dim() == 2 else (-1, -1)
-    stride = _matrix(me, "out", out, rows, cols, torch.float32, *b16)
+    stride = _matrix(me, "out", out, rows, cols, real)
     _codes(me, codes, scales, rows, cols)
-    with _On(me, stream, (out, codes, scales)) as on:
-        _check(me, load().zero_act8_unpack(_ptr(codes), _ptr(scales), rows, cols, _ptr(out),
-                                           int(out.dtype == torch.float32), stride, on.ptr))
+    _enqueue(me, stream, (out, codes, scales), lambda s, _: load().zero_act8_unpack(
+        codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(),
+        int(out.dtype == torch.float32), stride, s))
 
 
 def zero_embedding_lookup(layout: Layout, tensor: int, params, ids, out, scale: float = 1.0,
@@ -570,17 +581,16 @@ def zero_embedding_lookup(layout: Layout, tensor: int, params, ids, out, scale: 
     buffer `params`; ids: int32 or int64, any shape; out: (ids.numel(), cols),
     bfloat16 or float32.  A row of zeros where an id is outside the table."""
     me = "zero_embedding_lookup"
-    torch, b16, _ = _types()
+    torch, b16, _, whole, real, _ = _types()
     n = ids.numel()
     cols = out.shape[1] if out.dim() == 2 else -1
-    stride = _matrix(me, "out", out, n, cols, torch.float32, *b16)
+    stride = _matrix(me, "out", out, n, cols, real)
     _numel(me, layout, tensor)
-    _dense(me, "ids", ids, ids.shape, torch.int32, torch.int64)
-    _flat(me, "params", params, layout, *b16)
-    with _On(me, stream, (params, ids, out)) as on:
-        _check(me, load().zero_embedding_lookup(
-            layout.handle, tensor, cols, _ptr(params), _ptr(ids), ids.element_size(), n, scale,
-            _ptr(out), stride, int(out.dtype == torch.float32), on.ptr))
+    _dense(me, "ids", ids, ids.shape, whole)
+    _flat(me, "params", params, layout, b16)
+    _enqueue(me, stream, (params, ids, out), lambda s, _: load().zero_embedding_lookup(
+        layout.handle, tensor, cols, params.data_ptr(), ids.data_ptr(), ids.element_size(), n,
+        scale, out.data_ptr(), stride, int(out.dtype == torch.float32), s))
 
 
 def zero_embedding_grad(layout: Layout, tensor: int, ids, dy, acc, scale: float = 1.0,
@@ -589,21 +599,23 @@ def zero_embedding_grad(layout: Layout, tensor: int, ids, dy, acc, scale: float 
     the flat bf16 buffer `bf16_out` as the ACC_ flags say; dy: (ids.numel(),
     cols), bfloat16 or float32."""
     me = "zero_embedding_grad"
-    torch, b16, _ = _types()
+    torch, _, _, whole, real, _ = _types()
     n = ids.numel()
     cols = dy.shape[1] if dy.dim() == 2 else -1
-    stride = _matrix(me, "dy", dy, n, cols, torch.float32, *b16)
+    stride = _matrix(me, "dy", dy, n, cols, real)
     _numel(me, layout, tensor)
-    _dense(me, "ids", ids, ids.shape, torch.int32, torch.int64)
+    _dense(me, "ids", ids, ids.shape, whole)
     used = _grad_args(me, layout, acc, flags, bf16_out)
     lib = load()
-    with _On(me, stream, [ids, dy] + used) as on:
-        ws, ws_bytes = on.workspace(workspace, lib.zero_embedding_grad_workspace(
-            layout.handle, tensor, cols, n))
-        _check(me, lib.zero_embedding_grad(
-            layout.handle, tensor, cols, _ptr(ids), ids.element_size(), n, _ptr(dy), stride,
-            int(dy.dtype == torch.float32), scale, flags, _ptr(acc), _ptr(bf16_out), ws, ws_bytes,
-            on.ptr))
+
+    def call(s, device):
+        ws = _workspace(me, workspace, lib.zero_embedding_grad_workspace(
+            layout.handle, tensor, cols, n), device)
+        return lib.zero_embedding_grad(
+            layout.handle, tensor, cols, ids.data_ptr(), ids.element_size(), n, dy.data_ptr(),
+            stride, int(dy.dtype == torch.float32), scale, flags, _ptr(acc), _ptr(bf16_out),
+            _ptr(ws), _size(ws), s)
+    _enqueue(me, stream, [ids, dy] + used, call)
 
 
 def zero_rms_norm(layout: Layout, tensor: int, params, x, res, eps: float, h, rstd, codes, scales,
@@ -612,22 +624,27 @@ def zero_rms_norm(layout: Layout, tensor: int, params, x, res, eps: float, h, rs
     weighted rows in 8 bits; y: None, or the bf16 values that the codes stand
     for.  x, res: (rows, cols) bfloat16; cols = the weight's elements."""
     me = "zero_rms_norm"
-    torch, b16, _ = _types()
+    _, b16, _, _, _, f32 = _types()
     cols = _numel(me, layout, tensor)
     rows = rstd.numel()
-    xs = _matrix(me, "x", x, rows, cols, *b16)
-    rs = 0 if res is None else _matrix(me, "res", res, rows, cols, *b16)
-    _dense(me, "rstd", rstd, rstd.shape, torch.float32)
-    for name, t in (("h", h), ("y", y)):
-        if t is not None:
-            _dense(me, name, t, (rows, cols), *b16)
+    used = [params, x, rstd, codes, scales]
+    xs = _matrix(me, "x", x, rows, cols, b16)
+    rs = 0
+    if res is not None:
+        rs = _matrix(me, "res", res, rows, cols, b16)
+        used.append(res)
+    _dense(me, "rstd", rstd, rstd.shape, f32)
+    if h is not None:
+        _dense(me, "h", h, (rows, cols), b16)
+        used.append(h)
+    if y is not None:
+        _dense(me, "y", y, (rows, cols), b16)
+        used.append(y)
     _codes(me, codes, scales, rows, cols)
-    _flat(me, "params", params, layout, *b16)
-    with _On(me, stream, [t for t in (params, x, res, h, rstd, codes, scales, y)
-                          if t is not None]) as on:
-        _check(me, load().zero_rms_norm(
-            layout.handle, tensor, _ptr(params), _ptr(x), xs, _ptr(res), rs, rows, eps, _ptr(h),
-            _ptr(rstd), _ptr(codes), _ptr(scales), _ptr(y), on.ptr))
+    _flat(me, "params", params, layout, b16)
+    _enqueue(me, stream, used, lambda s, _: load().zero_rms_norm(
+        layout.handle, tensor, params.data_ptr(), x.data_ptr(), xs, _ptr(res), rs, rows, eps,
+        _ptr(h), rstd.data_ptr(), codes.data_ptr(), scales.data_ptr(), _ptr(y), s))
 
 
 def zero_rms_norm_grad(layout: Layout, tensor: int, params, dy, dh, h, rstd, dx, acc,
@@ -636,23 +653,30 @@ def zero_rms_norm_grad(layout: Layout, tensor: int, params, dy, dh, h, rstd, dx,
     """dx (the gradient of x and of res) from dy and the residual's gradient
     dh (or None); the weight's gradient, scaled, into `acc` / `bf16_out`."""
     me = "zero_rms_norm_grad"
-    torch, b16, _ = _types()
+    _, b16, _, _, _, f32 = _types()
     cols = _numel(me, layout, tensor)
     rows = rstd.numel()
-    ys = _matrix(me, "dy", dy, rows, cols, *b16)
-    hs = 0 if dh is None else _matrix(me, "dh", dh, rows, cols, *b16)
-    _dense(me, "rstd", rstd, rstd.shape, torch.float32)
-    _dense(me, "h", h, (rows, cols), *b16)
-    _dense(me, "dx", dx, (rows, cols), *b16)
-    _flat(me, "params", params, layout, *b16)
     used = _grad_args(me, layout, acc, flags, bf16_out)
+    used += [params, dy, h, rstd, dx]
+    ys = _matrix(me, "dy", dy, rows, cols, b16)
+    hs = 0
+    if dh is not None:
+        hs = _matrix(me, "dh", dh, rows, cols, b16)
+        used.append(dh)
+    _dense(me, "rstd", rstd, rstd.shape, f32)
+    _dense(me, "h", h, (rows, cols), b16)
+    _dense(me, "dx", dx, (rows, cols), b16)
+    _flat(me, "params", params, layout, b16)
     lib = load()
-    with _On(me, stream, [t for t in (params, dy, dh, h, rstd, dx) if t is not None] + used) as on:
-        ws, ws_bytes = on.workspace(workspace, lib.zero_rms_norm_grad_workspace(
-            layout.handle, tensor, rows))
-        _check(me, lib.zero_rms_norm_grad(
-            layout.handle, tensor, _ptr(params), _ptr(dy), ys, _ptr(dh), hs, _ptr(h), _ptr(rstd),
-            rows, scale, flags, _ptr(dx), _ptr(acc), _ptr(bf16_out), ws, ws_bytes, on.ptr))
+
+    def call(s, device):
+        ws = _workspace(me, workspace, lib.zero_rms_norm_grad_workspace(
+            layout.handle, tensor, rows), device)
+        return lib.zero_rms_norm_grad(
+            layout.handle, tensor, params.data_ptr(), dy.data_ptr(), ys, _ptr(dh), hs,
+            h.data_ptr(), rstd.data_ptr(), rows, scale, flags, dx.data_ptr(), _ptr(acc),
+            _ptr(bf16_out), _ptr(ws), _size(ws), s)
+    _enqueue(me, stream, used, call)
 
 
 def zero_linear_grad(layout: Layout, tensor: int, dy, codes, scales, acc, scale: float = 1.0,
@@ -663,18 +687,22 @@ def zero_linear_grad(layout: Layout, tensor: int, dy, codes, scales, acc, scale:
     checkpoint (tokens, in_features).  transposed: the weight is kept as
     (in_features, out_features)."""
     me = "zero_linear_grad"
-    torch, b16, _ = _types()
+    _, b16, _, _, _, _ = _types()
     if dy.dim() != 2 or codes.dim() != 2:
         raise ValueError(f"{me}: dy and codes need two dimensions")
     (tokens, o), i = dy.shape, codes.shape[1]
-    stride = _matrix(me, "dy", dy, tokens, o, *b16)
+    stride = _matrix(me, "dy", dy, tokens, o, b16)
     _codes(me, codes, scales, tokens, i)
     _numel(me, layout, tensor)
     used = _grad_args(me, layout, acc, flags, bf16_out)
+    used += [dy, codes, scales]
+    tr = int(transposed)
     lib = load()
-    with _On(me, stream, [dy, codes, scales] + used) as on:
-        ws, ws_bytes = on.workspace(workspace, lib.zero_linear_grad_workspace(
-            layout.handle, tensor, int(transposed), o, i, tokens))
-        _check(me, lib.zero_linear_grad(
-            layout.handle, tensor, int(transposed), _ptr(dy), stride, _ptr(codes), _ptr(scales),
-            tokens, o, i, scale, flags, _ptr(acc), _ptr(bf16_out), ws, ws_bytes, on.ptr))
+
+    def call(s, device):
+        ws = _workspace(me, workspace, lib.zero_linear_grad_workspace(
+            layout.handle, tensor, tr, o, i, tokens), device)
+        return lib.zero_linear_grad(
+            layout.handle, tensor, tr, dy.data_ptr(), stride, codes.data_ptr(), scales.data_ptr(),
+            tokens, o, i, scale, flags, _ptr(acc), _ptr(bf16_out), _ptr(ws), _size(ws), s)
+    _enqueue(me, stream, used, call)

@@ -577,9 +577,6 @@ Plan make_plan(const zero_layout* L, int32_t tensor, int64_t rows, int64_t cols,
   const bool direct = make_place(L, tensor, &lo, &hi).gap == 0;
   const Plan a = plan_for<Large>(direct, rows, cols, tokens);
   const Plan b = plan_for<Small>(direct, rows, cols, tokens);
-#ifdef TILE_SIDE
-  return TILE_SIDE == 256 ? a : b;
-#endif
   return a.us <= b.us ? a : b;
 }
 

@@ -503,7 +503,7 @@ int zero_act8_unpack(const uint8_t* codes_dev, const uint8_t* scales_dev, int64_
  * lookup: out[t] = scale * E[id_t] in binary32, rounded to out_dtype; a row of
  * zeros for a place without a token.
  * grad: dE[v] = sum over t with id_t = v, t ascending, of dY[t]: in pieces of
- * 64 tokens, then over the pieces.  Places without a token add nothing.  With
+ * 16 tokens, then over the pieces.  Places without a token add nothing.  With
  * flags 0 only the rows of ids that occur are touched; OVERWRITE and
  * EMIT_BF16 cover every row of the table, absent ids having a zero gradient. */
 int zero_embedding_lookup(const zero_layout* layout, int32_t tensor, int64_t cols,
