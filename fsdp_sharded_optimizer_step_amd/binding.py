@@ -112,7 +112,7 @@ def load():
     lib.zero_embedding_grad_workspace.argtypes = [vp, i32, i64, i64]
     lib.zero_embedding_grad.argtypes = [vp, i32, i64, vp, i32, i64, vp, i64, i32, f32, u32, vp, vp,
                                         vp, i64, vp]
-    lib.zero_rms_norm.argtypes = [vp, i32, vp, vp, i64, vp, i64, i64, f32, vp, vp, vp, vp, vp, vp]
+    lib.zero_rms_norm.argtypes = [vp, i32, vp, vp, i64, vp, i64, i64, C.c_double, vp, vp, vp, vp, vp, vp]
     lib.zero_rms_norm_grad_workspace.argtypes = [vp, i32, i64]
     lib.zero_rms_norm_grad.argtypes = [vp, i32, vp, vp, i64, vp, i64, vp, vp, i64, f32, u32, vp, vp,
                                        vp, vp, i64, vp]

@@ -63,16 +63,19 @@ struct Args {
   int32_t whole;       // tiles that one block sums over all tokens
   int32_t splits;      // blocks of each further tile
   int64_t tokens_per_split;
-  int32_t fast;        // columns come in whole chunks
+  int64_t fast_tokens; // tokens before this one can be read in whole chunks
   int32_t direct;      // whole tiles go straight to the gradient (else: like split ones)
   float* partial;      // per split and further tile, a tile of binary32 sums
   GradOut out;
 };
 
 // One thread's part of a tile of kSide columns and kStep tokens: chunks of 8
-// columns of dY or 16 of X (16 bytes each).  `fast` loads take whole chunks
-// of whole steps; a chunk past the last column is read from the last one (its
-// sums are not stored).  fill() checks every element and goes to LDS at once.
+// columns of dY or 16 of X (16 bytes each, at any alignment).  fast() takes
+// whole chunks of whole steps.  A chunk that begins past the last column is
+// read from the last chunk, and the last chunk of a row may run on into the
+// next row: what it finds there enters only sums that are not stored.  The
+// matrix's last tokens, from where it would run out of the matrix, are left to
+// fill(), which checks every element and goes to LDS at once.
 template <class S>
 struct DyTile {
   static constexpr int kPerRow = S::kSide / 8, kRows = S::kThreads / kPerRow, kN = S::kStep / kRows;
@@ -80,7 +83,7 @@ struct DyTile {
   static __device__ __forceinline__ int col() { return (threadIdx.x % kPerRow) * 8; }
   static __device__ __forceinline__ int row() { return threadIdx.x / kPerRow; }
   static __device__ __forceinline__ uint32_t fast_offset(const Args& A, int32_t c0) {
-    return (uint32_t)(row() * A.dy_stride + min(c0 + col(), A.O - 8)) * 2u;
+    return (uint32_t)(row() * A.dy_stride + min(c0 + col(), (A.O - 1) & ~7)) * 2u;
   }
   __device__ __forceinline__ void fast1(const Args& A, int64_t t0, uint32_t off, int k) {
     const char* p = (const char*)(A.dy + (t0 + k * kRows) * A.dy_stride);
@@ -127,10 +130,10 @@ struct XTile {
   static __device__ __forceinline__ int col() { return (threadIdx.x % kPerRow) * 16; }
   static __device__ __forceinline__ int row() { return threadIdx.x / kPerRow; }
   static __device__ __forceinline__ uint32_t fast_offset(const Args& A, int32_t c0) {
-    return (uint32_t)(row() * A.I + min(c0 + col(), A.I - 16));
+    return (uint32_t)(row() * A.I + min(c0 + col(), (A.I - 1) & ~15));
   }
   static __device__ __forceinline__ uint32_t fast_scale_offset(const Args& A, int32_t c0) {
-    return (uint32_t)(row() * A.nb + (min(c0 + col(), A.I - 16) >> 7));
+    return (uint32_t)(row() * A.nb + (min(c0 + col(), (A.I - 1) & ~15) >> 7));
   }
   __device__ __forceinline__ void fast1(const Args& A, int64_t t0, uint32_t off, uint32_t soff,
                                         int k) {
@@ -289,7 +292,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) grad_kernel(const Args A) {
   const lds_char* const fb = lds + kOperand + wn * W * kPanelBytes + group * 4096 + frag_offset();
 
   const int64_t steps = (tz - ta + kStep - 1) / kStep;
-  const int64_t full = A.fast ? (tz - ta) / kStep : 0;  // steps that fast loads can take
+  // steps that fast loads can take
+  const int64_t full = max((int64_t)0, min(tz, A.fast_tokens) - ta) / kStep;
   // full step k waits in set k % 2 of the registers
   auto load = [&](int64_t k, int set) {
     dy[set].fast(A, ta + k * kStep, dy_off);
@@ -666,7 +670,11 @@ int zero_linear_grad(const zero_layout* L, int32_t tensor, int32_t transposed, c
   A.tokens = tokens;
   A.tokens_per_split = p.tokens_per_split;
   A.whole = (int32_t)p.whole;
-  A.fast = O % 8 == 0 && I % 16 == 0;
+  // a row's last chunk reaches up to 7 (15) elements past its end
+  const int64_t past_dy = (O + 7) / 8 * 8 - O, past_x = (I + 15) / 16 * 16 - I;
+  const int64_t short_dy = (past_dy + std::max<int64_t>(dy_stride, 1) - 1) / std::max<int64_t>(dy_stride, 1);
+  const int64_t short_x = (past_x + I - 1) / I;
+  A.fast_tokens = tokens - std::max(short_dy, short_x);
   A.direct = p.direct;
   A.O = (int32_t)O;
   A.I = (int32_t)I;

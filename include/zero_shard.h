@@ -522,8 +522,8 @@ int zero_embedding_grad(const zero_layout* layout, int32_t tensor, int64_t cols,
  * (at most ZERO_MAX_NORM_COLS, else ZERO_ERANGE).
  *
  * forward, for every row: h = bf16(x + res) (res NULL: h = x),
- *   rstd = 1 / sqrt(mean(h^2) + eps), and h * rstd * w in the 8-bit format of
- *   zero_act8_pack.  h_dev: the new residual (may be NULL if res is);
+ *   rstd = 1 / sqrt(mean(h^2) + eps) in binary64 (stored in binary32), and
+ *   h * w * rstd, in binary64 too, in the 8-bit format of zero_act8_pack.  h_dev: the new residual (may be NULL if res is);
  *   y_dev: NULL, or the bf16 values that the codes stand for, so that the
  *   forward product reads exactly what the backward product will.
  * grad, for every row, with g = dy * w:
@@ -534,7 +534,7 @@ int zero_embedding_grad(const zero_layout* layout, int32_t tensor, int64_t cols,
 #define ZERO_MAX_NORM_COLS 32768
 int zero_rms_norm(const zero_layout* layout, int32_t tensor, const uint16_t* params_flat_dev,
                   const uint16_t* x_dev, int64_t x_stride, const uint16_t* res_dev,
-                  int64_t res_stride, int64_t rows, float eps, uint16_t* h_dev, float* rstd_dev,
+                  int64_t res_stride, int64_t rows, double eps, uint16_t* h_dev, float* rstd_dev,
                   uint8_t* codes_dev, uint8_t* scales_dev, uint16_t* y_dev, hipStream_t stream);
 int64_t zero_rms_norm_grad_workspace(const zero_layout* layout, int32_t tensor, int64_t rows);
 int zero_rms_norm_grad(const zero_layout* layout, int32_t tensor, const uint16_t* params_flat_dev,

@@ -316,6 +316,25 @@ def test_norm(gaps, rows, cols):
         assert torch.equal(q, q2) and torch.equal(e, e2)
 
 
+@pytest.mark.parametrize("rows,cols", [(200, 768), (64, 4096), (300, 129), (16, 16384)])
+def test_norm_codes_are_the_rounded_exact_values(rows, cols):
+    """Products and statistics are binary64, so a code differs from that of the
+    64-bit reference only where the value is within about 2^-40 of itself of a
+    halfway point: not among these inputs."""
+    L, pl = layout(cols, False)
+    pos = torch.from_numpy(positions(pl, cols)).to(DEV)
+    params = 1 + randn(cols, L.padded, scale=0.2)
+    x, res = randn(rows, rows, cols), randn(rows + 1, rows, cols, scale=4.0)
+    h = torch.empty(rows, cols, dtype=BF16, device=DEV)
+    rstd = torch.empty(rows, device=DEV)
+    q, e = codes_like(rows, cols)
+    z.zero_rms_norm(L, 1, params, x, res, 1e-5, h, rstd, q, e)
+    _, hd, r = norm_exact(x, res, params, 1e-5)
+    eq, ee = act8(hd * r[:, None] * f64(params[pos]))
+    assert np.array_equal(e.cpu().numpy(), ee) and np.array_equal(q.cpu().numpy(), eq)
+    assert np.array_equal(rstd.cpu().numpy(), r.astype(np.float32))
+
+
 def test_norm_zero_row_and_non_finite_row_stay_apart():
     rows, cols = 4, 300
     L, pl = layout(cols, False)
@@ -417,7 +436,8 @@ def test_norm_grad_against_differences():
 # ------------------------------------------------------------------ weight gradient
 LINEAR_SHAPES = [(1, 1, 1), (2, 3, 5), (64, 32, 32), (63, 33, 31), (65, 128, 128), (100, 129, 127),
                  (16, 300, 7), (16, 7, 300), (257, 256, 512), (700, 130, 260), (2048, 64, 48),
-                 (3000, 257, 129), (1, 1000, 1000), (130, 513, 640)]
+                 (3000, 257, 129), (1, 1000, 1000), (130, 513, 640),
+                 (200, 1, 1), (129, 1, 3), (256, 5, 16), (193, 8, 1), (640, 519, 271)]
 
 
 @pytest.mark.parametrize("tr", [False, True])
