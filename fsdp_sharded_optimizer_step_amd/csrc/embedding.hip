@@ -125,12 +125,22 @@ constexpr int kBatch = 16;
 
 struct PlanArgs {
   const void* ids;
-  int64_t vocab;
-  int32_t n, local;     // tokens; ids per slice
-  uint32_t slice_bits;  // S = 2^slice_bits slices
-  int32_t* start;       // S*local + 1 places: first place of (slice, id / S)
+  int32_t vocab, n, local;  // rows of the table; tokens; ids per slice
+  uint32_t slice_bits;      // S = 2^slice_bits slices
+  int32_t* start;           // S*local + 1 places: first place of (slice, id / S)
   Entry* order;
 };
+
+// The id at t as a number below vocab, or -1 (vocab <= 2^30).
+template <class ID>
+__device__ __forceinline__ int32_t token_at(const PlanArgs& A, int64_t t, int64_t tz) {
+  if (t >= tz) return -1;
+  const ID id = ((const ID*)A.ids)[t];
+  if constexpr (sizeof(ID) == 8) {
+    if ((uint64_t)id >> 32) return -1;
+  }
+  return (uint32_t)id < (uint32_t)A.vocab ? (int32_t)id : -1;
+}
 
 template <class ID>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs A) {
@@ -139,32 +149,29 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs A) {
   __shared__ int32_t first[kMaxLocal];            // its first place
   __shared__ int32_t wsum[kPlanWaves], wlow[kPlanWaves];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int64_t slice = blockIdx.x;
-  const int64_t mask = ((int64_t)1 << A.slice_bits) - 1;
+  const int32_t slice = (int32_t)blockIdx.x;
+  const int32_t mask = (int32_t)((1u << A.slice_bits) - 1u);
+  // each wave counts its own contiguous part of the tokens, kBatch loads at a
+  // time: the readings are bound by their latency
+  const int64_t per = ((int64_t)A.n + kPlanThreads - 1) / kPlanThreads * 64;
+  const int64_t ta = wave * per, tz = min((int64_t)A.n, ta + per);
+  int32_t id[kBatch];
+  auto read = [&](int64_t t0) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) id[k] = token_at<ID>(A, t0 + k * 64 + lane, tz);
+  };
+  if (ta < tz) read(ta);
   if (tid < A.local)
     for (int w = 0; w < kPlanWaves; ++w) cnt[w][tid] = 0;
   __syncthreads();
-  // each wave counts its own contiguous part of the tokens
-  const int64_t per = ((int64_t)A.n + kPlanThreads - 1) / kPlanThreads * 64;
-  const int64_t ta = wave * per, tz = min((int64_t)A.n, ta + per);
-  // (kBatch loads at a time: the readings are bound by their latency)
   int32_t low = 0;
-  int64_t id[kBatch];
-  auto read = [&](int64_t t0) {
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int64_t t = t0 + k * 64 + lane;
-      id[k] = t < tz ? id_at<ID>(A.ids, t) : -1;
-    }
-  };
   for (int64_t t0 = ta; t0 < tz; t0 += 64 * kBatch) {
-    read(t0);
+    if (t0 != ta) read(t0);
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const bool real = id[k] >= 0 && id[k] < A.vocab;
-      const int64_t s = id[k] & mask;
-      if (real && s < slice) ++low;
-      if (real && s == slice) atomicAdd(&cnt[wave][id[k] >> A.slice_bits], 1);
+      const int32_t s = id[k] & mask;
+      if (id[k] >= 0 && s < slice) ++low;
+      if (id[k] >= 0 && s == slice) atomicAdd(&cnt[wave][id[k] >> A.slice_bits], 1);
     }
   }
   for (int k = 32; k; k >>= 1) low += __shfl_xor(low, k, 64);
@@ -190,24 +197,24 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs A) {
   if (tid < A.local) {
     tot[tid] = mine;
     first[tid] = at;
-    A.start[slice * A.local + tid] = at;
+    A.start[(int64_t)slice * A.local + tid] = at;
     int32_t next = at;
     for (int w = 0; w < kPlanWaves; ++w) {
       const int32_t c = cnt[w][tid];
       cnt[w][tid] = next;
       next += c;
     }
-    if (slice == mask && tid == A.local - 1) A.start[(mask + 1) * A.local] = next;
+    if (slice == mask && tid == A.local - 1) A.start[((int64_t)mask + 1) * A.local] = next;
   }
   __syncthreads();
-  // second reading: tokens of this slice go to their places, in order (a wave
-  // walks its tokens upwards; equal ids among 64 tokens by lane)
+  // tokens of this slice go to their places, in order (a wave walks its
+  // tokens upwards; equal ids among 64 tokens by lane)
   for (int64_t t0 = ta; t0 < tz; t0 += 64 * kBatch) {
     if (tz - ta > 64 * kBatch) read(t0);  // one batch: still in registers
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const bool own = id[k] >= 0 && id[k] < A.vocab && (id[k] & mask) == slice;
-      const int32_t loc = own ? (int32_t)(id[k] >> A.slice_bits) : -1;
+      const bool own = id[k] >= 0 && (id[k] & mask) == slice;
+      const int32_t loc = own ? id[k] >> A.slice_bits : -1;
       uint64_t todo = __ballot(own);
       while (todo) {
         const int lead = __ffsll((unsigned long long)todo) - 1;
@@ -218,7 +225,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs A) {
         p0 = __builtin_amdgcn_readlane(p0, lead);
         if (loc == l) {
           const int32_t p = p0 + __popcll(same & (((uint64_t)1 << lane) - 1));
-          A.order[p] = Entry{(int32_t)(t0 + k * 64 + lane), (int32_t)id[k], p - first[l], tot[l]};
+          A.order[p] = Entry{(int32_t)(t0 + k * 64 + lane), id[k], p - first[l], tot[l]};
         }
         todo &= ~same;
       }
@@ -413,19 +420,31 @@ __global__ void __launch_bounds__(kThreads) table_kernel(const GradArgs A) {
 }
 
 // The rows of long ids from their pieces, in order; the grid's second side
-// covers the columns.
+// covers the columns.  Little data, so what counts is how many loads wait for
+// one another: the window's entries are read before the number of places is
+// known (behind it they hold nothing that is used), the accumulator before the
+// pieces.
 template <bool GAPS>
 __global__ void __launch_bounds__(kThreads) join_kernel(const GradArgs A) {
   const int32_t total = A.start[((int64_t)1 << A.slice_bits) * A.local];
   const int32_t c0 = (int32_t)(blockIdx.y * kThreads + threadIdx.x) * 4;
-  const int n = min(4, A.cols - c0);
-  for (int64_t w = blockIdx.x; w * kPiece < total; w += gridDim.x) {
-    const int32_t p = piece_in_window(A, total, (int32_t)w * kPiece, true);
-    if (p < 0 || n <= 0) continue;
-    const Entry e = A.order[p];
-    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  const int n = min(4, A.cols - c0), lane = threadIdx.x & 63;
+  for (int64_t w = blockIdx.x; w * kPiece < A.n; w += gridDim.x) {
+    const int32_t w0 = (int32_t)w * kPiece;
+    Entry e = {0, 0, 1, 0};
+    if (lane < kPiece && w0 + lane < A.n) e = A.order[w0 + lane];
+    const uint64_t found = __ballot(w0 + lane < total && e.rel == 0 && e.count > kPiece);
+    if (!found) continue;
+    const int at = __ffsll((unsigned long long)found) - 1;
+    const int32_t p = w0 + at, count = __builtin_amdgcn_readlane(e.count, at),
+                  row = __builtin_amdgcn_readlane(e.row, at);
+    if (n <= 0) continue;
+    const bool vec = !GAPS && n >= 4;
+    const int64_t to = vec ? place_at<false>(A.out.place, (int64_t)row * A.cols + c0) : 0;
+    f32x4 base = {0.f, 0.f, 0.f, 0.f}, s = base;
+    if (vec) base = grad_load4(A.out, to);
 #pragma unroll 8
-    for (int32_t j = 0; j < e.count; j += kPiece) {
+    for (int32_t j = 0; j < count; j += kPiece) {
       const float* q = A.partial + slot_of(p + j, j == 0) * A.cols + c0;
       if (n >= 4) {
         s += *(const f32x4_a4*)q;
@@ -435,7 +454,10 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const GradArgs A) {
           if (k < n) s[k] += q[k];
       }
     }
-    row_out<GAPS>(A, e.row, c0, n, s);
+    if (vec)
+      grad_store4(A.out, to, s, base);
+    else
+      row_out<GAPS>(A, row, c0, n, s);
   }
 }
 
@@ -611,7 +633,7 @@ int zero_embedding_grad(const zero_layout* L, int32_t tensor, int64_t cols, cons
 
   PlanArgs P;
   P.ids = ids;
-  P.vocab = numel / cols;
+  P.vocab = (int32_t)(numel / cols);
   P.n = (int32_t)n_ids;
   P.local = (int32_t)p.local;
   P.slice_bits = p.slice_bits;
