@@ -73,9 +73,10 @@ struct Args {
 // columns of dY or 16 of X (16 bytes each, at any alignment).  fast() takes
 // whole chunks of whole steps.  A chunk that begins past the last column is
 // read from the last chunk, and the last chunk of a row may run on into the
-// next row: what it finds there enters only sums that are not stored.  The
-// matrix's last tokens, from where it would run out of the matrix, are left to
-// fill(), which checks every element and goes to LDS at once.
+// next row: what it finds there enters only sums that are not stored.  part()
+// does the same for a step that is not whole, with zeros for the tokens from
+// `lim` on.  The matrix's last tokens, from where a chunk would run out of the
+// matrix (15 at most), are put into LDS by finish(), element by element.
 template <class S>
 struct DyTile {
   static constexpr int kPerRow = S::kSide / 8, kRows = S::kThreads / kPerRow, kN = S::kStep / kRows;
@@ -93,24 +94,26 @@ struct DyTile {
 #pragma unroll
     for (int k = 0; k < kN; ++k) fast1(A, t0, off, k);
   }
-  static __device__ __forceinline__ void fill(const Args& A, int64_t t0, int64_t tz, int32_t c0,
-                                              lds_char* lds) {
+  __device__ __forceinline__ void part(const Args& A, int64_t t0, int64_t lim, uint32_t off) {
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      v[k] = u32x4{0u, 0u, 0u, 0u};
+      if (t0 + k * kRows + row() < lim) fast1(A, t0, off, k);
+    }
+  }
+  static __device__ __forceinline__ void finish(const Args& A, int64_t t0, int64_t from, int64_t tz,
+                                                int32_t c0, lds_char* lds) {
     const int c = c0 + col();
-    lds_char* to = lds + (col() >> 5) * S::kPanelBytes + row() * 64 + (col() & 31) * 2;
 #pragma unroll 1
     for (int k = 0; k < kN; ++k) {
       const int64_t t = t0 + k * kRows + row();
+      if (t < from || t >= tz) continue;
       const uint16_t* p = A.dy + t * A.dy_stride + c;
-      const int n = t < tz ? A.O - c : 0;
       u32x4 w = {0u, 0u, 0u, 0u};
-      if (n >= 8) {
-        w = *(const u32x4_a2*)p;
-      } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < n) w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
-      }
-      *(lds_u32x4*)(to + k * kRows * 64) = w;
+      for (int j = 0; j < 8; ++j)
+        if (j < A.O - c) w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+      *(lds_u32x4*)(lds + (col() >> 5) * S::kPanelBytes + (k * kRows + row()) * 64 + (col() & 31) * 2) = w;
     }
   }
   __device__ __forceinline__ void store1(lds_char* lds, int k) const {
@@ -159,26 +162,30 @@ struct XTile {
     *(lds_u32x4*)(to + (swap ? 16 : 0)) = u32x4{a.x, a.y, b.x, b.y};
     *(lds_u32x4*)(to + (swap ? 0 : 16)) = u32x4{d.x, d.y, f.x, f.y};
   }
-  static __device__ __forceinline__ void fill(const Args& A, int64_t t0, int64_t tz, int32_t c0,
-                                              lds_char* lds) {
+  __device__ __forceinline__ void part(const Args& A, int64_t t0, int64_t lim, uint32_t off,
+                                       uint32_t soff) {
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      v[k] = u32x4{0u, 0u, 0u, 0u};
+      e[k] = 127u;
+      if (t0 + k * kRows + row() < lim) fast1(A, t0, off, soff, k);
+    }
+  }
+  static __device__ __forceinline__ void finish(const Args& A, int64_t t0, int64_t from, int64_t tz,
+                                                int32_t c0, lds_char* lds) {
     const int c = c0 + col();
-    lds_char* to = lds + (col() >> 5) * S::kPanelBytes + row() * 64 + (col() & 31) * 2;
 #pragma unroll 1
     for (int k = 0; k < kN; ++k) {
       const int64_t t = t0 + k * kRows + row();
+      if (t < from || t >= tz) continue;
       const uint8_t* p = A.codes + t * A.I + c;
-      const int n = t < tz ? A.I - c : 0;
       u32x4 w = {0u, 0u, 0u, 0u};
       uint32_t b = 127u;
-      if (n > 0) b = A.scales[t * A.nb + (c >> 7)];
-      if (n >= 16) {
-        w = *(const u32x4_a1*)p;
-      } else {
+      if (c < A.I) b = A.scales[t * A.nb + (c >> 7)];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (j < n) w[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
-      }
-      put(to + k * kRows * 64, w, b);
+      for (int j = 0; j < 16; ++j)
+        if (j < A.I - c) w[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
+      put(lds + (col() >> 5) * S::kPanelBytes + (k * kRows + row()) * 64 + (col() & 31) * 2, w, b);
     }
   }
   __device__ __forceinline__ void store1(lds_char* lds, int k) const {
@@ -292,16 +299,19 @@ __global__ void __launch_bounds__(S::kThreads, 1) grad_kernel(const Args A) {
   const lds_char* const fb = lds + kOperand + wn * W * kPanelBytes + group * 4096 + frag_offset();
 
   const int64_t steps = (tz - ta + kStep - 1) / kStep;
-  // steps that fast loads can take
-  const int64_t full = max((int64_t)0, min(tz, A.fast_tokens) - ta) / kStep;
-  // full step k waits in set k % 2 of the registers
+  // tokens and whole steps that chunk loads can take
+  const int64_t lim = min(tz, A.fast_tokens);
+  const int64_t full = max((int64_t)0, lim - ta) / kStep;
+  // step k waits in set k % 2 of the registers
   auto load = [&](int64_t k, int set) {
-    dy[set].fast(A, ta + k * kStep, dy_off);
-    x[set].fast(A, ta + k * kStep, x_off, s_off);
-  };
-  auto fill = [&](int64_t k, int buf) {
-    DyTile<S>::fill(A, ta + k * kStep, tz, dy_c, dy_lds + buf * kBuffer);
-    XTile<S>::fill(A, ta + k * kStep, tz, x_c, x_lds + buf * kBuffer);
+    const int64_t t0 = ta + k * kStep;
+    if (k < full) {
+      dy[set].fast(A, t0, dy_off);
+      x[set].fast(A, t0, x_off, s_off);
+    } else {
+      dy[set].part(A, t0, lim, dy_off);
+      x[set].part(A, t0, lim, x_off, s_off);
+    }
   };
   bf16x8 a[2][W], b[2][W];
   auto read1 = [&](int to, int buf, int s, int q) {
@@ -321,9 +331,15 @@ __global__ void __launch_bounds__(S::kThreads, 1) grad_kernel(const Args A) {
       for (int n = 0; n < W; ++n)
         acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[from][m], b[from][n], acc[m][n], 0, 0, 0);
   };
-  auto store = [&](int set, int buf) {
-    dy[set].store(dy_lds + buf * kBuffer);
-    x[set].store(x_lds + buf * kBuffer);
+  // step k from set k % 2 to buffer k % 2 (so both are `set`)
+  auto store = [&](int64_t k, int set) {
+    dy[set].store(dy_lds + set * kBuffer);
+    x[set].store(x_lds + set * kBuffer);
+    if (ta + (k + 1) * kStep > lim && lim < tz) {
+      // the same thread writes the same places: in order
+      DyTile<S>::finish(A, ta + k * kStep, lim, tz, dy_c, dy_lds + set * kBuffer);
+      XTile<S>::finish(A, ta + k * kStep, lim, tz, x_c, x_lds + set * kBuffer);
+    }
   };
   // Step k, in buffer `buf`: its products; step k + 1 goes from the registers
   // to the other buffer, step k + 3 is requested into the same registers.
@@ -350,14 +366,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) grad_kernel(const Args A) {
   };
 
   if (steps > 0) {
-    if (full > 0) {
-      load(0, 0);
-      store(0, 0);
-    } else {
-      fill(0, 0);
-    }
-    if (full > 1) load(1, 1);
-    if (full > 2) load(2, 0);
+    load(0, 0);
+    if (steps > 1) load(1, 1);
+    store(0, 0);
+    if (steps > 2) load(2, 0);
     __syncthreads();
     read(0, 0, 0);
     int64_t k = 0;
@@ -365,7 +377,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) grad_kernel(const Args A) {
       step(k, 0);
       step(k + 1, 1);
     }
-    // the last full steps, and those that need checks
+    // the last steps
     for (; k < steps; ++k) {
       const int buf = (int)(k & 1);
       read(1, buf, 1);
@@ -374,19 +386,17 @@ __global__ void __launch_bounds__(S::kThreads, 1) grad_kernel(const Args A) {
       multiply(1);
       read(1, buf, 3);
       multiply(0);
-      if (k + 1 < full) {
+      if (k + 1 < steps) {
         if (buf)
-          store(0, 0);
+          store(k + 1, 0);
         else
-          store(1, 1);
-        if (k + 3 < full) {
-          if (buf)
-            load(k + 3, 0);
-          else
-            load(k + 3, 1);
-        }
-      } else if (k + 1 < steps) {
-        fill(k + 1, buf ^ 1);
+          store(k + 1, 1);
+      }
+      if (k + 3 < steps) {
+        if (buf)
+          load(k + 3, 0);
+        else
+          load(k + 3, 1);
       }
       __syncthreads();
       if (k + 1 < steps) read(0, buf ^ 1, 0);
