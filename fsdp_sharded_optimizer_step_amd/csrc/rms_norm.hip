@@ -6,8 +6,8 @@
 // added to the rank's sum over micro-batches.
 //
 //   forward   h = bf16(x + r);  R = 1 / sqrt(mean(h^2) + eps);  y = act8(h*R*w)
-//   backward  g = dy*w;  c = mean(g*h) * R^2;  dx = bf16(dh + R*(g - c*h))
-//             dw = sum over rows of dy*h*R
+//   backward  g = dy*w;  n = h*R;  dx = bf16(dh + R*(g - n*mean(g*n)))
+//             dw = sum over rows of dy*n
 // (the rounding of y to 8 bits is passed straight through).  Between the
 // loads and the stores the forward pass is binary64, the backward binary32.
 //
@@ -153,6 +153,11 @@ __global__ void __launch_bounds__(kBlock<NT>) norm_kernel(const NormArgs A) {
     turn ^= 1;
     const double rstd = 1.0 / __builtin_sqrt(ss / A.cols + A.eps);
     if (live && tid == 0) A.rstd[r] = (float)rstd;
+    // rstd = rf * r2, r2 a power of two: h*r2 is a normed value's size, so
+    // that its product with w is exact in binary32 (16 bits) for any row size
+    const int rexp = min(max((int)((__double2hiint(rstd) >> 20) & 0x7ff) - 1022, -126), 127);
+    const float r2 = __uint_as_float((uint32_t)(rexp + 127) << 23);
+    const double rf = rstd * __builtin_bit_cast(double, (uint64_t)(1023 - rexp) << 52);
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
       const int c0 = (k * NT + tid) * 8, n = live ? A.cols - c0 : 0;
@@ -160,7 +165,7 @@ __global__ void __launch_bounds__(kBlock<NT>) norm_kernel(const NormArgs A) {
       uint32_t m = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v[j] = round_to_odd((double)(at8(h[k], j) * at8(w[k], j)) * rstd);
+        v[j] = round_to_odd((double)(at8(h[k], j) * r2 * at8(w[k], j)) * rf);
         m = max(m, j < n ? finite_mag(v[j]) : 0u);
       }
       const uint32_t e = act8_byte(max16(m));
@@ -228,14 +233,14 @@ __global__ void __launch_bounds__(NT) norm_grad_kernel(const NormGradArgs A) {
     for (int k = 0; k < NP; ++k) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float d = at8(dy[k], j), x = at8(h[k], j);
-        s += d * at8(w[k], j) * x;
-        dw[k][j] += d * x * R;
+        const float d = at8(dy[k], j), n = at8(h[k], j) * R;
+        s += d * at8(w[k], j) * n;
+        dw[k][j] += d * n;
       }
     }
     s = row_sum<NT>(s, &red[turn][0]);
     turn ^= 1;
-    const float c = s / (float)A.cols * R * R;
+    const float c = s / (float)A.cols;
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
       const int c0 = (k * NT + tid) * 8, n = A.cols - c0;
@@ -243,7 +248,7 @@ __global__ void __launch_bounds__(NT) norm_grad_kernel(const NormGradArgs A) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float g = at8(dy[k], j) * at8(w[k], j);
-        const float d = R * (g - c * at8(h[k], j));
+        const float d = R * (g - c * (at8(h[k], j) * R));
         v[j] = A.dh ? at8(dh[k], j) + d : d;
       }
       store8(A.dx + r * A.cols + c0, round8(v), n);

@@ -526,10 +526,10 @@ int zero_embedding_grad(const zero_layout* layout, int32_t tensor, int64_t cols,
  *   h * w * rstd, in binary64 too, in the 8-bit format of zero_act8_pack.  h_dev: the new residual (may be NULL if res is);
  *   y_dev: NULL, or the bf16 values that the codes stand for, so that the
  *   forward product reads exactly what the backward product will.
- * grad, for every row, with g = dy * w:
- *   dx = bf16(dh + rstd * (g - h * rstd^2 * mean(g * h)))   (dh NULL: 0)
+ * grad, for every row, with g = dy * w and n = h * rstd:
+ *   dx = bf16(dh + rstd * (g - n * mean(g * n)))   (dh NULL: 0)
  *   which is the gradient of both x and res; the weight's gradient is the sum
- *   over the rows of dy * h * rstd.  The rounding to 8 bits counts as the
+ *   over the rows of dy * n.  The rounding to 8 bits counts as the
  *   identity.  h_dev is the forward pass's h (x where there was none). */
 #define ZERO_MAX_NORM_COLS 32768
 int zero_rms_norm(const zero_layout* layout, int32_t tensor, const uint16_t* params_flat_dev,

@@ -335,6 +335,30 @@ def test_norm_codes_are_the_rounded_exact_values(rows, cols):
     assert np.array_equal(rstd.cpu().numpy(), r.astype(np.float32))
 
 
+@pytest.mark.parametrize("size", [2.0 ** 100, 2.0 ** -60])
+def test_norm_of_very_large_and_small_rows(size):
+    """Squares and products with the weight that binary32 cannot hold."""
+    rows, cols = 5, 400
+    L, pl = layout(cols, False)
+    pos = torch.from_numpy(positions(pl, cols)).to(DEV)
+    params = (1 + randn(cols, L.padded, scale=0.2)) * size
+    x = randn(rows, rows, cols) * size
+    rstd = torch.empty(rows, device=DEV)
+    q, e = codes_like(rows, cols)
+    z.zero_rms_norm(L, 1, params, x, None, 0.0, None, rstd, q, e)
+    _, hd, r = norm_exact(x, None, params, 0.0)
+    eq, ee = act8(hd * r[:, None] * f64(params[pos]))
+    assert np.array_equal(e.cpu().numpy(), ee) and np.array_equal(q.cpu().numpy(), eq)
+    assert (np.abs(f64(rstd) - r) <= U * r).all()
+    dy = randn(7, rows, cols)
+    dx = torch.empty(rows, cols, dtype=BF16, device=DEV)
+    f = Flat(L, pl, cols, DEV)
+    z.zero_rms_norm_grad(L, 1, params, dy, None, x, rstd, dx, f.acc, 1.0)
+    ex, lim, terms = norm_grad_exact(f64(dy), None, f64(x), f64(rstd)[:, None], f64(params[pos]))
+    assert (np.abs(f64(dx) - ex) <= lim).all()
+    f.check(terms.sum(0), (rows + 2) * U * np.abs(terms).sum(0), 1.0, 0, "weight")
+
+
 def test_norm_zero_row_and_non_finite_row_stay_apart():
     rows, cols = 4, 300
     L, pl = layout(cols, False)
