@@ -9,10 +9,12 @@
 // per element, unpack the reverse).  A lane takes 8 consecutive columns, the
 // 16 lanes of a DPP row take a block of 128, so the block's maximum needs
 // four lane rotations and no LDS.  Codes and scales of a block belong to one
-// lane group: the result does not depend on the launch shape.  Loads are
-// non-temporal: pack and unpack of 8192 x 14336 bf16 values take 115 us
-// together (705 MB, 6.1 TB/s, the codes partly still cached in between); with
-// temporal loads 130, with non-temporal stores as well 115.
+// lane group: the result does not depend on the launch shape.
+//
+// Cache hints as measured for 8192 x 14336 values: 16-bit and 8-bit loads are
+// non-temporal (bf16: pack and unpack together 115 us, 706 MB; temporal 130),
+// binary32 loads are not, since two of a lane's instructions share a line
+// (pack 107 us against 110), binary32 stores are (unpack 132 against 145).
 #include <algorithm>
 
 #include "act8.hpp"
@@ -36,7 +38,7 @@ __device__ __forceinline__ void load_row8(float (&x)[8], const uint16_t* p, int 
 }
 __device__ __forceinline__ void load_row8(float (&x)[8], const float* p, int n) {
   if (n >= 8) {
-    const f32x4 a = ld4_stream(p), b = ld4_stream(p + 4);
+    const f32x4 a = *(const f32x4_a4*)p, b = *(const f32x4_a4*)(p + 4);
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
   } else {
@@ -93,8 +95,8 @@ __device__ __forceinline__ void store_row8(float* p, u32x2 w, float s, int n) {
   const f32x2 c = act8_f32<false>(w.y, s), d = act8_f32<true>(w.y, s);
   const float o[8] = {a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
   if (n >= 8) {
-    *(f32x4_a4*)p = f32x4{o[0], o[1], o[2], o[3]};
-    *(f32x4_a4*)(p + 4) = f32x4{o[4], o[5], o[6], o[7]};
+    st4_stream(p, f32x4{o[0], o[1], o[2], o[3]});
+    st4_stream(p + 4, f32x4{o[4], o[5], o[6], o[7]});
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
