@@ -96,8 +96,9 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const LookupArgs A) {
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (id >= 0 && id < A.vocab) {
       const int64_t i = id * A.cols + c0;
-      if (!GAPS && n >= 8) {
-        const u32x4 w = *(const u32x4_a2*)(A.params + place_at<GAPS>(A.place, i));
+      int64_t at;
+      if (n >= 8 && place_run<GAPS>(A.place, i, 8, at)) {
+        const u32x4 w = *(const u32x4_a2*)(A.params + at);
         x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
         x[4] = bf16_lo(w.z); x[5] = bf16_hi(w.z); x[6] = bf16_lo(w.w); x[7] = bf16_hi(w.w);
       } else {
@@ -311,8 +312,9 @@ __device__ __forceinline__ f32x4 sum_places(const GradArgs& A, f32x4 s, int32_t 
 template <bool GAPS>
 __device__ __forceinline__ void row_out(const GradArgs& A, int64_t v, int32_t c0, int n, f32x4 s) {
   const int64_t i = v * A.cols + c0;
-  if (!GAPS && n >= 4) {
-    grad_store4(A.out, place_at<GAPS>(A.out.place, i), s);
+  int64_t at;
+  if (n >= 4 && place_run<GAPS>(A.out.place, i, 4, at)) {
+    grad_store4(A.out, at, s);
   } else {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -367,8 +369,9 @@ __global__ void __launch_bounds__(kThreads) places_kernel(const GradArgs A) {
        x += (int64_t)A.row_blocks * A.rows_per_block) {
     const Entry e = A.order[x];
     if (e.rel % kPiece != 0) continue;
-    const bool vec = !GAPS && n >= 4, whole = e.count <= kPiece;
-    const int64_t at = vec ? place_at<false>(A.out.place, (int64_t)e.row * A.cols + c0) : 0;
+    int64_t at;
+    const bool vec = place_run<GAPS>(A.out.place, (int64_t)e.row * A.cols + c0, 4, at) && n >= 4;
+    const bool whole = e.count <= kPiece;
     f32x4 base = {0.f, 0.f, 0.f, 0.f};
     if (vec && whole) base = grad_load4(A.out, at);
     f32x4 s = dy4<DY>(A, e.token, c0, n);
@@ -442,8 +445,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const GradArgs A) {
     const int32_t p = w0 + at, count = __builtin_amdgcn_readlane(e.count, at),
                   row = __builtin_amdgcn_readlane(e.row, at);
     if (n <= 0) continue;
-    const bool vec = !GAPS && n >= 4;
-    const int64_t to = vec ? place_at<false>(A.out.place, (int64_t)row * A.cols + c0) : 0;
+    int64_t to;
+    const bool vec = place_run<GAPS>(A.out.place, (int64_t)row * A.cols + c0, 4, to) && n >= 4;
     f32x4 base = {0.f, 0.f, 0.f, 0.f}, s = base;
     if (vec) base = grad_load4(A.out, to);
 #pragma unroll 8

@@ -530,8 +530,9 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const Args A, int32_t 
 #pragma unroll 8
     for (int k = 0; k < n_splits; ++k) s += *(const f32x4*)(from + (int64_t)k * SIDE * SIDE + g * 4);
     const int64_t e = (int64_t)r * A.cols + c;
-    if (!GAPS && n >= 4) {
-      grad_store4(A.out, place_at<GAPS>(A.out.place, e), s);
+    int64_t at;
+    if (n >= 4 && place_run<GAPS>(A.out.place, e, 4, at)) {
+      grad_store4(A.out, at, s);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)

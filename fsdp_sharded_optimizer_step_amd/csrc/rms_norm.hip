@@ -73,7 +73,8 @@ __device__ __forceinline__ u32x4 round8(const float (&x)[8]) {
 }
 template <bool GAPS>
 __device__ __forceinline__ Piece8 weight8(const uint16_t* params, const Place& pl, int c0, int n) {
-  if (!GAPS) return load8<false>(params + pl.x0 + c0, n);
+  int64_t at;
+  if (place_run<GAPS>(pl, c0, 8, at) || !GAPS) return load8<false>(params + at, n);
   u32x4 w = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int k = 0; k < 8; ++k)

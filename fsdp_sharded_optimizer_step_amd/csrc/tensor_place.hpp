@@ -37,15 +37,35 @@ __device__ __forceinline__ void st4_stream(float* p, f32x4 v) {
 // x + (x / cap) * gap with x = x0 + i its stream position.
 struct Place {
   int64_t x0, cap, gap;
+  double inv_cap;
 };
 
+// x / cap: the product is off by less than one for any x that memory holds
+// (x < 2^50), so the quotient is right or one off.
+__device__ __forceinline__ int64_t bucket_of(const Place& p, int64_t x) {
+  const int64_t b = (int64_t)((double)x * p.inv_cap), r = x - b * p.cap;
+  return b + (r >= p.cap ? 1 : 0) - (r < 0 ? 1 : 0);
+}
 template <bool GAPS>
 __device__ __forceinline__ int64_t place_at(const Place& p, int64_t i) {
   const int64_t x = p.x0 + i;
   if constexpr (!GAPS)
     return x;
   else
-    return x + (int64_t)((uint64_t)x / (uint64_t)p.cap) * p.gap;
+    return x + bucket_of(p, x) * p.gap;
+}
+// The flat position of element i, and whether elements i to i + n - 1 follow
+// each other there.
+template <bool GAPS>
+__device__ __forceinline__ bool place_run(const Place& p, int64_t i, int n, int64_t& at) {
+  const int64_t x = p.x0 + i;
+  at = x;
+  if constexpr (GAPS) {
+    const int64_t b = bucket_of(p, x);
+    at += b * p.gap;
+    return x - b * p.cap + n <= p.cap;
+  }
+  return true;
 }
 
 // What becomes of a gradient element g (the arithmetic and the flags of
@@ -102,8 +122,8 @@ inline FastDiv make_fast_div(uint32_t d) {
 // checked the tensor index.
 inline Place make_place(const zero_layout* L, int32_t t, int64_t* lo, int64_t* hi) {
   zero_layout_tensor_flat(L, t, lo, hi);
-  if (*hi - *lo == L->numel[(size_t)t]) return Place{*lo, 1, 0};
-  return Place{L->tensor_off[(size_t)t], L->cap, L->p_full - L->cap};
+  if (*hi - *lo == L->numel[(size_t)t]) return Place{*lo, 1, 0, 1.0};
+  return Place{L->tensor_off[(size_t)t], L->cap, L->p_full - L->cap, 1.0 / (double)L->cap};
 }
 
 inline bool tensor_ok(const zero_layout* L, int32_t t) {

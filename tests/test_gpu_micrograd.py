@@ -265,6 +265,32 @@ def test_emb_grad_rows_beyond_32_bits_and_no_tokens():
     assert not acc.any()
 
 
+def test_large_table_with_padding_inside_it():
+    """4.9e9 elements in buckets of 12,500,003 (5 elements of padding each):
+    rows on both sides of bucket borders and at the end of the table."""
+    vocab, cols, cap, n_d = 300_001, 16_384, 12_500_003, 8
+    L = z.Layout([vocab * cols], cap, n_d, 0)
+    gap = -cap % n_d
+    rows = sorted({0, 1, vocab - 1, vocab - 2} | {k * cap // cols + j for k in (1, 2, 77, 390)
+                                                  for j in (-1, 0, 1)})
+    x = torch.tensor(rows, device=DEV)[:, None] * cols + torch.arange(cols, device=DEV)
+    at = x + x // cap * gap
+    assert any(int(r[-1] - r[0]) != cols - 1 for r in at)      # a row that padding cuts
+    params = torch.zeros(L.padded, dtype=BF16, device=DEV)
+    vals = randn(5, len(rows), cols)
+    params[at.reshape(-1)] = vals.reshape(-1)
+    ids = torch.tensor(rows, device=DEV)
+    out = torch.empty(len(rows), cols, dtype=BF16, device=DEV)
+    z.zero_embedding_lookup(L, 0, params, ids, out)
+    assert torch.equal(out, vals)
+    del params
+    acc = torch.zeros(L.padded, device=DEV)
+    z.zero_embedding_grad(L, 0, ids, vals, acc)
+    assert torch.equal(acc[at.reshape(-1)].view(-1, cols), vals.float())
+    acc[at.reshape(-1)] = 0
+    assert not acc.any()
+
+
 # ------------------------------------------------------------------ norm
 def norm_exact(x, res, w, eps):
     h = x if res is None else (x.float() + res.float()).to(BF16)
