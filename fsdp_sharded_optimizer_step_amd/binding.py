@@ -109,7 +109,7 @@ def load():
     lib.zero_act8_pack.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
     lib.zero_act8_unpack.argtypes = [vp, vp, i64, i64, vp, i32, i64, vp]
     lib.zero_embedding_lookup.argtypes = [vp, i32, i64, vp, vp, i32, i64, f32, vp, i64, i32, vp]
-    lib.zero_embedding_grad_workspace.argtypes = [vp, i32, i64, i64]
+    lib.zero_embedding_grad_workspace.argtypes = [vp, i32, i64, i64, u32]
     lib.zero_embedding_grad.argtypes = [vp, i32, i64, vp, i32, i64, vp, i64, i32, f32, u32, vp, vp,
                                         vp, i64, vp]
     lib.zero_rms_norm.argtypes = [vp, i32, vp, vp, i64, vp, i64, i64, C.c_double, vp, vp, vp, vp, vp, vp]
@@ -610,7 +610,7 @@ def zero_embedding_grad(layout: Layout, tensor: int, ids, dy, acc, scale: float 
 
     def call(s, device):
         ws = _workspace(me, workspace, lib.zero_embedding_grad_workspace(
-            layout.handle, tensor, cols, n), device)
+            layout.handle, tensor, cols, n, flags), device)
         return lib.zero_embedding_grad(
             layout.handle, tensor, cols, ids.data_ptr(), ids.element_size(), n, dy.data_ptr(),
             stride, int(dy.dtype == torch.float32), scale, flags, _ptr(acc), _ptr(bf16_out),

@@ -454,7 +454,7 @@ int zero_step_scalars(const zero_adamw* hp, int64_t t, float out[8]);
  * stride argument are dense.  Any alignment is accepted.  No outputs may
  * overlap each other or an input; in particular nothing works in place.
  * A workspace (16-byte aligned, of the bytes that the call's _workspace
- * function gives for the same sizes) holds intermediate sums: its contents
+ * function gives for the same sizes; none where it gives 0) holds intermediate sums: its contents
  * before and after a call mean nothing, and two calls that may run at the
  * same time (or two captured graphs that may be replayed at the same time)
  * need a workspace each.  The _workspace functions run on the host only and
@@ -511,7 +511,7 @@ int zero_embedding_lookup(const zero_layout* layout, int32_t tensor, int64_t col
                           int64_t n_ids, float scale, void* out_dev, int64_t out_stride,
                           int32_t out_dtype, hipStream_t stream);
 int64_t zero_embedding_grad_workspace(const zero_layout* layout, int32_t tensor, int64_t cols,
-                                      int64_t n_ids);
+                                      int64_t n_ids, uint32_t flags);
 int zero_embedding_grad(const zero_layout* layout, int32_t tensor, int64_t cols,
                         const void* ids_dev, int32_t id_bytes, int64_t n_ids, const void* dy_dev,
                         int64_t dy_stride, int32_t dy_dtype, float scale, uint32_t flags,

@@ -42,7 +42,7 @@ def good_calls(L):
                                  stride=200, stream=None),
         "zero_embedding_lookup": dict(L=h, tensor=1, cols=30, params=at(1), ids=at(2), id_bytes=8,
                                       n=9, scale=1.0, out=at(3), stride=30, dtype=0, stream=None),
-        "zero_embedding_grad": dict(L=h, tensor=1, cols=30, ids=at(2), id_bytes=8, n=9, dy=at(3),
+        "zero_embedding_grad": dict(L=h, tensor=1, cols=30, ids=at(2), id_bytes=8, n=900, dy=at(3),
                                     stride=30, dtype=0, scale=1.0, flags=0, acc=at(4), out=at(5),
                                     ws=at(6), ws_bytes=1 << 20, stream=None),
         "zero_rms_norm": dict(L=h, tensor=2, params=at(1), x=at(2), stride=24, res=at(3),
@@ -132,9 +132,11 @@ def test_nothing_to_do_needs_no_buffers(L, name):
 
 def test_workspace_queries(L):
     lib, h = z.load(), L.handle
-    assert lib.zero_embedding_grad_workspace(h, 1, 30, 9) >= 9 * 16
-    assert lib.zero_embedding_grad_workspace(h, 1, 31, 9) == EINVAL
-    assert lib.zero_embedding_grad_workspace(h, 9, 30, 9) == ERANGE
+    assert lib.zero_embedding_grad_workspace(h, 1, 30, 512, 0) == 0     # few tokens, added
+    assert lib.zero_embedding_grad_workspace(h, 1, 30, 512, 2) >= 512 * 16
+    assert lib.zero_embedding_grad_workspace(h, 1, 30, 513, 0) >= 513 * 16
+    assert lib.zero_embedding_grad_workspace(h, 1, 31, 9, 0) == EINVAL
+    assert lib.zero_embedding_grad_workspace(h, 9, 30, 9, 0) == ERANGE
     assert lib.zero_rms_norm_grad_workspace(h, 2, 5) >= 24 * 4
     assert lib.zero_rms_norm_grad_workspace(None, 2, 5) == EINVAL
     assert lib.zero_linear_grad_workspace(h, 1, 0, 20, 30, 4000) >= 600 * 4
