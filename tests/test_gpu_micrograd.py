@@ -557,6 +557,35 @@ def test_linear_grad_large_tiles_and_dim0_layout(tr):
     assert np.array_equal(f64(f.acc)[f.pos], f.acc0[f.pos] + (g.T if tr else g).reshape(-1))
 
 
+@pytest.mark.parametrize("tr", [False, True])
+@pytest.mark.parametrize("gaps", [False, True])
+@pytest.mark.parametrize("tokens,o,i", [(1300, 4200, 4090), (1000, 4096, 4096), (700, 4100, 4090),
+                                        (20_000, 520, 1030), (513, 5000, 3100)])
+def test_linear_grad_sizes_of_both_tiles_exact_in_integers(tr, gaps, tokens, o, i):
+    """Sizes that take the 256-column tile, the 128-column tile, whole tiles
+    only, and whole and split ones, with every edge ragged or none."""
+    g = torch.Generator(device=DEV).manual_seed(tokens)
+    dy = torch.randint(-3, 4, (tokens, o), generator=g, device=DEV).to(BF16)
+    x = torch.randint(-8, 9, (tokens, i), generator=g, device=DEV).float()
+    q, e = codes_like(tokens, i)
+    z.zero_act8_pack(x, q, e)
+    L, pl = layout(o * i, gaps)
+    pos = torch.from_numpy(positions(pl, o * i)).to(DEV)
+    exact = dy.double().t().contiguous() @ x.double()          # below 2^53: exact
+    assert float(exact.abs().max()) < 2 ** 24 and 24 * tokens < 2 ** 24
+    exact = (exact.t() if tr else exact).reshape(-1)
+    acc = torch.randint(-9, 10, (L.padded,), generator=g, device=DEV).float()
+    out = torch.full((L.padded,), 3.0, dtype=BF16, device=DEV)
+    start = acc.clone()
+    z.zero_linear_grad(L, 1, dy, q, e, acc, 1.0, z.ACC_EMIT_BF16, out, transposed=tr)
+    exp = start.double()
+    exp[pos] += exact
+    assert torch.equal(acc.double(), exp)
+    rest = torch.ones(L.padded, dtype=torch.bool, device=DEV)
+    rest[pos] = False
+    assert torch.equal(out[pos], exp[pos].float().to(BF16)) and (out[rest] == 3.0).all()
+
+
 def test_linear_grad_non_finite_inputs_reach_only_their_row_and_column():
     tokens, o, i = 200, 150, 170
     L, pl = layout(o * i, False)
