@@ -18,6 +18,7 @@
 // and every value is a normal bf16 number), with one conversion per two
 // codes; products of bf16 are exact in binary32, sums are binary32.
 #include <algorithm>
+#include <utility>
 
 #include "act8.hpp"
 
@@ -238,6 +239,17 @@ __device__ __forceinline__ void tile_at(const Args& A, int32_t tile, int32_t& r,
   r = g * 8 + in - c * h;
 }
 
+// f(0), f(1) to f(N - 1) with constant arguments: a loop that indexes registers
+// and has to be unrolled whatever its size.
+template <class F, int... I>
+__device__ __forceinline__ void unrolled_of(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void unrolled(F f) {
+  unrolled_of(f, std::make_integer_sequence<int, N>{});
+}
+
 // The workspace's tiles: those that do not go out directly.
 __device__ __forceinline__ int64_t slot_of(const Args& A, int32_t tile, int32_t split) {
   const int64_t kept = A.direct ? 0 : A.whole;
@@ -450,51 +462,56 @@ __global__ void __launch_bounds__(S::kThreads, 1) grad_kernel(const Args A) {
 
   // lane l, register k: row 8*(k/4) + 4*(l/32) + k%4, column l%32
   if (A.direct && tile < A.whole) {
-    // Two 32 x 32 blocks at a time, every load before the first store: one
-    // wait for memory per 32 values (with a wait for each value this part
-    // took a quarter of the kernel's time).
+    // Two 32 x 32 blocks at a time; the accumulator's values of the next two
+    // are requested before these are stored (with a wait for each value this
+    // part took a quarter of the kernel's time).
     const uint32_t lane_off = (uint32_t)(4 * (lane >> 5)) * (uint32_t)A.cols + (lane & 31);
     const bool add = !(A.out.flags & ZERO_ACC_OVERWRITE);
     const bool keep = !(A.out.flags & ZERO_ACC_NO_STORE), emit = A.out.flags & ZERO_ACC_EMIT_BF16;
-#pragma unroll
-    for (int m = 0; m < kMine; ++m)
-#pragma unroll
-      for (int n0 = 0; n0 < W; n0 += 2) {
-        const int32_t rb = r0 + (wm * W + m0 + m) * 32, cb = c0 + (wn * W + n0) * 32;
+    constexpr int kPairs = kMine * W / 2;
+    float v[2][2][16];
+    // CHECKED: the tile goes past the matrix's last row or column
+    auto out = [&](auto checked) {
+      constexpr bool kChecked = decltype(checked)::value;
+      // pair p: row of blocks p / (W / 2), columns of blocks 2 * (p % (W / 2)) and the next
+      auto each = [&](int p, auto f) {
+        const int32_t rb = r0 + (wm * W + m0 + p / (W / 2)) * 32, cb = c0 + (wn * W + p % (W / 2) * 2) * 32;
         const int64_t at = A.out.place.x0 + (int64_t)rb * A.cols + cb;
-        float* const p = A.out.acc + at;
-        uint16_t* const q = A.out.out + at;
         const int32_t row_left = A.rows - rb - 4 * (lane >> 5), col_left = A.cols - cb - (lane & 31);
-        float v[2][16];
-        if (add) {
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const int32_t r = 8 * (k >> 2) + (k & 3);
-              if (r < row_left && n * 32 < col_left)
-                v[n][k] = __builtin_nontemporal_load(p + (int64_t)r * A.cols + n * 32 + lane_off);
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float g = A.out.scale * acc[m][n0 + n][k];
-            v[n][k] = add ? v[n][k] + g : g;
-          }
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const int32_t r = 8 * (k >> 2) + (k & 3);
-            if (r < row_left && n * 32 < col_left) {
-              const int64_t o = (int64_t)r * A.cols + n * 32;
-              if (keep) __builtin_nontemporal_store(v[n][k], p + o + lane_off);
-              if (emit) q[o + lane_off] = (uint16_t)bf16_round(v[n][k]);
-            }
+            if (!kChecked || (r < row_left && n * 32 < col_left)) f(n, k, at + (int64_t)r * A.cols + n * 32);
           }
-      }
+      };
+      auto fetch = [&](int p) {
+        each(p, [&](int n, int k, int64_t at) {
+          v[p & 1][n][k] = __builtin_nontemporal_load(A.out.acc + at + lane_off);
+        });
+      };
+      if (add) fetch(0);
+      unrolled<kPairs>([&](auto index) {
+        constexpr int p = decltype(index)::value;
+        if (add && p + 1 < kPairs) fetch(p + 1);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float g = A.out.scale * acc[p / (W / 2)][p % (W / 2) * 2 + n][k];
+            v[p & 1][n][k] = add ? v[p & 1][n][k] + g : g;
+          }
+        each(p, [&](int n, int k, int64_t at) {
+          if (keep) __builtin_nontemporal_store(v[p & 1][n][k], A.out.acc + at + lane_off);
+          if (emit) A.out.out[at + lane_off] = (uint16_t)bf16_round(v[p & 1][n][k]);
+        });
+      });
+    };
+    if (r0 + kSide <= A.rows && c0 + kSide <= A.cols)
+      out(std::false_type{});
+    else
+      out(std::true_type{});
     return;
   }
   // a tile of the workspace, rows of kSide columns
