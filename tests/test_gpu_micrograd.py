@@ -738,8 +738,10 @@ def test_two_micro_batches_then_the_step():
         assert np.array_equal(p.cpu().numpy().view(np.uint16)[fp], op)
 
 
-def test_captured_and_replayed_with_eager_work_between():
+@pytest.mark.parametrize("tokens", [50, 700])
+def test_captured_and_replayed_with_eager_work_between(tokens):
     net = Net(3)
+    net.T = tokens
     P = net.L[0].padded
     batches = [net.batch(s) for s in (1, 2, 3, 4)]
     ids, res, dout = (t.clone() for t in batches[0])
@@ -782,10 +784,12 @@ def test_captured_and_replayed_with_eager_work_between():
         torch.randn(1000, device=DEV).sum().item()     # the program's own work between
 
 
-def test_other_streams():
+@pytest.mark.parametrize("tokens", [50, 700])
+def test_other_streams(tokens):
     """A call on a stream that is not the current one, with its own
     workspace allocation, gives the same bits."""
     net = Net(5)
+    net.T = tokens
     ids, res, dout = net.batch(9)
     acc = [torch.zeros(net.L[0].padded, device=DEV) for _ in range(2)]
     net.W
