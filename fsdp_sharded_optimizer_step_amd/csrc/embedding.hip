@@ -371,9 +371,9 @@ __device__ __forceinline__ int32_t piece_in_window(const GradArgs& A, int32_t to
 // thread, the blocks of a row one after another.  Nearly every id of a batch
 // occurs once, so the row's accumulator and its first token are requested
 // together, before any of the sum.  Measured for 16384 tokens of 4096 columns
-// and 12000 distinct ids (520 MB): 120 us, 4.3 TB/s; with 8 columns per
-// thread 151 us, with a row's blocks spread over the grid 134, with
-// temporal accesses 125, with pieces of 32 and 64 tokens 10 and 25 us more.
+// and 12000 distinct ids (520 MB), all three kernels: 134 us (131 in runs, see
+// below); 8 columns per thread cost 18 us more, a row's blocks spread over the
+// grid 9, temporal accesses 5, pieces of 32 and 64 tokens 10 and 25.
 template <class DY, bool GAPS>
 __global__ void __launch_bounds__(kThreads) places_kernel(const GradArgs A) {
   const int32_t total = A.start[((int64_t)1 << A.slice_bits) * A.local];
@@ -400,6 +400,46 @@ __global__ void __launch_bounds__(kThreads) places_kernel(const GradArgs A) {
       grad_store4(A.out, at, s, base);
     else
       row_out<GAPS>(A, e.row, c0, n, s);
+  }
+}
+
+// The same for rows of 1024 columns and more: a block takes 1024 columns of
+// kRun places, of which only those that begin a row or a piece cost more than
+// their share of one load.  With a block for each place, the blocks that found
+// nothing to do took most of the time where ids repeat: 12000 tokens of 4096
+// columns and 600 ids 78 us in runs of 4, 96 one by one, 86 in twos, 74 in
+// eights; 16384 tokens and 12000 ids 131, 130, 129 and 133 us.
+constexpr int kRun = 4;
+template <class DY, bool GAPS>
+__global__ void __launch_bounds__(kThreads) wide_places_kernel(const GradArgs A) {
+  const int32_t total = A.start[((int64_t)1 << A.slice_bits) * A.local];
+  const uint32_t bx = fast_div(blockIdx.x, A.chunks);
+  const int32_t c0 = (int32_t)((blockIdx.x - bx * A.chunks.d) * kThreads + threadIdx.x) * 4;
+  const int n = min(4, A.cols - c0), lane = threadIdx.x & 63;
+  for (int64_t x0 = (int64_t)bx * kRun; x0 < total; x0 += (int64_t)A.row_blocks * kRun) {
+    Entry mine = {0, 0, 1, 0};
+    if (lane < kRun && x0 + lane < total) mine = A.order[x0 + lane];
+    uint64_t todo = __ballot(lane < kRun && x0 + lane < total && mine.rel % kPiece == 0);
+    if (n <= 0) continue;
+    while (todo) {
+      const int i = __ffsll((unsigned long long)todo) - 1;
+      todo &= todo - 1;
+      const Entry e = {__builtin_amdgcn_readlane(mine.token, i), __builtin_amdgcn_readlane(mine.row, i),
+                       __builtin_amdgcn_readlane(mine.rel, i), __builtin_amdgcn_readlane(mine.count, i)};
+      const int32_t x = (int32_t)x0 + i;
+      int64_t at;
+      const bool vec = place_run<GAPS>(A.out.place, (int64_t)e.row * A.cols + c0, 4, at) && n >= 4;
+      const bool whole = e.count <= kPiece;
+      f32x4 base = {0.f, 0.f, 0.f, 0.f};
+      if (vec && whole) base = grad_load4(A.out, at);
+      const f32x4 s = sum_places<DY>(A, e.token, x, min(kPiece, e.count - e.rel), c0, n);
+      if (!whole)
+        piece_out(A, x, e.rel == 0, c0, n, s);
+      else if (vec)
+        grad_store4(A.out, at, s, base);
+      else
+        row_out<GAPS>(A, e.row, c0, n, s);
+    }
   }
 }
 
@@ -466,7 +506,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const GradArgs A) {
     const bool vec = place_run<GAPS>(A.out.place, (int64_t)row * A.cols + c0, 4, to) && n >= 4;
     f32x4 base = {0.f, 0.f, 0.f, 0.f}, s = base;
     if (vec) base = grad_load4(A.out, to);
-#pragma unroll 8
+#pragma unroll 16
     for (int32_t j = 0; j < count; j += kPiece) {
       const float* q = A.partial + slot_of(p + j, j == 0) * A.cols + c0;
       if (n >= 4) {
@@ -580,9 +620,12 @@ int shape_ok(const zero_layout* L, int32_t tensor, int64_t cols, int64_t n) {
   return ZERO_OK;
 }
 
-// Rows of a block: about 4 units per thread, 1 row at least.
-int32_t rows_per_block(int64_t units_per_row) {
-  return (int32_t)std::max<int64_t>(1, 4 * kThreads / std::max<int64_t>(1, units_per_row));
+// Rows of a block, 1 at least: about 4 units per thread, or 1 where that leaves
+// fewer than 2048 blocks (8 for each CU).
+int32_t rows_per_block(int64_t rows, int64_t units_per_row) {
+  const int64_t units = std::max<int64_t>(1, units_per_row);
+  const int64_t per_thread = rows * units >= (int64_t)2048 * 4 * kThreads ? 4 : 1;
+  return (int32_t)std::max<int64_t>(1, per_thread * kThreads / units);
 }
 
 template <class ID, class OUT, bool GAPS>
@@ -620,12 +663,17 @@ int launch_sums(const GradArgs& B, bool dense, hipStream_t s) {
                        dim3(A.piece_blocks + (unsigned)std::min<int64_t>(blocks, 1 << 20)),
                        dim3(kThreads), 0, s, A);
   } else {
-    const int64_t blocks = (A.n + A.rows_per_block - 1) / A.rows_per_block;
-    const int64_t units = (int64_t)A.rows_per_block * A.pieces.d;
+    const bool wide = A.pieces.d >= kThreads;
+    const int64_t per = wide ? kRun : A.rows_per_block;
+    const int64_t units = wide ? A.pieces.d : (int64_t)A.rows_per_block * A.pieces.d;
     A.chunks = make_fast_div((uint32_t)((units + kThreads - 1) / kThreads));
-    A.row_blocks = (uint32_t)std::min<int64_t>(blocks, std::max<int64_t>(1, (1 << 22) / A.chunks.d));
-    hipLaunchKernelGGL((places_kernel<DY, GAPS>), dim3(A.row_blocks * A.chunks.d), dim3(kThreads), 0,
-                       s, A);
+    A.row_blocks = (uint32_t)std::min<int64_t>((A.n + per - 1) / per,
+                                               std::max<int64_t>(1, (1 << 22) / A.chunks.d));
+    const dim3 grid(A.row_blocks * A.chunks.d);
+    if (wide)
+      hipLaunchKernelGGL((wide_places_kernel<DY, GAPS>), grid, dim3(kThreads), 0, s, A);
+    else
+      hipLaunchKernelGGL((places_kernel<DY, GAPS>), grid, dim3(kThreads), 0, s, A);
   }
   const int rc = launched();
   if (rc != ZERO_OK || !pieces) return rc;
@@ -689,7 +737,7 @@ int zero_embedding_lookup(const zero_layout* L, int32_t tensor, int64_t cols,
   A.n = (int32_t)n_ids;
   A.cols = (int32_t)cols;
   A.pieces = make_fast_div((uint32_t)((cols + 7) / 8));
-  A.rows_per_block = rows_per_block(A.pieces.d);
+  A.rows_per_block = rows_per_block(n_ids, A.pieces.d);
   A.scale = scale;
   if (id_bytes == 4)
     return out_dtype == ZERO_DTYPE_F32 ? launch_lookup<int32_t, float>(A, stream)
@@ -747,7 +795,7 @@ int zero_embedding_grad(const zero_layout* L, int32_t tensor, int64_t cols, cons
   A.n = (int32_t)n_ids;
   A.cols = (int32_t)cols;
   A.pieces = make_fast_div((uint32_t)((cols + 3) / 4));
-  A.rows_per_block = rows_per_block(A.pieces.d);
+  A.rows_per_block = rows_per_block(dense ? A.vocab : n_ids, A.pieces.d);
   if (few)
     return id_bytes == 4 ? launch_few<int32_t>(A, ids, dy_dtype == ZERO_DTYPE_F32, stream)
                          : launch_few<int64_t>(A, ids, dy_dtype == ZERO_DTYPE_F32, stream);
