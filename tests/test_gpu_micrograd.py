@@ -222,11 +222,24 @@ def test_emb_grad_shapes_exact_in_integers(dtype, flags, vocab, cols, n, kind):
     assert np.array_equal(f64(f.acc)[rest], f.acc0[rest])
 
 
+@pytest.mark.parametrize("gaps", [False, True])
+@pytest.mark.parametrize("flags", FLAG_SETS)
+@pytest.mark.parametrize("kind", ["skewed", "holes"])
+def test_emb_grad_wide_rows(gaps, flags, kind):
+    vocab, cols, n = 40, 2050, 900
+    L, pl = layout(vocab * cols, gaps)
+    ids = some_ids(kind, n, vocab, 7)
+    dy = strided(randn(2, n, cols), 3, 1)
+    f = Flat(L, pl, vocab * cols, DEV)
+    z.zero_embedding_grad(L, 1, torch.from_numpy(ids).to(DEV), dy, f.acc, 0.25, flags, f.out)
+    f.check(*emb_exact(ids, f64(dy), vocab), 0.25, flags, f"{kind} {flags}")
+
+
 @pytest.mark.parametrize("n", [1, 17, 300, 512, 513, 5000])
 def test_emb_grad_is_the_same_every_time_and_in_token_order(n):
     """Magnitudes from 2^-12 to 2^12: another order would give other bits.
     The stated order: pieces of 16 tokens, each ascending."""
-    vocab, cols = 9, 260
+    vocab, cols = 9, 260 if n % 2 else 1060
     L, pl = layout(vocab * cols, False)
     ids = some_ids("skewed", n, vocab, 4)
     dy = randn(6, n, cols, dtype=F32) * torch.exp2(torch.randint(-12, 13, (n, 1), device=DEV).float())
