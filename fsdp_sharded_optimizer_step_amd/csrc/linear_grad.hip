@@ -272,7 +272,7 @@ __device__ __forceinline__ int64_t slot_of(const Args& A, int32_t tile, int32_t 
 // loads, 1.42 without the LDS reads, 1.06 without either and without the LDS
 // writes.  Requests two steps ahead instead of three take the same time;
 // fragments two stretches ahead spill at this tile (2.36 ms) and gain nothing
-// at the smaller one.  That one (4000 tokens, 1024 x 4096: 47-52 us) takes 13
+// at the smaller one.  That one (4000 tokens, 1024 x 4096: 42-50 us) takes 10
 // us at the ends and 1.07 us for 128 tokens, in which the matrix cores and the
 // LDS are busy for about 0.45 us each.
 template <class S, bool TR>
