@@ -188,7 +188,7 @@ def some_ids(kind, n, vocab, seed=0):
 @pytest.mark.parametrize("gaps", [False, True])
 @pytest.mark.parametrize("flags", FLAG_SETS)
 @pytest.mark.parametrize("kind", ["uniform", "skewed", "holes", "none"])
-@pytest.mark.parametrize("n", [200, 700])
+@pytest.mark.parametrize("n", [200, 700, 1024, 1025])
 def test_emb_grad_flags(gaps, flags, kind, n):
     vocab, cols = 301, 37
     L, pl = layout(vocab * cols, gaps)
@@ -226,7 +226,7 @@ def test_emb_grad_shapes_exact_in_integers(dtype, flags, vocab, cols, n, kind):
 @pytest.mark.parametrize("flags", FLAG_SETS)
 @pytest.mark.parametrize("kind", ["skewed", "holes"])
 def test_emb_grad_wide_rows(gaps, flags, kind):
-    vocab, cols, n = 40, 2050, 900
+    vocab, cols, n = 40, 2050, 1100
     L, pl = layout(vocab * cols, gaps)
     ids = some_ids(kind, n, vocab, 7)
     dy = strided(randn(2, n, cols), 3, 1)
@@ -235,8 +235,9 @@ def test_emb_grad_wide_rows(gaps, flags, kind):
     f.check(*emb_exact(ids, f64(dy), vocab), 0.25, flags, f"{kind} {flags}")
 
 
-@pytest.mark.parametrize("n", [1, 17, 300, 512, 513, 5000])
-def test_emb_grad_is_the_same_every_time_and_in_token_order(n):
+@pytest.mark.parametrize("flags", [0, z.ACC_OVERWRITE])
+@pytest.mark.parametrize("n", [1, 17, 300, 512, 513, 1024, 1025, 5000])
+def test_emb_grad_is_the_same_every_time_and_in_token_order(n, flags):
     """Magnitudes from 2^-12 to 2^12: another order would give other bits.
     The stated order: pieces of 16 tokens, each ascending."""
     vocab, cols = 9, 260 if n % 2 else 1060
@@ -246,7 +247,7 @@ def test_emb_grad_is_the_same_every_time_and_in_token_order(n):
     got = []
     for _ in range(3):
         acc = torch.zeros(L.padded, device=DEV)
-        z.zero_embedding_grad(L, 1, torch.from_numpy(ids).to(DEV), dy, acc, 1.0)
+        z.zero_embedding_grad(L, 1, torch.from_numpy(ids).to(DEV), dy, acc, 1.0, flags)
         got.append(acc.cpu().numpy()[positions(pl, vocab * cols)].reshape(vocab, cols))
     assert np.array_equal(got[0], got[1]) and np.array_equal(got[0], got[2])
     d = dy.cpu().numpy()
