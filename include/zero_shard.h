@@ -46,8 +46,11 @@
  *   - Arithmetic is binary32 with every operation rounded to nearest-even,
  *     no fused multiply-add, subnormals kept, correctly rounded division
  *     and square root.  Results do not depend on the launch configuration.
+ *     (The norm's forward pass is binary64 and the weight gradient's sums are
+ *     those of the matrix cores: see there.)
  *   - Any pointer alignment is accepted; 16-byte aligned buffers take the
- *     vector path, others a scalar path with the same results.
+ *     vector path, others a scalar path with the same results (the calls of
+ *     "gradients of a micro-batch" take vectors at any alignment).
  *   - Entry points may be called from several host threads at once (no
  *     mutable global state apart from a per-device count of compute units);
  *     calls that write the same buffers must be ordered by the caller.

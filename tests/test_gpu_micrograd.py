@@ -617,6 +617,21 @@ def test_linear_grad_non_finite_inputs_reach_only_their_row_and_column():
     assert np.array_equal(bad, exp)
 
 
+@pytest.mark.parametrize("a,b", [(2.0 ** -130, 2.0 ** 10), (2.0 ** -133, 2.0 ** 20),
+                                 (2.0 ** -100, 2.0 ** -30), (-2.0 ** -127, 1.0),
+                                 (2.0 ** -64, 2.0 ** -64)])
+def test_linear_grad_keeps_subnormals(a, b):
+    """bf16 inputs, products and sums below the normal range are exact too."""
+    L = z.Layout([8 * 16], 0, 1, 0)
+    dy, x = torch.zeros(20, 8, dtype=BF16, device=DEV), torch.zeros(20, 16, device=DEV)
+    dy[3], x[3] = a, b
+    q, e = codes_like(20, 16)
+    z.zero_act8_pack(x, q, e)
+    acc = torch.zeros(128, device=DEV)
+    z.zero_linear_grad(L, 0, dy, q, e, acc)
+    assert (acc.double() == a * b).all()
+
+
 def test_linear_grad_inputs_beyond_32_bits():
     tokens, o, i = 70_000, 65_536, 32     # dY: 4.6e9 elements
     L = z.Layout([o * i], 0, 8, 0)
