@@ -14,10 +14,13 @@
 // Both are HBM streams: each row is read once and stays in registers between
 // its statistics and its output, 8 consecutive columns per lane and piece; 16
 // lanes of a DPP row hold one block of 128 columns of the 8-bit output.  A
-// row takes 64 to 1024 threads, so that a thread keeps at most 32 columns.
-// The weight's gradient is summed over a fixed number of row groups in
-// registers, and over the groups, in order, by a second launch: the same sum
-// in every run.
+// row takes 16 to 1024 threads, so that a thread keeps at most 32 columns.
+// The threads are chosen by the width alone, with as few idle as a thread's
+// pieces allow: a backward pass of one row of 768 columns and 128
+// threads a block takes 109 us for 32768 rows, of eight rows of 64 threads 44.
+// The weight's gradient is summed over groups of rows whose number follows
+// from the shape, and over the groups, in order, by a second launch: the same
+// sum in every run.
 #include <algorithm>
 
 #include "act8.hpp"
@@ -87,7 +90,7 @@ __device__ __forceinline__ Piece8 weight8(const uint16_t* params, const Place& p
 template <int NT, class T>
 __device__ __forceinline__ T row_sum(T x, T* slot) {
 #pragma unroll
-  for (int k = 32; k; k >>= 1) x += __shfl_xor(x, k, 64);
+  for (int k = (NT < 64 ? NT : 64) / 2; k; k >>= 1) x += __shfl_xor(x, k, 64);
   if constexpr (NT > 64) {
     const int w = (threadIdx.x % NT) >> 6;
     if ((threadIdx.x & 63) == 0) slot[w] = x;
@@ -99,7 +102,8 @@ __device__ __forceinline__ T row_sum(T x, T* slot) {
   return x;
 }
 
-// Threads of a block for a row of NT threads: rows of one wave share a block.
+// Threads of a block for a row of NT threads: rows of up to one wave share a
+// block.
 template <int NT>
 constexpr int kBlock = NT < 256 ? 256 : NT;
 
@@ -130,7 +134,7 @@ __device__ __forceinline__ float round_to_odd(double x) {
 // for memory all the same: 16384 rows of 8192 columns with every output (1.21
 // GB) take 211 us, 5.7 TB/s; in binary32 alone it gains under 2 %.
 template <int NT, int NP, bool GAPS>
-__global__ void __launch_bounds__(kBlock<NT>) norm_kernel(const NormArgs A) {
+__global__ void __launch_bounds__(kBlock<NT>, 4) norm_kernel(const NormArgs A) {
   constexpr int kRows = kBlock<NT> / NT;
   __shared__ double red[2][kBlock<NT> / 64];
   const int tid = threadIdx.x % NT, sub = threadIdx.x / NT;
@@ -218,63 +222,119 @@ struct NormGradArgs {
   int32_t cols;
 };
 
-// One block per group of consecutive rows.
-template <int NT, int NP, bool GAPS>
-__global__ void __launch_bounds__(NT) norm_grad_kernel(const NormGradArgs A) {
-  __shared__ float red[2][NT / 64];
-  const int tid = threadIdx.x;
+// The operands of one row, and its 1/rms.
+template <int NP>
+struct GradRow {
+  Piece8 dy[NP], h[NP], dh[NP];
+  float R;
+};
+template <int NT, int NP>
+__device__ __forceinline__ GradRow<NP> load_row(const NormGradArgs& A, int64_t r, bool live, int t) {
+  GradRow<NP> x;
+  x.R = live ? A.rstd[r] : 0.f;
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    const int c0 = (k * NT + t) * 8, n = live ? A.cols - c0 : 0;
+    x.dy[k] = load8<true>(A.dy + r * A.dy_stride + c0, n);
+    x.h[k] = load8<true>(A.h + r * A.cols + c0, n);
+    if (A.dh) x.dh[k] = load8<true>(A.dh + r * A.dh_stride + c0, n);
+  }
+  return x;
+}
+// Keeps a piece packed: its widened values are not carried past this point.
+__device__ __forceinline__ void keep(Piece8& p) { asm volatile("" : "+v"(p.w)); }
+
+// One block per group of consecutive rows, WAYS rows at a time, each by NT
+// threads; the ways' sums for the weight are added in order at the end.  What
+// it needs is loads in flight: 16 waves on a CU, from several rows a block
+// where a row is short (65536 x 256: 195 us with a wave a block, 29 here; 1M x
+// 128: 2950, 190).  The next row's loads before this row's sum were no faster
+// (16384 x 4096: 108 us, 100 here) for the registers that they hold.
+// Rows of more than two pieces a thread keep the weight's sums in LDS, each
+// thread its own, 16 bytes apart: in registers they spill (4096 x 32768: 639
+// us, 209 here; 4096 x 12288: 90 in registers of 1024 threads, 84 here).
+template <int NT, int NP, int WAYS, bool GAPS>
+__global__ void __launch_bounds__(NT* WAYS, 4) norm_grad_kernel(const NormGradArgs A) {
+  constexpr int kWidth = NT * NP * 8;
+  constexpr bool kInLds = NP > 2;
+  static_assert(WAYS == 1 || !kInLds, "the sums of the ways take the same LDS");
+  __shared__ float red[2][(NT * WAYS + 63) / 64];
+  __shared__ alignas(16) float sum[WAYS > 1 || kInLds ? WAYS * kWidth : 1];
+  const int t = WAYS > 1 ? threadIdx.x % NT : threadIdx.x, way = WAYS > 1 ? threadIdx.x / NT : 0;
+  f32x4* mine = (f32x4*)sum + t;
   Piece8 w[NP];
   float dw[NP][8];
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
-    const int c0 = (k * NT + tid) * 8;
+    const int c0 = (k * NT + t) * 8;
     w[k] = weight8<GAPS>(A.params, A.place, c0, A.cols - c0);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[k][j] = 0.f;
+    if constexpr (kInLds) mine[2 * k * NT] = mine[(2 * k + 1) * NT] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
   const int64_t ra = (int64_t)blockIdx.x * A.rows_per_group;
   const int64_t rz = min(A.rows, ra + A.rows_per_group);
   int turn = 0;
-  for (int64_t r = ra; r < rz; ++r) {
-    Piece8 dy[NP], h[NP], dh[NP];
-    const float R = A.rstd[r];
+  for (int64_t r0 = ra; r0 < rz; r0 += WAYS) {
+    const int64_t r = r0 + way;
+    GradRow<NP> x = load_row<NT, NP>(A, r, r < rz, t);
     float s = 0.f;
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-      const int c0 = (k * NT + tid) * 8, n = A.cols - c0;
-      dy[k] = load8<true>(A.dy + r * A.dy_stride + c0, n);
-      h[k] = load8<true>(A.h + r * A.cols + c0, n);
-      if (A.dh) dh[k] = load8<true>(A.dh + r * A.dh_stride + c0, n);
-    }
-#pragma unroll
-    for (int k = 0; k < NP; ++k) {
+      if constexpr (kInLds) keep(w[k]);
+      f32x4 lo, hi;
+      if constexpr (kInLds) lo = mine[2 * k * NT], hi = mine[(2 * k + 1) * NT];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float d = at8(dy[k], j), n = at8(h[k], j) * R;
+        const float d = at8(x.dy[k], j), n = at8(x.h[k], j) * x.R;
         s += d * at8(w[k], j) * n;
-        dw[k][j] += d * n;
+        if constexpr (!kInLds) dw[k][j] += d * n;
+        else if (j < 4) lo[j] += d * n;
+        else hi[j - 4] += d * n;
       }
+      if constexpr (kInLds) mine[2 * k * NT] = lo, mine[(2 * k + 1) * NT] = hi;
     }
-    s = row_sum<NT>(s, &red[turn][0]);
+    s = row_sum<NT>(s, &red[turn][way * NT / 64]);
     turn ^= 1;
     const float c = s / (float)A.cols;
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-      const int c0 = (k * NT + tid) * 8, n = A.cols - c0;
+      const int c0 = (k * NT + t) * 8, n = r < rz ? A.cols - c0 : 0;
+      if constexpr (kInLds) keep(w[k]), keep(x.dy[k]), keep(x.h[k]);
       float v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float g = at8(dy[k], j) * at8(w[k], j);
-        const float d = R * (g - c * (at8(h[k], j) * R));
-        v[j] = A.dh ? at8(dh[k], j) + d : d;
+        const float g = at8(x.dy[k], j) * at8(w[k], j);
+        const float d = x.R * (g - c * (at8(x.h[k], j) * x.R));
+        v[j] = A.dh ? at8(x.dh[k], j) + d : d;
       }
       store8<false>(A.dx + r * A.cols + c0, round8(v), n);
     }
   }
+  if constexpr (WAYS > 1) {
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      float* p = &sum[way * kWidth + (k * NT + t) * 8];
+      *(f32x4*)p = f32x4{dw[k][0], dw[k][1], dw[k][2], dw[k][3]};
+      *(f32x4*)(p + 4) = f32x4{dw[k][4], dw[k][5], dw[k][6], dw[k][7]};
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < A.cols; c += NT * WAYS) {
+      float v = 0.f;
+#pragma unroll
+      for (int k = 0; k < WAYS; ++k) v += sum[k * kWidth + c];
+      A.partial[(int64_t)blockIdx.x * A.cols + c] = v;
+    }
+    return;
+  }
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
-    const int c0 = (k * NT + tid) * 8, n = A.cols - c0;
+    const int c0 = (k * NT + t) * 8, n = A.cols - c0;
     float* p = A.partial + (int64_t)blockIdx.x * A.cols + c0;
+    if constexpr (kInLds) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dw[k][j] = mine[(2 * k + j / 4) * NT][j & 3];
+    }
     if (n >= 8) {
       *(f32x4_a4*)p = f32x4{dw[k][0], dw[k][1], dw[k][2], dw[k][3]};
       *(f32x4_a4*)(p + 4) = f32x4{dw[k][4], dw[k][5], dw[k][6], dw[k][7]};
@@ -311,14 +371,20 @@ __global__ void __launch_bounds__(kSumCols* kSumWays)
 }
 
 // ------------------------------------------------------------------ host
-// Row groups of the weight's gradient: a function of the shape alone, so the
-// order of the sum is too.
-constexpr int64_t kMaxGroups = 512;
-int64_t rows_per_group(int64_t rows) {
-  return std::max<int64_t>(4, (rows + kMaxGroups - 1) / kMaxGroups);
+// Rows that a block of the backward pass takes at a time.
+int64_t grad_ways(int64_t cols) {
+  return cols <= 128 ? 32 : cols <= 256 ? 16 : cols <= 1024 ? 8 : cols <= 2048 ? 4 : cols <= 4096 ? 2 : 1;
 }
-int64_t groups_of(int64_t rows) {
-  return rows == 0 ? 0 : (rows + rows_per_group(rows) - 1) / rows_per_group(rows);
+// Row groups of the weight's gradient: a function of the shape alone, so the
+// order of the sum is too.  Two blocks per CU, or one where its LDS leaves no
+// room for another (4096 x 32768 in 512 groups: 227 us, in 256 209).
+int64_t rows_per_group(int64_t rows, int64_t cols) {
+  const int64_t groups = cols <= 16384 ? 512 : 256;
+  return std::max({(int64_t)4, grad_ways(cols), (rows + groups - 1) / groups});
+}
+int64_t groups_of(int64_t rows, int64_t cols) {
+  const int64_t n = rows_per_group(rows, cols);
+  return rows == 0 ? 0 : (rows + n - 1) / n;
 }
 
 int shape_ok(const zero_layout* L, int32_t tensor, int64_t rows) {
@@ -339,12 +405,13 @@ int launch_norm(const NormArgs& A, hipStream_t s) {
     hipLaunchKernelGGL((norm_kernel<NT, NP, false>), dim3(grid), dim3(kBlock<NT>), 0, s, A);
   return launched();
 }
-template <int NT, int NP>
+template <int NT, int NP, int WAYS>
 int launch_norm_grad(const NormGradArgs& A, int64_t groups, hipStream_t s) {
+  const dim3 grid((unsigned)groups), block(NT * WAYS);
   if (A.place.gap)
-    hipLaunchKernelGGL((norm_grad_kernel<NT, NP, true>), dim3((unsigned)groups), dim3(NT), 0, s, A);
+    hipLaunchKernelGGL((norm_grad_kernel<NT, NP, WAYS, true>), grid, block, 0, s, A);
   else
-    hipLaunchKernelGGL((norm_grad_kernel<NT, NP, false>), dim3((unsigned)groups), dim3(NT), 0, s, A);
+    hipLaunchKernelGGL((norm_grad_kernel<NT, NP, WAYS, false>), grid, block, 0, s, A);
   return launched();
 }
 
@@ -388,19 +455,24 @@ int zero_rms_norm(const zero_layout* L, int32_t tensor, const uint16_t* params_f
   A.cols = (int32_t)cols;
   A.nb = (int32_t)nb;
   A.eps = eps;
+  if (cols <= 128) return launch_norm<16, 1>(A, stream);
+  if (cols <= 256) return launch_norm<32, 1>(A, stream);
   if (cols <= 512) return launch_norm<64, 1>(A, stream);
   if (cols <= 1024) return launch_norm<64, 2>(A, stream);
   if (cols <= 2048) return launch_norm<256, 1>(A, stream);
   if (cols <= 4096) return launch_norm<256, 2>(A, stream);
+  if (cols <= 6144) return launch_norm<256, 3>(A, stream);
   if (cols <= 8192) return launch_norm<256, 4>(A, stream);
-  if (cols <= 16384) return launch_norm<512, 4>(A, stream);
+  if (cols <= 12288) return launch_norm<512, 3>(A, stream);
+  if (cols <= 16384) return launch_norm<1024, 2>(A, stream);
+  if (cols <= 24576) return launch_norm<1024, 3>(A, stream);
   return launch_norm<1024, 4>(A, stream);
 }
 
 int64_t zero_rms_norm_grad_workspace(const zero_layout* L, int32_t tensor, int64_t rows) {
   const int rc = shape_ok(L, tensor, rows);
   if (rc != ZERO_OK) return rc;
-  return groups_of(rows) * L->numel[(size_t)tensor] * 4;
+  return groups_of(rows, L->numel[(size_t)tensor]) * L->numel[(size_t)tensor] * 4;
 }
 
 int zero_rms_norm_grad(const zero_layout* L, int32_t tensor, const uint16_t* params_flat,
@@ -417,7 +489,7 @@ int zero_rms_norm_grad(const zero_layout* L, int32_t tensor, const uint16_t* par
   // without rows the gradient is zero, which changes something only where
   // the flags ask for an overwrite or an emission
   if (cols == 0 || (rows == 0 && !(flags & (ZERO_ACC_OVERWRITE | ZERO_ACC_EMIT_BF16)))) return ZERO_OK;
-  const int64_t groups = groups_of(rows), need = groups * cols * 4;
+  const int64_t groups = groups_of(rows, cols), need = groups * cols * 4;
   if (rows > 0) {
     if (!params_flat || !dy || !h || !rstd || !dx || !workspace) return ZERO_EINVAL;
     if (dy_stride < cols || (dh && dh_stride < cols)) return ZERO_EINVAL;
@@ -448,15 +520,19 @@ int zero_rms_norm_grad(const zero_layout* L, int32_t tensor, const uint16_t* par
     A.dx = dx;
     A.partial = (float*)workspace;
     A.rows = rows;
-    A.rows_per_group = rows_per_group(rows);
+    A.rows_per_group = rows_per_group(rows, cols);
     A.cols = (int32_t)cols;
-    if (cols <= 512) rc = launch_norm_grad<64, 1>(A, groups, stream);
-    else if (cols <= 1024) rc = launch_norm_grad<128, 1>(A, groups, stream);
-    else if (cols <= 2048) rc = launch_norm_grad<256, 1>(A, groups, stream);
-    else if (cols <= 4096) rc = launch_norm_grad<256, 2>(A, groups, stream);
-    else if (cols <= 8192) rc = launch_norm_grad<512, 2>(A, groups, stream);
-    else if (cols <= 16384) rc = launch_norm_grad<1024, 2>(A, groups, stream);
-    else rc = launch_norm_grad<1024, 4>(A, groups, stream);
+    if (cols <= 128) rc = launch_norm_grad<16, 1, 32>(A, groups, stream);
+    else if (cols <= 256) rc = launch_norm_grad<32, 1, 16>(A, groups, stream);
+    else if (cols <= 512) rc = launch_norm_grad<64, 1, 8>(A, groups, stream);
+    else if (cols <= 1024) rc = launch_norm_grad<64, 2, 8>(A, groups, stream);
+    else if (cols <= 2048) rc = launch_norm_grad<128, 2, 4>(A, groups, stream);
+    else if (cols <= 4096) rc = launch_norm_grad<256, 2, 2>(A, groups, stream);
+    else if (cols <= 8192) rc = launch_norm_grad<512, 2, 1>(A, groups, stream);
+    else if (cols <= 12288) rc = launch_norm_grad<512, 3, 1>(A, groups, stream);
+    else if (cols <= 16384) rc = launch_norm_grad<512, 4, 1>(A, groups, stream);
+    else if (cols <= 24576) rc = launch_norm_grad<1024, 3, 1>(A, groups, stream);
+    else rc = launch_norm_grad<1024, 4, 1>(A, groups, stream);
     if (rc != ZERO_OK) return rc;
   }
   out.acc = acc_flat;

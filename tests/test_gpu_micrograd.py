@@ -456,6 +456,25 @@ def test_norm_grad(gaps, rows, cols):
         f.check(terms.sum(0), (rows + 2) * U * np.abs(terms).sum(0), 0.5, flags, "weight")
 
 
+# several rows a block and several turns of it, the last ones short, at widths
+# on both sides of each change of the rows' threads
+NORM_MANY = [(533, 128), (17, 129), (16500, 130), (531, 256), (4100, 257), (77, 1000), (4105, 640),
+             (33, 2000), (2051, 1300), (1027, 2300), (1026, 4096), (515, 4104), (2060, 5000),
+             (5, 6144), (5, 6152), (514, 8200), (9, 12288), (9, 12296), (261, 16400), (9, 24576),
+             (1030, 24584)]
+
+
+@pytest.mark.parametrize("rows,cols", NORM_MANY)
+def test_norm_of_many_rows(rows, cols):
+    test_norm(rows % 2 == 1, rows, cols)
+
+
+@pytest.mark.parametrize("rows,cols", NORM_MANY)
+def test_norm_grad_of_many_rows(rows, cols):
+    test_norm_grad(rows % 2 == 1, rows, cols)
+    test_norm_grad(rows % 2 == 0, min(rows, 40), cols)
+
+
 @pytest.mark.parametrize("flags", FLAG_SETS)
 def test_norm_grad_flags_and_no_rows(flags):
     rows, cols = 40, 70
