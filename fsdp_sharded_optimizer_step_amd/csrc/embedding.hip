@@ -20,7 +20,9 @@
 //          n ids, counts its own and those of lower slices, which gives its
 //          place in the order without talking to other blocks, and places its
 //          tokens in a second pass.  n ids are read from the L2 by S blocks:
-//          12 us for 16384 ids, 5 us for 1000.
+//          10 us for 16384 ids, 5 us for 1000.  Of more ids a slice's block
+//          reads its own alone, put together by two launches before it (131072
+//          ids: 16 us in all, 80 without them).
 //   sums   an id of up to kPiece tokens is summed and added to its row of the
 //          accumulator; one with more is cut into pieces of kPiece, summed
 //          apart in binary32, so that a frequent token does not keep one row
@@ -133,6 +135,14 @@ struct PlanArgs {
   uint32_t slice_bits;      // S = 2^slice_bits slices
   int32_t* start;           // S*local + 1 places: first place of (slice, id / S)
   Entry* order;
+  // many tokens only: dealt to their slices by an earlier launch
+  int32_t chunk;       // tokens of one of its blocks
+  int32_t* counts;     // chunks x kMinSlices
+  int32_t* slice_at;   // kMinSlices + 1 places in `dealt`
+  struct Token* dealt;
+};
+struct Token {
+  int32_t token, id;
 };
 
 // The id at t as a number below vocab, or -1 (vocab <= 2^30).
@@ -146,7 +156,139 @@ __device__ __forceinline__ int32_t token_at(const PlanArgs& A, int64_t t, int64_
   return (uint32_t)id < (uint32_t)A.vocab ? (int32_t)id : -1;
 }
 
+// The lanes of `on` whose key of BITS bits is this lane's.
+template <int BITS>
+__device__ __forceinline__ uint64_t same_key(uint64_t on, int32_t key) {
+  uint32_t lo = (uint32_t)on, hi = (uint32_t)(on >> 32);
+#pragma unroll
+  for (int b = 0; b < BITS; ++b) {
+    const uint32_t x = (uint32_t)((int32_t)((uint32_t)key << (31 - b)) >> 31);
+    const uint64_t ones = __ballot(x != 0u);
+    lo &= ~((uint32_t)ones ^ x);
+    hi &= ~((uint32_t)(ones >> 32) ^ x);
+  }
+  return (uint64_t)hi << 32 | lo;
+}
+// A place for each lane that is `on`: the key's next free ones, by lane.  The
+// lanes of a few frequent keys are found one key at a time, the others by the
+// keys' bits.
+template <int BITS>
+__device__ __forceinline__ int32_t take_place(int32_t* next, bool on, int32_t key, int lane) {
+  const uint64_t me = (uint64_t)1 << lane;
+  uint64_t todo = __ballot(on), same = me;
+  for (int k = 0; todo && k < 3; ++k) {
+    const int32_t k0 = __builtin_amdgcn_readlane(key, __ffsll((unsigned long long)todo) - 1);
+    const uint64_t m = __ballot(key == k0) & todo;
+    if (m & me) same = m;
+    todo &= ~m;
+  }
+  if (todo) {
+    const uint64_t m = same_key<BITS>(todo, key);
+    if (todo & me) same = m;
+  }
+  const int lead = __ffsll((unsigned long long)same) - 1;
+  int32_t p = 0;
+  if (on && lane == lead) p = atomicAdd(&next[key], (int32_t)__popcll(same));
+  return __shfl(p, lead, 64) + (int32_t)__popcll(same & (me - 1));
+}
+// The same additions where the places are not asked for: one for the lanes of
+// the first lane's key, which may be most, one for each other lane.
+__device__ __forceinline__ void count_keys(int32_t* cnt, bool on, int32_t key, int lane) {
+  const uint64_t all = __ballot(on);
+  if (!all) return;
+  const int lead = __ffsll((unsigned long long)all) - 1;
+  const uint64_t m = __ballot(key == __builtin_amdgcn_readlane(key, lead)) & all;
+  if ((m >> lane) & 1) {
+    if (lane == lead) atomicAdd(&cnt[key], (int32_t)__popcll(m));
+  } else if (on) {
+    atomicAdd(&cnt[key], 1);
+  }
+}
+
+// Many tokens: dealt to the slices first, in order, so that a slice's block
+// reads its own alone.  count_kernel counts a chunk's tokens of each slice;
+// deal_kernel adds those of the chunks before its own and of the lower slices,
+// and places its tokens.
+constexpr int kMaxChunks = 256;
 template <class ID>
+__global__ void __launch_bounds__(kPlanThreads) count_kernel(const PlanArgs A) {
+  __shared__ int32_t cnt[kMinSlices];
+  const int tid = threadIdx.x;
+  const int64_t ta = (int64_t)blockIdx.x * A.chunk, tz = min((int64_t)A.n, ta + A.chunk);
+  if (tid < kMinSlices) cnt[tid] = 0;
+  __syncthreads();
+#pragma unroll 4
+  for (int64_t t = ta + tid; t < tz; t += kPlanThreads) {
+    const int32_t id = token_at<ID>(A, t, tz);
+    if (id >= 0) atomicAdd(&cnt[id & (kMinSlices - 1)], 1);
+  }
+  __syncthreads();
+  if (tid < kMinSlices) A.counts[(int64_t)blockIdx.x * kMinSlices + tid] = cnt[tid];
+}
+
+template <class ID>
+__global__ void __launch_bounds__(kPlanThreads) deal_kernel(const PlanArgs A) {
+  constexpr int kParts = kPlanThreads / kMinSlices;
+  __shared__ int32_t cnt[kPlanWaves][kMinSlices];  // counts, later the next free place
+  __shared__ int32_t part[2][kParts][kMinSlices];  // chunks before this one; all
+  __shared__ int32_t wsum[kMinSlices / 64];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int s = tid % kMinSlices, q = tid / kMinSlices;
+  const int64_t ca = (int64_t)blockIdx.x * A.chunk, cz = min((int64_t)A.n, ca + A.chunk);
+  // a wave takes consecutive tokens (the chunk is a multiple of 1024)
+  const int64_t ta = ca + (int64_t)wave * (A.chunk / kPlanWaves);
+  const int64_t tz = min(cz, ta + A.chunk / kPlanWaves);
+  for (int w = q; w < kPlanWaves; w += kParts) cnt[w][s] = 0;
+  int32_t before = 0, all = 0;
+#pragma unroll 8
+  for (int c = q; c < (int)gridDim.x; c += kParts) {
+    const int32_t k = A.counts[(int64_t)c * kMinSlices + s];
+    all += k;
+    if (c < (int)blockIdx.x) before += k;
+  }
+  part[0][q][s] = before;
+  part[1][q][s] = all;
+  __syncthreads();
+  for (int64_t t = ta + lane; t < tz; t += 64) {
+    const int32_t id = token_at<ID>(A, t, tz);
+    if (id >= 0) atomicAdd(&cnt[wave][id & (kMinSlices - 1)], 1);
+  }
+  int32_t run = 0, total = 0;
+  if (q == 0) {
+    for (int k = 0; k < kParts; ++k) total += part[1][k][s];
+    run = total;
+    for (int k = 1; k < 64; k <<= 1) {
+      const int32_t up = __shfl_up(run, k, 64);
+      if (lane >= k) run += up;
+    }
+    if (lane == 63) wsum[wave] = run;
+  }
+  __syncthreads();
+  if (q == 0) {
+    for (int w = 0; w < wave; ++w) run += wsum[w];
+    if (blockIdx.x == 0) {
+      A.slice_at[s] = run - total;
+      if (s == kMinSlices - 1) A.slice_at[kMinSlices] = run;
+    }
+    int32_t next = run - total;
+    for (int k = 0; k < kParts; ++k) next += part[0][k][s];
+    for (int w = 0; w < kPlanWaves; ++w) {
+      const int32_t k = cnt[w][s];
+      cnt[w][s] = next;
+      next += k;
+    }
+  }
+  __syncthreads();
+  for (int64_t t0 = ta; t0 < tz; t0 += 64) {
+    const int32_t id = token_at<ID>(A, t0 + lane, tz);
+    const int32_t p = take_place<8>(cnt[wave], id >= 0, id & (kMinSlices - 1), lane);
+    if (id >= 0) A.dealt[p] = Token{(int32_t)(t0 + lane), id};
+  }
+}
+static_assert(kMinSlices == 1 << 8, "take_place's bits");
+
+// DEALT: the slice's tokens come from A.dealt, none are another slice's.
+template <class ID, bool DEALT>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs A) {
   __shared__ int32_t cnt[kPlanWaves][kMaxLocal];  // counts, later the next free place
   __shared__ int32_t tot[kMaxLocal];              // an id's tokens
@@ -157,12 +299,21 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs A) {
   const int32_t mask = (int32_t)((1u << A.slice_bits) - 1u);
   // each wave counts its own contiguous part of the tokens, kBatch loads at a
   // time: the readings are bound by their latency
-  const int64_t per = ((int64_t)A.n + kPlanThreads - 1) / kPlanThreads * 64;
-  const int64_t ta = wave * per, tz = min((int64_t)A.n, ta + per);
-  int32_t id[kBatch];
+  const int64_t na = DEALT ? A.slice_at[slice] : 0, nz = DEALT ? A.slice_at[slice + 1] : A.n;
+  const int64_t per = (nz - na + kPlanThreads - 1) / kPlanThreads * 64;
+  const int64_t ta = na + wave * per, tz = min(nz, ta + per);
+  int32_t id[kBatch], token[kBatch];
   auto read = [&](int64_t t0) {
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) id[k] = token_at<ID>(A, t0 + k * 64 + lane, tz);
+    for (int k = 0; k < kBatch; ++k) {
+      const int64_t t = t0 + k * 64 + lane;
+      if constexpr (DEALT) {
+        const Token x = t < tz ? A.dealt[t] : Token{-1, -1};
+        id[k] = x.id, token[k] = x.token;
+      } else {
+        id[k] = token_at<ID>(A, t, tz);
+      }
+    }
   };
   if (ta < tz) read(ta);
   if (tid < A.local)
@@ -174,8 +325,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs A) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int32_t s = id[k] & mask;
-      if (id[k] >= 0 && s < slice) ++low;
-      if (id[k] >= 0 && s == slice) atomicAdd(&cnt[wave][id[k] >> A.slice_bits], 1);
+      if (!DEALT && id[k] >= 0 && s < slice) ++low;
+      const bool own = id[k] >= 0 && s == slice;
+      if (DEALT)
+        count_keys(cnt[wave], own, id[k] >> A.slice_bits, lane);
+      else if (own)
+        atomicAdd(&cnt[wave][id[k] >> A.slice_bits], 1);
     }
   }
   for (int k = 32; k; k >>= 1) low += __shfl_xor(low, k, 64);
@@ -183,7 +338,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs A) {
   __syncthreads();
   // one id per thread (local <= kMaxLocal = kPlanThreads): its total, then
   // the running sum over the slice's ids
-  int32_t base = 0;
+  int32_t base = (int32_t)na;
   for (int w = 0; w < kPlanWaves; ++w) base += wlow[w];
   int32_t mine = 0;
   if (tid < A.local)
@@ -217,8 +372,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs A) {
     if (tz - ta > 64 * kBatch) read(t0);  // one batch: still in registers
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
+      if (DEALT && t0 + k * 64 >= tz) break;
       const bool own = id[k] >= 0 && (id[k] & mask) == slice;
       const int32_t loc = own ? id[k] >> A.slice_bits : -1;
+      if constexpr (DEALT) {
+        const int32_t p = take_place<10>(cnt[wave], own, loc, lane);
+        if (own) A.order[p] = Entry{token[k], id[k], p - first[loc], tot[loc]};
+        continue;
+      }
       uint64_t todo = __ballot(own);
       while (todo) {
         const int lead = __ffsll((unsigned long long)todo) - 1;
@@ -236,11 +397,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs A) {
     }
   }
 }
+static_assert(kMaxLocal == 1 << 10, "take_place's bits");
 
 // ------------------------------------------------------------------ sums
 // Tokens summed by one thread without a break; more go to pieces.
 constexpr int kPiece = 16;
 static_assert(kPiece <= 64, "a window fits a wave");
+// Tokens from which on an id's pieces are joined by blocks of 64 columns.
+constexpr int kLong = 1024;
 
 struct GradArgs {
   const void* dy;
@@ -257,6 +421,7 @@ struct GradArgs {
   uint32_t piece_blocks;
   FastDiv chunks;       // blocks of a row (or of rows_per_block rows)
   uint32_t row_blocks;  // groups of rows that the grid covers at once
+  unsigned long_blocks;  // of the join, for ids of kLong tokens or more
 };
 
 // The partial row of the piece that begins at place p: among the places of a
@@ -487,41 +652,127 @@ __global__ void __launch_bounds__(kThreads) table_kernel(const GradArgs A) {
 // one another: the window's entries are read before the number of places is
 // known (behind it they hold nothing that is used), the accumulator before the
 // pieces.
+// Four columns of the pieces of `count` tokens from place p, N loads at once.
+template <int N>
+__device__ __forceinline__ void join_pieces(const GradArgs& A, int32_t p, int32_t count, int32_t c0,
+                                            f32x4& s) {
+  const int32_t last = (count - 1) / kPiece * kPiece;
+  for (int32_t j0 = 0; j0 <= last; j0 += N * kPiece) {
+    f32x4 v[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {  // behind the last piece: that one again
+      const int32_t j = min(j0 + k * kPiece, last);
+      v[k] = *(const f32x4_a4*)(A.partial + slot_of(p + j, j == 0) * A.cols + c0);
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (j0 + k * kPiece <= last) s += v[k];
+  }
+}
+
 template <bool GAPS>
-__global__ void __launch_bounds__(kThreads) join_kernel(const GradArgs A) {
-  const int32_t total = A.start[((int64_t)1 << A.slice_bits) * A.local];
-  const int32_t c0 = (int32_t)(blockIdx.y * kThreads + threadIdx.x) * 4;
+__device__ __forceinline__ void join_window(const GradArgs& A, int32_t w0, int32_t c0,
+                                            int32_t total) {
   const int n = min(4, A.cols - c0), lane = threadIdx.x & 63;
-  for (int64_t w = blockIdx.x; w * kPiece < A.n; w += gridDim.x) {
-    const int32_t w0 = (int32_t)w * kPiece;
-    Entry e = {0, 0, 1, 0};
-    if (lane < kPiece && w0 + lane < A.n) e = A.order[w0 + lane];
-    const uint64_t found = __ballot(w0 + lane < total && e.rel == 0 && e.count > kPiece);
-    if (!found) continue;
-    const int at = __ffsll((unsigned long long)found) - 1;
-    const int32_t p = w0 + at, count = __builtin_amdgcn_readlane(e.count, at),
-                  row = __builtin_amdgcn_readlane(e.row, at);
-    if (n <= 0) continue;
-    int64_t to;
-    const bool vec = place_run<GAPS>(A.out.place, (int64_t)row * A.cols + c0, 4, to) && n >= 4;
-    f32x4 base = {0.f, 0.f, 0.f, 0.f}, s = base;
-    if (vec) base = grad_load4(A.out, to);
-#pragma unroll 16
+  Entry e = {0, 0, 1, 0};
+  if (lane < kPiece && w0 + lane < A.n) e = A.order[w0 + lane];
+  const uint64_t found =
+      __ballot(w0 + lane < total && e.rel == 0 && e.count > kPiece && e.count < kLong);
+  if (!found) return;
+  const int at = __ffsll((unsigned long long)found) - 1;
+  const int32_t p = w0 + at, count = __builtin_amdgcn_readlane(e.count, at),
+                row = __builtin_amdgcn_readlane(e.row, at);
+  if (n <= 0) return;
+  int64_t to;
+  const bool vec = place_run<GAPS>(A.out.place, (int64_t)row * A.cols + c0, 4, to) && n >= 4;
+  f32x4 base = {0.f, 0.f, 0.f, 0.f}, s = base;
+  if (vec) base = grad_load4(A.out, to);
+  if (n >= 4) {
+    if (count <= 4 * kPiece)
+      join_pieces<4>(A, p, count, c0, s);
+    else
+      join_pieces<8>(A, p, count, c0, s);
+  } else {
     for (int32_t j = 0; j < count; j += kPiece) {
       const float* q = A.partial + slot_of(p + j, j == 0) * A.cols + c0;
-      if (n >= 4) {
-        s += *(const f32x4_a4*)q;
-      } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (k < n) s[k] += q[k];
+      for (int k = 0; k < 4; ++k)
+        if (k < n) s[k] += q[k];
+    }
+  }
+  if (vec)
+    grad_store4(A.out, to, s, base);
+  else
+    row_out<GAPS>(A, row, c0, n, s);
+}
+
+// 64 columns of a row of kLong tokens or more: the block loads 64 pieces at a
+// time, one wave adds them, in order, a column per lane, while the next are
+// on their way (an id of 21600 tokens of 64 columns: 26 us, 350 with a thread's
+// own loads of its columns).  There is one such id at most that has place `m` (a multiple
+// of kLong) as the first such place of its own.
+template <bool GAPS>
+__device__ __forceinline__ void join_long(const GradArgs& A, int32_t m, int32_t cb, int32_t total,
+                                          float (&stage)[64][64]) {
+  if (cb >= A.cols || m >= total) return;
+  const Entry e = A.order[m];
+  if (e.count < kLong || e.rel >= kLong) return;
+  const int32_t p = m - e.rel, pieces = (e.count + kPiece - 1) / kPiece;
+  const int col = threadIdx.x & 63, part = threadIdx.x >> 6;
+  constexpr int kParts = kThreads / 64, kEach = 64 / kParts;
+  const bool live = cb + col < A.cols;
+  float v[kEach], s = 0.f;
+  auto load = [&](int32_t j0) {
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int32_t j = j0 + k * kParts + part;
+      v[k] = live && j < pieces ? A.partial[slot_of(p + j * kPiece, j == 0) * A.cols + cb + col] : 0.f;
+    }
+  };
+  load(0);
+  for (int32_t j0 = 0; j0 < pieces; j0 += 64) {
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) stage[k * kParts + part][col] = v[k];
+    __syncthreads();
+    if (j0 + 64 < pieces) load(j0 + 64);
+    if (part == 0) {
+      const int rest = min(64, pieces - j0);
+      if (rest == 64) {
+#pragma unroll
+        for (int k = 0; k < 64; ++k) s += stage[k][col];
+      } else {
+        for (int k = 0; k < rest; ++k) s += stage[k][col];
       }
     }
-    if (vec)
-      grad_store4(A.out, to, s, base);
-    else
-      row_out<GAPS>(A, row, c0, n, s);
+    __syncthreads();
   }
+  if (part == 0 && live)
+    grad_store(A.out, place_at<GAPS>(A.out.place, (int64_t)e.row * A.cols + cb + col), s);
+}
+
+__host__ __device__ inline bool join_narrow(const GradArgs& A) { return A.pieces.d <= 64; }
+
+// The first long_blocks of a row of the grid are for the longest ids, kSub
+// blocks of 64 columns each, the others for windows.
+template <bool GAPS>
+__global__ void __launch_bounds__(kThreads) join_kernel(const GradArgs A) {
+  constexpr int kSub = kThreads * 4 / 64;
+  __shared__ float stage[64][64];
+  const int32_t total = A.start[((int64_t)1 << A.slice_bits) * A.local];
+  if (blockIdx.x < A.long_blocks) {
+    const int32_t cb = (int32_t)(blockIdx.y * kSub + blockIdx.x % kSub) * 64;
+    for (int64_t m = (int64_t)(blockIdx.x / kSub) * kLong; m < A.n; m += (int64_t)(A.long_blocks / kSub) * kLong)
+      join_long<GAPS>(A, (int32_t)m, cb, total, stage);
+    return;
+  }
+  // a window for each wave where a wave covers a row, for each block otherwise
+  const bool narrow = join_narrow(A);
+  const int32_t c0 = narrow ? (threadIdx.x & 63) * 4 : (blockIdx.y * kThreads + threadIdx.x) * 4;
+  const int per = narrow ? kThreads / 64 : 1;
+  const int64_t step = (int64_t)(gridDim.x - A.long_blocks) * per * kPiece;
+  for (int64_t w0 = ((int64_t)(blockIdx.x - A.long_blocks) * per + (narrow ? threadIdx.x >> 6 : 0)) * kPiece;
+       w0 < A.n; w0 += step)
+    join_window<GAPS>(A, (int32_t)w0, c0, total);
 }
 
 // ------------------------------------------------------------------ few tokens
@@ -590,10 +841,16 @@ __global__ void __launch_bounds__(kThreads)
 struct Plan {
   uint32_t slice_bits;
   int64_t slices, local;
+  int64_t chunk, chunks;  // of the dealing launches, 0: none
   int64_t start_bytes, order_bytes, partial_bytes, bytes;
 };
 int64_t up16(int64_t n) { return (n + 15) & ~(int64_t)15; }
 
+// Up to this many tokens every slice's block reads all ids; more are dealt to
+// the slices first, which costs two launches, but where each id is read 3 times
+// instead of 512.  The whole call, 64 columns, direct and dealt: 16384 tokens
+// 17 and 23 us, 24576 25 and 23, 65536 48 and 29, 2^20 905 and 204.
+constexpr int64_t kMaxDirect = 16384;
 Plan make_plan(int64_t vocab, int64_t cols, int64_t n) {
   Plan p;
   p.slice_bits = 8;
@@ -602,7 +859,15 @@ Plan make_plan(int64_t vocab, int64_t cols, int64_t n) {
   p.local = std::max<int64_t>(1, (vocab + p.slices - 1) / p.slices);
   p.start_bytes = up16((p.slices * p.local + 1) * 4);
   p.order_bytes = n * (int64_t)sizeof(Entry);
-  p.partial_bytes = 2 * (n / kPiece + 1) * cols * 4;
+  p.chunk = p.chunks = 0;
+  int64_t dealt_bytes = 0;
+  if (n > kMaxDirect && p.slices == kMinSlices) {
+    p.chunk = (n + kMaxChunks * kPlanThreads - 1) / (kMaxChunks * kPlanThreads) * kPlanThreads;
+    p.chunks = (n + p.chunk - 1) / p.chunk;
+    dealt_bytes = (p.chunks + 1) * kMinSlices * 4 + 16 + n * (int64_t)sizeof(Token);
+  }
+  // the dealt tokens are read before the first partial sum is written
+  p.partial_bytes = std::max(2 * (n / kPiece + 1) * cols * 4, dealt_bytes);
   p.bytes = p.start_bytes + p.order_bytes + p.partial_bytes;
   return p;
 }
@@ -677,8 +942,10 @@ int launch_sums(const GradArgs& B, bool dense, hipStream_t s) {
   }
   const int rc = launched();
   if (rc != ZERO_OK || !pieces) return rc;
+  const int64_t per = join_narrow(A) ? kThreads / 64 : 1;
+  A.long_blocks = kThreads * 4 / 64 * (unsigned)std::min<int64_t>(A.n / kLong, 1 << 12);
   hipLaunchKernelGGL(join_kernel<GAPS>,
-                     dim3((unsigned)std::min<int64_t>(windows, 1 << 16),
+                     dim3(A.long_blocks + (unsigned)std::min<int64_t>((windows + per - 1) / per, 1 << 16),
                           (A.pieces.d + kThreads - 1) / kThreads),
                      dim3(kThreads), 0, s, A);
   return launched();
@@ -697,6 +964,19 @@ int launch_few(const GradArgs& A, const void* ids, hipStream_t s) {
 template <class ID>
 int launch_few(const GradArgs& A, const void* ids, bool f32, hipStream_t s) {
   return f32 ? launch_few<ID, float>(A, ids, s) : launch_few<ID, uint16_t>(A, ids, s);
+}
+
+template <class ID>
+int launch_plan(const PlanArgs& P, const Plan& p, hipStream_t s) {
+  const dim3 slices((unsigned)p.slices), chunks((unsigned)p.chunks), block(kPlanThreads);
+  if (p.chunks == 0) {
+    hipLaunchKernelGGL((plan_kernel<ID, false>), slices, block, 0, s, P);
+  } else {
+    hipLaunchKernelGGL(count_kernel<ID>, chunks, block, 0, s, P);
+    hipLaunchKernelGGL(deal_kernel<ID>, chunks, block, 0, s, P);
+    hipLaunchKernelGGL((plan_kernel<ID, true>), slices, block, 0, s, P);
+  }
+  return launched();
 }
 
 template <class DY>
@@ -808,11 +1088,11 @@ int zero_embedding_grad(const zero_layout* L, int32_t tensor, int64_t cols, cons
   P.slice_bits = p.slice_bits;
   P.start = (int32_t*)workspace;
   P.order = (Entry*)((char*)workspace + p.start_bytes);
-  if (id_bytes == 4)
-    hipLaunchKernelGGL(plan_kernel<int32_t>, dim3((unsigned)p.slices), dim3(kPlanThreads), 0, stream, P);
-  else
-    hipLaunchKernelGGL(plan_kernel<int64_t>, dim3((unsigned)p.slices), dim3(kPlanThreads), 0, stream, P);
-  rc = launched();
+  P.chunk = (int32_t)p.chunk;
+  P.counts = (int32_t*)((char*)workspace + p.start_bytes + p.order_bytes);
+  P.slice_at = P.counts + p.chunks * kMinSlices;
+  P.dealt = (Token*)(P.slice_at + kMinSlices + 4);
+  rc = id_bytes == 4 ? launch_plan<int32_t>(P, p, stream) : launch_plan<int64_t>(P, p, stream);
   if (rc != ZERO_OK) return rc;
 
   A.start = P.start;

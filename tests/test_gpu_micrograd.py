@@ -235,6 +235,38 @@ def test_emb_grad_wide_rows(gaps, flags, kind):
     f.check(*emb_exact(ids, f64(dy), vocab), 0.25, flags, f"{kind} {flags}")
 
 
+# so many tokens that they are dealt to the slices first: one more than are
+# not, chunks of 1024 and of more, a last chunk of one token, wide and narrow
+# rows, ids of 1023 tokens and more
+@pytest.mark.parametrize("id_dtype", [np.int32, np.int64])
+@pytest.mark.parametrize("flags", [0, z.ACC_OVERWRITE | z.ACC_EMIT_BF16])
+@pytest.mark.parametrize("vocab,cols,n,kind", [
+    (50257, 3, 16384, "skewed"), (50257, 3, 16385, "skewed"), (300, 66, 20000, "same"),
+    (1000, 130, 20000, "holes"), (262144, 2, 40961, "uniform"), (262145, 2, 40961, "uniform"),
+    (2, 5, 300_000, "uniform"), (257, 1, 262_145, "skewed"), (17, 1030, 17000, "skewed"),
+    (1, 261, 33000, "uniform"), (5000, 257, 17001, "same"), (1500, 8, 1151, "same"),
+    (1500, 8, 1152, "same"), (3, 65, 1600, "holes"), (3, 1100, 2500, "uniform")])
+def test_emb_grad_of_many_tokens_exact_in_integers(vocab, cols, n, kind, flags, id_dtype):
+    L, pl = layout(vocab * cols, vocab * cols > 8 and n % 2 == 1)
+    ids = some_ids(kind, n, vocab, n).astype(id_dtype)
+    ids[::9] = np.array([-1, vocab, 0, np.iinfo(id_dtype).max], id_dtype)[np.arange(len(ids[::9])) % 4]
+    dy = torch.from_numpy(np.random.default_rng(n).integers(-4, 5, (n, cols))).to(BF16).to(DEV)
+    f = Flat(L, pl, vocab * cols, DEV, ints=True)
+    z.zero_embedding_grad(L, 1, torch.from_numpy(ids).to(DEV), dy, f.acc, 1.0, flags, f.out)
+    at = (ids >= 0) & (ids < vocab)
+    g = np.zeros((vocab, cols))
+    np.add.at(g, ids[at], f64(dy)[at])
+    want = (0 if flags & z.ACC_OVERWRITE else f.acc0[f.pos]) + g.reshape(-1)
+    assert np.array_equal(f64(f.acc)[f.pos], want)
+    f.check(g.reshape(-1), np.zeros(g.size), 1.0, flags, kind)
+
+
+@pytest.mark.parametrize("flags", [0, z.ACC_OVERWRITE])
+@pytest.mark.parametrize("n", [1500, 16385, 40000])
+def test_emb_grad_order_of_many_tokens(n, flags):
+    test_emb_grad_is_the_same_every_time_and_in_token_order(n, flags)
+
+
 @pytest.mark.parametrize("flags", [0, z.ACC_OVERWRITE])
 @pytest.mark.parametrize("n", [1, 17, 300, 512, 513, 1024, 1025, 5000])
 def test_emb_grad_is_the_same_every_time_and_in_token_order(n, flags):
