@@ -568,19 +568,25 @@ __global__ void __launch_bounds__(kThreads) places_kernel(const GradArgs A) {
   }
 }
 
-// The same for rows of 1024 columns and more: a block takes 1024 columns of
-// kRun places, of which only those that begin a row or a piece cost more than
-// their share of one load.  With a block for each place, the blocks that found
-// nothing to do took most of the time where ids repeat: 12000 tokens of 4096
-// columns and 600 ids 78 us in runs of 4, 96 one by one, 86 in twos, 74 in
-// eights; 16384 tokens and 12000 ids 131, 130, 129 and 133 us.
+// The same for rows of more than 124 columns: a wave takes 256 columns of kRun
+// places, of which only those that begin a row or a piece cost more than their
+// share of one load.  With threads for each place, those that found nothing to
+// do took most of the time where ids repeat: 12000 tokens of 4096 columns and
+// 600 ids 78 us in runs of 4, 96 one by one, 86 in twos, 74 in eights; 16384
+// tokens and 12000 ids 131, 130, 129 and 133 us; 65536 tokens of 768 columns
+// and 36651 ids 88 us in runs, 112 one by one (of 64 columns 32 and 28, which
+// is why narrow rows stay with the kernel above).
+constexpr uint32_t kMinWide = 32;  // pieces of 4 columns
 constexpr int kRun = 4;
 template <class DY, bool GAPS>
 __global__ void __launch_bounds__(kThreads) wide_places_kernel(const GradArgs A) {
   const int32_t total = A.start[((int64_t)1 << A.slice_bits) * A.local];
-  const uint32_t bx = fast_div(blockIdx.x, A.chunks);
-  const int32_t c0 = (int32_t)((blockIdx.x - bx * A.chunks.d) * kThreads + threadIdx.x) * 4;
-  const int n = min(4, A.cols - c0), lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63;
+  const uint32_t wave = blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t bx = fast_div(wave, A.chunks);
+  if (bx >= A.row_blocks) return;
+  const int32_t c0 = (int32_t)((wave - bx * A.chunks.d) * 64 + lane) * 4;
+  const int n = min(4, A.cols - c0);
   for (int64_t x0 = (int64_t)bx * kRun; x0 < total; x0 += (int64_t)A.row_blocks * kRun) {
     Entry mine = {0, 0, 1, 0};
     if (lane < kRun && x0 + lane < total) mine = A.order[x0 + lane];
@@ -647,11 +653,6 @@ __global__ void __launch_bounds__(kThreads) table_kernel(const GradArgs A) {
   }
 }
 
-// The rows of long ids from their pieces, in order; the grid's second side
-// covers the columns.  Little data, so what counts is how many loads wait for
-// one another: the window's entries are read before the number of places is
-// known (behind it they hold nothing that is used), the accumulator before the
-// pieces.
 // Four columns of the pieces of `count` tokens from place p, N loads at once.
 template <int N>
 __device__ __forceinline__ void join_pieces(const GradArgs& A, int32_t p, int32_t count, int32_t c0,
@@ -670,6 +671,11 @@ __device__ __forceinline__ void join_pieces(const GradArgs& A, int32_t p, int32_
   }
 }
 
+// The row of the long id that begins in the window from w0, from its pieces,
+// in order.  Little data, so what counts is how many loads wait for
+// one another: the window's entries are read before the number of places is
+// known (behind it they hold nothing that is used), the accumulator before the
+// pieces.
 template <bool GAPS>
 __device__ __forceinline__ void join_window(const GradArgs& A, int32_t w0, int32_t c0,
                                             int32_t total) {
@@ -709,8 +715,8 @@ __device__ __forceinline__ void join_window(const GradArgs& A, int32_t w0, int32
 // 64 columns of a row of kLong tokens or more: the block loads 64 pieces at a
 // time, one wave adds them, in order, a column per lane, while the next are
 // on their way (an id of 21600 tokens of 64 columns: 26 us, 350 with a thread's
-// own loads of its columns).  There is one such id at most that has place `m` (a multiple
-// of kLong) as the first such place of its own.
+// own loads of its columns).  The row is that whose places hold place `m`, a
+// multiple of kLong, and no lower one.
 template <bool GAPS>
 __device__ __forceinline__ void join_long(const GradArgs& A, int32_t m, int32_t cb, int32_t total,
                                           float (&stage)[64][64]) {
@@ -928,13 +934,14 @@ int launch_sums(const GradArgs& B, bool dense, hipStream_t s) {
                        dim3(A.piece_blocks + (unsigned)std::min<int64_t>(blocks, 1 << 20)),
                        dim3(kThreads), 0, s, A);
   } else {
-    const bool wide = A.pieces.d >= kThreads;
+    const bool wide = A.pieces.d >= kMinWide;
     const int64_t per = wide ? kRun : A.rows_per_block;
     const int64_t units = wide ? A.pieces.d : (int64_t)A.rows_per_block * A.pieces.d;
-    A.chunks = make_fast_div((uint32_t)((units + kThreads - 1) / kThreads));
+    const int each = wide ? 64 : kThreads;  // a chunk's threads
+    A.chunks = make_fast_div((uint32_t)((units + each - 1) / each));
     A.row_blocks = (uint32_t)std::min<int64_t>((A.n + per - 1) / per,
-                                               std::max<int64_t>(1, (1 << 22) / A.chunks.d));
-    const dim3 grid(A.row_blocks * A.chunks.d);
+                                               std::max<int64_t>(1, (1 << 22) * (kThreads / each) / A.chunks.d));
+    const dim3 grid((unsigned)(((int64_t)A.row_blocks * A.chunks.d * each + kThreads - 1) / kThreads));
     if (wide)
       hipLaunchKernelGGL((wide_places_kernel<DY, GAPS>), grid, dim3(kThreads), 0, s, A);
     else
