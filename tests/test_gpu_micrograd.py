@@ -261,6 +261,21 @@ def test_emb_grad_of_many_tokens_exact_in_integers(vocab, cols, n, kind, flags, 
     f.check(g.reshape(-1), np.zeros(g.size), 1.0, flags, kind)
 
 
+@pytest.mark.parametrize("gaps", [False, True])
+@pytest.mark.parametrize("flags", [0, z.ACC_OVERWRITE, z.ACC_NO_STORE | z.ACC_EMIT_BF16])
+@pytest.mark.parametrize("vocab,cols,n,kind", [
+    (50257, 300, 3000, "skewed"), (25001, 260, 17000, "skewed"), (30003, 125, 1000, "holes")])
+def test_emb_grad_large_tables(vocab, cols, n, kind, flags, gaps):
+    """Several rows of the table a wave, and one."""
+    L, pl = layout(vocab * cols, gaps)
+    ids = some_ids(kind, n, vocab, n)
+    dy = torch.from_numpy(np.random.default_rng(n).integers(-4, 5, (n, cols))).to(BF16).to(DEV)
+    f = Flat(L, pl, vocab * cols, DEV, ints=True)
+    z.zero_embedding_grad(L, 1, torch.from_numpy(ids).to(DEV), dy, f.acc, 0.5, flags, f.out)
+    g, _ = emb_exact(ids, f64(dy), vocab)
+    f.check(g, np.zeros(g.size), 0.5, flags, f"{kind} {flags}")
+
+
 @pytest.mark.parametrize("flags", [0, z.ACC_OVERWRITE])
 @pytest.mark.parametrize("n", [1500, 16385, 40000])
 def test_emb_grad_order_of_many_tokens(n, flags):
