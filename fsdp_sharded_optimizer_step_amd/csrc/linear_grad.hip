@@ -265,12 +265,12 @@ __device__ __forceinline__ int64_t slot_of(const Args& A, int32_t tile, int32_t 
 // three ahead are requested.  One barrier a step, before its last stretch,
 // whose fragments are already in registers.
 //
-// Measured (16384 tokens, 14336 x 4096): 1.59 ms, 1210 TFLOP/s, against 1.88
+// Measured (16384 tokens, 14336 x 4096): 1.51 ms, 1275 TFLOP/s, against 1.88
 // ms of a library bf16 product of that shape alone.  The matrix cores are busy
-// 67 % of the cycles, at a clock that the load itself brings down to 1.75 GHz:
-// with parts left out (for timing only) it runs in 1.35 ms without the global
-// loads, 1.42 without the LDS reads, 1.06 without either and without the LDS
-// writes.  Requests two steps ahead instead of three take the same time;
+// two thirds of the cycles, at a clock that the load itself brings down to
+// 1.75 GHz: when it took 1.59 ms, it took 1.35 without the global loads, 1.42
+// without the LDS reads, 1.06 without either and without the LDS writes (for
+// timing only).  Requests two steps ahead instead of three take the same time;
 // fragments two stretches ahead spill at this tile (2.36 ms) and gain nothing
 // at the smaller one.  That one (4000 tokens, 1024 x 4096: 42-50 us) takes 10
 // us at the ends and 1.07 us for 128 tokens, in which the matrix cores and the
@@ -462,49 +462,87 @@ __global__ void __launch_bounds__(S::kThreads, 1) grad_kernel(const Args A) {
 
   // lane l, register k: row 8*(k/4) + 4*(l/32) + k%4, column l%32
   if (A.direct && tile < A.whole) {
-    // Two 32 x 32 blocks at a time; the accumulator's values of the next two
-    // are requested before these are stored (with a wait for each value this
-    // part took a quarter of the kernel's time).
-    const uint32_t lane_off = (uint32_t)(4 * (lane >> 5)) * (uint32_t)A.cols + (lane & 31);
+    // A wave's sums leave 32 rows at a time, through LDS of its own (the
+    // buffers are free), from where a lane gets 4 columns of a row; the
+    // accumulator's values of the next strip are requested before this one's
+    // are stored.  Single values from the registers to memory left half of its
+    // rate unused: 1024 tokens, 8192 x 8192, added 292 us, 239 here, emitted
+    // 292, 222; 16384 tokens, 14336 x 4096: 1537, 1501.
+    constexpr int kCols = W * 32, kStride = kCols + 8;  // 4 rows are 32 banks apart
+    constexpr int kAcross = kCols / 4, kDown = 64 / kAcross, kVecs = 32 / kDown;
+    static_assert(S::kThreads / 64 * 32 * kStride * 4 <= 2 * kBuffer, "the strips fit the buffers");
+    typedef __attribute__((address_space(3))) float lds_f32;
+    typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+    __syncthreads();
+    lds_f32* const strip = (lds_f32*)lds + (threadIdx.x >> 6) * 32 * kStride;
+    const int down = lane / kAcross, across = lane % kAcross * 4;
+    auto put = [&](auto index) {
+      constexpr int m = decltype(index)::value;
+#pragma unroll
+      for (int n = 0; n < W; ++n)
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          strip[(8 * (k >> 2) + (k & 3) + 4 * (lane >> 5)) * kStride + n * 32 + (lane & 31)] = acc[m][n][k];
+    };
+    auto get = [&](int i) {
+      return *(const lds_f32x4*)(strip + (i * kDown + down) * kStride + across);
+    };
+    const uint32_t lane_off = (uint32_t)down * (uint32_t)A.cols + across;
     const bool add = !(A.out.flags & ZERO_ACC_OVERWRITE);
     const bool keep = !(A.out.flags & ZERO_ACC_NO_STORE), emit = A.out.flags & ZERO_ACC_EMIT_BF16;
-    constexpr int kPairs = kMine * W / 2;
-    float v[2][2][16];
+    f32x4 v[2][kVecs];
     // CHECKED: the tile goes past the matrix's last row or column
     auto out = [&](auto checked) {
       constexpr bool kChecked = decltype(checked)::value;
-      // pair p: row of blocks p / (W / 2), columns of blocks 2 * (p % (W / 2)) and the next
-      auto each = [&](int p, auto f) {
-        const int32_t rb = r0 + (wm * W + m0 + p / (W / 2)) * 32, cb = c0 + (wn * W + p % (W / 2) * 2) * 32;
+      const int32_t cb = c0 + wn * kCols;
+      // f(i, position, columns left): vector i of strip m
+      auto each = [&](int m, auto f) {
+        const int32_t rb = r0 + (wm * W + m0 + m) * 32;
         const int64_t at = A.out.place.x0 + (int64_t)rb * A.cols + cb;
-        const int32_t row_left = A.rows - rb - 4 * (lane >> 5), col_left = A.cols - cb - (lane & 31);
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int32_t r = 8 * (k >> 2) + (k & 3);
-            if (!kChecked || (r < row_left && n * 32 < col_left)) f(n, k, at + (int64_t)r * A.cols + n * 32);
-          }
+        for (int i = 0; i < kVecs; ++i) {
+          int left = 4;
+          if (kChecked) left = rb + i * kDown + down < A.rows ? A.cols - cb - across : 0;
+          if (!kChecked || left > 0) f(i, at + (int64_t)(i * kDown) * A.cols, left);
+        }
       };
-      auto fetch = [&](int p) {
-        each(p, [&](int n, int k, int64_t at) {
-          v[p & 1][n][k] = __builtin_nontemporal_load(A.out.acc + at + lane_off);
+      auto fetch = [&](int m) {
+        each(m, [&](int i, int64_t at, int left) {
+          const float* q = A.out.acc + at + lane_off;
+          if (left >= 4) {
+            v[m & 1][i] = __builtin_nontemporal_load((const f32x4_a4*)q);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+              if (j < left) v[m & 1][i][j] = q[j];
+          }
         });
       };
       if (add) fetch(0);
-      unrolled<kPairs>([&](auto index) {
-        constexpr int p = decltype(index)::value;
-        if (add && p + 1 < kPairs) fetch(p + 1);
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float g = A.out.scale * acc[p / (W / 2)][p % (W / 2) * 2 + n][k];
-            v[p & 1][n][k] = add ? v[p & 1][n][k] + g : g;
+      unrolled<kMine>([&](auto index) {
+        constexpr int m = decltype(index)::value;
+        put(index);
+        if (add && m + 1 < kMine) fetch(m + 1);
+        each(m, [&](int i, int64_t at, int left) {
+          const f32x4 s = get(i);
+          f32x4 x = {A.out.scale * s.x, A.out.scale * s.y, A.out.scale * s.z, A.out.scale * s.w};
+          if (add) {
+            const f32x4 b = v[m & 1][i];
+            x = f32x4{b.x + x.x, b.y + x.y, b.z + x.z, b.w + x.w};
           }
-        each(p, [&](int n, int k, int64_t at) {
-          if (keep) __builtin_nontemporal_store(v[p & 1][n][k], A.out.acc + at + lane_off);
-          if (emit) A.out.out[at + lane_off] = (uint16_t)bf16_round(v[p & 1][n][k]);
+          float* q = A.out.acc + at + lane_off;
+          uint16_t* o = A.out.out + at + lane_off;
+          if (left >= 4) {
+            if (keep) __builtin_nontemporal_store(x, (f32x4_a4*)q);
+            if (emit) *(u32x2_a2*)o = u32x2{bf16_pack2(x.x, x.y), bf16_pack2(x.z, x.w)};
+          } else {
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+              if (j < left) {
+                if (keep) q[j] = x[j];
+                if (emit) o[j] = (uint16_t)bf16_round(x[j]);
+              }
+          }
         });
       });
     };
@@ -514,7 +552,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) grad_kernel(const Args A) {
       out(std::true_type{});
     return;
   }
-  // a tile of the workspace, rows of kSide columns
+  // a tile of the workspace, rows of kSide columns (through LDS no faster: 1000
+  // tokens, 2304 x 768, 25 us against 22)
   float* const to = A.partial + slot_of(A, tile, split) * kSide * kSide + 4 * (lane >> 5) * kSide + (lane & 31);
 #pragma unroll
   for (int m = 0; m < kMine; ++m)
