@@ -14,7 +14,7 @@
 // Cache hints as measured for 8192 x 14336 values: 16-bit and 8-bit loads are
 // non-temporal (bf16: pack and unpack together 115 us, 706 MB; temporal 130),
 // binary32 loads are not, since two of a lane's instructions share a line
-// (pack 107 us against 110), binary32 stores are (unpack 132 against 145).
+// (pack 107 us against 110), binary32 stores are (unpack 104 against 107).
 #include <algorithm>
 
 #include "act8.hpp"

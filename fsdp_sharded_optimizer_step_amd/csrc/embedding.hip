@@ -8,7 +8,7 @@
 // gradient goes.
 //
 // lookup: out[t] = scale * E[id_t].  A stream of 2*cols bytes in and out per
-// token with whole rows, so no LDS; a thread takes 8 columns.  16384 tokens of
+// token with whole rows, so no LDS.  16384 tokens of
 // 8192 columns take 91 us (467 MB, 5.1 TB/s) with non-temporal stores, 98 with
 // temporal ones or with non-temporal loads as well.
 //
@@ -53,15 +53,18 @@ struct LookupArgs {
   Place place;
   int64_t vocab;
   int32_t n, cols;
-  FastDiv pieces;     // pieces of 8 columns per row
+  FastDiv pieces;     // threads of a row
   int32_t rows_per_block;
   float scale;
 };
 
+// Columns of a thread: 16 bytes of output, so that a wave's store is one run of
+// them (to binary32, 16384 rows of 4096 columns: 59 us, with 8 columns and two
+// stores 32 bytes apart 97; of 8192 columns 166 and 153).
 template <class OUT>
-__device__ __forceinline__ void put8(OUT* p, const float (&x)[8], int n);
-template <>
-__device__ __forceinline__ void put8<uint16_t>(uint16_t* p, const float (&x)[8], int n) {
+constexpr int kPerThread = 16 / (int)sizeof(OUT);
+
+__device__ __forceinline__ void put(uint16_t* p, const float (&x)[8], int n) {
   if (n >= 8) {
     const u32x4 w = {bf16_pack2(x[0], x[1]), bf16_pack2(x[2], x[3]), bf16_pack2(x[4], x[5]),
                      bf16_pack2(x[6], x[7])};
@@ -72,46 +75,48 @@ __device__ __forceinline__ void put8<uint16_t>(uint16_t* p, const float (&x)[8],
       if (k < n) p[k] = (uint16_t)bf16_round(x[k]);
   }
 }
-template <>
-__device__ __forceinline__ void put8<float>(float* p, const float (&x)[8], int n) {
-  if (n >= 8) {
+__device__ __forceinline__ void put(float* p, const float (&x)[4], int n) {
+  if (n >= 4) {
     st4_stream(p, f32x4{x[0], x[1], x[2], x[3]});
-    st4_stream(p + 4, f32x4{x[4], x[5], x[6], x[7]});
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < 4; ++k)
       if (k < n) p[k] = x[k];
   }
 }
 
 template <class ID, class OUT, bool GAPS>
 __global__ void __launch_bounds__(kThreads) lookup_kernel(const LookupArgs A) {
+  constexpr int kN = kPerThread<OUT>;
   const int64_t t0 = (int64_t)blockIdx.x * A.rows_per_block;
   const uint32_t units = (uint32_t)A.rows_per_block * A.pieces.d;
   for (uint32_t u = threadIdx.x; u < units; u += kThreads) {
     const uint32_t r = fast_div(u, A.pieces);
-    const int32_t c0 = (int32_t)(u - r * A.pieces.d) * 8;
+    const int32_t c0 = (int32_t)(u - r * A.pieces.d) * kN;
     const int64_t t = t0 + r;
     if (t >= A.n) break;
-    const int n = min(8, A.cols - c0);
+    const int n = min(kN, A.cols - c0);
     const int64_t id = id_at<ID>(A.ids, t);
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float x[kN];
+#pragma unroll
+    for (int k = 0; k < kN; ++k) x[k] = 0.f;
     if (id >= 0 && id < A.vocab) {
       const int64_t i = id * A.cols + c0;
       int64_t at;
-      if (n >= 8 && place_run<GAPS>(A.place, i, 8, at)) {
-        const u32x4 w = *(const u32x4_a2*)(A.params + at);
-        x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
-        x[4] = bf16_lo(w.z); x[5] = bf16_hi(w.z); x[6] = bf16_lo(w.w); x[7] = bf16_hi(w.w);
+      if (n >= kN && place_run<GAPS>(A.place, i, kN, at)) {
+        typedef uint32_t words __attribute__((ext_vector_type(kN / 2), aligned(2)));
+        const words w = *(const words*)(A.params + at);
+#pragma unroll
+        for (int k = 0; k < kN; k += 2) x[k] = bf16_lo(w[k >> 1]), x[k + 1] = bf16_hi(w[k >> 1]);
       } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < kN; ++k)
           if (k < n) x[k] = bf16_one(A.params[place_at<GAPS>(A.place, i + k)]);
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = A.scale * x[k];
+      for (int k = 0; k < kN; ++k) x[k] = A.scale * x[k];
     }
-    put8<OUT>((OUT*)A.out + t * A.out_stride + c0, x, n);
+    put((OUT*)A.out + t * A.out_stride + c0, x, n);
   }
 }
 
@@ -1111,7 +1116,8 @@ int zero_embedding_lookup(const zero_layout* L, int32_t tensor, int64_t cols,
   A.vocab = numel / cols;
   A.n = (int32_t)n_ids;
   A.cols = (int32_t)cols;
-  A.pieces = make_fast_div((uint32_t)((cols + 7) / 8));
+  const int64_t per = out_dtype == ZERO_DTYPE_F32 ? kPerThread<float> : kPerThread<uint16_t>;
+  A.pieces = make_fast_div((uint32_t)((cols + per - 1) / per));
   A.rows_per_block = rows_per_block(n_ids, A.pieces.d);
   A.scale = scale;
   if (id_bytes == 4)
