@@ -8,9 +8,9 @@
 // gradient goes.
 //
 // lookup: out[t] = scale * E[id_t].  A stream of 2*cols bytes in and out per
-// token with whole rows, so no LDS.  16384 tokens of
-// 8192 columns take 91 us (467 MB, 5.1 TB/s) with non-temporal stores, 98 with
-// temporal ones or with non-temporal loads as well.
+// token with whole rows, so no LDS.  16384 tokens of 8192 columns take 91 us
+// (467 MB, 5.1 TB/s) with non-temporal stores, 98 with temporal ones or with
+// non-temporal loads as well.
 //
 // gradient: dE[v] = sum over the t with id_t = v of dY[t], t ascending, so
 // that the result is the same in every run.  Three launches:
