@@ -405,6 +405,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs A) {
 static_assert(kMaxLocal == 1 << 10, "take_place's bits");
 
 // ------------------------------------------------------------------ sums
+// Keeps x computed here, by all lanes: it is read from other lanes after those
+// without columns have left.
+__device__ __forceinline__ void for_all_lanes(int32_t& x) { asm volatile("" : "+v"(x)); }
+__device__ __forceinline__ void for_all_lanes(Entry& e) {
+  for_all_lanes(e.token), for_all_lanes(e.row), for_all_lanes(e.rel), for_all_lanes(e.count);
+}
+
 // Tokens summed by one thread without a break; more go to pieces.
 constexpr int kPiece = 16;
 static_assert(kPiece <= 64, "a window fits a wave");
@@ -597,6 +604,7 @@ __global__ void __launch_bounds__(kThreads) wide_places_kernel(const GradArgs A)
   for (int64_t x0 = (int64_t)bx * kRun; x0 < total; x0 += (int64_t)A.row_blocks * kRun) {
     Entry mine = {0, 0, 1, 0};
     if (lane < kRun && x0 + lane < total) mine = A.order[x0 + lane];
+    for_all_lanes(mine);
     uint64_t todo = __ballot(lane < kRun && x0 + lane < total && mine.rel % kPiece == 0);
     if (n <= 0) continue;
     while (todo) {
@@ -693,6 +701,7 @@ __global__ void __launch_bounds__(kThreads) wide_table_kernel(const GradArgs A) 
     for (int64_t w0 = (int64_t)bx * kPiece; w0 < total; w0 += (int64_t)A.window_rows * kPiece) {
       Entry mine = {0, 0, 1, 0};
       if (lane < kPiece && w0 + lane < total) mine = A.order[w0 + lane];
+      for_all_lanes(mine);
       uint64_t todo = __ballot(mine.count > kPiece && mine.rel % kPiece == 0);
       if (n <= 0) continue;
       while (todo) {
@@ -718,6 +727,7 @@ __global__ void __launch_bounds__(kThreads) wide_table_kernel(const GradArgs A) 
       p0 = at[0], count0 = at[1] - p0;
       if (count0 > 0) token0 = A.order[p0].token;
     }
+    for_all_lanes(p0), for_all_lanes(count0), for_all_lanes(token0);
     if (n <= 0) continue;
     const int rows = (int)min((int64_t)A.table_rows, A.vocab - v0);
     for (int i = 0; i < rows; ++i) {
@@ -761,6 +771,7 @@ __device__ __forceinline__ void join_window(const GradArgs& A, int32_t w0, int32
   const int n = min(4, A.cols - c0), lane = threadIdx.x & 63;
   Entry e = {0, 0, 1, 0};
   if (lane < kPiece && w0 + lane < A.n) e = A.order[w0 + lane];
+  for_all_lanes(e);
   const uint64_t found =
       __ballot(w0 + lane < total && e.rel == 0 && e.count > kPiece && e.count < kLong);
   if (!found) return;
