@@ -879,6 +879,36 @@ def test_captured_and_replayed_with_eager_work_between(tokens):
         torch.randn(1000, device=DEV).sum().item()     # the program's own work between
 
 
+@pytest.mark.parametrize("flags", [0, z.ACC_OVERWRITE])
+def test_many_tokens_captured_and_replayed(flags):
+    vocab, cols, n = 2000, 130, 20000
+    L, _ = layout(vocab * cols, True)
+    ids = torch.from_numpy(some_ids("skewed", n, vocab, 1)).to(DEV)
+    dy, acc = randn(1, n, cols), torch.zeros(L.padded, device=DEV)
+
+    def body():
+        z.zero_embedding_grad(L, 1, ids, dy, acc, 0.5, flags)
+
+    body()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        body()
+    for k, kind in enumerate(("uniform", "skewed", "same", "holes", "uniform")):
+        ids.copy_(torch.from_numpy(some_ids(kind, n, vocab, k)).to(DEV))
+        dy.copy_(randn(k + 5, n, cols))
+        acc.normal_()
+        start = acc.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = acc.clone()
+        acc.copy_(start)
+        body()
+        torch.cuda.synchronize()
+        assert torch.equal(acc, got)
+        torch.randn(1000, device=DEV).sum().item()
+
+
 @pytest.mark.parametrize("tokens", [50, 700])
 def test_other_streams(tokens):
     """A call on a stream that is not the current one, with its own
