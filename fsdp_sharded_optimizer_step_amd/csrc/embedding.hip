@@ -405,13 +405,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs A) {
 static_assert(kMaxLocal == 1 << 10, "take_place's bits");
 
 // ------------------------------------------------------------------ sums
-// Keeps x computed here, by all lanes: it is read from other lanes after those
-// without columns have left.
-__device__ __forceinline__ void for_all_lanes(int32_t& x) { asm volatile("" : "+v"(x)); }
-__device__ __forceinline__ void for_all_lanes(Entry& e) {
-  for_all_lanes(e.token), for_all_lanes(e.row), for_all_lanes(e.rel), for_all_lanes(e.count);
-}
-
 // Tokens summed by one thread without a break; more go to pieces.
 constexpr int kPiece = 16;
 static_assert(kPiece <= 64, "a window fits a wave");
@@ -590,6 +583,9 @@ __global__ void __launch_bounds__(kThreads) places_kernel(const GradArgs A) {
 // tokens and 12000 ids 131, 130, 129 and 133 us; 65536 tokens of 768 columns
 // and 36651 ids 88 us in runs, 112 one by one (of 64 columns 32 and 28, which
 // is why narrow rows stay with the kernel above).
+// The places' entries lie in the first lanes, and all lanes read them, also
+// those past the row's end: a lane's registers are only sure to hold its values
+// for others while it is active itself.
 constexpr uint32_t kMinWide = 32;  // pieces of 4 columns
 constexpr int kRun = 4;
 template <class DY, bool GAPS>
@@ -604,14 +600,13 @@ __global__ void __launch_bounds__(kThreads) wide_places_kernel(const GradArgs A)
   for (int64_t x0 = (int64_t)bx * kRun; x0 < total; x0 += (int64_t)A.row_blocks * kRun) {
     Entry mine = {0, 0, 1, 0};
     if (lane < kRun && x0 + lane < total) mine = A.order[x0 + lane];
-    for_all_lanes(mine);
     uint64_t todo = __ballot(lane < kRun && x0 + lane < total && mine.rel % kPiece == 0);
-    if (n <= 0) continue;
     while (todo) {
       const int i = __ffsll((unsigned long long)todo) - 1;
       todo &= todo - 1;
       const Entry e = {__builtin_amdgcn_readlane(mine.token, i), __builtin_amdgcn_readlane(mine.row, i),
                        __builtin_amdgcn_readlane(mine.rel, i), __builtin_amdgcn_readlane(mine.count, i)};
+      if (n <= 0) continue;  // this lane only; it takes part in the next entry's reads
       const int32_t x = (int32_t)x0 + i;
       int64_t at;
       const bool vec = place_run<GAPS>(A.out.place, (int64_t)e.row * A.cols + c0, 4, at) && n >= 4;
@@ -681,7 +676,8 @@ __device__ __forceinline__ void table_out(const GradArgs& A, int64_t v, int32_t 
   *(f32x4_a4*)(A.out.acc + at) = f32x4{m * s.x, m * s.y, m * s.z, m * s.w};
 }
 
-// The same for rows of more than 124 columns, 256 columns per wave: the waves
+// The same for rows of more than 124 columns, 256 columns per wave (all lanes
+// of which read the entries, as in wide_places_kernel): the waves
 // of the first piece_blocks blocks take a window each, the others table_rows
 // rows of the table, whose places and first tokens are requested together.
 // 16384 tokens, 50257 x 768, overwritten: 61 us, with a thread's rows one after
@@ -701,18 +697,17 @@ __global__ void __launch_bounds__(kThreads) wide_table_kernel(const GradArgs A) 
     for (int64_t w0 = (int64_t)bx * kPiece; w0 < total; w0 += (int64_t)A.window_rows * kPiece) {
       Entry mine = {0, 0, 1, 0};
       if (lane < kPiece && w0 + lane < total) mine = A.order[w0 + lane];
-      for_all_lanes(mine);
       uint64_t todo = __ballot(mine.count > kPiece && mine.rel % kPiece == 0);
-      if (n <= 0) continue;
       while (todo) {
         const int i = __ffsll((unsigned long long)todo) - 1;
         todo &= todo - 1;
-        const int32_t rel = __builtin_amdgcn_readlane(mine.rel, i),
+        const int32_t token = __builtin_amdgcn_readlane(mine.token, i),
+                      rel = __builtin_amdgcn_readlane(mine.rel, i),
                       count = __builtin_amdgcn_readlane(mine.count, i);
         const int32_t p = (int32_t)w0 + i;
-        piece_out(A, p, rel == 0, c0, n,
-                  sum_places<DY>(A, __builtin_amdgcn_readlane(mine.token, i), p,
-                                 min(kPiece, count - rel), c0, n));
+        if (n > 0)
+          piece_out(A, p, rel == 0, c0, n,
+                    sum_places<DY>(A, token, p, min(kPiece, count - rel), c0, n));
       }
     }
     return;
@@ -727,17 +722,19 @@ __global__ void __launch_bounds__(kThreads) wide_table_kernel(const GradArgs A) 
       p0 = at[0], count0 = at[1] - p0;
       if (count0 > 0) token0 = A.order[p0].token;
     }
-    for_all_lanes(p0), for_all_lanes(count0), for_all_lanes(token0);
-    if (n <= 0) continue;
+    // waited for here, once, and not in the loop, where it would be for the
+    // stores of the rows before too (65536 tokens, 32000 x 2048: 145 us, 155)
+    asm volatile("" : "+v"(p0), "+v"(count0), "+v"(token0));
     const int rows = (int)min((int64_t)A.table_rows, A.vocab - v0);
     for (int i = 0; i < rows; ++i) {
       const int32_t count = __builtin_amdgcn_readlane(count0, i);
       if (count > kPiece) continue;
-      f32x4 s = {0.f, 0.f, 0.f, 0.f};
-      if (count > 0)
-        s = sum_places<DY>(A, __builtin_amdgcn_readlane(token0, i),
-                           __builtin_amdgcn_readlane(p0, i), count, c0, n);
-      table_out<GAPS>(A, v0 + i, c0, n, s);
+      if (count > 0) {
+        const int32_t token = __builtin_amdgcn_readlane(token0, i), p = __builtin_amdgcn_readlane(p0, i);
+        if (n > 0) table_out<GAPS>(A, v0 + i, c0, n, sum_places<DY>(A, token, p, count, c0, n));
+      } else if (n > 0) {
+        table_out<GAPS>(A, v0 + i, c0, n, f32x4{0.f, 0.f, 0.f, 0.f});
+      }
     }
   }
 }
@@ -771,7 +768,6 @@ __device__ __forceinline__ void join_window(const GradArgs& A, int32_t w0, int32
   const int n = min(4, A.cols - c0), lane = threadIdx.x & 63;
   Entry e = {0, 0, 1, 0};
   if (lane < kPiece && w0 + lane < A.n) e = A.order[w0 + lane];
-  for_all_lanes(e);
   const uint64_t found =
       __ballot(w0 + lane < total && e.rel == 0 && e.count > kPiece && e.count < kLong);
   if (!found) return;
