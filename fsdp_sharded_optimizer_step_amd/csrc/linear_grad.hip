@@ -239,6 +239,16 @@ __device__ __forceinline__ void tile_at(const Args& A, int32_t tile, int32_t& r,
   r = g * 8 + in - c * h;
 }
 
+// Between a wave's LDS accesses where its lanes read what others wrote, or write
+// over what others read.  The LDS takes a wave's accesses in order; this keeps
+// the compiler, which sees one lane's addresses, from changing that order.  No
+// instruction comes of it.
+__device__ __forceinline__ void lanes_meet_in_lds() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // f(0), f(1) to f(N - 1) with constant arguments: a loop that indexes registers
 // and has to be unrolled whatever its size.
 template <class F, int... I>
@@ -522,6 +532,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) grad_kernel(const Args A) {
       unrolled<kMine>([&](auto index) {
         constexpr int m = decltype(index)::value;
         put(index);
+        lanes_meet_in_lds();
         if (add && m + 1 < kMine) fetch(m + 1);
         each(m, [&](int i, int64_t at, int left) {
           const f32x4 s = get(i);
@@ -544,6 +555,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) grad_kernel(const Args A) {
               }
           }
         });
+        lanes_meet_in_lds();
       });
     };
     if (r0 + kSide <= A.rows && c0 + kSide <= A.cols)

@@ -91,3 +91,28 @@ def parted(blocks):
             todo += [s for s in blocks[x].next if s not in pd[b] - {b}]
         out |= seen
     return out
+
+
+def instructions(ir, keep):
+    """The same from the IR alone, without the analysis, which takes minutes on
+    kernels of many unrolled instructions."""
+    found, blocks, block = {}, None, None
+    with open(ir) as f:
+        for line in f:
+            if line.startswith("define "):
+                name = re.search(r"@([\w.]+)\(", line).group(1)
+                blocks = block = None
+                if any(k in name for k in keep):
+                    blocks = found[name] = {}
+                    block = blocks[""] = Block()
+            elif blocks is None:
+                continue
+            elif line.startswith("}"):
+                blocks = None
+            elif re.match(r"[\w.]+:", line):
+                block = blocks[line.split(":")[0]] = Block()
+            elif line.strip():
+                block.lines.append(line.strip())
+                # a switch's targets stand in lines of their own
+                block.next += re.findall(r"label %([\w.]+)", line)
+    return found

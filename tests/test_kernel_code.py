@@ -26,3 +26,38 @@ def test_lanes_are_active_where_their_entries_are_read(embedding):
             reads += n
             assert n == 0 or label not in apart, f"{name}: block {label}"
         assert reads > 0, name
+
+
+@pytest.fixture(scope="module")
+def linear_grad(tmp_path_factory):
+    return kernel_code.compile_ir("linear_grad.hip", tmp_path_factory.mktemp("ir"))
+
+
+def test_lanes_exchange_sums_through_lds_in_order(linear_grad):
+    """The weight gradient's sums change lanes through LDS, as binary32 values.
+    On every path something orders a lane's write before another lane's read,
+    and that read before the next write: a fence (with or without a barrier)."""
+    kernels = kernel_code.instructions(linear_grad, ("grad_kernel",))
+    assert len(kernels) == 4                       # two tiles, transposed or not
+    for name, blocks in kernels.items():
+        before = {label: set() for label in blocks}
+        todo, writes, reads = list(blocks), 0, 0
+        while todo:
+            label = todo.pop(0)
+            open_ = set(before[label])             # accesses that nothing was put behind yet
+            for line in blocks[label].lines:
+                if line.startswith("fence "):
+                    open_ = set()
+                elif line.startswith("store float") and "addrspace(3)" in line:
+                    assert "read" not in open_, f"{name}: block {label}: {line}"
+                    open_.add("write")
+                    writes += 1
+                elif " = load " in line and "float" in line and "addrspace(3)" in line:
+                    assert "write" not in open_, f"{name}: block {label}: {line}"
+                    open_.add("read")
+                    reads += 1
+            for s in blocks[label].next:
+                if not open_ <= before[s]:
+                    before[s] |= open_
+                    todo.append(s)
+        assert writes > 0 and reads > 0, name
