@@ -39,9 +39,12 @@ using namespace zs;
 
 constexpr int kThreads = 256;
 
+// An id at any address.  Saying so matters where all lanes read the same one:
+// the scalar load that the compiler then takes ignores the address's last two bits.
 template <class T>
-__device__ __forceinline__ int64_t id_at(const void* ids, int64_t t) {
-  return (int64_t)((const T*)ids)[t];
+__device__ __forceinline__ T id_at(const void* ids, int64_t t) {
+  typedef T any __attribute__((aligned(1)));
+  return ((const any*)ids)[t];
 }
 
 // ------------------------------------------------------------------ lookup
@@ -154,7 +157,7 @@ struct Token {
 template <class ID>
 __device__ __forceinline__ int32_t token_at(const PlanArgs& A, int64_t t, int64_t tz) {
   if (t >= tz) return -1;
-  const ID id = ((const ID*)A.ids)[t];
+  const ID id = id_at<ID>(A.ids, t);
   if constexpr (sizeof(ID) == 8) {
     if ((uint64_t)id >> 32) return -1;
   }

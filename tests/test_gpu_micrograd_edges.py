@@ -43,3 +43,58 @@ def test_emb_grad_of_rows_that_leave_lanes_without_columns(cols, flags, gaps):
     want = (0 if flags & z.ACC_OVERWRITE else f.acc0[f.pos]) + g
     assert np.array_equal(f64(f.acc)[f.pos], want)
     f.check(g, np.zeros(g.size), 1.0, flags, f"{cols}")
+
+
+# ------------------------------------------------------------------ addresses
+class At:
+    """A tensor's bytes `shift` bytes into a buffer of their own."""
+
+    def __init__(self, t, shift):
+        t = t.contiguous()
+        self.dtype, self.shape, self.shift = t.dtype, t.shape, shift
+        self.n = t.numel() * t.element_size()
+        self.buf = torch.full((self.n + 64,), 0xA5, dtype=torch.uint8, device=DEV)
+        self.buf[shift:shift + self.n] = t.to(DEV).view(-1).view(torch.uint8)
+
+    @property
+    def p(self):
+        return self.buf.data_ptr() + self.shift
+
+    def get(self):
+        assert (self.buf[:self.shift] == 0xA5).all() and (self.buf[self.shift + self.n:] == 0xA5).all()
+        return self.buf[self.shift:self.shift + self.n].clone().view(self.dtype).view(self.shape)
+
+
+def stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+@pytest.mark.parametrize("shift", [1, 2, 4, 7])
+@pytest.mark.parametrize("id_dtype", [torch.int32, torch.int64])
+@pytest.mark.parametrize("n,cols,flags", [(1, 8, 0), (60, 37, 0), (512, 260, 0), (600, 260, 0),
+                                          (700, 37, z.ACC_OVERWRITE | z.ACC_EMIT_BF16)])
+def test_embedding_at_any_address(n, cols, flags, id_dtype, shift):
+    """Through the C entry points: torch's own tensors are aligned."""
+    vocab = 300
+    lib, L = z.load(), z.Layout([vocab * cols], 0, 4, 0)
+    ids = torch.from_numpy(some_ids("skewed", n, vocab, 3)).to(id_dtype)
+    ids[n // 2] = vocab - 1
+    table, dy = small_ints(1, L.padded), small_ints(2, n, cols)
+    acc, out = small_ints(3, L.padded, dtype=torch.float32), torch.zeros(L.padded, dtype=BF16)
+    i, t, d, a, o = (At(x, shift) for x in (ids, table, dy, acc, out))
+    x = At(torch.zeros(n, cols, dtype=BF16), shift)
+    size = ids.element_size()
+    assert lib.zero_embedding_lookup(L.handle, 0, cols, t.p, i.p, size, n, 1.0, x.p, cols, 0, stream()) == 0
+    ws = torch.empty(lib.zero_embedding_grad_workspace(L.handle, 0, cols, n, flags) + 16,
+                     dtype=torch.uint8, device=DEV)
+    assert lib.zero_embedding_grad(L.handle, 0, cols, i.p, size, n, d.p, cols, 0, 1.0, flags, a.p, o.p,
+                                   ws.data_ptr(), ws.numel(), stream()) == 0
+    rows = table[:vocab * cols].view(vocab, cols)
+    assert torch.equal(x.get(), rows[ids.long().to(DEV)])
+    g, _ = emb_exact(ids.numpy(), f64(dy), vocab)
+    want = (0 if flags & z.ACC_OVERWRITE else f64(acc)[:vocab * cols]) + g
+    assert np.array_equal(f64(a.get())[:vocab * cols], want)
+    if flags & z.ACC_EMIT_BF16:
+        assert torch.equal(o.get()[:vocab * cols], a.get()[:vocab * cols].to(BF16))
+    else:
+        assert not o.get().any()
