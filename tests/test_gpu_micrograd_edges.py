@@ -98,3 +98,57 @@ def test_embedding_at_any_address(n, cols, flags, id_dtype, shift):
         assert torch.equal(o.get()[:vocab * cols], a.get()[:vocab * cols].to(BF16))
     else:
         assert not o.get().any()
+
+
+@pytest.mark.parametrize("shift", [1, 2, 7])
+@pytest.mark.parametrize("rows,cols", [(1, 8), (5, 37), (9, 768), (40, 2056)])
+def test_norm_and_act8_at_any_address(rows, cols, shift):
+    """The same bits as from aligned memory."""
+    lib, L = z.load(), z.Layout([cols], 0, 4, 0)
+    r = np.random.default_rng(rows)
+    real = lambda *s, dtype=BF16: torch.from_numpy(r.standard_normal(s)).to(dtype).to(DEV)  # noqa: E731
+    w, x, res, dy, dh = real(L.padded), *(real(rows, cols) for _ in range(4))
+    a0, nb = real(L.padded, dtype=torch.float32), -(-cols // 128)
+    got = []
+    for s in (0, shift):
+        W, X, R, DY, DH, ACC = (At(t, s) for t in (w, x, res, dy, dh, a0))
+        H, Y, DX, V = (At(torch.zeros(rows, cols, dtype=BF16), s) for _ in range(4))
+        Q, E = At(torch.zeros(rows, cols, dtype=torch.uint8), s), At(torch.zeros(rows, nb, dtype=torch.uint8), s)
+        RS, XF, VF = (At(t, s) for t in (torch.zeros(rows), x.float(), torch.zeros(rows, cols)))
+        Q2, E2 = At(torch.zeros(rows, cols, dtype=torch.uint8), s), At(torch.zeros(rows, nb, dtype=torch.uint8), s)
+        h = L.handle
+        assert lib.zero_rms_norm(h, 0, W.p, X.p, cols, R.p, cols, rows, 1e-5, H.p, RS.p, Q.p, E.p,
+                                 Y.p, stream()) == 0
+        ws = torch.empty(lib.zero_rms_norm_grad_workspace(h, 0, rows) + 16, dtype=torch.uint8, device=DEV)
+        assert lib.zero_rms_norm_grad(h, 0, W.p, DY.p, cols, DH.p, cols, H.p, RS.p, rows, 0.5, 0, DX.p,
+                                      ACC.p, None, ws.data_ptr(), ws.numel(), stream()) == 0
+        assert lib.zero_act8_unpack(Q.p, E.p, rows, cols, V.p, 0, cols, stream()) == 0
+        assert lib.zero_act8_pack(XF.p, 1, rows, cols, cols, Q2.p, E2.p, stream()) == 0
+        assert lib.zero_act8_unpack(Q2.p, E2.p, rows, cols, VF.p, 1, cols, stream()) == 0
+        assert torch.equal(Y.get(), V.get())
+        got.append([t.get() for t in (H, Y, DX, Q, E, RS, ACC, Q2, E2, VF)])
+    for a, b in zip(*got):
+        assert torch.equal(a, b) and a.float().abs().sum() > 0
+
+
+@pytest.mark.parametrize("tr", [0, 1])
+@pytest.mark.parametrize("shift", [1, 2, 7])
+@pytest.mark.parametrize("tokens,o,i", [(1, 3, 5), (70, 33, 130), (300, 256, 512), (1000, 300, 260),
+                                        (700, 4100, 4090)])
+def test_linear_grad_at_any_address(tokens, o, i, shift, tr):
+    lib, L = z.load(), z.Layout([o * i], 0, 4, 0)
+    dy, x = small_ints(tokens, tokens, o), small_ints(i, tokens, i)
+    a0 = small_ints(o, L.padded, dtype=torch.float32)
+    q = torch.empty(tokens, i, dtype=torch.uint8, device=DEV)
+    e = torch.empty(tokens, -(-i // 128), dtype=torch.uint8, device=DEV)
+    z.zero_act8_pack(x, q, e)
+    D, Q, E, A, O = (At(t, shift) for t in (dy, q, e, a0, torch.zeros(L.padded, dtype=BF16)))
+    ws = torch.empty(lib.zero_linear_grad_workspace(L.handle, 0, tr, o, i, tokens) + 16,
+                     dtype=torch.uint8, device=DEV)
+    assert lib.zero_linear_grad(L.handle, 0, tr, D.p, o, Q.p, E.p, tokens, o, i, 1.0, z.ACC_EMIT_BF16,
+                                A.p, O.p, ws.data_ptr(), ws.numel(), stream()) == 0
+    g = dy.double().t().contiguous() @ x.double()              # sums below 16 * 1000: exact
+    want = a0.double()
+    want[:o * i] += (g.t() if tr else g).reshape(-1)
+    assert torch.equal(A.get().double(), want)
+    assert torch.equal(O.get()[:o * i], want[:o * i].float().to(BF16))
