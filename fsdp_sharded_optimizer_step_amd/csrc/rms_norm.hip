@@ -230,8 +230,10 @@ struct GradRow {
 };
 template <int NT, int NP>
 __device__ __forceinline__ GradRow<NP> load_row(const NormGradArgs& A, int64_t r, bool live, int t) {
+  // at any address, which a scalar load of a row's one value would not be
+  typedef float any __attribute__((aligned(1)));
   GradRow<NP> x;
-  x.R = live ? A.rstd[r] : 0.f;
+  x.R = live ? ((const any*)A.rstd)[r] : 0.f;
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
     const int c0 = (k * NT + t) * 8, n = live ? A.cols - c0 : 0;

@@ -61,3 +61,16 @@ def test_lanes_exchange_sums_through_lds_in_order(linear_grad):
                     before[s] |= open_
                     todo.append(s)
         assert writes > 0 and reads > 0, name
+
+
+def test_a_rows_root_mean_square_is_read_at_any_address(tmp_path):
+    """A load that states an alignment of four bytes may become a scalar load
+    where a row's threads all read the same value, and those ignore the
+    address's last two bits."""
+    kernels = kernel_code.instructions(kernel_code.compile_ir("rms_norm.hip", tmp_path),
+                                       ("norm_grad_kernel",))
+    assert len(kernels) == 22                      # eleven widths, padding or none
+    for name, blocks in kernels.items():
+        loads = [line for b in blocks.values() for line in b.lines
+                 if "load float, ptr addrspace(1)" in line]
+        assert loads and all("align 1" in line for line in loads), name
