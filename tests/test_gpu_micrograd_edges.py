@@ -1,12 +1,14 @@
 """The micro-batch operators on the GPU at the edges of their kernels: last,
 partly filled groups of columns, turns of a block, addresses, calls at the same
 time."""
+import threading
+
 import numpy as np
 import pytest
 import torch
 
 import fsdp_sharded_optimizer_step_amd as z
-from micrograd_ref import Flat, f64, layout
+from micrograd_ref import Flat, U, act8, f64, layout
 from test_gpu_micrograd import BF16, DEV, emb_exact, some_ids
 
 pytestmark = pytest.mark.gpu
@@ -152,3 +154,213 @@ def test_linear_grad_at_any_address(tokens, o, i, shift, tr):
     want[:o * i] += (g.t() if tr else g).reshape(-1)
     assert torch.equal(A.get().double(), want)
     assert torch.equal(O.get()[:o * i], want[:o * i].float().to(BF16))
+
+
+# ------------------------------------------------------------------ turns of a block
+def codes_like(rows, cols):
+    return (torch.full((rows, cols), 0x55, dtype=torch.uint8, device=DEV),
+            torch.full((rows, -(-cols // 128)), 0x55, dtype=torch.uint8, device=DEV))
+
+
+# a launch has at most 16384 blocks of 16, 8, 4 or 1 rows: two or three turns of
+# a block, the last one short
+@pytest.mark.parametrize("rows,cols,per_turn", [
+    (262_150, 12, 16 << 14), (131_080, 200, 8 << 14), (65_541, 520, 4 << 14),
+    (16_389, 1032, 1 << 14), (33_000, 1032, 1 << 14), (16_390, 4104, 1 << 14),
+    (16_385, 8200, 1 << 14), (16_387, 16_392, 1 << 14)])
+def test_norm_of_more_rows_than_a_launch_has_blocks_for(rows, cols, per_turn):
+    """Every row as in a call on fewer rows, which one turn covers, and rows on
+    both sides of a turn as the 64-bit reference has them, the codes exactly and
+    1/rms by one rounding to binary32 (2^-24 of it, and what binary64 adds)."""
+    g = torch.Generator(device=DEV).manual_seed(cols)
+    real = lambda *s: torch.randn(*s, generator=g, device=DEV).to(BF16)  # noqa: E731
+    L = z.Layout([cols], 0, 4, 0)
+    params, x, res = 1 + 0.2 * real(L.padded), real(rows, cols), 4 * real(rows, cols)
+    x *= torch.exp2(torch.randint(-6, 7, (rows, 1), generator=g, device=DEV).float()).to(BF16)
+
+    def norm(a, b):
+        h, y = (torch.empty(b - a, cols, dtype=BF16, device=DEV) for _ in range(2))
+        rstd, (q, e) = torch.empty(b - a, device=DEV), codes_like(b - a, cols)
+        z.zero_rms_norm(L, 0, params, x[a:b], res[a:b], 1e-5, h, rstd, q, e, y)
+        return h, rstd, q, e, y
+
+    whole = norm(0, rows)
+    for a in range(0, rows, per_turn // 2):
+        b = min(rows, a + per_turn // 2)
+        for t, part in zip(whole, norm(a, b)):
+            assert torch.equal(t[a:b], part), f"rows {a} to {b}"
+    at = sorted({0, 1, rows - 1, rows - 2} | {k * per_turn + j for k in range(1, rows // per_turn + 1)
+                                              for j in (-2, -1, 0, 1, 2) if k * per_turn + j < rows})
+    at = torch.tensor(at, device=DEV)
+    h = (x[at].float() + res[at].float()).to(BF16)
+    hd = f64(h)
+    r = 1 / np.sqrt((hd ** 2).mean(1) + 1e-5)
+    eq, ee = act8(hd * r[:, None] * f64(params[:cols]))
+    assert torch.equal(whole[0][at], h)
+    assert (np.abs(f64(whole[1][at]) - r) <= U * r * (1 + 2.0 ** -20)).all()
+    assert np.array_equal(whole[2][at].cpu().numpy(), eq)
+    assert np.array_equal(whole[3][at].cpu().numpy(), ee)
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+def test_act8_of_more_blocks_than_a_launch_takes_at_once(dtype):
+    rows, cols = 40_001, 1033                        # 360009 blocks of 128, 262144 at once
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn(rows, cols, generator=g, device=DEV).to(dtype)
+    (q, e), out = codes_like(rows, cols), torch.empty(rows, cols, dtype=dtype, device=DEV)
+    z.zero_act8_pack(x, q, e)
+    z.zero_act8_unpack(q, e, out)
+    for a in range(0, rows, 20_000):
+        b = min(rows, a + 20_000)
+        (q1, e1), o1 = codes_like(b - a, cols), torch.empty(b - a, cols, dtype=dtype, device=DEV)
+        z.zero_act8_pack(x[a:b], q1, e1)
+        z.zero_act8_unpack(q1, e1, o1)
+        assert torch.equal(q[a:b], q1) and torch.equal(e[a:b], e1) and torch.equal(out[a:b], o1)
+    eq, ee = act8(f64(x[-300:]))
+    assert np.array_equal(q[-300:].cpu().numpy(), eq) and np.array_equal(e[-300:].cpu().numpy(), ee)
+
+
+# ------------------------------------------------------------------ emitted values
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+@pytest.mark.parametrize("flags", [z.ACC_EMIT_BF16, z.ACC_EMIT_BF16 | z.ACC_NO_STORE,
+                                   z.ACC_OVERWRITE | z.ACC_EMIT_BF16 | z.ACC_NO_STORE])
+@pytest.mark.parametrize("vocab,cols,n,kind", [
+    (1, 1, 1, "uniform"), (5, 4, 64, "same"), (3, 130, 1000, "uniform"), (300_000, 3, 5000, "skewed"),
+    (50257, 16, 3000, "skewed"), (100, 1000, 129, "same"), (257, 4100, 64, "holes"),
+    (2, 8, 20000, "uniform"), (7, 1030, 513, "same"), (40, 2050, 511, "skewed")])
+def test_emb_grad_emits_what_it_sums(dtype, flags, vocab, cols, n, kind):
+    """Sums of small integers: the emitted value is the exact sum, rounded once
+    (integers up to 256 not at all), and nothing else is written."""
+    L, pl = layout(vocab * cols, n % 2 == 1 and vocab * cols > 8)
+    ids = some_ids(kind, n, vocab, n)
+    dy = small_ints(n, n, cols, dtype=dtype)
+    f = Flat(L, pl, vocab * cols, DEV, ints=True)
+    z.zero_embedding_grad(L, 1, torch.from_numpy(ids.astype(np.int32)).to(DEV), dy, f.acc, 1.0,
+                          flags, f.out)
+    g, _ = emb_exact(ids, f64(dy), vocab)
+    want = (0 if flags & z.ACC_OVERWRITE else f.acc0[f.pos]) + g
+    assert torch.equal(f.out[torch.from_numpy(f.pos).to(DEV)].cpu(), torch.from_numpy(want).float().to(BF16))
+    f.check(g, np.zeros(g.size), 1.0, flags, kind)
+
+
+# ------------------------------------------------------------------ calls at the same time
+class Work:
+    """One micro-batch through all calls, with its own inputs, outputs and
+    workspaces; results() of two passes have to be the same bits."""
+
+    def __init__(self, seed, tokens, d, o, vocab):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        real = lambda *s: torch.randn(*s, generator=g, device=DEV).to(BF16)  # noqa: E731
+        self.L = L = z.Layout([vocab * d, d, o * d], 0, 4, 0)
+        self.ids = torch.randint(-1, vocab, (tokens,), generator=g, device=DEV)
+        self.ids[: tokens // 4] = 3
+        self.params, self.res, self.dout = real(L.padded), real(tokens, d), real(tokens, o)
+        new = lambda *s, dtype=BF16: torch.zeros(*s, dtype=dtype, device=DEV)  # noqa: E731
+        self.x, self.h, self.y, self.dx, self.v = (new(tokens, d) for _ in range(5))
+        self.rstd = new(tokens, dtype=torch.float32)
+        self.acc, self.out = new(L.padded, dtype=torch.float32), new(L.padded)
+        (self.q, self.e), lib = codes_like(tokens, d), z.load()
+        flags = z.ACC_OVERWRITE | z.ACC_EMIT_BF16
+        self.ws = [torch.empty(k + 16, dtype=torch.uint8, device=DEV) for k in (
+            lib.zero_linear_grad_workspace(L.handle, 2, 0, o, d, tokens),
+            lib.zero_rms_norm_grad_workspace(L.handle, 1, tokens),
+            lib.zero_embedding_grad_workspace(L.handle, 0, d, tokens, flags))]
+        self.flags = flags
+
+    def run(self, stream=None):
+        L, kw = self.L, {"stream": stream}
+        z.zero_embedding_lookup(L, 0, self.params, self.ids, self.x, 2.0, **kw)
+        z.zero_rms_norm(L, 1, self.params, self.x, self.res, 1e-5, self.h, self.rstd, self.q, self.e,
+                        self.y, **kw)
+        z.zero_act8_unpack(self.q, self.e, self.v, **kw)
+        z.zero_linear_grad(L, 2, self.dout, self.q, self.e, self.acc, 0.5, self.flags, self.out,
+                           workspace=self.ws[0], **kw)
+        z.zero_rms_norm_grad(L, 1, self.params, self.v, self.res, self.h, self.rstd, self.dx, self.acc,
+                             0.5, self.flags, self.out, workspace=self.ws[1], **kw)
+        z.zero_embedding_grad(L, 0, self.ids, self.dx, self.acc, 0.5, self.flags, self.out,
+                              workspace=self.ws[2], **kw)
+
+    def results(self):
+        return [t.clone() for t in (self.x, self.h, self.y, self.dx, self.v, self.rstd, self.acc,
+                                    self.out, self.q, self.e)]
+
+    def clear(self):
+        for t in (self.x, self.h, self.y, self.dx, self.v, self.rstd, self.acc, self.out, self.q, self.e,
+                  *self.ws):
+            t.zero_()
+
+
+def works():
+    w = [Work(1, 700, 260, 300, 500), Work(2, 17_000, 136, 520, 300), Work(3, 3000, 1032, 264, 2000)]
+    for one in w:
+        one.run()
+    torch.cuda.synchronize()
+    return w, [one.results() for one in w]
+
+
+def same(w, want):
+    torch.cuda.synchronize()
+    for k, (one, exp) in enumerate(zip(w, want)):
+        for j, (a, b) in enumerate(zip(one.results(), exp)):
+            assert torch.equal(a, b), f"micro-batch {k}, result {j}"
+
+
+def test_calls_on_several_streams_at_once():
+    w, want = works()
+    streams = [torch.cuda.Stream() for _ in w]
+    for turn in range(3):
+        for one in w:
+            one.clear()
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for one, s in zip(w, streams):
+                one.run(s)
+        same(w, want)
+
+
+def test_calls_from_several_host_threads_at_once():
+    w, want = works()
+    for one in w:
+        one.clear()
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(one):
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(6):
+                one.run(s)
+            s.synchronize()
+        except Exception as e:                         # reported by the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(one,)) for one in w]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    same(w, want)
+
+
+def test_captured_graphs_replayed_at_once():
+    """Each with its own workspaces, on streams of their own, with eager work
+    between the replays."""
+    w, want = works()
+    graphs = []
+    for one in w:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            one.run()
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in w]
+    for turn in range(4):
+        for one in w:
+            one.clear()
+        torch.cuda.synchronize()
+        for _ in range(2):
+            for g, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+        same(w, want)
+        torch.randn(1000, device=DEV).sum().item()     # the program's own work between
