@@ -680,6 +680,12 @@ int shape_ok(const zero_layout* L, int32_t tensor, int64_t O, int64_t I, int64_t
   return ZERO_OK;
 }
 
+// The dispatch grids count work-items in 32 bits: 2^22 tiles of 512 threads.
+// Any weight of up to 2^35 elements has fewer.
+int plan_ok(const Plan& p) {
+  return p.row_tiles * p.col_tiles > ((int64_t)1 << 22) ? ZERO_ERANGE : ZERO_OK;
+}
+
 template <class S, bool TR>
 int launch(const Args& A, const Plan& p, hipStream_t s) {
   hipLaunchKernelGGL((grad_kernel<S, TR>), dim3((unsigned)(p.whole + p.further * p.splits)),
@@ -714,9 +720,9 @@ int64_t zero_linear_grad_workspace(const zero_layout* L, int32_t tensor, int32_t
   const int rc = shape_ok(L, tensor, out_features, in_features, tokens);
   if (rc != ZERO_OK) return rc;
   if (transposed != 0 && transposed != 1) return ZERO_EINVAL;
-  return make_plan(L, tensor, transposed ? in_features : out_features,
-                   transposed ? out_features : in_features, tokens)
-      .bytes;
+  const Plan p = make_plan(L, tensor, transposed ? in_features : out_features,
+                           transposed ? out_features : in_features, tokens);
+  return plan_ok(p) == ZERO_OK ? p.bytes : ZERO_ERANGE;
 }
 
 int zero_linear_grad(const zero_layout* L, int32_t tensor, int32_t transposed, const uint16_t* dy,
@@ -736,10 +742,9 @@ int zero_linear_grad(const zero_layout* L, int32_t tensor, int32_t transposed, c
   if (dy_stride > ZERO_MAX_STRIDE) return ZERO_ERANGE;
   const int64_t rows = transposed ? I : O, cols = transposed ? O : I;
   const Plan p = make_plan(L, tensor, rows, cols, tokens);
+  if (plan_ok(p) != ZERO_OK) return ZERO_ERANGE;
   if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes || ((uintptr_t)workspace & 15u)))
     return ZERO_EINVAL;
-  // the dispatch grids count work-items in 32 bits
-  if (p.row_tiles * p.col_tiles > ((int64_t)1 << 18)) return ZERO_ERANGE;
   Args A;
   int64_t lo, hi;
   A.out.place = make_place(L, tensor, &lo, &hi);

@@ -553,7 +553,8 @@ int zero_rms_norm_grad(const zero_layout* layout, int32_t tensor, const uint16_t
  * (out_features, in_features), or with transposed = 1 (in_features,
  * out_features).  dY: bf16.  X: codes and scales of zero_act8_pack or
  * zero_rms_norm, tokens x in_features.  Products are exact, sums binary32 in
- * the matrix cores (their order depends on the sizes alone). */
+ * the matrix cores (their order depends on the sizes alone).  Weights of up to
+ * 2^35 elements are accepted, larger ones may be refused (ZERO_ERANGE). */
 int64_t zero_linear_grad_workspace(const zero_layout* layout, int32_t tensor, int32_t transposed,
                                    int64_t out_features, int64_t in_features, int64_t tokens);
 int zero_linear_grad(const zero_layout* layout, int32_t tensor, int32_t transposed,

@@ -364,3 +364,22 @@ def test_captured_graphs_replayed_at_once():
                     g.replay()
         same(w, want)
         torch.randn(1000, device=DEV).sum().item()     # the program's own work between
+
+
+# ------------------------------------------------------------------ very large weights
+@pytest.mark.parametrize("tr", [False, True])
+def test_linear_grad_of_a_weight_beyond_32_bits(tr):
+    """5.0e9 elements, 393216 tiles."""
+    tokens, o, i = 3, 300, 1 << 24
+    L = z.Layout([o * i], 0, 1, 0)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    dy = torch.randint(-3, 4, (tokens, o), generator=g, device=DEV).to(BF16)
+    x = torch.randint(-8, 9, (tokens, i), generator=g, device=DEV).to(BF16)
+    q, e = codes_like(tokens, i)
+    z.zero_act8_pack(x, q, e)
+    acc = torch.ones(L.padded, device=DEV)
+    z.zero_linear_grad(L, 0, dy, q, e, acc, 2.0, transposed=tr)
+    dw = acc[:o * i].view(i, o) if tr else acc[:o * i].view(o, i)
+    for k in range(0, i, 1 << 20):
+        part = dy.float().t().contiguous() @ x[:, k:k + (1 << 20)].float() * 2 + 1   # small integers
+        assert torch.equal(dw[k:k + (1 << 20)].t() if tr else dw[:, k:k + (1 << 20)], part)

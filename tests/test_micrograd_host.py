@@ -222,3 +222,26 @@ def test_reference_codes_agree_with_the_type_of_torch():
     assert np.abs(v - x.double().numpy()).max() <= 2.0 ** -4 * np.abs(x.numpy()).max()
     bf = torch.from_numpy(v).to(torch.bfloat16).double().numpy()
     assert np.array_equal(bf, v)
+
+
+# ------------------------------------------------------------------ very large weights
+@pytest.mark.parametrize("o,i", [(300, 1 << 24), (1 << 24, 130), (1 << 17, 1 << 18), (129, 1 << 24)])
+def test_weights_of_up_to_2_35_elements_are_accepted(o, i):
+    """Checked by the one refusal that comes after all others: an overlap."""
+    big = z.Layout([o * i], 0, 1, 0)
+    lib = z.load()
+    for tr in (0, 1):
+        for tokens in (1, 1000):
+            size = lib.zero_linear_grad_workspace(big.handle, 0, tr, o, i, tokens)
+            assert size >= 0
+            assert lib.zero_linear_grad(big.handle, 0, tr, at(1), o, at(1 << 20), at(1 << 21), tokens, o, i,
+                                        1.0, 0, at(1), None, at(1 << 22), size, None) == EOVERLAP
+
+
+def test_larger_weights_are_refused_by_the_call_and_its_workspace_alike():
+    o = i = 1 << 24
+    big = z.Layout([o * i], 0, 1, 0)
+    lib = z.load()
+    assert lib.zero_linear_grad_workspace(big.handle, 0, 0, o, i, 5) == ERANGE
+    assert lib.zero_linear_grad(big.handle, 0, 0, at(1), o, at(2), at(3), 5, o, i, 1.0, 0, at(4), None,
+                                None, 0, None) == ERANGE
