@@ -493,6 +493,8 @@ def _matrix(where, name, t, rows, cols, types):
         raise _bad_type(where, name, t, types)
     if t.shape != (rows, cols):
         raise ValueError(f"{where}: {name}: needs shape {(rows, cols)}, got {tuple(t.shape)}")
+    if rows == 0:
+        return max(cols, 1)
     s0, s1 = t.stride()
     if cols > 1 and s1 != 1:
         raise ValueError(f"{where}: {name}: columns are not adjacent (strides {t.stride()})")

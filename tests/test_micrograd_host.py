@@ -245,3 +245,17 @@ def test_larger_weights_are_refused_by_the_call_and_its_workspace_alike():
     assert lib.zero_linear_grad_workspace(big.handle, 0, 0, o, i, 5) == ERANGE
     assert lib.zero_linear_grad(big.handle, 0, 0, at(1), o, at(2), at(3), 5, o, i, 1.0, 0, at(4), None,
                                 None, 0, None) == ERANGE
+
+
+def test_wrappers_take_empty_batches_whatever_their_strides(L):
+    """An empty array's strides say nothing (numpy's are zero in torch)."""
+    for name in ("pack", "lookup", "emb_grad", "norm", "norm_grad", "linear"):
+        fn, args = wrapper_calls(L)[name]
+        rows = {"pack": 5, "lookup": 9, "emb_grad": 9, "norm": 5, "norm_grad": 5, "linear": 50}[name]
+        none = []
+        for v in args:
+            if torch.is_tensor(v) and v.shape[0] == rows:
+                v = v[:0].as_strided((0, *v.shape[1:]), (0,) * v.dim())
+            none.append(v)
+        with pytest.raises(ValueError, match="needs CUDA tensors"):
+            fn(*none)
