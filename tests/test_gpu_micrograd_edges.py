@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import fsdp_sharded_optimizer_step_amd as z
-from micrograd_ref import Flat, U, act8, f64, layout
+from micrograd_ref import Flat, U, act8, act8_values, f64, layout
 from test_gpu_micrograd import BF16, DEV, emb_exact, some_ids
 
 pytestmark = pytest.mark.gpu
@@ -383,3 +383,109 @@ def test_linear_grad_of_a_weight_beyond_32_bits(tr):
     for k in range(0, i, 1 << 20):
         part = dy.float().t().contiguous() @ x[:, k:k + (1 << 20)].float() * 2 + 1   # small integers
         assert torch.equal(dw[k:k + (1 << 20)].t() if tr else dw[:, k:k + (1 << 20)], part)
+
+
+# ------------------------------------------------------------------ calls that the header allows
+@pytest.mark.parametrize("gaps", [False, True])
+def test_emission_without_an_accumulator(gaps):
+    """OVERWRITE with NO_STORE needs none."""
+    flags = z.ACC_OVERWRITE | z.ACC_EMIT_BF16 | z.ACC_NO_STORE
+    for cols, n in ((37, 700), (260, 700), (260, 0)):
+        vocab = 90
+        L, pl = layout(vocab * cols, gaps)
+        ids, dy = some_ids("skewed", n, vocab, 1), small_ints(1, n, cols)
+        f = Flat(L, pl, vocab * cols, DEV, ints=True)
+        z.zero_embedding_grad(L, 1, torch.from_numpy(ids).to(DEV), dy, None, 0.5, flags, f.out)
+        g, _ = emb_exact(ids, f64(dy), vocab)
+        f.check(g, np.zeros(g.size), 0.5, flags, f"table {cols} {n}")
+    rows, cols = 50, 300
+    L, pl = layout(cols, gaps)
+    dy, h = small_ints(2, rows, cols), small_ints(3, rows, cols)
+    f, r, dx = Flat(L, pl, cols, DEV), torch.ones(rows, device=DEV), torch.empty(rows, cols, dtype=BF16, device=DEV)
+    z.zero_rms_norm_grad(L, 1, torch.ones(L.padded, dtype=BF16, device=DEV), dy, None, h, r, dx, None, 0.5,
+                         flags, f.out)
+    f.check((f64(dy) * f64(h)).sum(0), np.zeros(cols), 0.5, flags, "norm")
+    tokens, o, i = 300, 70, 130
+    L, pl = layout(o * i, gaps)
+    dy, x, (q, e) = small_ints(4, tokens, o), small_ints(5, tokens, i), codes_like(tokens, i)
+    z.zero_act8_pack(x, q, e)
+    f = Flat(L, pl, o * i, DEV)
+    z.zero_linear_grad(L, 1, dy, q, e, None, 0.5, flags, f.out)
+    f.check((f64(dy).T @ f64(x)).reshape(-1), np.zeros(o * i), 0.5, flags, "linear")
+
+
+@pytest.mark.parametrize("flags", [0, z.ACC_OVERWRITE | z.ACC_EMIT_BF16])
+@pytest.mark.parametrize("cols,n", [(7, 300), (7, 900), (264, 900)])
+def test_table_and_norm_of_a_per_parameter_layout(cols, n, flags):
+    """Each tensor in a slot of its own, padded behind its rows."""
+    vocab = 61
+    L, pl = layout(vocab * cols, False, dim0_rows=vocab)
+    ids, dy = some_ids("holes", n, vocab, 2), small_ints(1, n, cols)
+    idt, params = torch.from_numpy(ids).to(DEV), small_ints(6, L.padded)
+    f = Flat(L, pl, vocab * cols, DEV, ints=True)
+    z.zero_embedding_grad(L, 1, idt, dy, f.acc, 1.0, flags, f.out)
+    g, _ = emb_exact(ids, f64(dy), vocab)
+    f.check(g, np.zeros(g.size), 1.0, flags, "table")
+    out = torch.empty(n, cols, dtype=torch.float32, device=DEV)
+    z.zero_embedding_lookup(L, 1, params, idt, out, 0.5)
+    rows = f64(params)[f.pos].reshape(vocab, cols)
+    real = (ids >= 0) & (ids < vocab)
+    assert np.array_equal(f64(out), np.where(real[:, None], rows[np.clip(ids, 0, vocab - 1)] * 0.5, 0.0))
+    L, pl = layout(cols, False, dim0_rows=cols)
+    f, h, r = Flat(L, pl, cols, DEV, ints=True), small_ints(7, n, cols), torch.ones(n, device=DEV)
+    z.zero_rms_norm_grad(L, 1, torch.ones(L.padded, dtype=BF16, device=DEV), dy, None, h, r,
+                         torch.empty(n, cols, dtype=BF16, device=DEV), f.acc, 1.0, flags, f.out)
+    f.check((f64(dy) * f64(h)).sum(0), np.zeros(cols), 1.0, flags, "norm")
+
+
+def test_an_empty_table_has_no_tokens():
+    L = z.Layout([0, 40], 0, 4, 0)
+    params, acc = torch.ones(L.padded, dtype=BF16, device=DEV), torch.ones(L.padded, device=DEV)
+    ids = torch.tensor([0, -1, 5], device=DEV)
+    out = torch.full((3, 8), 7.0, dtype=BF16, device=DEV)
+    z.zero_embedding_lookup(L, 0, params, ids, out)
+    assert not out.any()
+    z.zero_embedding_grad(L, 0, ids, out, acc, 1.0, z.ACC_OVERWRITE)
+    assert (acc == 1).all()
+
+
+@pytest.mark.parametrize("n,flags", [(300, 0), (900, 0), (20_000, 0), (900, z.ACC_OVERWRITE)])
+@pytest.mark.parametrize("cols", [37, 260])
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+def test_what_lies_in_places_without_a_token_is_not_used(n, flags, cols, dtype):
+    """NaN and infinities there, and ids that are valid in their low bits only."""
+    vocab = 50
+    L, pl = layout(vocab * cols, False)
+    ids = some_ids("uniform", n, vocab, 9)
+    no = np.arange(n) % 3 == 1
+    ids[no] = np.array([-1, 2 ** 32 + 4, -2 ** 63, 2 ** 63 - 1, vocab, -2 ** 32 + 7])[np.arange(no.sum()) % 6]
+    dy = small_ints(1, n, cols, dtype=dtype)
+    want, _ = emb_exact(np.where(no, -1, ids), f64(dy), vocab)
+    bad = torch.from_numpy(no).to(DEV)
+    dy[bad, ::2], dy[bad, 1::2] = float("nan"), float("inf")
+    f = Flat(L, pl, vocab * cols, DEV, ints=True)
+    z.zero_embedding_grad(L, 1, torch.from_numpy(ids).to(DEV), dy, f.acc, 1.0, flags)
+    f.check(want, np.zeros(want.size), 1.0, flags, "gradient")
+    params = torch.full((L.padded,), float("nan"), dtype=BF16, device=DEV)
+    out = torch.full((n, cols), 7.0, dtype=dtype, device=DEV)
+    z.zero_embedding_lookup(L, 1, params, torch.from_numpy(np.where(no, ids, -1)).to(DEV), out)
+    assert not out.any()
+
+
+def test_act8_of_the_smallest_and_largest_binary32_values():
+    """Around the smallest code value 2^-126, halves of it among them, and up to
+    the largest finite value, each in a block of its own."""
+    k = np.arange(1, 65, dtype=np.float64)
+    v = np.concatenate([k * 2.0 ** -130, (k + 0.5) * 2.0 ** -127, k * 2.0 ** -149,
+                        (2.0 - 2.0 ** -23) * 2.0 ** np.arange(-126, 128), 1.75 * 2.0 ** np.arange(-126, 128),
+                        (1.75 + 2.0 ** -22) * 2.0 ** np.arange(-126, 128)])
+    v = np.concatenate([v, -v]).astype(np.float32)
+    x = torch.from_numpy(v).view(-1, 1).to(DEV)
+    (q, e), out = codes_like(v.size, 1), torch.empty(v.size, 1, device=DEV)
+    z.zero_act8_pack(x, q, e)
+    z.zero_act8_unpack(q, e, out)
+    eq, ee = act8(v.astype(np.float64).reshape(-1, 1))
+    assert np.array_equal(e.cpu().numpy(), ee) and np.array_equal(q.cpu().numpy(), eq)
+    r = act8_values(eq, ee)
+    r = np.where(np.abs(r) == 2.0 ** 128, np.copysign(np.inf, r), r)
+    assert np.array_equal(f64(out), r)
