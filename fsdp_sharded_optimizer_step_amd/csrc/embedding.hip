@@ -20,7 +20,7 @@
 //          n ids, counts its own and those of lower slices, which gives its
 //          place in the order without talking to other blocks, and places its
 //          tokens in a second pass.  n ids are read from the L2 by S blocks:
-//          10 us for 16384 ids, 5 us for 1000.  Of more ids a slice's block
+//          12 us for 16384 ids, 6 us for 1000.  Of more ids a slice's block
 //          reads its own alone, put together by two launches before it (131072
 //          ids: 16 us in all, 80 without them).
 //   sums   an id of up to kPiece tokens is summed and added to its row of the
@@ -546,9 +546,9 @@ __device__ __forceinline__ int32_t piece_in_window(const GradArgs& A, int32_t to
 // thread, the blocks of a row one after another.  Nearly every id of a batch
 // occurs once, so the row's accumulator and its first token are requested
 // together, before any of the sum.  Measured for 16384 tokens of 4096 columns
-// and 12000 distinct ids (520 MB), all three kernels: 134 us (131 in runs, see
-// below); 8 columns per thread cost 18 us more, a row's blocks spread over the
-// grid 9, temporal accesses 5, pieces of 32 and 64 tokens 10 and 25.
+// and 12000 distinct ids (520 MB), all three kernels at 134 us (127 with what
+// came later): 8 columns per thread cost 18 us more, a row's blocks spread over
+// the grid 9, temporal accesses 5, pieces of 32 and 64 tokens 10 and 25.
 template <class DY, bool GAPS>
 __global__ void __launch_bounds__(kThreads) places_kernel(const GradArgs A) {
   const int32_t total = A.start[((int64_t)1 << A.slice_bits) * A.local];
@@ -581,11 +581,11 @@ __global__ void __launch_bounds__(kThreads) places_kernel(const GradArgs A) {
 // The same for rows of more than 124 columns: a wave takes 256 columns of kRun
 // places, of which only those that begin a row or a piece cost more than their
 // share of one load.  With threads for each place, those that found nothing to
-// do took most of the time where ids repeat: 12000 tokens of 4096 columns and
-// 600 ids 78 us in runs of 4, 96 one by one, 86 in twos, 74 in eights; 16384
-// tokens and 12000 ids 131, 130, 129 and 133 us; 65536 tokens of 768 columns
-// and 36651 ids 88 us in runs, 112 one by one (of 64 columns 32 and 28, which
-// is why narrow rows stay with the kernel above).
+// do took most of the time where ids repeat.  In runs of 4, one by one, in twos
+// and in eights (us): 12000 tokens of 4096 columns and 600 ids 52, 64, 56, 50;
+// 16384 tokens and 12700 ids 132, 130, 130, 133; 65536 tokens of 768 columns and
+// 36600 ids 88, 98, 90, 90; 131072 tokens 128, 155, 134, 127.  Narrow rows stay
+// with the kernel above: 65536 tokens of 64 columns took 28 us there, 32 here.
 // The places' entries lie in the first lanes, and all lanes read them, also
 // those past the row's end: a lane's registers are only sure to hold its values
 // for others while it is active itself.
@@ -667,8 +667,9 @@ __global__ void __launch_bounds__(kThreads) table_kernel(const GradArgs A) {
 }
 
 // row_out for a table that is written whole.  Where that is all (no sum read,
-// no bf16) it goes through the caches: 1.0 GB of zeros and 16384 rows take 440
-// us, 462 with non-temporal stores.
+// no bf16) it goes through the caches.  So, and with non-temporal stores (us, of
+// 16384 tokens): 128256 x 2048 218 and 228, 61036 x 4096 264 and 276, 32000 x
+// 8192 308 and 329, 50257 x 768 59 and 57.
 template <bool GAPS>
 __device__ __forceinline__ void table_out(const GradArgs& A, int64_t v, int32_t c0, int n, f32x4 s) {
   int64_t at;
@@ -683,7 +684,7 @@ __device__ __forceinline__ void table_out(const GradArgs& A, int64_t v, int32_t 
 // of which read the entries, as in wide_places_kernel): the waves
 // of the first piece_blocks blocks take a window each, the others table_rows
 // rows of the table, whose places and first tokens are requested together.
-// 16384 tokens, 50257 x 768, overwritten: 61 us, with a thread's rows one after
+// 16384 tokens, 50257 x 768, overwritten: 58 us, with a thread's rows one after
 // another, each with its three loads in turn, 71.
 template <class DY, bool GAPS>
 __global__ void __launch_bounds__(kThreads) wide_table_kernel(const GradArgs A) {
@@ -944,7 +945,10 @@ int64_t up16(int64_t n) { return (n + 15) & ~(int64_t)15; }
 // Up to this many tokens every slice's block reads all ids; more are dealt to
 // the slices first, which costs two launches, but where each id is read 3 times
 // instead of 512.  The whole call, 64 columns, direct and dealt: 16384 tokens
-// 17 and 23 us, 24576 25 and 23, 65536 48 and 29, 2^20 905 and 204.
+// 17 and 23 us, 24576 25 and 23, 65536 48 and 27, 2^20 905 and 203.
+// Tables of more than 2^18 rows have more than kMinSlices slices and are not
+// dealt: a row more costs 65536 tokens of 128 columns 84 us instead of 38, 2^20
+// tokens of 64 columns 1588 instead of 214.
 constexpr int64_t kMaxDirect = 16384;
 Plan make_plan(int64_t vocab, int64_t cols, int64_t n) {
   Plan p;
@@ -1024,8 +1028,9 @@ int launch_sums(const GradArgs& B, bool dense, hipStream_t s) {
     A.window_rows = pieces ? (uint32_t)std::min(windows, most) : 0u;
     A.piece_blocks = (unsigned)((A.window_rows * (int64_t)A.chunks.d + kWaves - 1) / kWaves);
     // 4 rows a wave, or fewer where that leaves less than three waves for each
-    // that the card holds at once (16384 tokens overwritten, 4, 2 and 1 rows:
-    // 50257 x 768 61, 64 and 71 us, 50257 x 256 49, 41 and 38)
+    // of the 8192 that the card's 256 CUs hold at once (16384 tokens overwritten,
+    // 4, 2 and 1 rows: 128256 x 2048 218, 277 and 334 us, 50257 x 768 59, 61 and
+    // 70, 20000 x 256 29, 26 and 27, 5000 x 256 25, 21 and 19)
     A.table_rows = 4;
     while (A.table_rows > 1 && A.vocab * A.chunks.d < A.table_rows * (int64_t)(3 * 8192)) A.table_rows /= 2;
     A.row_blocks = (uint32_t)std::min((A.vocab + A.table_rows - 1) / A.table_rows, most);

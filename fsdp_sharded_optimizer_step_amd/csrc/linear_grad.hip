@@ -275,16 +275,18 @@ __device__ __forceinline__ int64_t slot_of(const Args& A, int32_t tile, int32_t 
 // three ahead are requested.  One barrier a step, before its last stretch,
 // whose fragments are already in registers.
 //
-// Measured (16384 tokens, 14336 x 4096): 1.51 ms, 1275 TFLOP/s, against 1.88
-// ms of a library bf16 product of that shape alone.  The matrix cores are busy
-// two thirds of the cycles, at a clock that the load itself brings down to
-// 1.75 GHz: when it took 1.59 ms, it took 1.35 without the global loads, 1.42
-// without the LDS reads, 1.06 without either and without the LDS writes (for
-// timing only).  Requests two steps ahead instead of three take the same time;
-// fragments two stretches ahead spill at this tile (2.36 ms) and gain nothing
-// at the smaller one.  That one (4000 tokens, 1024 x 4096: 42-50 us) takes 10
-// us at the ends and 1.07 us for 128 tokens, in which the matrix cores and the
-// LDS are busy for about 0.45 us each.
+// Measured (16384 tokens, 14336 x 4096): 1.47 to 1.54 ms from card to card, 1310
+// to 1250 TFLOP/s, against 1.91 to 1.96 ms of a library bf16 product of that
+// shape alone.  The matrix cores are busy 71 % of the cycles, at a clock that the
+// load itself brings down to about 1.75 GHz: when it took 1.59 ms, it took 1.35
+// without the global loads, 1.42 without the LDS reads, 1.06 without either and
+// without the LDS writes (for timing only).  Requests two steps ahead instead of
+// three take the same time; fragments two stretches ahead spill at this tile
+// (2.36 ms) and gain nothing at the smaller one.  As it is, 32 of this tile's
+// registers are spilled, none of them inside the loop of whole steps.
+// The smaller tile (4000 tokens, 1024 x 4096: 41 us) takes 11 us at the ends and
+// 1.02 us for 128 tokens, in which the matrix cores and the LDS are busy for
+// about 0.45 us each.
 template <class S, bool TR>
 __global__ void __launch_bounds__(S::kThreads, 1) grad_kernel(const Args A) {
   constexpr int W = S::W, G = S::G, kSide = S::kSide, kStep = S::kStep;
@@ -476,8 +478,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) grad_kernel(const Args A) {
     // buffers are free), from where a lane gets 4 columns of a row; the
     // accumulator's values of the next strip are requested before this one's
     // are stored.  Single values from the registers to memory left half of its
-    // rate unused: 1024 tokens, 8192 x 8192, added 292 us, 239 here, emitted
-    // 292, 222; 16384 tokens, 14336 x 4096: 1537, 1501.
+    // rate unused: 1024 tokens, 8192 x 8192, added 294 us, 239 here, overwritten
+    // 231, 172; 16384 tokens, 14336 x 4096: 1541, 1499.
     constexpr int kCols = W * 32, kStride = kCols + 8;  // 4 rows are 32 banks apart
     constexpr int kAcross = kCols / 4, kDown = 64 / kAcross, kVecs = 32 / kDown;
     static_assert(S::kThreads / 64 * 32 * kStride * 4 <= 2 * kBuffer, "the strips fit the buffers");
@@ -620,7 +622,9 @@ struct Plan {
 // the tiles, fewer than 256, share the CUs, each tile's tokens being split
 // over as many blocks as there is room for, kMinSplit tokens each at least.
 // Where padding falls inside the tensor every tile goes through the
-// workspace, and the sum places it.
+// workspace, and the sum places it.  The number of CUs is the card's, and a
+// constant: the splits, and with them the order of a sum and the workspace's
+// size, follow from the sizes alone.
 constexpr int64_t kCus = 256, kMinSplit = 256, kGrain = 128, kMaxSplits = 32;
 
 template <class S>
@@ -661,9 +665,11 @@ Plan plan_for(bool direct, int64_t rows, int64_t cols, int64_t tokens) {
 
 // The larger tile does twice the products per byte of LDS, the smaller one
 // leaves fewer CUs idle and fewer sums to the workspace.  Measured, 256 against
-// 128 columns (us): 8192 tokens, 4096 x 4096: 235, 302; 16384 tokens, 1024 x
-// 4096: 135, 151; 4000 tokens, 1024 x 4096: 61, 48; 4096 tokens, 2048 x 2048:
-// 59, 46; 1024 tokens, 768 x 768: 28, 17.  The estimate tells them apart.
+// 128 columns (us): 8192 tokens, 4096 x 4096: 229, 288; 16384 tokens, 1024 x
+// 4096: 129, 135; 64 tokens, 4096 x 4096: 27, 34; 4000 tokens, 1024 x 4096: 57,
+// 41; 4096 tokens, 2048 x 2048: 57, 42; 1024 tokens, 768 x 768: 22, 15.  The
+// estimate takes the faster one in 14 of 15 sizes tried (not for 512 tokens, 8192
+// x 8192: 196, 186).
 Plan make_plan(const zero_layout* L, int32_t tensor, int64_t rows, int64_t cols, int64_t tokens) {
   int64_t lo, hi;
   const bool direct = make_place(L, tensor, &lo, &hi).gap == 0;

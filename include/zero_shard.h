@@ -457,11 +457,11 @@ int zero_step_scalars(const zero_adamw* hp, int64_t t, float out[8]);
  * stride argument are dense.  Any alignment is accepted.  No outputs may
  * overlap each other or an input; in particular nothing works in place.
  * A workspace (16-byte aligned, of the bytes that the call's _workspace
- * function gives for the same sizes; none where it gives 0) holds intermediate sums: its contents
- * before and after a call mean nothing, and two calls that may run at the
- * same time (or two captured graphs that may be replayed at the same time)
- * need a workspace each.  The _workspace functions run on the host only and
- * return bytes, or a negative status.
+ * function gives for the same sizes; none where it gives 0) holds intermediate
+ * sums: its contents before and after a call mean nothing, and two calls that
+ * may run at the same time (or two captured graphs that may be replayed at the
+ * same time) need a workspace each.  The _workspace functions run on the host
+ * only and return bytes, or a negative status.
  *
  * Sums have a fixed order: the same call gives the same bits every time.
  * Common errors: ZERO_EINVAL (null pointer, negative size, sizes that do not
@@ -506,9 +506,10 @@ int zero_act8_unpack(const uint8_t* codes_dev, const uint8_t* scales_dev, int64_
  * lookup: out[t] = scale * E[id_t] in binary32, rounded to out_dtype; a row of
  * zeros for a place without a token.
  * grad: dE[v] = sum over t with id_t = v, t ascending, of dY[t]: in pieces of
- * 16 tokens, then over the pieces.  Places without a token add nothing.  With
- * flags 0 only the rows of ids that occur are touched; OVERWRITE and
- * EMIT_BF16 cover every row of the table, absent ids having a zero gradient. */
+ * 16 tokens, then over the pieces (so the grouping depends on the ids).
+ * Places without a token add nothing.  With flags 0 only the rows of ids that
+ * occur are touched; OVERWRITE and EMIT_BF16 cover every row of the table,
+ * absent ids having a zero gradient. */
 int zero_embedding_lookup(const zero_layout* layout, int32_t tensor, int64_t cols,
                           const uint16_t* params_flat_dev, const void* ids_dev, int32_t id_bytes,
                           int64_t n_ids, float scale, void* out_dev, int64_t out_stride,
@@ -526,9 +527,10 @@ int zero_embedding_grad(const zero_layout* layout, int32_t tensor, int64_t cols,
  *
  * forward, for every row: h = bf16(x + res) (res NULL: h = x),
  *   rstd = 1 / sqrt(mean(h^2) + eps) in binary64 (stored in binary32), and
- *   h * w * rstd, in binary64 too, in the 8-bit format of zero_act8_pack.  h_dev: the new residual (may be NULL if res is);
- *   y_dev: NULL, or the bf16 values that the codes stand for, so that the
- *   forward product reads exactly what the backward product will.
+ *   h * w * rstd, in binary64 too, in the 8-bit format of zero_act8_pack.
+ *   h_dev: the new residual (may be NULL if res is); y_dev: NULL, or the bf16
+ *   values that the codes stand for, so that the forward product reads exactly
+ *   what the backward product will.  There is no unquantised output.
  * grad, for every row, with g = dy * w and n = h * rstd:
  *   dx = bf16(dh + rstd * (g - n * mean(g * n)))   (dh NULL: 0)
  *   which is the gradient of both x and res; the weight's gradient is the sum
@@ -552,8 +554,10 @@ int zero_rms_norm_grad(const zero_layout* layout, int32_t tensor, const uint16_t
  * dW[o, i] = sum over tokens t of dY[t, o] * X[t, i]; the tensor holds
  * (out_features, in_features), or with transposed = 1 (in_features,
  * out_features).  dY: bf16.  X: codes and scales of zero_act8_pack or
- * zero_rms_norm, tokens x in_features.  Products are exact, sums binary32 in
- * the matrix cores (their order depends on the sizes alone).  Weights of up to
+ * zero_rms_norm, tokens x in_features (an input kept in bf16 is packed first).
+ * Products are exact where binary32 holds them (no bit below 2^-149, not past
+ * its largest value), sums binary32 in the matrix cores (their order depends on
+ * the sizes alone).  Weights of up to
  * 2^35 elements are accepted, larger ones may be refused (ZERO_ERANGE). */
 int64_t zero_linear_grad_workspace(const zero_layout* layout, int32_t tensor, int32_t transposed,
                                    int64_t out_features, int64_t in_features, int64_t tokens);
