@@ -32,7 +32,8 @@ EXPORTS = ("zero_layout_create", "zero_layout_destroy", "zero_layout_psi", "zero
            "zero_layout_tensor_flat", "zero_act8_pack", "zero_act8_unpack",
            "zero_embedding_lookup", "zero_embedding_grad", "zero_embedding_grad_workspace",
            "zero_rms_norm", "zero_rms_norm_grad", "zero_rms_norm_grad_workspace",
-           "zero_linear_grad", "zero_linear_grad_workspace")
+           "zero_linear_grad", "zero_linear_grad_workspace", "zero_layout_moment_blocks",
+           "zero_shard_step_moments8", "zero_moments8_pack", "zero_moments8_unpack")
 
 
 class ZeroError(RuntimeError):
@@ -119,6 +120,12 @@ def load():
     lib.zero_linear_grad_workspace.argtypes = [vp, i32, i32, i64, i64, i64]
     lib.zero_linear_grad.argtypes = [vp, i32, i32, vp, i64, vp, vp, i64, i64, i64, f32, u32, vp, vp,
                                      vp, i64, vp]
+    lib.zero_layout_moment_blocks.argtypes = [vp]
+    lib.zero_layout_moment_blocks.restype = i64
+    lib.zero_shard_step_moments8.argtypes = [vp, C.POINTER(_AdamW), i64, i64, i64, C.POINTER(vp), i32,
+                                             i32, vp, vp, vp, vp, vp, vp, i32, C.c_uint64, vp]
+    lib.zero_moments8_pack.argtypes = [vp] * 8
+    lib.zero_moments8_unpack.argtypes = [vp] * 8
     for name in ("zero_embedding_grad_workspace", "zero_rms_norm_grad_workspace",
                  "zero_linear_grad_workspace"):
         getattr(lib, name).restype = i64
@@ -190,6 +197,7 @@ class Layout:
     n_d = property(lambda self: load().zero_layout_n_d(self._h))
     rank = property(lambda self: load().zero_layout_rank(self._h))
     kind = property(lambda self: load().zero_layout_kind(self._h))
+    moment_blocks = property(lambda self: load().zero_layout_moment_blocks(self._h))
 
     def bucket(self, b: int):
         """-> (stream_off, len, padded_off, padded_len, shard_off)"""
@@ -370,6 +378,96 @@ def zero_shard_step_accumulate(layout: Layout, hp: AdamW, t: int, rank_acc, rank
         grad_layout, _dev32(master, "master", ns), _dev32(exp_avg, "exp_avg", ns),
         _dev32(exp_avg_sq, "exp_avg_sq", ns), _dev16(param_out, "param_out", no), out_mode,
         _dev32(reduced_grad_out, "reduced_grad_out", ns), C.byref(opt), _stream_ptr(stream)))
+
+
+@dataclass
+class Moments8:
+    """Both moments of a shard in 8 bits: code bytes (S elements) and scale
+    bytes (layout.moment_blocks) of the first and of the second one, uint8."""
+    exp_avg: object
+    exp_avg_scales: object
+    exp_avg_sq: object
+    exp_avg_sq_scales: object
+
+    @staticmethod
+    def zeros(layout: Layout, device):
+        """Moments of zero."""
+        import torch
+        new = lambda n: torch.zeros(n, dtype=torch.uint8, device=device)  # noqa: E731
+        n, blocks = layout.shard, layout.moment_blocks
+        return Moments8(new(n), new(blocks), new(n), new(blocks))
+
+
+def _moments8(where, layout, moments):
+    """The four tensors, checked."""
+    torch = _types()[0]
+    n, blocks = layout.shard, layout.moment_blocks
+    ts = []
+    for name, need in (("exp_avg", n), ("exp_avg_scales", blocks), ("exp_avg_sq", n),
+                       ("exp_avg_sq_scales", blocks)):
+        t = getattr(moments, name)
+        _need(t, f"{where}: {name}", need)
+        if t.dtype != torch.uint8 or not t.is_contiguous():
+            raise ValueError(f"{where}: {name}: needs a contiguous uint8 tensor")
+        ts.append(t)
+    return ts
+
+
+def _whole(where, name, t, n, types):
+    """A contiguous tensor of n elements or more and one of those types."""
+    if t.dtype not in types:
+        raise _bad_type(where, name, t, types)
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {name}: needs a contiguous tensor")
+    _need(t, f"{where}: {name}", n)
+
+
+def zero_shard_step_moments8(layout: Layout, hp: AdamW, t: int, rank_grads, grad_layout: int, master,
+                             moments: Moments8, param_out, out_mode: int, seed: int,
+                             bucket_begin: int = 0, bucket_end: int | None = None, stream=None):
+    """zero_shard_step with both moments in 8 bits, rounded at random with bits
+    that `seed`, t and an element's place in the shard determine (seed: any 64
+    bits).  Contributions: 16-bit or float32 tensors, all of one type."""
+    me = "zero_shard_step_moments8"
+    torch, b16, _, _, _, f32 = _types()
+    if len(rank_grads) != layout.n_d:
+        raise ValueError(f"{me}: one contribution per rank is required")
+    ng, ns, no = _step_sizes(layout, grad_layout, out_mode)
+    wide = rank_grads[0].dtype == torch.float32
+    arr = (C.c_void_p * len(rank_grads))()
+    for q, g in enumerate(rank_grads):
+        _whole(me, f"rank_grads[{q}]", g, ng, f32 if wide else b16)
+        arr[q] = g.data_ptr()
+    _whole(me, "master", master, ns, f32)
+    _whole(me, "param_out", param_out, no, b16)
+    m = _moments8(me, layout, moments)
+    end = layout.n_buckets if bucket_end is None else bucket_end
+    _enqueue(me, stream, [master, param_out, *m, *rank_grads], lambda s, _: load().zero_shard_step_moments8(
+        layout.handle, C.byref(hp._c()), int(t), int(bucket_begin), int(end), arr, int(wide), grad_layout,
+        master.data_ptr(), *[x.data_ptr() for x in m], param_out.data_ptr(), out_mode,
+        int(seed) & 0xFFFFFFFFFFFFFFFF, s))
+
+
+def zero_moments8_pack(layout: Layout, exp_avg, exp_avg_sq, moments: Moments8, stream=None):
+    """float32 moments of a shard to 8 bits, rounded to the nearest code."""
+    me = "zero_moments8_pack"
+    f32 = _types()[5]
+    _whole(me, "exp_avg", exp_avg, layout.shard, f32)
+    _whole(me, "exp_avg_sq", exp_avg_sq, layout.shard, f32)
+    m = _moments8(me, layout, moments)
+    _enqueue(me, stream, [exp_avg, exp_avg_sq, *m], lambda s, _: load().zero_moments8_pack(
+        layout.handle, exp_avg.data_ptr(), exp_avg_sq.data_ptr(), *[x.data_ptr() for x in m], s))
+
+
+def zero_moments8_unpack(layout: Layout, moments: Moments8, exp_avg, exp_avg_sq, stream=None):
+    """The float32 values that the codes stand for."""
+    me = "zero_moments8_unpack"
+    f32 = _types()[5]
+    _whole(me, "exp_avg", exp_avg, layout.shard, f32)
+    _whole(me, "exp_avg_sq", exp_avg_sq, layout.shard, f32)
+    m = _moments8(me, layout, moments)
+    _enqueue(me, stream, [exp_avg, exp_avg_sq, *m], lambda s, _: load().zero_moments8_unpack(
+        layout.handle, *[x.data_ptr() for x in m], exp_avg.data_ptr(), exp_avg_sq.data_ptr(), s))
 
 
 def zero_gather_params(layout: Layout, rank_shards, full_out, bucket_begin: int = 0,

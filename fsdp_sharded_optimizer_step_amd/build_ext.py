@@ -7,7 +7,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libzero_shard.so")
-SOURCES = ["layout.cpp", "placement.cpp", "shard_step.hip", "pack_accumulate.hip",
+SOURCES = ["layout.cpp", "placement.cpp", "shard_step.hip", "shard_step8.hip", "pack_accumulate.hip",
            "gather_reshard.hip", "act8.hip", "embedding.hip", "rms_norm.hip", "linear_grad.hip"]
 
 # Floating point: no contraction into FMA, correctly rounded binary32 divide

@@ -30,16 +30,13 @@
 #include <cstdint>
 #include <vector>
 
+#include "adamw.hpp"
 #include "device_common.hpp"
 #include "layout.hpp"
 #include "zero_shard.h"
 
 namespace {
 using namespace zs;
-
-struct Scalars {
-  float s, rho, a_wd, B1, C1, B2, C2, E;
-};
 
 // The shard range [i0, i0 + n) of one launch and its flat addresses (used for
 // FLAT contributions and All-Gather slot stores).  Part 0, the first n0
@@ -94,16 +91,6 @@ __device__ __forceinline__ float average(float a, const Args& A) {
     return a * A.inv_nd;
   else
     return A.pow2 ? a * A.inv_nd : a / A.nd_f;
-}
-
-// The AdamW element update, binary32, one rounding per operation.
-__device__ __forceinline__ void adamw(float g, float& th, float& m, float& v, const Scalars& k) {
-  const float m1 = k.B1 * m + k.C1 * g;
-  const float v1 = k.B2 * v + k.C2 * (g * g);
-  const float d = __builtin_sqrtf(v1) * k.rho + k.E;
-  th = k.a_wd * th - k.s * (m1 / d);
-  m = m1;
-  v = v1;
 }
 
 // 8 contributions of one rank, two pieces of 4 consecutive elements (a:
@@ -795,28 +782,6 @@ Span span(const void* p, int64_t bytes) {
   return Span{(uintptr_t)p, (uintptr_t)p + (uintptr_t)(bytes > 0 ? bytes : 0)};
 }
 bool overlaps(Span a, Span b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
-
-bool hp_ok(const zero_adamw& hp) {
-  return std::isfinite(hp.lr) && std::isfinite(hp.eps) && std::isfinite(hp.weight_decay) &&
-         std::isfinite(hp.beta1) && std::isfinite(hp.beta2) && hp.beta1 >= 0.0 &&
-         hp.beta1 < 1.0 && hp.beta2 >= 0.0 && hp.beta2 < 1.0;
-}
-
-// Per-call scalars: binary64, each rounded once to binary32.
-Scalars make_scalars(const zero_adamw& hp, int64_t t) {
-  const double bc1 = 1.0 - std::pow(hp.beta1, (double)t);
-  const double bc2 = 1.0 - std::pow(hp.beta2, (double)t);
-  Scalars k;
-  k.s = (float)(hp.lr / bc1);
-  k.rho = (float)(1.0 / std::sqrt(bc2));
-  k.a_wd = (float)(1.0 - hp.lr * hp.weight_decay);
-  k.B1 = (float)hp.beta1;
-  k.C1 = (float)(1.0 - hp.beta1);
-  k.B2 = (float)hp.beta2;
-  k.C2 = (float)(1.0 - hp.beta2);
-  k.E = (float)hp.eps;
-  return k;
-}
 
 struct LaunchShape {
   int threads = 0, blocks_cap = 0, path = 0;  // 0: the policy's choice

@@ -348,6 +348,73 @@ int zero_shard_step_buckets(const zero_layout* layout, const zero_adamw* hp, int
                             float* reduced_grad_out_dev, const zero_step_options* opt,
                             hipStream_t stream);
 
+/* ------------------------------------------- shard step with 8-bit moments
+ * ("Zero Redundancy Optimizer (ZeRO)": the optimizer state, k = 12 bytes per
+ * parameter, is what a rank holds most of; here k = 6.)
+ *
+ * The update of zero_shard_step with both moments kept in 8 bits: 2*n_d + 14
+ * bytes moved per shard element instead of 2*n_d + 26 (bf16 contributions).
+ *
+ * Format.  Every bucket's slice is cut into blocks of 128 elements
+ * (ZERO_ACT8_BLOCK; the last may be shorter); zero_layout_moment_blocks gives
+ * their number over the whole shard.  A moment is S code bytes in shard order
+ * and one scale byte e for each block, buckets in order.
+ *   exp_avg:    the e4m3 codes and scale bytes of zero_act8_pack (e of 10 to 247).
+ *   exp_avg_sq: a code c of 0 to 254 stands for f(c) * 2^(e-127), f(c) =
+ *     c * 2^-18 below 16, (1 + (c%16)/16) * 2^(c/16 - 15) from there on; 255 is
+ *     a NaN.  With a = m*2^k (1 <= m < 2) the block's largest finite value,
+ *     e = 127 + k + (m > 1.875 ? 1 : 0), at least 19 and at most 253 (values
+ *     past 1.875 * 2^126 saturate).
+ * Bytes of zero everywhere are moments of zero.
+ *
+ * Rounding.  m' and v' (binary32, as in zero_shard_step; the parameter's
+ * update uses them as they are) are rounded to codes at random: with u =
+ * |value| / 2^(e-127) in units of its code's lowest bit (units of the smallest
+ * code for smaller ones, where u is first rounded to 20 fraction bits, 19 for
+ * exp_avg_sq), the code is floor(u + (r + 0.5) / 65536), the largest code at
+ * most.  A positive v' keeps a code of 1 at least.  Infinities and NaN become
+ * NaN codes and do not count for the scale.  The expected value is the moment,
+ * also where it changes by less than the distance of two codes.
+ * r are 16 bits for each element: the lower (exp_avg) and upper half
+ * (exp_avg_sq) of h, in 32-bit arithmetic, i the shard index,
+ *   h = lo32(i) * 0x9E3779B1 + hi32(i) * 0x85EBCA77 + k0
+ *   h = (h ^ (h >> 16)) * 0xC2B2AE3D + k1;  h = (h ^ (h >> 15)) * 0x27D4EB2F
+ *   h = h ^ (h >> 16)
+ * with k0 and k1 the lower and upper half of x: x = seed ^ (t *
+ * 0x9E3779B97F4A7C15), twice x = (x ^ (x >> 32)) * 0xD6E8FEB86659FD93, then
+ * x = x ^ (x >> 32), in 64 bits.  The same arguments give the same bits.
+ *
+ * grad_dtype: ZERO_DTYPE_BF16 or ZERO_DTYPE_F32, the contributions' type.
+ * Buckets [bucket_begin, bucket_end) are stepped (zero_shard_step_buckets);
+ * all buffers are whole ones.  m_codes_dev, v_codes_dev: S bytes;
+ * m_scales_dev, v_scales_dev: zero_layout_moment_blocks bytes; updated in
+ * place.  The other arguments and the errors are those of
+ * zero_shard_step_buckets.  Vectors go to any alignment. */
+int64_t zero_layout_moment_blocks(const zero_layout* layout); /* -1 for a null layout */
+
+int zero_shard_step_moments8(const zero_layout* layout, const zero_adamw* hp, int64_t t,
+                             int64_t bucket_begin, int64_t bucket_end,
+                             const void* const* rank_grads_dev, int32_t grad_dtype,
+                             int32_t grad_layout, float* master_dev, uint8_t* m_codes_dev,
+                             uint8_t* m_scales_dev, uint8_t* v_codes_dev, uint8_t* v_scales_dev,
+                             uint16_t* param_out_dev, int32_t out_mode, uint64_t seed,
+                             hipStream_t stream);
+
+/* binary32 moments (S floats each) to 8 bits, rounded to the nearest code (ties
+ * to even; a negative second moment counts as zero), and the values that codes
+ * stand for back to binary32, exactly: to start from a binary32 state, to save
+ * one, or to re-cut it for another layout (unpack, zero_reshard, pack).
+ * pack of what unpack gave restores values, except where a lowered scale
+ * byte's limits intervene.  Errors: ZERO_EINVAL, ZERO_ERANGE (more than 2^39
+ * elements), ZERO_EOVERLAP, ZERO_EHIP. */
+int zero_moments8_pack(const zero_layout* layout, const float* exp_avg_dev,
+                       const float* exp_avg_sq_dev, uint8_t* m_codes_dev, uint8_t* m_scales_dev,
+                       uint8_t* v_codes_dev, uint8_t* v_scales_dev, hipStream_t stream);
+int zero_moments8_unpack(const zero_layout* layout, const uint8_t* m_codes_dev,
+                         const uint8_t* m_scales_dev, const uint8_t* v_codes_dev,
+                         const uint8_t* v_scales_dev, float* exp_avg_dev, float* exp_avg_sq_dev,
+                         hipStream_t stream);
+
 /* --------------------------------------------------------- parameter gather
  * ("Zero Redundancy Optimizer (ZeRO)": ZeRO-1/2 All-Gather the updated
  * parameters after the step; ZeRO-3 All-Gathers each layer's parameters
