@@ -33,7 +33,9 @@ EXPORTS = ("zero_layout_create", "zero_layout_destroy", "zero_layout_psi", "zero
            "zero_embedding_lookup", "zero_embedding_grad", "zero_embedding_grad_workspace",
            "zero_rms_norm", "zero_rms_norm_grad", "zero_rms_norm_grad_workspace",
            "zero_linear_grad", "zero_linear_grad_workspace", "zero_layout_moment_blocks",
-           "zero_shard_step_moments8", "zero_moments8_pack", "zero_moments8_unpack")
+           "zero_shard_step_moments8", "zero_moments8_pack", "zero_moments8_unpack",
+           "zero_head_norm_rotate", "zero_head_norm_rotate_grad",
+           "zero_head_norm_rotate_grad_workspace")
 
 
 class ZeroError(RuntimeError):
@@ -45,6 +47,22 @@ class ZeroError(RuntimeError):
 class _AdamW(C.Structure):
     _fields_ = [("lr", C.c_double), ("beta1", C.c_double), ("beta2", C.c_double),
                 ("eps", C.c_double), ("weight_decay", C.c_double)]
+
+
+class _View(C.Structure):
+    _fields_ = [("data_dev", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class _Heads(C.Structure):
+    _fields_ = [("tensor", C.c_int32), ("heads", C.c_int32), ("x", _View), ("dy", _View), ("out", _View)]
+
+
+MAX_AXES = 4
+
+
+class _Rotation(C.Structure):
+    _fields_ = [("positions_dev", C.c_void_p), ("freqs_dev", C.c_void_p), ("position_bytes", C.c_int32),
+                ("n_axes", C.c_int32), ("sections", C.c_int32 * MAX_AXES), ("interleaved", C.c_int32)]
 
 
 DTYPE_BF16, DTYPE_F32 = 0, 1
@@ -126,8 +144,13 @@ def load():
                                              i32, vp, vp, vp, vp, vp, vp, i32, C.c_uint64, vp]
     lib.zero_moments8_pack.argtypes = [vp] * 8
     lib.zero_moments8_unpack.argtypes = [vp] * 8
+    heads, turn = C.POINTER(_Heads), C.POINTER(_Rotation)
+    lib.zero_head_norm_rotate.argtypes = [vp, vp, i64, i32, C.c_double, turn, heads, heads, vp]
+    lib.zero_head_norm_rotate_grad_workspace.argtypes = [vp, i64, i32, heads, heads]
+    lib.zero_head_norm_rotate_grad.argtypes = [vp, vp, i64, i32, C.c_double, turn, heads, heads, f32, u32,
+                                               vp, vp, vp, i64, vp]
     for name in ("zero_embedding_grad_workspace", "zero_rms_norm_grad_workspace",
-                 "zero_linear_grad_workspace"):
+                 "zero_linear_grad_workspace", "zero_head_norm_rotate_grad_workspace"):
         getattr(lib, name).restype = i64
     lib.zero_strerror.argtypes = [C.c_int]
     lib.zero_strerror.restype = C.c_char_p
@@ -805,4 +828,139 @@ def zero_linear_grad(layout: Layout, tensor: int, dy, codes, scales, acc, scale:
         return lib.zero_linear_grad(
             layout.handle, tensor, tr, dy.data_ptr(), stride, codes.data_ptr(), scales.data_ptr(),
             tokens, o, i, scale, flags, _ptr(acc), _ptr(bf16_out), _ptr(ws), _size(ws), s)
+    _enqueue(me, stream, used, call)
+
+
+@dataclass
+class Rotation:
+    """What turns the pairs of a head's columns: positions (tokens) or (axes,
+    tokens), int32 or int64; freqs: float64, radians a position, one for each
+    pair; sections: pairs of each axis, in order (None: one axis).
+    interleaved: a pair is two neighbouring columns instead of two that lie
+    half the turning columns apart."""
+    positions: object
+    freqs: object
+    sections: object = None
+    interleaved: bool = False
+
+
+def _rotation(where, turn, tokens, used):
+    """(C structure or None, to be kept until the call), the tensors added to
+    `used`."""
+    if turn is None:
+        return None
+    torch, _, _, whole, _, _ = _types()
+    p, f = turn.positions, turn.freqs
+    axes = 1 if p.dim() == 1 else p.shape[0]
+    sections = [f.numel()] if turn.sections is None else [int(n) for n in turn.sections]
+    if len(sections) != axes or axes > MAX_AXES or any(n < 0 for n in sections):
+        raise ValueError(f"{where}: sections {sections} do not fit {axes} axes of positions "
+                         f"(at most {MAX_AXES})")
+    _dense(where, "positions", p, (tokens,) if p.dim() == 1 else (axes, tokens), whole)
+    _dense(where, "freqs", f, (sum(sections),), (torch.float64,))
+    used += [p, f]
+    return C.byref(_Rotation(p.data_ptr(), f.data_ptr(), p.element_size(), axes,
+                             (C.c_int32 * MAX_AXES)(*sections), int(turn.interleaved)))
+
+
+_no_view = _View(None, 0, 0)
+
+
+def _view(where, name, t, shape, used):
+    """A (tokens, heads, columns) tensor whose columns are adjacent."""
+    _, b16, _, _, _, _ = _types()
+    if t.dtype not in b16:
+        raise _bad_type(where, name, t, b16)
+    if t.shape != shape:
+        raise ValueError(f"{where}: {name}: needs shape {tuple(shape)}, got {tuple(t.shape)}")
+    if shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{where}: {name}: columns are not adjacent (strides {t.stride()})")
+    used.append(t)
+    return _View(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _side(where, layout, name, tensor, x, dy, out, used):
+    """zero_heads of the queries or the keys (None: neither)."""
+    if out is None:
+        if x is not None or dy is not None:
+            raise ValueError(f"{where}: {name}: has no output")
+        return None
+    if out.dim() != 3:
+        raise ValueError(f"{where}: {name}: needs (tokens, heads, columns)")
+    if tensor is not None:
+        _numel(where, layout, tensor)
+    h = _Heads(-1 if tensor is None else tensor, out.shape[1], _no_view, _no_view,
+               _view(where, name + " output", out, out.shape, used))
+    if x is not None:
+        h.x = _view(where, name, x, out.shape, used)
+    if dy is not None:
+        h.dy = _view(where, name + " gradient", dy, out.shape, used)
+    return h
+
+
+def _shape3(where, q, k):
+    t = q if q is not None else k
+    if t is None:
+        raise ValueError(f"{where}: neither queries nor keys")
+    if q is not None and k is not None and (q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0]
+                                            or q.shape[2] != k.shape[2]):
+        raise ValueError(f"{where}: queries {tuple(q.shape)} and keys {tuple(k.shape)} differ in tokens or columns")
+    if t.dim() != 3:
+        raise ValueError(f"{where}: needs (tokens, heads, columns)")
+    return t.shape[0], t.shape[2]
+
+
+def zero_head_norm_rotate(layout: Layout, q_tensor, k_tensor, params, q, k, eps: float, rotation,
+                          q_out, k_out, stream=None):
+    """Norm of every query and key head by the weights q_tensor and k_tensor of
+    the gathered flat buffer `params` (None: no norm), then the rotation
+    (None: none).  q, k (either may be None with its output): (tokens, heads,
+    columns) bfloat16, any strides with adjacent columns."""
+    me = "zero_head_norm_rotate"
+    _, b16, _, _, _, _ = _types()
+    tokens, cols = _shape3(me, q_out, k_out)
+    used = []
+    sides = [_side(me, layout, n, w, x, None, o, used)
+             for n, w, x, o in (("q", q_tensor, q, q_out), ("k", k_tensor, k, k_out))]
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise ValueError(f"{me}: an input without its output, or an output without its input")
+    if any(s is not None and s.tensor >= 0 for s in sides):
+        _flat(me, "params", params, layout, b16)
+        used.append(params)
+    turn = _rotation(me, rotation, tokens, used)
+    sides = [None if s is None else C.byref(s) for s in sides]
+    _enqueue(me, stream, used, lambda s, _: load().zero_head_norm_rotate(
+        layout.handle, _ptr(params), tokens, cols, eps, turn, *sides, s))
+
+
+def zero_head_norm_rotate_grad(layout: Layout, q_tensor, k_tensor, params, dq, dk, q, k, eps: float,
+                               rotation, q_dx, k_dx, acc=None, scale: float = 1.0, flags: int = 0,
+                               bf16_out=None, workspace=None, stream=None):
+    """The gradients q_dx and k_dx of the forward pass's q and k (which a side
+    without a norm does not need) from dq and dk; the weights' gradients,
+    scaled, into `acc` / `bf16_out` (added up where q_tensor is k_tensor)."""
+    me = "zero_head_norm_rotate_grad"
+    _, b16, _, _, _, _ = _types()
+    tokens, cols = _shape3(me, q_dx, k_dx)
+    used = []
+    sides = []
+    for n, w, x, dy, o in (("q", q_tensor, q, dq, q_dx), ("k", k_tensor, k, dk, k_dx)):
+        s = _side(me, layout, n, w, x if w is not None else None, dy, o, used)
+        if s is not None and (dy is None or (w is not None and x is None)):
+            raise ValueError(f"{me}: {n}: its gradient or its input is missing")
+        sides.append(s)
+    if any(s is not None and s.tensor >= 0 for s in sides):
+        _flat(me, "params", params, layout, b16)
+        used.append(params)
+        used += _grad_args(me, layout, acc, flags, bf16_out)
+    turn = _rotation(me, rotation, tokens, used)
+    sides = [None if s is None else C.byref(s) for s in sides]
+    lib = load()
+
+    def call(s, device):
+        ws = _workspace(me, workspace, lib.zero_head_norm_rotate_grad_workspace(
+            layout.handle, tokens, cols, *sides), device)
+        return lib.zero_head_norm_rotate_grad(
+            layout.handle, _ptr(params), tokens, cols, eps, turn, *sides, scale, flags, _ptr(acc),
+            _ptr(bf16_out), _ptr(ws), _size(ws), s)
     _enqueue(me, stream, used, call)

@@ -616,6 +616,67 @@ int zero_rms_norm_grad(const zero_layout* layout, int32_t tensor, const uint16_t
                        float* acc_flat_dev, uint16_t* bf16_flat_dev, void* workspace_dev,
                        int64_t workspace_bytes, hipStream_t stream);
 
+/* Norm of query and key heads, and their rotation by position, in one pass.
+ *
+ * q and k (either may be NULL, or have no heads) hold rows of head_dim columns
+ * (at most ZERO_MAX_HEAD_DIM), one for each token and head, at
+ * data_dev + t*token_stride + h*head_stride (bf16, strides in elements), so
+ * that parts of one projection's output, or outputs with the heads in front,
+ * need no copy.  The rows of an output must not meet; two outputs may take
+ * turns in one buffer (equal token strides, or equal head strides).
+ *
+ * forward, for every row x, out from x (dy is not used):
+ *   u = x * w / sqrt(mean(x^2) + eps), w the head_dim elements of `tensor`
+ *   (tensor -1: u = x, no norm), then for every pair j of columns (a, b)
+ *   out_a = u_a cos - u_b sin, out_b = u_a sin + u_b cos,
+ *   angle = positions[axis(j)][t] * freqs[j]; bf16(out).
+ *   Pairs: R/2 = the sum of `sections` (R <= head_dim); columns (j, j + R/2), or
+ *   with interleaved = 1 (2j, 2j + 1); columns from R on do not turn.  The
+ *   first sections[0] pairs turn by axis 0, the next sections[1] by axis 1, and
+ *   so on (time, height, width).  rotation NULL, or without pairs: no rotation.
+ *   positions_dev: n_axes x tokens signed numbers of position_bytes (4 or 8)
+ *   bytes; freqs_dev: R/2 binary64 values, radians a position.  Angles are
+ *   binary64; rows binary32 (so are their squares: mean(x^2) up to 3e38).
+ * grad, for every row, out = dx from dy and the forward pass's x:
+ *   u' = dy turned back; g = u'*w, n = x/rms: dx = bf16((g - n*mean(g*n))/rms);
+ *   without a norm dx = bf16(u'), and x is not read.  The gradient of the
+ *   weight, the sum over tokens and heads of u'*n, goes into the flat buffers
+ *   as `scale` and `flags` say; where q and k name one tensor it is their sum.
+ *   The acc_flat_dev and bf16_flat_dev rules are those above; with no norm
+ *   neither is used.
+ * Common errors, and ZERO_EINVAL for a tensor of another size than head_dim,
+ * more than head_dim / 2 pairs, an output whose rows meet; ZERO_ERANGE for more
+ * than ZERO_MAX_HEADS heads or an operand over 2^50 elements. */
+#define ZERO_MAX_HEAD_DIM 512
+#define ZERO_MAX_HEADS (1 << 14)
+#define ZERO_MAX_AXES 4
+typedef struct {
+  void* data_dev;
+  int64_t token_stride, head_stride;
+} zero_head_view;
+typedef struct {
+  int32_t tensor, heads;
+  zero_head_view x, dy, out;
+} zero_heads;
+typedef struct {
+  const void* positions_dev;
+  const double* freqs_dev;
+  int32_t position_bytes, n_axes, sections[ZERO_MAX_AXES], interleaved;
+} zero_rotation;
+int zero_head_norm_rotate(const zero_layout* layout, const uint16_t* params_flat_dev,
+                          int64_t tokens, int32_t head_dim, double eps,
+                          const zero_rotation* rotation, const zero_heads* q,
+                          const zero_heads* k, hipStream_t stream);
+int64_t zero_head_norm_rotate_grad_workspace(const zero_layout* layout, int64_t tokens,
+                                             int32_t head_dim, const zero_heads* q,
+                                             const zero_heads* k);
+int zero_head_norm_rotate_grad(const zero_layout* layout, const uint16_t* params_flat_dev,
+                               int64_t tokens, int32_t head_dim, double eps,
+                               const zero_rotation* rotation, const zero_heads* q,
+                               const zero_heads* k, float scale, uint32_t flags,
+                               float* acc_flat_dev, uint16_t* bf16_flat_dev, void* workspace_dev,
+                               int64_t workspace_bytes, hipStream_t stream);
+
 /* A linear weight's gradient from an 8-bit checkpoint of the layer's input.
  *
  * dW[o, i] = sum over tokens t of dY[t, o] * X[t, i]; the tensor holds
