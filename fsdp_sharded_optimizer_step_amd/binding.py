@@ -35,7 +35,9 @@ EXPORTS = ("zero_layout_create", "zero_layout_destroy", "zero_layout_psi", "zero
            "zero_linear_grad", "zero_linear_grad_workspace", "zero_layout_moment_blocks",
            "zero_shard_step_moments8", "zero_moments8_pack", "zero_moments8_unpack",
            "zero_head_norm_rotate", "zero_head_norm_rotate_grad",
-           "zero_head_norm_rotate_grad_workspace")
+           "zero_head_norm_rotate_grad_workspace", "zero_linear", "zero_linear_workspace",
+           "zero_linear_input_grad", "zero_linear_input_grad_workspace", "zero_bias_grad",
+           "zero_bias_grad_workspace")
 
 
 class ZeroError(RuntimeError):
@@ -149,8 +151,17 @@ def load():
     lib.zero_head_norm_rotate_grad_workspace.argtypes = [vp, i64, i32, heads, heads]
     lib.zero_head_norm_rotate_grad.argtypes = [vp, vp, i64, i32, C.c_double, turn, heads, heads, f32, u32,
                                                vp, vp, vp, i64, vp]
+    lib.zero_linear_workspace.argtypes = [vp, i32, i32, vp, vp, i64, i64, i64, i64]
+    lib.zero_linear.argtypes = [vp, i32, i32, i32, vp, vp, i64, i64, i64, i64, i32, vp, i64, vp, i64, i32,
+                                vp, vp, i64, vp]
+    lib.zero_linear_input_grad_workspace.argtypes = [vp, i32, i32, vp, vp, i64, i64, i64, i64]
+    lib.zero_linear_input_grad.argtypes = [vp, i32, i32, vp, vp, i64, i64, i64, i64, i32, vp, vp, i64, vp,
+                                           i64, vp, i64, vp]
+    lib.zero_bias_grad_workspace.argtypes = [vp, i32, i64]
+    lib.zero_bias_grad.argtypes = [vp, i32, vp, i64, vp, i32, i64, f32, u32, vp, vp, vp, vp, i64, vp]
     for name in ("zero_embedding_grad_workspace", "zero_rms_norm_grad_workspace",
-                 "zero_linear_grad_workspace", "zero_head_norm_rotate_grad_workspace"):
+                 "zero_linear_grad_workspace", "zero_head_norm_rotate_grad_workspace",
+                 "zero_linear_workspace", "zero_linear_input_grad_workspace", "zero_bias_grad_workspace"):
         getattr(lib, name).restype = i64
     lib.zero_strerror.argtypes = [C.c_int]
     lib.zero_strerror.restype = C.c_char_p
@@ -962,5 +973,122 @@ def zero_head_norm_rotate_grad(layout: Layout, q_tensor, k_tensor, params, dq, d
             layout.handle, tokens, cols, *sides), device)
         return lib.zero_head_norm_rotate_grad(
             layout.handle, _ptr(params), tokens, cols, eps, turn, *sides, scale, flags, _ptr(acc),
+            _ptr(bf16_out), _ptr(ws), _size(ws), s)
+    _enqueue(me, stream, used, call)
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def _activation(where, name):
+    if name not in ACTIVATIONS:
+        raise ValueError(f"{where}: activation {name!r} is not one of {sorted(ACTIVATIONS)}")
+    return ACTIVATIONS[name]
+
+
+def _activation_of(where, name, pre):
+    """The activation's number; pre has to be there exactly where it is needed."""
+    if (name != "none") != (pre is not None):
+        raise ValueError(f"{where}: pre goes with an activation, and only with one")
+    return _activation(where, name)
+
+
+def zero_linear(layout: Layout, tensor: int, params, x, out, bias=None, activation: str = "none",
+                res=None, pre=None, transposed: bool = False, workspace=None, stream=None):
+    """out = act(x W^T + b) + res with the weight `tensor` and the bias `bias`
+    (a tensor's index, or None) of the gathered flat buffer `params`.
+    x: (tokens, in_features), res: (tokens, out_features) or None, bfloat16;
+    out: (tokens, out_features), bfloat16 or float32; pre: None, or a
+    bfloat16 tensor that receives x W^T + b.  activation: none, relu, gelu,
+    gelu_tanh or silu.  transposed: the weight is (in_features,
+    out_features)."""
+    me = "zero_linear"
+    torch, b16, _, _, real, _ = _types()
+    if x.dim() != 2 or out.dim() != 2:
+        raise ValueError(f"{me}: x and out need two dimensions")
+    (tokens, i), o = x.shape, out.shape[1]
+    act = _activation(me, activation)
+    xs, os_ = _matrix(me, "x", x, tokens, i, b16), _matrix(me, "out", out, tokens, o, real)
+    used, rs = [params, x, out], 0
+    if res is not None:
+        rs = _matrix(me, "res", res, tokens, o, b16)
+        used.append(res)
+    if pre is not None:
+        _dense(me, "pre", pre, (tokens, o), b16)
+        used.append(pre)
+    _numel(me, layout, tensor)
+    if bias is not None:
+        _numel(me, layout, bias)
+    _flat(me, "params", params, layout, b16)
+    tr = int(transposed)
+    lib = load()
+
+    def call(s, device):
+        ws = _workspace(me, workspace, lib.zero_linear_workspace(
+            layout.handle, tensor, tr, params.data_ptr(), x.data_ptr(), xs, tokens, o, i), device)
+        return lib.zero_linear(
+            layout.handle, tensor, tr, -1 if bias is None else bias, params.data_ptr(), x.data_ptr(), xs, tokens,
+            o, i, act, _ptr(res), rs, out.data_ptr(), os_, int(out.dtype == torch.float32), _ptr(pre), _ptr(ws),
+            _size(ws), s)
+    _enqueue(me, stream, used, call)
+
+
+def zero_linear_input_grad(layout: Layout, tensor: int, params, dy, dx, activation: str = "none", pre=None,
+                           add=None, transposed: bool = False, workspace=None, stream=None):
+    """dx = (dy W + add) * act'(pre): the gradient of what went into the
+    activation that made the layer's input (pre: (tokens, in_features), as
+    zero_linear kept it), or of the input itself.  dy: (tokens, out_features);
+    add: None, or a gradient that the input has from elsewhere; bfloat16."""
+    me = "zero_linear_input_grad"
+    _, b16, _, _, _, _ = _types()
+    if dy.dim() != 2 or dx.dim() != 2:
+        raise ValueError(f"{me}: dy and dx need two dimensions")
+    (tokens, o), i = dy.shape, dx.shape[1]
+    act = _activation_of(me, activation, pre)
+    ys, xs = _matrix(me, "dy", dy, tokens, o, b16), _matrix(me, "dx", dx, tokens, i, b16)
+    used, as_ = [params, dy, dx], 0
+    if add is not None:
+        as_ = _matrix(me, "add", add, tokens, i, b16)
+        used.append(add)
+    if pre is not None:
+        _dense(me, "pre", pre, (tokens, i), b16)
+        used.append(pre)
+    _numel(me, layout, tensor)
+    _flat(me, "params", params, layout, b16)
+    tr = int(transposed)
+    lib = load()
+
+    def call(s, device):
+        ws = _workspace(me, workspace, lib.zero_linear_input_grad_workspace(
+            layout.handle, tensor, tr, params.data_ptr(), dy.data_ptr(), ys, tokens, o, i), device)
+        return lib.zero_linear_input_grad(
+            layout.handle, tensor, tr, params.data_ptr(), dy.data_ptr(), ys, tokens, o, i, act, _ptr(pre), _ptr(add),
+            as_, dx.data_ptr(), xs, _ptr(ws), _size(ws), s)
+    _enqueue(me, stream, used, call)
+
+
+def zero_bias_grad(layout: Layout, tensor: int, dy, acc, scale: float = 1.0, flags: int = 0, bf16_out=None,
+                   activation: str = "none", pre=None, dpre=None, workspace=None, stream=None):
+    """g = dy * act'(pre) (dy without an activation) into dpre (or None), and
+    its sum over the rows, the bias's gradient, scaled, into `acc` /
+    `bf16_out`.  dy, pre, dpre: (rows, cols) bfloat16."""
+    me = "zero_bias_grad"
+    _, b16, _, _, _, _ = _types()
+    cols = _numel(me, layout, tensor)
+    rows = dy.shape[0] if dy.dim() == 2 else -1
+    act = _activation_of(me, activation, pre)
+    ys = _matrix(me, "dy", dy, rows, cols, b16)
+    used = [dy]
+    for name, t in (("pre", pre), ("dpre", dpre)):
+        if t is not None:
+            _dense(me, name, t, (rows, cols), b16)
+            used.append(t)
+    used += _grad_args(me, layout, acc, flags, bf16_out)
+    lib = load()
+
+    def call(s, device):
+        ws = _workspace(me, workspace, lib.zero_bias_grad_workspace(layout.handle, tensor, rows), device)
+        return lib.zero_bias_grad(
+            layout.handle, tensor, dy.data_ptr(), ys, _ptr(pre), act, rows, scale, flags, _ptr(dpre), _ptr(acc),
             _ptr(bf16_out), _ptr(ws), _size(ws), s)
     _enqueue(me, stream, used, call)

@@ -1,0 +1,727 @@
+// zero_linear and zero_linear_input_grad: products with a weight that lies in
+// the flat buffer of gathered parameters.
+//
+// Page "Infra: Data Parallel" (pufanyi.com), section "Zero Redundancy
+// Optimizer (ZeRO)": parameters are gathered before forward and backward; the
+// products read them where the gather put them.
+//
+//   forward     pre = x W^T + b;  out = act(pre) + res
+//   input grad  dx = (dy W + add) * act'(pre)
+//
+// Both are C[m, n] = sum over k of A[m, k] * B(k, n), m a token, A (x or dy)
+// with k adjacent.  B has k adjacent where the weight is kept as (out, in)
+// and x is multiplied, or (in, out) and dy; n adjacent in the other two.
+//
+// A block's tiles of A and B go from memory straight to LDS, 16 bytes a lane,
+// two buffers of 64 k in turn: the next buffer but one is requested as soon as
+// every wave has read this one.  A request puts a wave's 1024 bytes next to
+// each other in LDS, 8 rows of 128 bytes; which 16 bytes of its row a lane
+// fetches is permuted, so that the rows that a fragment read meets at a time
+// use all banks.  A fragment of k adjacent is one 16-byte read a lane, one
+// of n adjacent two transposing reads of 8 bytes.  Products of bf16 are exact
+// in binary32, sums are binary32.
+//
+// Requests of 16 bytes need addresses of 16 bytes and rows of whole chunks.
+// An operand that has not (an odd width, a tensor at an odd place of the flat
+// buffer, padding inside it) is first copied to the workspace.
+#include <algorithm>
+
+#include "activation.hpp"
+#include "matrix.hpp"
+
+namespace {
+using namespace zs;
+
+constexpr int kThreads = 256;
+constexpr int kStep = 64;  // k of an LDS buffer: 128 bytes of a row
+
+// What becomes of a sum.
+struct Epilogue {
+  const uint16_t* bias;  // flat parameters; null: none
+  Place bias_place;
+  const uint16_t* add;  // res, or the gradient's other part; null: none
+  int64_t add_stride;
+  const uint16_t* pre_in;  // input gradient: what the activation was taken of
+  uint16_t* pre_out;       // forward: kept for the backward pass
+  void* out;
+  int64_t out_stride;
+  int32_t act, f32, grad;
+};
+
+struct Args {
+  const uint16_t *a, *b;
+  int64_t a_stride, b_stride;  // elements
+  int32_t M, N, K;             // K: whole chunks of 8 where k is adjacent
+  int32_t Kb;                  // rows of a B with n adjacent
+  int32_t row_tiles, col_tiles;
+  int32_t whole;               // tiles of one block each
+  int32_t splits, per_split;   // blocks of each further tile, steps of each
+  float* partial;
+  Epilogue e;
+};
+
+// The shape of a block's tile: 64*W rows and columns, four waves two by two,
+// W panels of 32 along each side of a wave.
+template <int W_>
+struct Shape {
+  static constexpr int W = W_, kSide = 64 * W;
+  static constexpr int kOperand = kSide * 128, kBuffer = 2 * kOperand;
+  static constexpr int kLoads = 2 * W;  // requests of a wave for an operand
+};
+
+// 16 bytes a lane from base + off to LDS at `lds` + 16 * lane.  Written out:
+// the compiler does not know that the address is read at issue and would wait
+// for the data before the next LDS read.  No register is written; the wait is
+// requests_done().
+__device__ __forceinline__ void request(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(lds), "v"(off), "s"(base));
+}
+__device__ __forceinline__ void requests_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// One wave's requests for an operand with k adjacent: rows 8 * (wave * kLoads +
+// j) to + 7 of the tile; lane l fetches chunk (l % 8) ^ (l / 8) of row l / 8.
+template <class S>
+struct KRows {
+  uint32_t off[S::kLoads];
+  static __device__ __forceinline__ int chunk() { return ((threadIdx.x & 7) ^ ((threadIdx.x >> 3) & 7)); }
+  __device__ __forceinline__ void set(int32_t r0, int32_t rows, int64_t stride) {
+    const int wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int j = 0; j < S::kLoads; ++j) {
+      const int r = min((wave * S::kLoads + j) * 8 + (int)((threadIdx.x >> 3) & 7), rows - 1 - r0);
+      off[j] = (uint32_t)(r * stride) * 2u + chunk() * 16;
+    }
+  }
+  // `left`: k of this step that there are (kStep: all)
+  __device__ __forceinline__ uint32_t at(int j, int left) const {
+    return left >= kStep || chunk() * 8 < left ? off[j] : off[j] - chunk() * 16;
+  }
+  static __device__ __forceinline__ bool missing(int, int left) { return chunk() * 8 >= left; }
+  static __device__ __forceinline__ int64_t step_bytes(int64_t) { return kStep * 2; }
+  // fragment: 32 rows x 16 k; lane l holds row l % 32, k 8 * (l / 32) to + 7
+  static __device__ __forceinline__ int frag_offset() { return (threadIdx.x & 31) * 128; }
+  static __device__ __forceinline__ bf16x8 frag(const lds_char* p, int panel, int s) {
+    const int c = (2 * s + (int)((threadIdx.x >> 5) & 1)) ^ (int)(threadIdx.x & 7);
+    typedef __attribute__((address_space(3))) bf16x8 lds_t;
+    return *(const lds_t*)(p + panel * 4096 + c * 16);
+  }
+  static constexpr int kReads = 1;
+};
+
+// The same for an operand with n adjacent, in panels of 64 columns: request j
+// of a wave is rows 8 * (i % 8) to + 7 of panel i / 8, i = wave * kLoads + j;
+// lane l fetches chunk (l % 8) ^ 2 * (row % 4) of its row.
+template <class S>
+struct NRows {
+  uint32_t off[S::kLoads];
+  static __device__ __forceinline__ int chunk() { return ((threadIdx.x & 7) ^ (2 * ((threadIdx.x >> 3) & 3))); }
+  static __device__ __forceinline__ int row(int j) {
+    return (((int)(threadIdx.x >> 6) * S::kLoads + j) & 7) * 8 + (int)((threadIdx.x >> 3) & 7);
+  }
+  int64_t stride;
+  __device__ __forceinline__ void set(int32_t n0, int32_t cols, int64_t stride_) {
+    stride = stride_;
+#pragma unroll
+    for (int j = 0; j < S::kLoads; ++j) {
+      const int panel = ((int)(threadIdx.x >> 6) * S::kLoads + j) >> 3;
+      const int c = min(n0 + panel * 64 + chunk() * 8, (cols - 1) & ~7) - n0;
+      off[j] = (uint32_t)(row(j) * stride + c) * 2u;
+    }
+  }
+  __device__ __forceinline__ uint32_t at(int j, int left) const {
+    return row(j) < left ? off[j] : off[j] - (uint32_t)((row(j) - left + 1) * stride) * 2u;
+  }
+  static __device__ __forceinline__ bool missing(int j, int left) { return row(j) >= left; }
+  static __device__ __forceinline__ int64_t step_bytes(int64_t stride) { return kStep * stride * 2; }
+  // 16 lanes read 4 rows of 16 columns and each gets a column's 4 rows
+  static __device__ __forceinline__ int frag_offset() { return 0; }
+  static __device__ __forceinline__ bf16x8 frag(const lds_char* p, int panel, int s) {
+    typedef __attribute__((address_space(3))) s16x4 lds_t;
+    const int l = threadIdx.x & 63, g = l >> 4, i = l & 15;
+    const int k = i >> 2;  // row % 4 of both reads
+    const int c = (panel & 1) * 4 + (g & 1) * 2 + ((i & 3) >> 1);
+    const lds_char* q = p + (panel >> 1) * 8192 + (16 * s + 8 * (g >> 1) + k) * 128 + (c ^ (2 * k)) * 16 + (i & 1) * 8;
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)q);
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(q + 512));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+  static constexpr int kReads = 2;
+};
+
+__device__ __forceinline__ f32x4 bf16x4_at(const uint16_t* p, int left) {
+  u32x2 w = {0u, 0u};
+  if (left >= 4) {
+    w = *(const u32x2_a2*)p;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      if (j < left) w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+  }
+  return f32x4{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+}
+__device__ __forceinline__ void bf16x4_to(uint16_t* p, f32x4 v, int left) {
+  if (left >= 4) {
+    *(u32x2_a2*)p = u32x2{bf16_pack2(v.x, v.y), bf16_pack2(v.z, v.w)};
+  } else {
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      if (j < left) p[j] = (uint16_t)bf16_round(v[j]);
+  }
+}
+
+// Four columns of bias, from column c; `left` of them exist.
+__device__ __forceinline__ f32x4 bias_at(const Epilogue& e, int32_t c, int left) {
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if (e.bias) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < left) v[j] = bf16_one(e.bias[place_at<true>(e.bias_place, c + j)]);
+  }
+  return v;
+}
+
+// Four sums of row r, columns c to c + 3, of which `left` exist.  N: the
+// matrix's columns (rows of pre lie densely).
+__device__ __forceinline__ void finish4(const Epilogue& e, int32_t N, int64_t r, int32_t c, int left, f32x4 v,
+                                        f32x4 bias) {
+  f32x4 add = {0.f, 0.f, 0.f, 0.f};
+  if (e.add) add = bf16x4_at(e.add + r * e.add_stride + c, left);
+  if (e.grad) {
+    v = v + add;
+    if (e.act != ZERO_ACT_NONE) v = v * apply4<true>(e.act, bf16x4_at(e.pre_in + r * N + c, left));
+  } else {
+    v = v + bias;
+    if (e.pre_out) bf16x4_to(e.pre_out + r * N + c, v, left);
+    v = apply4<false>(e.act, v) + add;
+  }
+  if (e.f32) {
+    float* o = (float*)e.out + r * e.out_stride + c;
+    if (left >= 4) {
+      *(f32x4_a4*)o = v;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+        if (j < left) o[j] = v[j];
+    }
+  } else {
+    bf16x4_to((uint16_t*)e.out + r * e.out_stride + c, v, left);
+  }
+}
+
+template <class S, bool NC>
+__global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(const Args A) {
+  constexpr int W = S::W, kSide = S::kSide;
+  using BRows = std::conditional_t<NC, NRows<S>, KRows<S>>;
+  __shared__ __align__(1024) char shared[2 * S::kBuffer];
+  lds_char* lds = (lds_char*)shared;
+  const uint32_t lds_base = (uint32_t)(uintptr_t)lds;
+
+  // whole tiles first, dealt to the XCDs (block b runs on XCD b % 8) in runs
+  const int32_t all_steps = (max(A.K, NC ? A.Kb : 0) + kStep - 1) / kStep;
+  int32_t tile, split = 0, sa = 0, sz = all_steps;
+  if ((int32_t)blockIdx.x < A.whole) {
+    tile = (A.whole & 7) ? (int32_t)blockIdx.x
+                         : (int32_t)(blockIdx.x & 7) * (A.whole >> 3) + (int32_t)(blockIdx.x >> 3);
+  } else {
+    // quotients come from the vector unit; what follows from them is one
+    // value for the wave
+    const int32_t x = (int32_t)blockIdx.x - A.whole, t = __builtin_amdgcn_readfirstlane(x / A.splits);
+    split = x - t * A.splits;
+    tile = A.whole + t;
+    sa = split * A.per_split;
+    sz = min(all_steps, sa + A.per_split);
+  }
+  int32_t r0, c0;
+  tile_place(tile, A.row_tiles, A.col_tiles, r0, c0);
+  r0 = __builtin_amdgcn_readfirstlane(r0) * kSide;
+  c0 = __builtin_amdgcn_readfirstlane(c0) * kSide;
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 1, wn = wave & 1;
+  const int lane = threadIdx.x & 63;
+  f32x16 acc[W][W];
+#pragma unroll
+  for (int m = 0; m < W; ++m)
+#pragma unroll
+    for (int n = 0; n < W; ++n)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) acc[m][n][k] = 0.f;
+
+  KRows<S> ra;
+  BRows rb;
+  ra.set(r0, A.M, A.a_stride);
+  rb.set(c0, A.N, A.b_stride);
+  const char* const pa = (const char*)(A.a + r0 * A.a_stride);
+  const char* const pb = (const char*)(A.b + (NC ? (int64_t)c0 : c0 * A.b_stride));
+  const int32_t steps = sz - sa;
+  // The step that may not be whole, the last one of k, is a block's first: the
+  // others need no checks.  at: the number in k of a block's step i.
+  const bool has_end = sz == all_steps;
+  const auto at = [&](int32_t i) { return has_end ? (i == 0 ? all_steps - 1 : sa + i - 1) : sa + i; };
+  const uint32_t mine = lds_base + wave * S::kLoads * 1024;
+  // request j for step i; 0 to kLoads - 1 are A's
+  const auto fetch1 = [&](const char* a_at, const char* b_at, int buf, auto index) {
+    constexpr int j = decltype(index)::value;
+    if constexpr (j < S::kLoads)
+      request(a_at, ra.off[j], mine + buf * S::kBuffer + j * 1024);
+    else
+      request(b_at, rb.off[j - S::kLoads], mine + buf * S::kBuffer + S::kOperand + (j - S::kLoads) * 1024);
+  };
+  const auto a_of = [&](int32_t i) { return pa + (int64_t)at(i) * KRows<S>::step_bytes(A.a_stride); };
+  const auto b_of = [&](int32_t i) { return pb + (int64_t)at(i) * BRows::step_bytes(A.b_stride); };
+  const auto fetch = [&](int32_t i, int buf) {
+    const char *a_at = a_of(i), *b_at = b_of(i);
+    unrolled<2 * S::kLoads>([&](auto j) { fetch1(a_at, b_at, buf, j); });
+  };
+  // The first step, its k from `left` on replaced by zeros.
+  const auto fetch_first = [&]() {
+    const char *a_at = a_of(0), *b_at = b_of(0);
+    const int left_a = A.K - at(0) * kStep, left_b = (NC ? A.Kb : A.K) - at(0) * kStep;
+#pragma unroll
+    for (int j = 0; j < S::kLoads; ++j) {
+      request(a_at, ra.at(j, left_a), mine + j * 1024);
+      request(b_at, rb.at(j, left_b), mine + S::kOperand + j * 1024);
+    }
+    requests_done();
+    if (left_a < kStep || left_b < kStep) {
+      lds_char* p = lds + wave * S::kLoads * 1024 + lane * 16;
+#pragma unroll 1
+      for (int j = 0; j < S::kLoads; ++j) {
+        if (KRows<S>::missing(j, left_a)) *(lds_u32x4*)(p + j * 1024) = u32x4{0u, 0u, 0u, 0u};
+        if (BRows::missing(j, left_b)) *(lds_u32x4*)(p + S::kOperand + j * 1024) = u32x4{0u, 0u, 0u, 0u};
+      }
+    }
+  };
+
+  const lds_char* const fa = lds + wm * W * 4096 + KRows<S>::frag_offset();
+  const lds_char* const fb = lds + S::kOperand + wn * W * 4096 + BRows::frag_offset();
+  bf16x8 a[2][W], b[2][W];
+  const auto read1 = [&](auto set, int buf, int s, auto index) {
+    constexpr int to = decltype(set)::value, j = decltype(index)::value;
+    if constexpr (j < W)
+      a[to][j] = KRows<S>::frag(fa + buf * S::kBuffer, j, s);
+    else
+      b[to][j - W] = BRows::frag(fb + buf * S::kBuffer, j - W, s);
+  };
+  constexpr std::integral_constant<int, 0> k0;  // the two sets of fragments
+  constexpr std::integral_constant<int, 1> k1;
+  const auto read = [&](auto set, int buf, int s) {
+    unrolled<2 * W>([&](auto j) { read1(set, buf, s, j); });
+  };
+  // The products of one stretch of 16 k; after each of them `beside` puts its
+  // share of other work.
+  constexpr int kM = W * W;
+  const auto multiply = [&](auto set, auto beside) {
+    constexpr int from = decltype(set)::value;
+    unrolled<kM>([&](auto index) {
+      constexpr int i = decltype(index)::value;
+      acc[i / W][i % W] =
+          __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[from][i / W], b[from][i % W], acc[i / W][i % W], 0, 0, 0);
+      beside(index);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  // f(j) for those of N things that go beside product I
+  const auto share = [](auto index, auto count, auto f) {
+    constexpr int i = decltype(index)::value, n = decltype(count)::value;
+    constexpr int first = (i * n + kM - 1) / kM, next = ((i + 1) * n + kM - 1) / kM;
+    unrolled<next - first>([&](auto j) { f(std::integral_constant<int, first + decltype(j)::value>{}); });
+  };
+  constexpr std::integral_constant<int, 2 * W> kReads;
+  constexpr std::integral_constant<int, 2 * S::kLoads> kRequests;
+  const auto with_reads = [&](auto from, auto to, int buf, int s) {
+    multiply(from, [&](auto index) { share(index, kReads, [&](auto j) { read1(to, buf, s, j); }); });
+  };
+  // Step i, in buffer `buf`.  NEXT: steps that follow, two or more of which
+  // the first of those is requested.
+  const auto step = [&](auto next, int32_t i, int buf) {
+    constexpr int kNext = decltype(next)::value;
+    with_reads(k0, k1, buf, 1);
+    with_reads(k1, k0, buf, 2);
+    with_reads(k0, k1, buf, 3);
+    if (kNext > 0) requests_done();
+    __syncthreads();
+    if constexpr (kNext > 1) {
+      const char *a_at = a_of(i + 2), *b_at = b_of(i + 2);
+      multiply(k1, [&](auto index) {
+        share(index, kReads, [&](auto j) { read1(k0, buf ^ 1, 0, j); });
+        share(index, kRequests, [&](auto j) { fetch1(a_at, b_at, buf, j); });
+      });
+    } else if constexpr (kNext > 0) {
+      with_reads(k1, k0, buf ^ 1, 0);
+    } else {
+      multiply(k1, [](auto) {});
+    }
+  };
+  if (steps > 0) {
+    fetch_first();
+    __syncthreads();
+    if (steps > 1) fetch(1, 1);
+    read(k0, 0, 0);
+    int32_t i = 0;
+#pragma unroll 1
+    for (; i + 2 < steps; ++i) step(std::integral_constant<int, 2>{}, i, i & 1);
+    if (i + 1 < steps) {
+      step(std::integral_constant<int, 1>{}, i, i & 1);
+      ++i;
+    }
+    step(std::integral_constant<int, 0>{}, i, i & 1);
+  }
+
+  // lane l, register k: row 8*(k/4) + 4*(l/32) + k%4, column l%32
+  if (tile < A.whole) {
+    // A wave's sums leave 32 rows at a time through LDS of its own, from where
+    // a lane gets 4 columns of a row.
+    constexpr int kCols = W * 32, kStride = kCols + 8;  // 4 rows are 32 banks apart
+    constexpr int kAcross = kCols / 4, kDown = 64 / kAcross, kVecs = 32 / kDown;
+    static_assert(4 * 32 * kStride * 4 <= 2 * S::kBuffer, "the strips fit the buffers");
+    typedef __attribute__((address_space(3))) float lds_f32;
+    typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+    __syncthreads();
+    lds_f32* const strip = (lds_f32*)lds + wave * 32 * kStride;
+    const int down = lane / kAcross, across = lane % kAcross * 4;
+    const int32_t c = c0 + wn * kCols + across;
+    const int left = A.N - c;
+    const f32x4 bias = bias_at(A.e, c, left);
+    const auto put = [&](auto index) {
+      constexpr int m = decltype(index)::value;
+#pragma unroll
+      for (int n = 0; n < W; ++n)
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          strip[(8 * (k >> 2) + (k & 3) + 4 * (lane >> 5)) * kStride + n * 32 + (lane & 31)] = acc[m][n][k];
+    };
+    unrolled<W>([&](auto index) {
+      constexpr int m = decltype(index)::value;
+      put(index);
+      lanes_meet_in_lds();
+      const int32_t rb = r0 + (wm * W + m) * 32 + down;
+#pragma unroll 1
+      for (int i = 0; i < kVecs; ++i) {
+        const f32x4 v = *(const lds_f32x4*)(strip + (i * kDown + down) * kStride + across);
+        const int32_t r = rb + i * kDown;
+        if (r < A.M && left > 0) finish4(A.e, A.N, r, c, left, v, bias);
+      }
+      lanes_meet_in_lds();
+    });
+    return;
+  }
+  // a tile of the workspace, rows of kSide columns
+  float* const to = A.partial + ((int64_t)(tile - A.whole) * A.splits + split) * kSide * kSide +
+                    4 * (lane >> 5) * kSide + (lane & 31);
+#pragma unroll
+  for (int m = 0; m < W; ++m)
+#pragma unroll
+    for (int n = 0; n < W; ++n)
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        to[((wm * W + m) * 32 + 8 * (k >> 2) + (k & 3)) * kSide + (wn * W + n) * 32] = acc[m][n][k];
+}
+
+// Adds up a tile's splits, in order, and finishes the sums: `parts` blocks to
+// a tile.
+template <int SIDE>
+__global__ void __launch_bounds__(kThreads) sum_kernel(const Args A, int32_t parts) {
+  const int32_t at = (int32_t)blockIdx.x / parts, part = (int32_t)blockIdx.x % parts;
+  int32_t r0, c0;
+  tile_place(A.whole + at, A.row_tiles, A.col_tiles, r0, c0);
+  const float* from = A.partial + (int64_t)at * A.splits * SIDE * SIDE;
+  const int per = SIDE * SIDE / 4 / parts;
+  for (int g = part * per + threadIdx.x; g < (part + 1) * per; g += kThreads) {
+    const int32_t r = r0 * SIDE + g / (SIDE / 4), c = c0 * SIDE + (g % (SIDE / 4)) * 4;
+    const int left = A.N - c;
+    if (r >= A.M || left <= 0) continue;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int k = 0; k < A.splits; ++k) s += *(const f32x4*)(from + (int64_t)k * SIDE * SIDE + g * 4);
+    finish4(A.e, A.N, r, c, left, s, bias_at(A.e, c, left));
+  }
+}
+
+// Copies of operands that requests cannot take, rows filled up with zeros to
+// whole chunks: the weight from its places in the flat buffer, then A.
+struct Copy {
+  const uint16_t* from;
+  uint16_t* to;
+  Place place;     // the weight's; A: x0 0, no gap
+  int64_t stride;  // of the source
+  int64_t rows;
+  int32_t cols, chunks;
+};
+__global__ void __launch_bounds__(kThreads) copy_kernel(const Copy w, const Copy a) {
+  const int64_t nw = w.rows * w.chunks, n = nw + a.rows * a.chunks;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
+    const bool first = i < nw;
+    const Copy& c = first ? w : a;
+    const int64_t j = first ? i : i - nw;
+    const int64_t r = j / c.chunks;
+    const int32_t col = (int32_t)(j - r * c.chunks) * 8;
+    const int left = c.cols - col;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    int64_t at;
+    if (place_run<true>(c.place, r * c.stride + col, 8, at) && left >= 8) {
+      v = *(const u32x4_a2*)(c.from + at);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < left)
+          v[k >> 1] |= (uint32_t)c.from[place_at<true>(c.place, r * c.stride + col + k)] << (16 * (k & 1));
+    }
+    *(u32x4*)(c.to + (r * c.chunks * 8 + col)) = v;
+  }
+}
+
+// ------------------------------------------------------------------ host
+// Tiles that fill the chip's 256 CUs are summed by one block each; the rest of
+// the tiles share the CUs, each tile's k being split over as many blocks as
+// there is room for, kMinSteps steps each at least.  The number of CUs is a
+// constant: the order of a sum and the workspace's size follow from the sizes
+// alone.
+constexpr int64_t kCus = 256, kMinSteps = 4, kMaxSplits = 32;
+constexpr int64_t kMaxStride = (int64_t)1 << 22;  // a tile's rows lie within 32 bits
+
+struct Plan {
+  int64_t side, row_tiles, col_tiles, whole, further, splits, per_split;
+  int64_t w_bytes, a_bytes, bytes;  // copies, and everything
+  double us;
+};
+
+template <class S>
+Plan plan_for(int64_t M, int64_t N, int64_t K) {
+  Plan p{};
+  p.side = S::kSide;
+  p.row_tiles = (M + p.side - 1) / p.side;
+  p.col_tiles = (N + p.side - 1) / p.side;
+  const int64_t tiles = p.row_tiles * p.col_tiles, steps = (K + kStep - 1) / kStep;
+  const int64_t at_once = kCus * (S::W == 4 ? 1 : 2);
+  p.whole = tiles / at_once * at_once;
+  p.further = tiles - p.whole;
+  p.splits = 1;
+  p.per_split = std::max<int64_t>(steps, 1);
+  if (p.further > 0) {
+    const int64_t most = std::max<int64_t>(1, steps / kMinSteps);
+    p.splits = std::max<int64_t>(1, std::min({most, at_once / p.further, kMaxSplits}));
+    p.per_split = std::max<int64_t>(1, (steps + p.splits - 1) / p.splits);
+    p.splits = std::max<int64_t>(1, (steps + p.per_split - 1) / p.per_split);
+    if (p.splits == 1) {
+      p.whole = tiles;
+      p.further = 0;
+    }
+  }
+  const double step = S::W == 4 ? 1.1 : 0.55;
+  const double tile_io = (double)(p.side * p.side) * 8 / 4.7e6;
+  const double rounds = (double)((p.whole + at_once - 1) / at_once);
+  p.us = rounds * ((double)steps * step + 2);
+  if (p.further > 0) p.us += (double)p.per_split * step + (double)(p.further * (p.splits + 1)) * tile_io + 4;
+  return p;
+}
+
+typedef Shape<4> Large;
+typedef Shape<2> Small;
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+// A call's sizes: M tokens, N columns of the result, K of the sum.  n_adjacent:
+// B's neighbouring elements differ in n.
+struct Sizes {
+  int64_t M, N, K;
+  bool n_adjacent;
+  int64_t w_rows, w_cols;
+};
+Sizes sizes_of(int64_t tokens, int64_t out_f, int64_t in_f, bool transposed, bool grad) {
+  Sizes z;
+  z.M = tokens;
+  z.N = grad ? in_f : out_f;
+  z.K = grad ? out_f : in_f;
+  z.n_adjacent = transposed != grad;
+  z.w_rows = transposed ? in_f : out_f;
+  z.w_cols = transposed ? out_f : in_f;
+  return z;
+}
+
+Plan make_plan(const zero_layout* L, int32_t tensor, const Sizes& z, const uint16_t* params, const uint16_t* a,
+               int64_t a_stride) {
+  const Plan x = plan_for<Large>(z.M, z.N, z.K), y = plan_for<Small>(z.M, z.N, z.K);
+  Plan p = x.us <= y.us ? x : y;
+  int64_t lo, hi;
+  const Place pl = make_place(L, tensor, &lo, &hi);
+  const bool copy_w = pl.gap != 0 || z.w_cols % 8 || !aligned16(params + lo);
+  const bool copy_a = z.K % 8 || a_stride % 8 || a_stride > kMaxStride || !aligned16(a);
+  p.w_bytes = copy_w ? z.w_rows * ((z.w_cols + 7) / 8) * 16 : 0;
+  p.a_bytes = copy_a ? z.M * ((z.K + 7) / 8) * 16 : 0;
+  p.bytes = p.w_bytes + p.a_bytes + p.further * p.splits * p.side * p.side * 4;
+  return p;
+}
+
+int shape_ok(const zero_layout* L, int32_t tensor, int32_t transposed, int64_t O, int64_t I, int64_t tokens) {
+  if (!L || O < 0 || I < 0 || tokens < 0 || (transposed != 0 && transposed != 1)) return ZERO_EINVAL;
+  if (!tensor_ok(L, tensor)) return ZERO_ERANGE;
+  if (O > ZERO_MAX_FEATURES || I > ZERO_MAX_FEATURES || tokens > ZERO_MAX_ROWS) return ZERO_ERANGE;
+  if (O * I != L->numel[(size_t)tensor]) return ZERO_EINVAL;
+  return ZERO_OK;
+}
+// The dispatch grids count work-items in 32 bits.
+int plan_ok(const Plan& p) { return p.row_tiles * p.col_tiles > ((int64_t)1 << 23) ? ZERO_ERANGE : ZERO_OK; }
+
+template <class S>
+int launch(const Args& A, const Plan& p, bool n_adjacent, hipStream_t s) {
+  const dim3 grid((unsigned)(p.whole + p.further * p.splits));
+  if (n_adjacent)
+    hipLaunchKernelGGL((product_kernel<S, true>), grid, dim3(kThreads), 0, s, A);
+  else
+    hipLaunchKernelGGL((product_kernel<S, false>), grid, dim3(kThreads), 0, s, A);
+  const int rc = launched();
+  if (rc != ZERO_OK || p.further == 0) return rc;
+  int32_t parts = S::kSide * S::kSide / 1024;
+  while (parts > 1 && parts * p.further > 2048) parts >>= 1;
+  hipLaunchKernelGGL(sum_kernel<S::kSide>, dim3((unsigned)(p.further * parts)), dim3(kThreads), 0, s, A, parts);
+  return launched();
+}
+
+int64_t workspace_of(const zero_layout* L, int32_t tensor, int32_t transposed, const uint16_t* params,
+                     const uint16_t* a, int64_t a_stride, int64_t tokens, int64_t O, int64_t I, bool grad) {
+  const int rc = shape_ok(L, tensor, transposed, O, I, tokens);
+  if (rc != ZERO_OK) return rc;
+  if (O == 0 || I == 0 || tokens == 0) return 0;
+  const Sizes z = sizes_of(tokens, O, I, transposed != 0, grad);
+  if (a_stride < z.K) return ZERO_EINVAL;
+  const Plan p = make_plan(L, tensor, z, params, a, a_stride);
+  return plan_ok(p) == ZERO_OK ? p.bytes : ZERO_ERANGE;
+}
+
+// What both directions do once their own arguments are checked and the
+// epilogue is filled in.  The memory of the outputs is in `outs`, what the
+// epilogue reads in `ins`.
+int run(const zero_layout* L, int32_t tensor, const uint16_t* params, const uint16_t* a, int64_t a_stride,
+        const Sizes& z, const Epilogue& e, const Bytes (&out)[2], const Bytes (&in)[3], void* workspace,
+        int64_t workspace_bytes, hipStream_t stream) {
+  const Plan p = make_plan(L, tensor, z, params, a, a_stride);
+  if (plan_ok(p) != ZERO_OK) return ZERO_ERANGE;
+  if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes || ((uintptr_t)workspace & 15u))) return ZERO_EINVAL;
+  int64_t lo, hi;
+  const Place place = make_place(L, tensor, &lo, &hi);
+  const Bytes outs[] = {out[0], out[1], Bytes{workspace, p.bytes}};
+  const Bytes ins[] = {in[0], in[1], in[2], Bytes{params + lo, 2 * (hi - lo)}, rows_of(a, z.M, z.K, a_stride, 2)};
+  if (any_overlap(outs, ins)) return ZERO_EOVERLAP;
+  if (hip_error_pending()) return ZERO_EHIP;
+  Args A{};
+  A.M = (int32_t)z.M;
+  A.N = (int32_t)z.N;
+  A.K = (int32_t)((z.K + 7) / 8 * 8);
+  A.Kb = (int32_t)z.K;
+  A.row_tiles = (int32_t)p.row_tiles;
+  A.col_tiles = (int32_t)p.col_tiles;
+  A.whole = (int32_t)p.whole;
+  A.splits = (int32_t)p.splits;
+  A.per_split = (int32_t)p.per_split;
+  A.e = e;
+  char* ws = (char*)workspace;
+  A.a = p.a_bytes ? (const uint16_t*)(ws + p.w_bytes) : a;
+  A.a_stride = p.a_bytes ? A.K : a_stride;
+  const int64_t w_stride = (z.w_cols + 7) / 8 * 8;
+  A.b = p.w_bytes ? (const uint16_t*)ws : params + lo;
+  A.b_stride = p.w_bytes ? w_stride : z.w_cols;
+  A.partial = (float*)(ws + p.w_bytes + p.a_bytes);
+  if (p.w_bytes || p.a_bytes) {
+    // without padding every run of elements lies in one piece
+    const Place plain{0, (int64_t)1 << 62, 0, 0.0}, whole{place.x0, plain.cap, 0, 0.0};
+    const Copy w{params, (uint16_t*)ws, place.gap ? place : whole, z.w_cols, p.w_bytes ? z.w_rows : 0, (int32_t)z.w_cols,
+                 (int32_t)((z.w_cols + 7) / 8)};
+    const Copy c{a, (uint16_t*)(ws + p.w_bytes), plain, a_stride, p.a_bytes ? z.M : 0, (int32_t)z.K,
+                 (int32_t)((z.K + 7) / 8)};
+    const int64_t n = w.rows * w.chunks + c.rows * c.chunks;
+    const unsigned grid = (unsigned)std::min<int64_t>((n + kThreads - 1) / kThreads, 16 * kCus);
+    hipLaunchKernelGGL(copy_kernel, dim3(grid), dim3(kThreads), 0, stream, w, c);
+    const int rc = launched();
+    if (rc != ZERO_OK) return rc;
+  }
+  return p.side == Large::kSide ? launch<Large>(A, p, z.n_adjacent, stream)
+                                : launch<Small>(A, p, z.n_adjacent, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t zero_linear_workspace(const zero_layout* L, int32_t tensor, int32_t transposed,
+                              const uint16_t* params_flat, const uint16_t* x, int64_t x_stride, int64_t tokens,
+                              int64_t out_features, int64_t in_features) {
+  return workspace_of(L, tensor, transposed, params_flat, x, x_stride, tokens, out_features, in_features, false);
+}
+
+int zero_linear(const zero_layout* L, int32_t tensor, int32_t transposed, int32_t bias_tensor,
+                const uint16_t* params_flat, const uint16_t* x, int64_t x_stride, int64_t tokens,
+                int64_t out_features, int64_t in_features, int32_t activation, const uint16_t* res,
+                int64_t res_stride, void* out, int64_t out_stride, int32_t out_dtype, uint16_t* pre,
+                void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  const int rc = shape_ok(L, tensor, transposed, out_features, in_features, tokens);
+  if (rc != ZERO_OK) return rc;
+  const int64_t O = out_features, I = in_features;
+  if (bias_tensor < -1 || !activation_ok(activation)) return ZERO_EINVAL;
+  if (out_dtype != ZERO_DTYPE_BF16 && out_dtype != ZERO_DTYPE_F32) return ZERO_EINVAL;
+  if (bias_tensor >= 0) {
+    if (!tensor_ok(L, bias_tensor)) return ZERO_ERANGE;
+    if (L->numel[(size_t)bias_tensor] != O) return ZERO_EINVAL;
+  }
+  // a sum over nothing would still be the bias: not a layer
+  if (I == 0 && O > 0 && tokens > 0) return ZERO_EINVAL;
+  if (tokens == 0 || O == 0) return ZERO_OK;
+  if (!params_flat || !x || !out || x_stride < I || out_stride < O || (res && res_stride < O)) return ZERO_EINVAL;
+  if (x_stride > ZERO_MAX_STRIDE || out_stride > ZERO_MAX_STRIDE || (res && res_stride > ZERO_MAX_STRIDE))
+    return ZERO_ERANGE;
+  Epilogue e{};
+  int64_t lo = 0, hi = 0;
+  if (bias_tensor >= 0) {
+    e.bias = params_flat;
+    e.bias_place = make_place(L, bias_tensor, &lo, &hi);
+  }
+  e.add = res;
+  e.add_stride = res_stride;
+  e.pre_out = pre;
+  e.out = out;
+  e.out_stride = out_stride;
+  e.act = activation;
+  e.f32 = out_dtype == ZERO_DTYPE_F32;
+  const Bytes outs[2] = {rows_of(out, tokens, O, out_stride, e.f32 ? 4 : 2), Bytes{pre, 2 * tokens * O}};
+  const Bytes ins[3] = {rows_of(res, tokens, O, res_stride, 2), Bytes{params_flat + lo, 2 * (hi - lo)}, Bytes{}};
+  return run(L, tensor, params_flat, x, x_stride, sizes_of(tokens, O, I, transposed != 0, false), e, outs, ins,
+             workspace, workspace_bytes, stream);
+}
+
+int64_t zero_linear_input_grad_workspace(const zero_layout* L, int32_t tensor, int32_t transposed,
+                                         const uint16_t* params_flat, const uint16_t* dy, int64_t dy_stride,
+                                         int64_t tokens, int64_t out_features, int64_t in_features) {
+  return workspace_of(L, tensor, transposed, params_flat, dy, dy_stride, tokens, out_features, in_features, true);
+}
+
+int zero_linear_input_grad(const zero_layout* L, int32_t tensor, int32_t transposed, const uint16_t* params_flat,
+                           const uint16_t* dy, int64_t dy_stride, int64_t tokens, int64_t out_features,
+                           int64_t in_features, int32_t activation, const uint16_t* pre, const uint16_t* add,
+                           int64_t add_stride, uint16_t* dx, int64_t dx_stride, void* workspace,
+                           int64_t workspace_bytes, hipStream_t stream) {
+  const int rc = shape_ok(L, tensor, transposed, out_features, in_features, tokens);
+  if (rc != ZERO_OK) return rc;
+  const int64_t O = out_features, I = in_features;
+  if (!activation_ok(activation)) return ZERO_EINVAL;
+  if (O == 0 && I > 0 && tokens > 0) return ZERO_EINVAL;
+  if (tokens == 0 || I == 0) return ZERO_OK;
+  if (!params_flat || !dy || !dx || dy_stride < O || dx_stride < I || (add && add_stride < I)) return ZERO_EINVAL;
+  if ((activation != ZERO_ACT_NONE) != (pre != nullptr)) return ZERO_EINVAL;
+  if (dy_stride > ZERO_MAX_STRIDE || dx_stride > ZERO_MAX_STRIDE || (add && add_stride > ZERO_MAX_STRIDE))
+    return ZERO_ERANGE;
+  Epilogue e{};
+  e.add = add;
+  e.add_stride = add_stride;
+  e.pre_in = pre;
+  e.out = dx;
+  e.out_stride = dx_stride;
+  e.act = activation;
+  e.grad = 1;
+  const Bytes outs[2] = {rows_of(dx, tokens, I, dx_stride, 2), Bytes{}};
+  const Bytes ins[3] = {rows_of(add, tokens, I, add_stride, 2), Bytes{pre, 2 * tokens * I}, Bytes{}};
+  return run(L, tensor, params_flat, dy, dy_stride, sizes_of(tokens, O, I, transposed != 0, true), e, outs, ins,
+             workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -18,19 +18,12 @@
 // and every value is a normal bf16 number), with one conversion per two
 // codes; products of bf16 are exact in binary32, sums are binary32.
 #include <algorithm>
-#include <utility>
 
 #include "act8.hpp"
+#include "matrix.hpp"
 
 namespace {
 using namespace zs;
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-typedef __attribute__((address_space(3))) char lds_char;
-typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 
 // The shape of a block: G groups of 4 waves; the waves of a group lie two by
 // two over the tile, W panels of 32 columns along each side of a wave, and
@@ -230,34 +223,8 @@ __device__ __forceinline__ void interleave() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// Tile number to place: groups of 8 rows of tiles, column by column within a
-// group, so that tiles worked on together share their operands in the L2.
 __device__ __forceinline__ void tile_at(const Args& A, int32_t tile, int32_t& r, int32_t& c) {
-  const int32_t per = 8 * A.col_tiles, g = tile / per, in = tile - g * per;
-  const int32_t h = min(8, A.row_tiles - g * 8);
-  c = in / h;
-  r = g * 8 + in - c * h;
-}
-
-// Between a wave's LDS accesses where its lanes read what others wrote, or write
-// over what others read.  The LDS takes a wave's accesses in order; this keeps
-// the compiler, which sees one lane's addresses, from changing that order.  No
-// instruction comes of it.
-__device__ __forceinline__ void lanes_meet_in_lds() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
-}
-
-// f(0), f(1) to f(N - 1) with constant arguments: a loop that indexes registers
-// and has to be unrolled whatever its size.
-template <class F, int... I>
-__device__ __forceinline__ void unrolled_of(F f, std::integer_sequence<int, I...>) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, class F>
-__device__ __forceinline__ void unrolled(F f) {
-  unrolled_of(f, std::make_integer_sequence<int, N>{});
+  tile_place(tile, A.row_tiles, A.col_tiles, r, c);
 }
 
 // The workspace's tiles: those that do not go out directly.

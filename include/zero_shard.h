@@ -677,6 +677,77 @@ int zero_head_norm_rotate_grad(const zero_layout* layout, const uint16_t* params
                                float* acc_flat_dev, uint16_t* bf16_flat_dev, void* workspace_dev,
                                int64_t workspace_bytes, hipStream_t stream);
 
+/* Activations of a linear layer: none, max(x, 0), x * Phi(x) with the normal
+ * distribution's function Phi, its approximation 0.5 x (1 + tanh(sqrt(2/pi) *
+ * (x + 0.044715 x^3))), x / (1 + exp(-x)). */
+#define ZERO_ACT_NONE 0
+#define ZERO_ACT_RELU 1
+#define ZERO_ACT_GELU 2
+#define ZERO_ACT_GELU_TANH 3
+#define ZERO_ACT_SILU 4
+
+/* A linear layer and the gradient of its input, the weight read from the
+ * gathered flat buffer.
+ *
+ * W[o, i]: the tensor holds (out_features, in_features), or with transposed =
+ * 1 (in_features, out_features).  Activations are bf16, products exact, sums
+ * binary32 in the matrix cores (their order depends on the sizes alone), and
+ * so is everything up to the one rounding of each output.
+ *
+ * zero_linear:  pre[t, o] = sum over i of x[t, i] * W[o, i] + b[o], b the
+ *   out_features elements of bias_tensor (-1: none);
+ *   out = act(pre) + res (res NULL: none), in bf16 or binary32 (out_dtype);
+ *   pre_dev: NULL, or tokens x out_features bf16, dense: kept for the backward
+ *   pass.
+ * zero_linear_input_grad:  dx[t, i] = (sum over o of dy[t, o] * W[o, i] +
+ *   add[t, i]) * act'(pre[t, i]): the gradient of what went into the activation
+ *   whose output was this layer's input (pre_dev: tokens x in_features, dense,
+ *   as zero_linear kept it; NULL exactly where activation is ZERO_ACT_NONE).
+ *   add: NULL, or the gradient that the input has from elsewhere.  The
+ *   gradient of an activation at a layer's own output is zero_bias_grad's.
+ *
+ * The workspace functions take the operands' addresses: one that does not
+ * begin at 16 bytes, or whose rows are not whole multiples of 16 bytes, is
+ * copied there first (the weight also where padding falls inside it).
+ * Common errors; ZERO_EINVAL also for a sum over no features, ZERO_ERANGE for
+ * more than ZERO_MAX_FEATURES features, or more than 2^23 tiles of 128 x 128
+ * outputs. */
+#define ZERO_MAX_FEATURES (1 << 22)
+int64_t zero_linear_workspace(const zero_layout* layout, int32_t tensor, int32_t transposed,
+                              const uint16_t* params_flat_dev, const uint16_t* x_dev,
+                              int64_t x_stride, int64_t tokens, int64_t out_features,
+                              int64_t in_features);
+int zero_linear(const zero_layout* layout, int32_t tensor, int32_t transposed, int32_t bias_tensor,
+                const uint16_t* params_flat_dev, const uint16_t* x_dev, int64_t x_stride,
+                int64_t tokens, int64_t out_features, int64_t in_features, int32_t activation,
+                const uint16_t* res_dev, int64_t res_stride, void* out_dev, int64_t out_stride,
+                int32_t out_dtype, uint16_t* pre_dev, void* workspace_dev,
+                int64_t workspace_bytes, hipStream_t stream);
+int64_t zero_linear_input_grad_workspace(const zero_layout* layout, int32_t tensor,
+                                         int32_t transposed, const uint16_t* params_flat_dev,
+                                         const uint16_t* dy_dev, int64_t dy_stride, int64_t tokens,
+                                         int64_t out_features, int64_t in_features);
+int zero_linear_input_grad(const zero_layout* layout, int32_t tensor, int32_t transposed,
+                           const uint16_t* params_flat_dev, const uint16_t* dy_dev,
+                           int64_t dy_stride, int64_t tokens, int64_t out_features,
+                           int64_t in_features, int32_t activation, const uint16_t* pre_dev,
+                           const uint16_t* add_dev, int64_t add_stride, uint16_t* dx_dev,
+                           int64_t dx_stride, void* workspace_dev, int64_t workspace_bytes,
+                           hipStream_t stream);
+
+/* The gradient through a layer's own activation, and its bias's gradient.
+ *
+ * g = dy * act'(pre) (pre: rows x cols bf16, dense; NULL exactly where
+ * activation is ZERO_ACT_NONE: g = dy); dpre_dev: NULL, or bf16(g), rows x
+ * cols, dense; the tensor's gradient (cols = its elements) is the sum over the
+ * rows of g, not rounded to bf16 before. */
+int64_t zero_bias_grad_workspace(const zero_layout* layout, int32_t tensor, int64_t rows);
+int zero_bias_grad(const zero_layout* layout, int32_t tensor, const uint16_t* dy_dev,
+                   int64_t dy_stride, const uint16_t* pre_dev, int32_t activation, int64_t rows,
+                   float scale, uint32_t flags, uint16_t* dpre_dev, float* acc_flat_dev,
+                   uint16_t* bf16_flat_dev, void* workspace_dev, int64_t workspace_bytes,
+                   hipStream_t stream);
+
 /* A linear weight's gradient from an 8-bit checkpoint of the layer's input.
  *
  * dW[o, i] = sum over tokens t of dY[t, o] * X[t, i]; the tensor holds
