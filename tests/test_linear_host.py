@@ -64,7 +64,7 @@ BAD = [
         dict(wb=8), dict(ws=at(6, 2))]),
     ("zero_bias_grad", ERANGE, [dict(tensor=5), dict(t=(1 << 30) + 1), dict(ys=BIG)]),
     ("zero_bias_grad", EOVERLAP, [dict(dpre=at(1)), dict(dpre=at(2)), dict(acc=at(1, -4 * (17 + O * I + 24))), dict(ws=at(1)),
-                                  dict(flags=2, out=at(4)), dict(ws=at(3))]),
+                                  dict(flags=2, out=at(4, 2 * (17 + O * I + 24))), dict(ws=at(3))]),
 ]
 
 
