@@ -28,15 +28,7 @@ struct Args {
 };
 
 __device__ __forceinline__ u32x4 load8(const uint16_t* p, int n) {
-  if (n >= 8) return __builtin_nontemporal_load((const u32x4_a2*)p);
-  u32x4 w = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    if (k < n) w[k >> 1] |= (uint32_t)p[k] << (16 * (k & 1));
-  return w;
-}
-__device__ __forceinline__ f32x4 half4(u32x4 w, int h) {
-  return f32x4{bf16_lo(w[2 * h]), bf16_hi(w[2 * h]), bf16_lo(w[2 * h + 1]), bf16_hi(w[2 * h + 1])};
+  return n >= 8 ? __builtin_nontemporal_load((const u32x4_a2*)p) : load_some(p, n);
 }
 
 // ACROSS lanes along a row (8 columns each), the rest of the block down.
@@ -47,7 +39,7 @@ __global__ void __launch_bounds__(kThreads) bias_kernel(const Args A) {
   const int32_t c = ((int32_t)blockIdx.x * ACROSS + across) * 8;
   const int n = min(8, A.cols - c);
   const int64_t ra = (int64_t)blockIdx.y * A.rows_per_group, rz = min(A.rows, ra + A.rows_per_group);
-  f32x4 sum[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int64_t r0 = ra + down; r0 < rz; r0 += kDown * kAhead) {
     u32x4 dy[kAhead], pre[ACT ? kAhead : 1];
 #pragma unroll
@@ -60,32 +52,31 @@ __global__ void __launch_bounds__(kThreads) bias_kernel(const Args A) {
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int64_t r = r0 + k * kDown;
-      f32x4 g[2] = {half4(dy[k], 0), half4(dy[k], 1)};
+      float g[8];
+      widen8(dy[k], g);
       if constexpr (ACT) {
         if (r >= rz) continue;
+        float s[8];
+        widen8(pre[k], s);
+        apply8<true>(A.act, s);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) g[h] = g[h] * apply4<true>(A.act, half4(pre[k], h));
+        for (int j = 0; j < 8; ++j) g[j] *= s[j];
       }
       if (A.dpre && r < rz) {
-        const u32x4 w = {bf16_pack2(g[0].x, g[0].y), bf16_pack2(g[0].z, g[0].w), bf16_pack2(g[1].x, g[1].y),
-                         bf16_pack2(g[1].z, g[1].w)};
         uint16_t* p = A.dpre + r * A.cols + c;
-        if (n >= 8) {
-          __builtin_nontemporal_store(w, (u32x4_a2*)p);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < n) p[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
-        }
+        if (n >= 8)
+          __builtin_nontemporal_store(round8(g), (u32x4_a2*)p);
+        else
+          store_some(p, round8(g), n);
       }
-      sum[0] = sum[0] + g[0];
-      sum[1] = sum[1] + g[1];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += g[j];
     }
   }
   if constexpr (kDown > 1) {
     __shared__ alignas(16) f32x4 all[kThreads * 2];
-    all[threadIdx.x * 2] = sum[0];
-    all[threadIdx.x * 2 + 1] = sum[1];
+    all[threadIdx.x * 2] = f32x4{sum[0], sum[1], sum[2], sum[3]};
+    all[threadIdx.x * 2 + 1] = f32x4{sum[4], sum[5], sum[6], sum[7]};
     __syncthreads();
     // thread k sums 4 columns (k / 2, k % 2) over the rows of threads
     if (threadIdx.x >= ACROSS * 2) return;
@@ -101,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) bias_kernel(const Args A) {
     float* p = A.partial + (int64_t)blockIdx.y * A.cols + c;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (j < n) p[j] = sum[j >> 2][j & 3];
+      if (j < n) p[j] = sum[j];
   }
 }
 

@@ -32,6 +32,9 @@
 namespace {
 using namespace zs;
 
+// For closures: called out of line, what they capture would go through memory.
+#define ZERO_INLINE __attribute__((always_inline))
+
 constexpr int kThreads = 256;
 constexpr int kStep = 64;  // k of an LDS buffer: 128 bytes of a row
 
@@ -67,7 +70,21 @@ struct Shape {
   static constexpr int W = W_, kSide = 64 * W;
   static constexpr int kOperand = kSide * 128, kBuffer = 2 * kOperand;
   static constexpr int kLoads = 2 * W;  // requests of a wave for an operand
+  // The way out: a strip of 32 rows of a wave's sums, its rows 32 bytes apart
+  // from each other's banks, and what the epilogue reads beside them, 16 bytes
+  // a lane and piece of 8 columns.
+  static constexpr int kCols = W * 32, kRow = kCols + 8;
+  static constexpr int kAcross = kCols / 8, kDown = 64 / kAcross, kVecs = 32 / kDown;
+  static constexpr int kStrip = 32 * kRow * 4, kWay = kStrip + 2 * kVecs * 1024;
+  static constexpr int kLds = 2 * kBuffer > 4 * kWay ? 2 * kBuffer : 4 * kWay;
 };
+
+// An address that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ const char* uniform(const char* p) {
+  const uint64_t x = (uint64_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+  return (const char*)((uint64_t)hi << 32 | lo);
+}
 
 // 16 bytes a lane from base + off to LDS at `lds` + 16 * lane.  Written out:
 // the compiler does not know that the address is read at issue and would wait
@@ -150,63 +167,76 @@ struct NRows {
   static constexpr int kReads = 2;
 };
 
-__device__ __forceinline__ f32x4 bf16x4_at(const uint16_t* p, int left) {
-  u32x2 w = {0u, 0u};
-  if (left >= 4) {
-    w = *(const u32x2_a2*)p;
-  } else {
+// Eight columns of bias, from column c; `left` of them exist.
+__device__ __forceinline__ void bias_at(const Epilogue& e, int32_t c, int left, float (&v)[8]) {
 #pragma unroll
-    for (int j = 0; j < 3; ++j)
-      if (j < left) w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
-  }
-  return f32x4{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
-}
-__device__ __forceinline__ void bf16x4_to(uint16_t* p, f32x4 v, int left) {
-  if (left >= 4) {
-    *(u32x2_a2*)p = u32x2{bf16_pack2(v.x, v.y), bf16_pack2(v.z, v.w)};
-  } else {
-#pragma unroll
-    for (int j = 0; j < 3; ++j)
-      if (j < left) p[j] = (uint16_t)bf16_round(v[j]);
-  }
+  for (int j = 0; j < 8; ++j)
+    v[j] = e.bias && j < left ? bf16_one(e.bias[place_at<true>(e.bias_place, c + j)]) : 0.f;
 }
 
-// Four columns of bias, from column c; `left` of them exist.
-__device__ __forceinline__ f32x4 bias_at(const Epilogue& e, int32_t c, int left) {
-  f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  if (e.bias) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < left) v[j] = bf16_one(e.bias[place_at<true>(e.bias_place, c + j)]);
+// What the epilogue reads beside the sums: 8 columns from column c of row r.
+// N: the matrix's columns (rows of pre lie densely).
+struct Beside {
+  u32x4 add, pre;
+};
+__device__ __forceinline__ Beside beside_at(const Epilogue& e, int32_t N, int64_t r, int32_t c, int left) {
+  Beside b{{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
+  if (e.add) {
+    const uint16_t* p = e.add + r * e.add_stride + c;
+    b.add = left >= 8 ? *(const u32x4_a2*)p : load_some(p, left);
   }
-  return v;
+  if (e.pre_in) {
+    const uint16_t* p = e.pre_in + r * N + c;
+    b.pre = left >= 8 ? *(const u32x4_a2*)p : load_some(p, left);
+  }
+  return b;
 }
 
-// Four sums of row r, columns c to c + 3, of which `left` exist.  N: the
-// matrix's columns (rows of pre lie densely).
-__device__ __forceinline__ void finish4(const Epilogue& e, int32_t N, int64_t r, int32_t c, int left, f32x4 v,
-                                        f32x4 bias) {
-  f32x4 add = {0.f, 0.f, 0.f, 0.f};
-  if (e.add) add = bf16x4_at(e.add + r * e.add_stride + c, left);
+// Eight sums of row r, columns c to c + 7, of which `left` exist.
+__device__ __forceinline__ void finish8(const Epilogue& e, int32_t N, int64_t r, int32_t c, int left, float (&v)[8],
+                                        const Beside& b, const float (&bias)[8]) {
+  float add[8];
+  widen8(b.add, add);
   if (e.grad) {
-    v = v + add;
-    if (e.act != ZERO_ACT_NONE) v = v * apply4<true>(e.act, bf16x4_at(e.pre_in + r * N + c, left));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += add[j];
+    if (e.act != ZERO_ACT_NONE) {
+      float s[8];
+      widen8(b.pre, s);
+      apply8<true>(e.act, s);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= s[j];
+    }
   } else {
-    v = v + bias;
-    if (e.pre_out) bf16x4_to(e.pre_out + r * N + c, v, left);
-    v = apply4<false>(e.act, v) + add;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += bias[j];
+    if (e.pre_out) {
+      uint16_t* p = e.pre_out + r * N + c;
+      if (left >= 8)
+        *(u32x4_a2*)p = round8(v);
+      else
+        store_some(p, round8(v), left);
+    }
+    apply8<false>(e.act, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += add[j];
   }
   if (e.f32) {
     float* o = (float*)e.out + r * e.out_stride + c;
-    if (left >= 4) {
-      *(f32x4_a4*)o = v;
+    if (left >= 8) {
+      *(f32x4_a4*)o = f32x4{v[0], v[1], v[2], v[3]};
+      *(f32x4_a4*)(o + 4) = f32x4{v[4], v[5], v[6], v[7]};
     } else {
 #pragma unroll
-      for (int j = 0; j < 3; ++j)
+      for (int j = 0; j < 7; ++j)
         if (j < left) o[j] = v[j];
     }
   } else {
-    bf16x4_to((uint16_t*)e.out + r * e.out_stride + c, v, left);
+    uint16_t* o = (uint16_t*)e.out + r * e.out_stride + c;
+    if (left >= 8)
+      *(u32x4_a2*)o = round8(v);
+    else
+      store_some(o, round8(v), left);
   }
 }
 
@@ -214,7 +244,7 @@ template <class S, bool NC>
 __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(const Args A) {
   constexpr int W = S::W, kSide = S::kSide;
   using BRows = std::conditional_t<NC, NRows<S>, KRows<S>>;
-  __shared__ __align__(1024) char shared[2 * S::kBuffer];
+  __shared__ __align__(1024) char shared[S::kLds];
   lds_char* lds = (lds_char*)shared;
   const uint32_t lds_base = (uint32_t)(uintptr_t)lds;
 
@@ -252,30 +282,30 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
   BRows rb;
   ra.set(r0, A.M, A.a_stride);
   rb.set(c0, A.N, A.b_stride);
-  const char* const pa = (const char*)(A.a + r0 * A.a_stride);
-  const char* const pb = (const char*)(A.b + (NC ? (int64_t)c0 : c0 * A.b_stride));
+  const char* const pa = uniform((const char*)(A.a + r0 * A.a_stride));
+  const char* const pb = uniform((const char*)(A.b + (NC ? (int64_t)c0 : c0 * A.b_stride)));
   const int32_t steps = sz - sa;
   // The step that may not be whole, the last one of k, is a block's first: the
   // others need no checks.  at: the number in k of a block's step i.
   const bool has_end = sz == all_steps;
-  const auto at = [&](int32_t i) { return has_end ? (i == 0 ? all_steps - 1 : sa + i - 1) : sa + i; };
+  const auto at = [&](int32_t i) ZERO_INLINE { return has_end ? (i == 0 ? all_steps - 1 : sa + i - 1) : sa + i; };
   const uint32_t mine = lds_base + wave * S::kLoads * 1024;
   // request j for step i; 0 to kLoads - 1 are A's
-  const auto fetch1 = [&](const char* a_at, const char* b_at, int buf, auto index) {
+  const auto fetch1 = [&](const char* a_at, const char* b_at, int buf, auto index) ZERO_INLINE {
     constexpr int j = decltype(index)::value;
     if constexpr (j < S::kLoads)
       request(a_at, ra.off[j], mine + buf * S::kBuffer + j * 1024);
     else
       request(b_at, rb.off[j - S::kLoads], mine + buf * S::kBuffer + S::kOperand + (j - S::kLoads) * 1024);
   };
-  const auto a_of = [&](int32_t i) { return pa + (int64_t)at(i) * KRows<S>::step_bytes(A.a_stride); };
-  const auto b_of = [&](int32_t i) { return pb + (int64_t)at(i) * BRows::step_bytes(A.b_stride); };
-  const auto fetch = [&](int32_t i, int buf) {
+  const auto a_of = [&](int32_t i) ZERO_INLINE { return uniform(pa + (int64_t)at(i) * KRows<S>::step_bytes(A.a_stride)); };
+  const auto b_of = [&](int32_t i) ZERO_INLINE { return uniform(pb + (int64_t)at(i) * BRows::step_bytes(A.b_stride)); };
+  const auto fetch = [&](int32_t i, int buf) ZERO_INLINE {
     const char *a_at = a_of(i), *b_at = b_of(i);
-    unrolled<2 * S::kLoads>([&](auto j) { fetch1(a_at, b_at, buf, j); });
+    unrolled<2 * S::kLoads>([&](auto j) ZERO_INLINE { fetch1(a_at, b_at, buf, j); });
   };
   // The first step, its k from `left` on replaced by zeros.
-  const auto fetch_first = [&]() {
+  const auto fetch_first = [&]() ZERO_INLINE {
     const char *a_at = a_of(0), *b_at = b_of(0);
     const int left_a = A.K - at(0) * kStep, left_b = (NC ? A.Kb : A.K) - at(0) * kStep;
 #pragma unroll
@@ -297,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
   const lds_char* const fa = lds + wm * W * 4096 + KRows<S>::frag_offset();
   const lds_char* const fb = lds + S::kOperand + wn * W * 4096 + BRows::frag_offset();
   bf16x8 a[2][W], b[2][W];
-  const auto read1 = [&](auto set, int buf, int s, auto index) {
+  const auto read1 = [&](auto set, int buf, int s, auto index) ZERO_INLINE {
     constexpr int to = decltype(set)::value, j = decltype(index)::value;
     if constexpr (j < W)
       a[to][j] = KRows<S>::frag(fa + buf * S::kBuffer, j, s);
@@ -306,15 +336,15 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
   };
   constexpr std::integral_constant<int, 0> k0;  // the two sets of fragments
   constexpr std::integral_constant<int, 1> k1;
-  const auto read = [&](auto set, int buf, int s) {
-    unrolled<2 * W>([&](auto j) { read1(set, buf, s, j); });
+  const auto read = [&](auto set, int buf, int s) ZERO_INLINE {
+    unrolled<2 * W>([&](auto j) ZERO_INLINE { read1(set, buf, s, j); });
   };
   // The products of one stretch of 16 k; after each of them `beside` puts its
   // share of other work.
   constexpr int kM = W * W;
-  const auto multiply = [&](auto set, auto beside) {
+  const auto multiply = [&](auto set, auto beside) ZERO_INLINE {
     constexpr int from = decltype(set)::value;
-    unrolled<kM>([&](auto index) {
+    unrolled<kM>([&](auto index) ZERO_INLINE {
       constexpr int i = decltype(index)::value;
       acc[i / W][i % W] =
           __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[from][i / W], b[from][i % W], acc[i / W][i % W], 0, 0, 0);
@@ -323,19 +353,19 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
     });
   };
   // f(j) for those of N things that go beside product I
-  const auto share = [](auto index, auto count, auto f) {
+  const auto share = [](auto index, auto count, auto f) ZERO_INLINE {
     constexpr int i = decltype(index)::value, n = decltype(count)::value;
     constexpr int first = (i * n + kM - 1) / kM, next = ((i + 1) * n + kM - 1) / kM;
-    unrolled<next - first>([&](auto j) { f(std::integral_constant<int, first + decltype(j)::value>{}); });
+    unrolled<next - first>([&](auto j) ZERO_INLINE { f(std::integral_constant<int, first + decltype(j)::value>{}); });
   };
   constexpr std::integral_constant<int, 2 * W> kReads;
   constexpr std::integral_constant<int, 2 * S::kLoads> kRequests;
-  const auto with_reads = [&](auto from, auto to, int buf, int s) {
-    multiply(from, [&](auto index) { share(index, kReads, [&](auto j) { read1(to, buf, s, j); }); });
+  const auto with_reads = [&](auto from, auto to, int buf, int s) ZERO_INLINE {
+    multiply(from, [&](auto index) ZERO_INLINE { share(index, kReads, [&](auto j) ZERO_INLINE { read1(to, buf, s, j); }); });
   };
   // Step i, in buffer `buf`.  NEXT: steps that follow, two or more of which
   // the first of those is requested.
-  const auto step = [&](auto next, int32_t i, int buf) {
+  const auto step = [&](auto next, int32_t i, int buf) ZERO_INLINE {
     constexpr int kNext = decltype(next)::value;
     with_reads(k0, k1, buf, 1);
     with_reads(k1, k0, buf, 2);
@@ -344,14 +374,14 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
     __syncthreads();
     if constexpr (kNext > 1) {
       const char *a_at = a_of(i + 2), *b_at = b_of(i + 2);
-      multiply(k1, [&](auto index) {
-        share(index, kReads, [&](auto j) { read1(k0, buf ^ 1, 0, j); });
-        share(index, kRequests, [&](auto j) { fetch1(a_at, b_at, buf, j); });
+      multiply(k1, [&](auto index) ZERO_INLINE {
+        share(index, kReads, [&](auto j) ZERO_INLINE { read1(k0, buf ^ 1, 0, j); });
+        share(index, kRequests, [&](auto j) ZERO_INLINE { fetch1(a_at, b_at, buf, j); });
       });
     } else if constexpr (kNext > 0) {
       with_reads(k1, k0, buf ^ 1, 0);
     } else {
-      multiply(k1, [](auto) {});
+      multiply(k1, [](auto) ZERO_INLINE {});
     }
   };
   if (steps > 0) {
@@ -372,36 +402,58 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
   // lane l, register k: row 8*(k/4) + 4*(l/32) + k%4, column l%32
   if (tile < A.whole) {
     // A wave's sums leave 32 rows at a time through LDS of its own, from where
-    // a lane gets 4 columns of a row.
-    constexpr int kCols = W * 32, kStride = kCols + 8;  // 4 rows are 32 banks apart
-    constexpr int kAcross = kCols / 4, kDown = 64 / kAcross, kVecs = 32 / kDown;
-    static_assert(4 * 32 * kStride * 4 <= 2 * S::kBuffer, "the strips fit the buffers");
+    // a lane gets 8 columns of a row.  What the epilogue reads of the next 32
+    // rows is on its way meanwhile; it waits in LDS too, so that the
+    // activations stand in a loop and not in every piece's code.
+    constexpr int kVecs = S::kVecs, kDown = S::kDown, kRow = S::kRow;
     typedef __attribute__((address_space(3))) float lds_f32;
     typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
-    __syncthreads();
-    lds_f32* const strip = (lds_f32*)lds + wave * 32 * kStride;
-    const int down = lane / kAcross, across = lane % kAcross * 4;
-    const int32_t c = c0 + wn * kCols + across;
+    lds_char* const way = lds + wave * S::kWay;
+    lds_f32* const strip = (lds_f32*)way;
+    lds_u32x4* const kept = (lds_u32x4*)(way + S::kStrip) + lane;
+    const int down = lane / S::kAcross, across = lane % S::kAcross * 8;
+    const int32_t c = c0 + wn * S::kCols + across;
     const int left = A.N - c;
-    const f32x4 bias = bias_at(A.e, c, left);
-    const auto put = [&](auto index) {
+    const bool reads = A.e.add || A.e.pre_in;
+    float bias[8];
+    bias_at(A.e, c, left, bias);
+    Beside b[kVecs];
+    const auto fetch_beside = [&](int m) ZERO_INLINE {
+      if (!reads) return;
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        const int32_t r = r0 + (wm * W + m) * 32 + i * kDown + down;
+        b[i] = beside_at(A.e, A.N, r, c, r < A.M ? left : 0);
+      }
+    };
+    fetch_beside(0);
+    __syncthreads();
+    unrolled<W>([&](auto index) ZERO_INLINE {
       constexpr int m = decltype(index)::value;
 #pragma unroll
       for (int n = 0; n < W; ++n)
 #pragma unroll
         for (int k = 0; k < 16; ++k)
-          strip[(8 * (k >> 2) + (k & 3) + 4 * (lane >> 5)) * kStride + n * 32 + (lane & 31)] = acc[m][n][k];
-    };
-    unrolled<W>([&](auto index) {
-      constexpr int m = decltype(index)::value;
-      put(index);
+          strip[(8 * (k >> 2) + (k & 3) + 4 * (lane >> 5)) * kRow + n * 32 + (lane & 31)] = acc[m][n][k];
+      if (reads) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+          kept[i * 128] = b[i].add;
+          kept[i * 128 + 64] = b[i].pre;
+        }
+      }
       lanes_meet_in_lds();
+      if constexpr (m + 1 < W) fetch_beside(m + 1);
       const int32_t rb = r0 + (wm * W + m) * 32 + down;
 #pragma unroll 1
       for (int i = 0; i < kVecs; ++i) {
-        const f32x4 v = *(const lds_f32x4*)(strip + (i * kDown + down) * kStride + across);
+        const lds_f32x4* p = (const lds_f32x4*)(strip + (i * kDown + down) * kRow + across);
+        const f32x4 lo = p[0], hi = p[1];
+        float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        Beside x{{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
+        if (reads) x = Beside{kept[i * 128], kept[i * 128 + 64]};
         const int32_t r = rb + i * kDown;
-        if (r < A.M && left > 0) finish4(A.e, A.N, r, c, left, v, bias);
+        if (r < A.M && left > 0) finish8(A.e, A.N, r, c, left, v, x, bias);
       }
       lanes_meet_in_lds();
     });
@@ -427,15 +479,23 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const Args A, int32_t par
   int32_t r0, c0;
   tile_place(A.whole + at, A.row_tiles, A.col_tiles, r0, c0);
   const float* from = A.partial + (int64_t)at * A.splits * SIDE * SIDE;
-  const int per = SIDE * SIDE / 4 / parts;
+  const int per = SIDE * SIDE / 8 / parts;
   for (int g = part * per + threadIdx.x; g < (part + 1) * per; g += kThreads) {
-    const int32_t r = r0 * SIDE + g / (SIDE / 4), c = c0 * SIDE + (g % (SIDE / 4)) * 4;
+    const int32_t r = r0 * SIDE + g / (SIDE / 8), c = c0 * SIDE + (g % (SIDE / 8)) * 8;
     const int left = A.N - c;
     if (r >= A.M || left <= 0) continue;
-    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    const Beside b = beside_at(A.e, A.N, r, c, left);
+    float bias[8];
+    bias_at(A.e, c, left, bias);
+    f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-    for (int k = 0; k < A.splits; ++k) s += *(const f32x4*)(from + (int64_t)k * SIDE * SIDE + g * 4);
-    finish4(A.e, A.N, r, c, left, s, bias_at(A.e, c, left));
+    for (int k = 0; k < A.splits; ++k) {
+      const f32x4* p = (const f32x4*)(from + (int64_t)k * SIDE * SIDE + g * 8);
+      lo += p[0];
+      hi += p[1];
+    }
+    float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    finish8(A.e, A.N, r, c, left, v, b, bias);
   }
 }
 
@@ -573,7 +633,7 @@ int launch(const Args& A, const Plan& p, bool n_adjacent, hipStream_t s) {
     hipLaunchKernelGGL((product_kernel<S, false>), grid, dim3(kThreads), 0, s, A);
   const int rc = launched();
   if (rc != ZERO_OK || p.further == 0) return rc;
-  int32_t parts = S::kSide * S::kSide / 1024;
+  int32_t parts = S::kSide * S::kSide / 2048;
   while (parts > 1 && parts * p.further > 2048) parts >>= 1;
   hipLaunchKernelGGL(sum_kernel<S::kSide>, dim3((unsigned)(p.further * parts)), dim3(kThreads), 0, s, A, parts);
   return launched();
