@@ -87,8 +87,14 @@ __device__ __forceinline__ void widen8(u32x4 w, float (&x)[8]) {
     x[2 * k + 1] = bf16_hi(w[k]);
   }
 }
+// To nearest, ties to even, subnormals kept, by the conversion instruction.
+__device__ __forceinline__ uint32_t round2(float lo, float hi) {
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{lo, hi}), v2b));
+}
 __device__ __forceinline__ u32x4 round8(const float (&x)[8]) {
-  return u32x4{bf16_pack2(x[0], x[1]), bf16_pack2(x[2], x[3]), bf16_pack2(x[4], x[5]), bf16_pack2(x[6], x[7])};
+  return u32x4{round2(x[0], x[1]), round2(x[2], x[3]), round2(x[4], x[5]), round2(x[6], x[7])};
 }
 // The first n of 8 neighbouring values, n below 8; the others are zeros.
 __device__ __forceinline__ u32x4 load_some(const uint16_t* p, int n) {

@@ -95,7 +95,11 @@ __device__ __forceinline__ void request(const void* base, uint32_t off, uint32_t
                :
                : "s"(lds), "v"(off), "s"(base));
 }
-__device__ __forceinline__ void requests_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// All but the last N of them.
+template <int N = 0>
+__device__ __forceinline__ void requests_done() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
 
 // One wave's requests for an operand with k adjacent: rows 8 * (wave * kLoads +
 // j) to + 7 of the tile; lane l fetches chunk (l % 8) ^ (l / 8) of row l / 8.
@@ -304,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
     const char *a_at = a_of(i), *b_at = b_of(i);
     unrolled<2 * S::kLoads>([&](auto j) ZERO_INLINE { fetch1(a_at, b_at, buf, j); });
   };
-  // The first step, its k from `left` on replaced by zeros.
+  // The first two steps, the first one's k from `left` on replaced by zeros.
   const auto fetch_first = [&]() ZERO_INLINE {
     const char *a_at = a_of(0), *b_at = b_of(0);
     const int left_a = A.K - at(0) * kStep, left_b = (NC ? A.Kb : A.K) - at(0) * kStep;
@@ -313,7 +317,12 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
       request(a_at, ra.at(j, left_a), mine + j * 1024);
       request(b_at, rb.at(j, left_b), mine + S::kOperand + j * 1024);
     }
-    requests_done();
+    if (steps > 1) {
+      fetch(1, 1);
+      requests_done<2 * S::kLoads>();
+    } else {
+      requests_done();
+    }
     if (left_a < kStep || left_b < kStep) {
       lds_char* p = lds + wave * S::kLoads * 1024 + lane * 16;
 #pragma unroll 1
@@ -387,7 +396,6 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
   if (steps > 0) {
     fetch_first();
     __syncthreads();
-    if (steps > 1) fetch(1, 1);
     read(k0, 0, 0);
     int32_t i = 0;
 #pragma unroll 1
@@ -445,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
       lanes_meet_in_lds();
       if constexpr (m + 1 < W) fetch_beside(m + 1);
       const int32_t rb = r0 + (wm * W + m) * 32 + down;
-#pragma unroll 1
+#pragma unroll 2
       for (int i = 0; i < kVecs; ++i) {
         const lds_f32x4* p = (const lds_f32x4*)(strip + (i * kDown + down) * kRow + across);
         const f32x4 lo = p[0], hi = p[1];
