@@ -102,29 +102,33 @@ __device__ __forceinline__ void requests_done() {
 }
 
 // One wave's requests for an operand with k adjacent: rows 8 * (wave * kLoads +
-// j) to + 7 of the tile; lane l fetches chunk (l % 8) ^ (l / 8) of row l / 8.
+// j) to + 7 of the tile; in LDS chunk c of row r lies at c ^ (r / 2 % 8), so
+// that the 16 rows of which 16 lanes read one chunk each fill the 64 banks.
 template <class S>
 struct KRows {
   uint32_t off[S::kLoads];
-  static __device__ __forceinline__ int chunk() { return ((threadIdx.x & 7) ^ ((threadIdx.x >> 3) & 7)); }
+  // the chunk that a lane fetches in request j (kLoads is even)
+  static __device__ __forceinline__ int chunk(int j) {
+    return (threadIdx.x & 7) ^ (((threadIdx.x >> 4) & 3) + 4 * (j & 1));
+  }
   __device__ __forceinline__ void set(int32_t r0, int32_t rows, int64_t stride) {
     const int wave = threadIdx.x >> 6;
 #pragma unroll
     for (int j = 0; j < S::kLoads; ++j) {
       const int r = min((wave * S::kLoads + j) * 8 + (int)((threadIdx.x >> 3) & 7), rows - 1 - r0);
-      off[j] = (uint32_t)(r * stride) * 2u + chunk() * 16;
+      off[j] = (uint32_t)(r * stride) * 2u + chunk(j) * 16;
     }
   }
   // `left`: k of this step that there are (kStep: all)
   __device__ __forceinline__ uint32_t at(int j, int left) const {
-    return left >= kStep || chunk() * 8 < left ? off[j] : off[j] - chunk() * 16;
+    return left >= kStep || chunk(j) * 8 < left ? off[j] : off[j] - chunk(j) * 16;
   }
-  static __device__ __forceinline__ bool missing(int, int left) { return chunk() * 8 >= left; }
+  static __device__ __forceinline__ bool missing(int j, int left) { return chunk(j) * 8 >= left; }
   static __device__ __forceinline__ int64_t step_bytes(int64_t) { return kStep * 2; }
   // fragment: 32 rows x 16 k; lane l holds row l % 32, k 8 * (l / 32) to + 7
   static __device__ __forceinline__ int frag_offset() { return (threadIdx.x & 31) * 128; }
   static __device__ __forceinline__ bf16x8 frag(const lds_char* p, int panel, int s) {
-    const int c = (2 * s + (int)((threadIdx.x >> 5) & 1)) ^ (int)(threadIdx.x & 7);
+    const int c = (2 * s + (int)((threadIdx.x >> 5) & 1)) ^ (int)((threadIdx.x >> 1) & 7);
     typedef __attribute__((address_space(3))) bf16x8 lds_t;
     return *(const lds_t*)(p + panel * 4096 + c * 16);
   }
