@@ -15,10 +15,11 @@
 // in NL neighbouring lanes, 8 pairs (16 columns) each, so the two columns of a
 // pair meet in one lane, and a lane's cosines and sines stay in its registers
 // for all the heads of a token that the lane works on.  The sums over a row go
-// through data-parallel moves between the lanes; nothing waits for LDS.
+// through data-parallel moves between the lanes.
 #include <algorithm>
 
-#include "tensor_place.hpp"
+#include "act8.hpp"
+#include "matrix.hpp"
 
 namespace {
 using namespace zs;
@@ -40,6 +41,8 @@ struct Heads {
   View x, dy, out;
   Place place;
   int32_t heads, normed;
+  int32_t log_across;  // a wave's rows at a time: 2^log_across heads of a token, the rest tokens
+  int32_t per_chunk;   // heads of a block
 };
 struct Args {
   Heads side[2];
@@ -52,7 +55,7 @@ struct Args {
   int32_t d, half;            // columns of a head, pairs that turn
   int32_t upto[kMaxAxes];     // pairs below upto[a] (and not below upto[a - 1]) turn by axis a
   int32_t neighbours;         // pairs are neighbouring columns
-  int32_t per_chunk, chunks;  // heads of a block; chunks of the first side
+  int32_t chunks;             // of the first side
   float eps;
 };
 
@@ -183,31 +186,22 @@ __device__ __forceinline__ void store_row(const Args& A, uint16_t* p, const Cols
   }
 }
 
-// Cosines and sines of a lane's pairs for one token.  The angle is counted in
-// turns in 64 bits, where whole turns fall away without loss: position 10^6
-// at frequency 1 is off by 10^-10 of a turn.
+// Cosine and sine of pair m of lane `lane` of a row for token t.  The angle is
+// counted in turns in 64 bits, where whole turns fall away without loss:
+// position 10^6 at frequency 1 is off by 10^-10 of a turn.
 template <int NL, int MODE>
-__device__ __forceinline__ void turns(const Args& A, int64_t t, int lane, float (&co)[8], float (&si)[8]) {
-  int last = -1;
-  double pos = 0;
+__device__ __forceinline__ f32x2 turn(const Args& A, int64_t t, int lane, int m) {
+  const int j = pair_of<NL, MODE>(A, lane, m);
+  if (j >= A.half) return f32x2{1.f, 0.f};
+  int axis = 0;
 #pragma unroll
-  for (int m = 0; m < 8; ++m) {
-    const int j = pair_of<NL, MODE>(A, lane, m);
-    co[m] = 1.f;
-    si[m] = 0.f;
-    if (j < A.half) {
-      int axis = 0;
-#pragma unroll
-      for (int a = 0; a < kMaxAxes - 1; ++a) axis += j >= A.upto[a] ? 1 : 0;
-      if (axis != last) {
-        const int64_t at = axis * A.tokens + t;
-        pos = A.wide ? (double)((const int64_t*)A.positions)[at] : (double)((const int32_t*)A.positions)[at];
-        last = axis;
-      }
-      const double x = pos * (A.freqs[j] * 0.15915494309189533577);
-      sincospif(2.f * (float)(x - __builtin_rint(x)), &si[m], &co[m]);
-    }
-  }
+  for (int a = 0; a < kMaxAxes - 1; ++a) axis += j >= A.upto[a] ? 1 : 0;
+  const int64_t at = axis * A.tokens + t;
+  const double pos = A.wide ? (double)((const int64_t*)A.positions)[at] : (double)((const int32_t*)A.positions)[at];
+  const double x = pos * (A.freqs[j] * 0.15915494309189533577);
+  float si, co;
+  sincospif(2.f * (float)(x - __builtin_rint(x)), &si, &co);
+  return f32x2{co, si};
 }
 
 // A side's weights as binary32, in LDS in the lanes' order: x's of a lane, then y's.
@@ -231,22 +225,30 @@ __device__ __forceinline__ void weights_to_lds(const Args& A, const Heads& s, fl
   }
 }
 
-// Heads whose loads a lane has in flight.
+// Rows whose loads a lane has in flight.
 constexpr int kAhead = 4;
 
 template <int NL, int MODE, bool GRAD>
 __global__ void __launch_bounds__(kThreads) rotate_kernel(const Args A) {
-  constexpr int kGroups = kThreads / NL;
-  __shared__ alignas(16) float w_lds[NL * 16];
-  const int lane = threadIdx.x % NL, group = threadIdx.x / NL;
+  constexpr int kGroups = 64 / NL, kWaves = kThreads / 64;
+  constexpr int kLane = 17;  // a lane's 16 sums, apart by one against bank conflicts
+  // the weights at first, then each wave's cosines and sines, at last the sums
+  constexpr int kTable = kGroups * NL * 8;  // of 512 pairs at most
+  __shared__ alignas(16) char shared[GRAD && kThreads * kLane * 4 > kWaves * kTable * 8 ? kThreads * kLane * 4
+                                                                                        : kWaves * kTable * 8];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
+  const int lane = l % NL, group = l / NL;
   const int side = (int)blockIdx.y >= A.chunks ? 1 : 0;
   const Heads& s = A.side[side];
   const int chunk = side ? (int)blockIdx.y - A.chunks : (int)blockIdx.y;
-  const int h0 = chunk * A.per_chunk, h1 = min(s.heads, h0 + A.per_chunk);
+  const int across = 1 << s.log_across, down = kGroups >> s.log_across;
+  const int head_in = group & (across - 1), token_in = group >> s.log_across;
+  const int h0 = chunk * s.per_chunk, h1 = min(s.heads, h0 + s.per_chunk);
   const Cols c = cols_of<NL, MODE>(A, lane);
   const bool normed = s.normed;
   float wx[8], wy[8];
   if (normed) {
+    float* w_lds = (float*)shared;
     weights_to_lds<NL, MODE>(A, s, w_lds);
     __syncthreads();
 #pragma unroll
@@ -254,6 +256,7 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const Args A) {
       wx[m] = w_lds[lane * 16 + m];
       wy[m] = w_lds[lane * 16 + 8 + m];
     }
+    __syncthreads();
   } else {
 #pragma unroll
     for (int m = 0; m < 8; ++m) wx[m] = wy[m] = 1.f;
@@ -263,14 +266,29 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const Args A) {
 #pragma unroll
     for (int m = 0; m < 8; ++m) dwx[m] = dwy[m] = 0.f;
   }
+  f32x2* const table = (f32x2*)shared + wave * kTable;
   const float inv_d = 1.f / (float)A.d;
   // all lanes of a wave stay in the loops together: their rows' sums meet
-  for (int64_t t0 = (int64_t)blockIdx.x * kGroups; t0 < A.tokens; t0 += (int64_t)gridDim.x * kGroups) {
-    const int64_t t = t0 + group;
+  for (int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * down; t0 < A.tokens;
+       t0 += (int64_t)gridDim.x * kWaves * down) {
+    const int64_t t = t0 + token_in;
     const bool here = t < A.tokens;
     float co[8], si[8];
-    if (A.half > 0 && here) {
-      turns<NL, MODE>(A, t, lane, co, si);
+    if (A.half > 0) {
+      // The pairs of the wave's tokens are dealt to its lanes, and collected
+      // by those that need them.
+      for (int v = l; v < down * NL * 8; v += 64) {
+        const int64_t u = t0 + v / (NL * 8);
+        if (u < A.tokens) table[v] = turn<NL, MODE>(A, u, v / 8 % NL, v % 8);
+      }
+      lanes_meet_in_lds();
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        const f32x2 q = table[(token_in * NL + lane) * 8 + m];
+        co[m] = q.x;
+        si[m] = q.y;
+      }
+      lanes_meet_in_lds();
     } else {
 #pragma unroll
       for (int m = 0; m < 8; ++m) co[m] = 1.f, si[m] = 0.f;
@@ -278,19 +296,19 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const Args A) {
     const uint16_t* px = (const uint16_t*)s.x.p + t * s.x.token;
     const uint16_t* py = GRAD ? (const uint16_t*)s.dy.p + t * s.dy.token : nullptr;
     uint16_t* po = (uint16_t*)s.out.p + t * s.out.token;
-    for (int hb = h0; hb < h1; hb += kAhead) {
+    for (int hb = h0; hb < h1; hb += kAhead * across) {
       Row rx[kAhead], ry[GRAD ? kAhead : 1];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const int h = hb + k;
+        const int h = hb + k * across + head_in;
         const bool live = here && h < h1;
         if (!GRAD || normed) rx[k] = load_row<MODE, NL>(A, px + h * s.x.head, c, lane, live);
         if constexpr (GRAD) ry[k] = load_row<MODE, NL>(A, py + h * s.dy.head, c, lane, live);
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const int h = hb + k;
-        if (h >= h1) break;
+        if (hb + k * across >= h1) break;
+        const int h = hb + k * across + head_in;
         float x[8], y[8], ox[8], oy[8];
         if constexpr (!GRAD) {
           widen<MODE>(rx[k], x, y);
@@ -335,16 +353,15 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const Args A) {
             }
           }
         }
-        store_row<MODE, NL>(A, po + h * s.out.head, c, lane, here, ox, oy);
+        store_row<MODE, NL>(A, po + h * s.out.head, c, lane, here && h < h1, ox, oy);
       }
     }
   }
   if constexpr (GRAD) {
     if (!normed) return;
-    // the groups' sums, in order; 16 columns of a lane apart by one against
-    // bank conflicts
-    constexpr int kLane = 17;
-    __shared__ float sum[kThreads * kLane];
+    // the groups' sums, in order
+    __syncthreads();
+    float* sum = (float*)shared;
 #pragma unroll
     for (int m = 0; m < 8; ++m) {
       sum[threadIdx.x * kLane + m] = dwx[m];
@@ -354,7 +371,7 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const Args A) {
     float* to = A.partial + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (NL * 16);
     for (int k = threadIdx.x; k < NL * 16; k += kThreads) {
       float v = 0.f;
-      for (int g = 0; g < kGroups; ++g) v += sum[(g * NL + (k >> 4)) * kLane + (k & 15)];
+      for (int g = 0; g < kThreads / NL; ++g) v += sum[(g * NL + (k >> 4)) * kLane + (k & 15)];
       to[k] = v;
     }
   }
@@ -413,29 +430,39 @@ int lanes_for(int32_t d) {
   return n;
 }
 
-// The launch: heads of a block so that about 2048 blocks have work, or one
-// where there are fewer tokens; a block's tokens at a time; at most 512 blocks
-// along the tokens.  A function of the shape alone, and so is the order of
-// the weights' sums.
-constexpr int64_t kBlocks = 2048, kMaxAlong = 512;
+// The launch.  A wave works on neighbouring heads of a token, so that what it
+// reads and writes at a time lies together, and on several tokens where there
+// are fewer heads than its groups of lanes.  All heads of a token go to one
+// block, or, where that leaves fewer than kBlocks, parts of them to several.
+// Backward, at most kMaxAlong blocks share the tokens.  A function of the shape
+// alone, and so is the order of the weights' sums.
+constexpr int64_t kBlocks = 1024, kMaxAlong = 512;
 struct Plan {
   int nl;
-  int32_t per_chunk, chunks[2];
+  int32_t log_across[2], per_chunk[2], chunks[2];
   int64_t along, bytes;
 };
-Plan make_plan(int64_t tokens, int32_t d, int32_t q_heads, int32_t k_heads) {
+Plan make_plan(int64_t tokens, int32_t d, const int32_t (&heads)[2], bool grad) {
   Plan p;
   p.nl = lanes_for(d);
-  const int64_t groups = kThreads / p.nl;
-  const int64_t need = std::max<int64_t>(1, (tokens + groups - 1) / groups);
-  p.along = std::min(need, kMaxAlong);
-  const int64_t heads = (int64_t)q_heads + k_heads;
-  const int64_t wanted = std::min<int64_t>(std::max<int64_t>(1, heads), (kBlocks + p.along - 1) / p.along);
-  int64_t per = std::max<int64_t>(1, (heads + wanted - 1) / wanted);
-  if (per > kAhead) per = (per + kAhead - 1) / kAhead * kAhead;
-  p.per_chunk = (int32_t)per;
-  p.chunks[0] = (int32_t)((q_heads + per - 1) / per);
-  p.chunks[1] = (int32_t)((k_heads + per - 1) / per);
+  const int groups = 64 / p.nl;
+  int64_t need[2] = {1, 1};
+  p.along = 1;
+  for (int n = 0; n < 2; ++n) {
+    p.log_across[n] = 0;
+    while ((1 << p.log_across[n]) < std::min<int64_t>(heads[n], groups)) ++p.log_across[n];
+    const int64_t at_once = (int64_t)(kThreads / 64) * (groups >> p.log_across[n]);
+    need[n] = std::max<int64_t>(1, (tokens + at_once - 1) / at_once);
+    if (heads[n] > 0) p.along = std::max(p.along, need[n]);
+  }
+  p.along = std::min(p.along, grad ? kMaxAlong : (int64_t)1 << 22);
+  for (int n = 0; n < 2; ++n) {
+    const int64_t turns = ((int64_t)heads[n] + (1 << p.log_across[n]) - 1) >> p.log_across[n];
+    const int64_t parts = std::min(std::max<int64_t>(1, turns), (kBlocks + p.along - 1) / p.along);
+    const int64_t per = (turns + parts - 1) / parts;
+    p.per_chunk[n] = (int32_t)std::max<int64_t>(1, per << p.log_across[n]);
+    p.chunks[n] = (heads[n] + p.per_chunk[n] - 1) / p.per_chunk[n];
+  }
   p.bytes = (int64_t)(p.chunks[0] + p.chunks[1]) * p.along * p.nl * 16 * 4;
   return p;
 }
@@ -565,7 +592,7 @@ int run(const zero_layout* L, const uint16_t* params, int64_t tokens, int32_t d,
   const bool work = tokens > 0 && heads[0] + heads[1] > 0;
   const bool clears = g && (normed[0] || normed[1]) && (g->flags & (ZERO_ACC_OVERWRITE | ZERO_ACC_EMIT_BF16));
   if (!work && !clears) return ZERO_OK;
-  Plan p = make_plan(tokens, d, heads[0], heads[1]);
+  const Plan p = make_plan(tokens, d, heads, g != nullptr);
   const bool sums = g && work && (normed[0] || normed[1]);
   Args A{};
   int64_t lo[2] = {0, 0}, hi[2] = {0, 0};
@@ -637,6 +664,8 @@ int run(const zero_layout* L, const uint16_t* params, int64_t tokens, int32_t d,
       Heads& s = A.side[n];
       s.heads = heads[n];
       s.normed = normed[n] ? 1 : 0;
+      s.log_across = p.log_across[n];
+      s.per_chunk = p.per_chunk[n];
       if (heads[n] == 0) continue;
       s.x = View{(char*)side[n]->x.data_dev, side[n]->x.token_stride, side[n]->x.head_stride};
       s.dy = View{(char*)side[n]->dy.data_dev, side[n]->dy.token_stride, side[n]->dy.head_stride};
@@ -657,7 +686,6 @@ int run(const zero_layout* L, const uint16_t* params, int64_t tokens, int32_t d,
         A.upto[a] = n;
       }
     }
-    A.per_chunk = p.per_chunk;
     A.chunks = p.chunks[0];
     A.eps = (float)eps;
     A.partial = sums ? (float*)g->workspace : nullptr;
@@ -704,10 +732,10 @@ int64_t zero_head_norm_rotate_grad_workspace(const zero_layout* L, int64_t token
   const zero_heads* const side[2] = {q, k};
   const int rc = shape_ok(L, tokens, head_dim, side);
   if (rc != ZERO_OK) return rc;
-  const int32_t hq = q ? q->heads : 0, hk = k ? k->heads : 0;
+  const int32_t heads[2] = {q ? q->heads : 0, k ? k->heads : 0};
   const bool normed = (q && q->tensor >= 0) || (k && k->tensor >= 0);
-  if (!normed || tokens == 0 || hq + hk == 0) return 0;
-  return make_plan(tokens, head_dim, hq, hk).bytes;
+  if (!normed || tokens == 0 || heads[0] + heads[1] == 0) return 0;
+  return make_plan(tokens, head_dim, heads, true).bytes;
 }
 
 int zero_head_norm_rotate_grad(const zero_layout* L, const uint16_t* params_flat, int64_t tokens,
