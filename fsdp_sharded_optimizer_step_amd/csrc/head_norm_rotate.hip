@@ -141,6 +141,7 @@ __device__ __forceinline__ Row load_row(const Args& A, const uint16_t* p, const 
   return r;
 }
 __device__ __forceinline__ float half_of(uint32_t w, int k) { return k & 1 ? bf16_hi(w) : bf16_lo(w); }
+__device__ __forceinline__ float weight(const u32x4& w, int m) { return half_of(w[m >> 1], m); }
 template <int MODE>
 __device__ __forceinline__ void widen(const Row& r, float (&x)[8], float (&y)[8]) {
 #pragma unroll
@@ -204,9 +205,9 @@ __device__ __forceinline__ f32x2 turn(const Args& A, int64_t t, int lane, int m)
   return f32x2{co, si};
 }
 
-// A side's weights as binary32, in LDS in the lanes' order: x's of a lane, then y's.
+// A side's weights in LDS in the lanes' order: x's of a lane, then y's.
 template <int NL, int MODE>
-__device__ __forceinline__ void weights_to_lds(const Args& A, const Heads& s, float* w) {
+__device__ __forceinline__ void weights_to_lds(const Args& A, const Heads& s, uint16_t* w) {
   for (int k = threadIdx.x; k < NL * 16; k += kThreads) {
     const int lane = k >> 4, m = k & 7;
     int x, y;
@@ -221,15 +222,13 @@ __device__ __forceinline__ void weights_to_lds(const Args& A, const Heads& s, fl
       y = x + 1;
     }
     const int col = (k & 8) ? y : x;
-    w[k] = col < A.d ? bf16_one(A.params[place_at<true>(s.place, col)]) : 0.f;
+    w[k] = col < A.d ? A.params[place_at<true>(s.place, col)] : (uint16_t)0;
   }
 }
 
-// Rows whose loads a lane has in flight.
-constexpr int kAhead = 4;
-
 template <int NL, int MODE, bool GRAD>
-__global__ void __launch_bounds__(kThreads) rotate_kernel(const Args A) {
+__global__ void __launch_bounds__(kThreads, GRAD ? 3 : 4) rotate_kernel(const Args A) {
+  constexpr int kAhead = GRAD ? 2 : 4;  // rows whose loads a lane has in flight
   constexpr int kGroups = 64 / NL, kWaves = kThreads / 64;
   constexpr int kLane = 17;  // a lane's 16 sums, apart by one against bank conflicts
   // the weights at first, then each wave's cosines and sines, at last the sums
@@ -246,20 +245,13 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const Args A) {
   const int h0 = chunk * s.per_chunk, h1 = min(s.heads, h0 + s.per_chunk);
   const Cols c = cols_of<NL, MODE>(A, lane);
   const bool normed = s.normed;
-  float wx[8], wy[8];
+  u32x4 wx = {0u, 0u, 0u, 0u}, wy = wx;  // bf16, widened where they are used
   if (normed) {
-    float* w_lds = (float*)shared;
-    weights_to_lds<NL, MODE>(A, s, w_lds);
+    weights_to_lds<NL, MODE>(A, s, (uint16_t*)shared);
     __syncthreads();
-#pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      wx[m] = w_lds[lane * 16 + m];
-      wy[m] = w_lds[lane * 16 + 8 + m];
-    }
+    wx = ((const u32x4*)shared)[lane * 2];
+    wy = ((const u32x4*)shared)[lane * 2 + 1];
     __syncthreads();
-  } else {
-#pragma unroll
-    for (int m = 0; m < 8; ++m) wx[m] = wy[m] = 1.f;
   }
   float dwx[8], dwy[8];
   if constexpr (GRAD) {
@@ -318,7 +310,7 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const Args A) {
             for (int m = 0; m < 8; ++m) ss += x[m] * x[m] + y[m] * y[m];
             const float r = 1.f / __builtin_sqrtf(lanes_sum<NL>(ss) * inv_d + A.eps);
 #pragma unroll
-            for (int m = 0; m < 8; ++m) x[m] = x[m] * r * wx[m], y[m] = y[m] * r * wy[m];
+            for (int m = 0; m < 8; ++m) x[m] = x[m] * r * weight(wx, m), y[m] = y[m] * r * weight(wy, m);
           }
 #pragma unroll
           for (int m = 0; m < 8; ++m) {
@@ -339,7 +331,7 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const Args A) {
 #pragma unroll
             for (int m = 0; m < 8; ++m) {
               ss += x[m] * x[m] + y[m] * y[m];
-              sg += ox[m] * wx[m] * x[m] + oy[m] * wy[m] * y[m];
+              sg += ox[m] * weight(wx, m) * x[m] + oy[m] * weight(wy, m) * y[m];
             }
             const float r = 1.f / __builtin_sqrtf(lanes_sum<NL>(ss) * inv_d + A.eps);
             const float mean = lanes_sum<NL>(sg) * inv_d * r;  // of g*n
@@ -348,8 +340,8 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const Args A) {
               const float nx = x[m] * r, ny = y[m] * r;
               dwx[m] += ox[m] * nx;
               dwy[m] += oy[m] * ny;
-              ox[m] = r * (ox[m] * wx[m] - nx * mean);
-              oy[m] = r * (oy[m] * wy[m] - ny * mean);
+              ox[m] = r * (ox[m] * weight(wx, m) - nx * mean);
+              oy[m] = r * (oy[m] * weight(wy, m) - ny * mean);
             }
           }
         }
