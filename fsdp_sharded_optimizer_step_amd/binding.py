@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from dataclasses import dataclass
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -51,20 +52,11 @@ class _AdamW(C.Structure):
                 ("eps", C.c_double), ("weight_decay", C.c_double)]
 
 
-class _View(C.Structure):
-    _fields_ = [("data_dev", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
-
-
-class _Heads(C.Structure):
-    _fields_ = [("tensor", C.c_int32), ("heads", C.c_int32), ("x", _View), ("dy", _View), ("out", _View)]
-
-
+# zero_heads (tensor, heads, and address, token and head stride of x, dy and
+# out) and zero_rotation, packed: a call makes several of them
+_pack_heads = struct.Struct("@iiQqqQqqQqq").pack
+_pack_rotation = struct.Struct("@QQ7i4x").pack
 MAX_AXES = 4
-
-
-class _Rotation(C.Structure):
-    _fields_ = [("positions_dev", C.c_void_p), ("freqs_dev", C.c_void_p), ("position_bytes", C.c_int32),
-                ("n_axes", C.c_int32), ("sections", C.c_int32 * MAX_AXES), ("interleaved", C.c_int32)]
 
 
 DTYPE_BF16, DTYPE_F32 = 0, 1
@@ -146,10 +138,9 @@ def load():
                                              i32, vp, vp, vp, vp, vp, vp, i32, C.c_uint64, vp]
     lib.zero_moments8_pack.argtypes = [vp] * 8
     lib.zero_moments8_unpack.argtypes = [vp] * 8
-    heads, turn = C.POINTER(_Heads), C.POINTER(_Rotation)
-    lib.zero_head_norm_rotate.argtypes = [vp, vp, i64, i32, C.c_double, turn, heads, heads, vp]
-    lib.zero_head_norm_rotate_grad_workspace.argtypes = [vp, i64, i32, heads, heads]
-    lib.zero_head_norm_rotate_grad.argtypes = [vp, vp, i64, i32, C.c_double, turn, heads, heads, f32, u32,
+    lib.zero_head_norm_rotate.argtypes = [vp, vp, i64, i32, C.c_double, vp, vp, vp, vp]
+    lib.zero_head_norm_rotate_grad_workspace.argtypes = [vp, i64, i32, vp, vp]
+    lib.zero_head_norm_rotate_grad.argtypes = [vp, vp, i64, i32, C.c_double, vp, vp, vp, f32, u32,
                                                vp, vp, vp, i64, vp]
     lib.zero_linear_workspace.argtypes = [vp, i32, i32, vp, vp, i64, i64, i64, i64]
     lib.zero_linear.argtypes = [vp, i32, i32, i32, vp, vp, i64, i64, i64, i64, i32, vp, i64, vp, i64, i32,
@@ -210,9 +201,11 @@ class Layout:
             _check("zero_layout_create_dim0", lib.zero_layout_create_dim0(
                 arr, rarr, len(numel), int(n_d), int(rank), C.byref(h)))
         self._h = h
+        self._blocks = None
         self.n_tensors = len(numel)
         self.numel = [int(n) for n in numel]
         self.flat_len = lib.zero_layout_padded(h)
+        self.shard_len = lib.zero_layout_shard(h)
 
     @property
     def handle(self):
@@ -231,7 +224,13 @@ class Layout:
     n_d = property(lambda self: load().zero_layout_n_d(self._h))
     rank = property(lambda self: load().zero_layout_rank(self._h))
     kind = property(lambda self: load().zero_layout_kind(self._h))
-    moment_blocks = property(lambda self: load().zero_layout_moment_blocks(self._h))
+
+    @property
+    def moment_blocks(self):
+        """Scale bytes of a moment in 8 bits."""
+        if self._blocks is None:
+            self._blocks = load().zero_layout_moment_blocks(self._h)
+        return self._blocks
 
     def bucket(self, b: int):
         """-> (stream_off, len, padded_off, padded_len, shard_off)"""
@@ -434,16 +433,14 @@ class Moments8:
 
 def _moments8(where, layout, moments):
     """The four tensors, checked."""
-    torch = _types()[0]
-    n, blocks = layout.shard, layout.moment_blocks
-    ts = []
-    for name, need in (("exp_avg", n), ("exp_avg_scales", blocks), ("exp_avg_sq", n),
-                       ("exp_avg_sq_scales", blocks)):
-        t = getattr(moments, name)
-        _need(t, f"{where}: {name}", need)
-        if t.dtype != torch.uint8 or not t.is_contiguous():
+    u8 = _types()[0].uint8
+    n, blocks = layout.shard_len, layout.moment_blocks
+    ts = (moments.exp_avg, moments.exp_avg_scales, moments.exp_avg_sq, moments.exp_avg_sq_scales)
+    for t, need, name in zip(ts, (n, blocks, n, blocks),
+                             ("exp_avg", "exp_avg_scales", "exp_avg_sq", "exp_avg_sq_scales")):
+        if t.dtype is not u8 or t.numel() < need or not t.is_contiguous():
+            _need(t, f"{where}: {name}", need)
             raise ValueError(f"{where}: {name}: needs a contiguous uint8 tensor")
-        ts.append(t)
     return ts
 
 
@@ -453,7 +450,8 @@ def _whole(where, name, t, n, types):
         raise _bad_type(where, name, t, types)
     if not t.is_contiguous():
         raise ValueError(f"{where}: {name}: needs a contiguous tensor")
-    _need(t, f"{where}: {name}", n)
+    if t.numel() < n:
+        _need(t, f"{where}: {name}", n)
 
 
 def zero_shard_step_moments8(layout: Layout, hp: AdamW, t: int, rank_grads, grad_layout: int, master,
@@ -466,12 +464,12 @@ def zero_shard_step_moments8(layout: Layout, hp: AdamW, t: int, rank_grads, grad
     torch, b16, _, _, _, f32 = _types()
     if len(rank_grads) != layout.n_d:
         raise ValueError(f"{me}: one contribution per rank is required")
-    ng, ns, no = _step_sizes(layout, grad_layout, out_mode)
-    wide = rank_grads[0].dtype == torch.float32
-    arr = (C.c_void_p * len(rank_grads))()
-    for q, g in enumerate(rank_grads):
-        _whole(me, f"rank_grads[{q}]", g, ng, f32 if wide else b16)
-        arr[q] = g.data_ptr()
+    ns, P = layout.shard_len, layout.flat_len
+    ng, no = P if grad_layout == GRAD_FLAT else ns, P if out_mode == OUT_AG_SLOT else ns
+    wide = rank_grads[0].dtype is torch.float32
+    for g in rank_grads:
+        _whole(me, "rank_grads", g, ng, f32 if wide else b16)
+    arr = (C.c_void_p * len(rank_grads))(*[g.data_ptr() for g in rank_grads])
     _whole(me, "master", master, ns, f32)
     _whole(me, "param_out", param_out, no, b16)
     m = _moments8(me, layout, moments)
@@ -486,8 +484,8 @@ def zero_moments8_pack(layout: Layout, exp_avg, exp_avg_sq, moments: Moments8, s
     """float32 moments of a shard to 8 bits, rounded to the nearest code."""
     me = "zero_moments8_pack"
     f32 = _types()[5]
-    _whole(me, "exp_avg", exp_avg, layout.shard, f32)
-    _whole(me, "exp_avg_sq", exp_avg_sq, layout.shard, f32)
+    _whole(me, "exp_avg", exp_avg, layout.shard_len, f32)
+    _whole(me, "exp_avg_sq", exp_avg_sq, layout.shard_len, f32)
     m = _moments8(me, layout, moments)
     _enqueue(me, stream, [exp_avg, exp_avg_sq, *m], lambda s, _: load().zero_moments8_pack(
         layout.handle, exp_avg.data_ptr(), exp_avg_sq.data_ptr(), *[x.data_ptr() for x in m], s))
@@ -497,8 +495,8 @@ def zero_moments8_unpack(layout: Layout, moments: Moments8, exp_avg, exp_avg_sq,
     """The float32 values that the codes stand for."""
     me = "zero_moments8_unpack"
     f32 = _types()[5]
-    _whole(me, "exp_avg", exp_avg, layout.shard, f32)
-    _whole(me, "exp_avg_sq", exp_avg_sq, layout.shard, f32)
+    _whole(me, "exp_avg", exp_avg, layout.shard_len, f32)
+    _whole(me, "exp_avg_sq", exp_avg_sq, layout.shard_len, f32)
     m = _moments8(me, layout, moments)
     _enqueue(me, stream, [exp_avg, exp_avg_sq, *m], lambda s, _: load().zero_moments8_unpack(
         layout.handle, *[x.data_ptr() for x in m], exp_avg.data_ptr(), exp_avg_sq.data_ptr(), s))
@@ -856,38 +854,38 @@ class Rotation:
 
 
 def _rotation(where, turn, tokens, used):
-    """(C structure or None, to be kept until the call), the tensors added to
-    `used`."""
+    """zero_rotation (None without one), its tensors added to `used`."""
     if turn is None:
         return None
     torch, _, _, whole, _, _ = _types()
     p, f = turn.positions, turn.freqs
     axes = 1 if p.dim() == 1 else p.shape[0]
-    sections = [f.numel()] if turn.sections is None else [int(n) for n in turn.sections]
-    if len(sections) != axes or axes > MAX_AXES or any(n < 0 for n in sections):
+    sections = [f.numel()] if turn.sections is None else list(turn.sections)
+    if len(sections) != axes or axes > MAX_AXES or min(sections, default=0) < 0:
         raise ValueError(f"{where}: sections {sections} do not fit {axes} axes of positions "
                          f"(at most {MAX_AXES})")
     _dense(where, "positions", p, (tokens,) if p.dim() == 1 else (axes, tokens), whole)
     _dense(where, "freqs", f, (sum(sections),), (torch.float64,))
-    used += [p, f]
-    return C.byref(_Rotation(p.data_ptr(), f.data_ptr(), p.element_size(), axes,
-                             (C.c_int32 * MAX_AXES)(*sections), int(turn.interleaved)))
+    used += (p, f)
+    return _pack_rotation(p.data_ptr(), f.data_ptr(), p.element_size(), axes,
+                          *sections, *[0] * (MAX_AXES - axes), int(turn.interleaved))
 
 
-_no_view = _View(None, 0, 0)
-
-
-def _view(where, name, t, shape, used):
-    """A (tokens, heads, columns) tensor whose columns are adjacent."""
-    _, b16, _, _, _, _ = _types()
+def _rows3(where, name, t, shape, b16, used):
+    """Address and strides of a (tokens, heads, columns) tensor whose columns
+    are adjacent."""
     if t.dtype not in b16:
         raise _bad_type(where, name, t, b16)
     if t.shape != shape:
         raise ValueError(f"{where}: {name}: needs shape {tuple(shape)}, got {tuple(t.shape)}")
-    if shape[2] > 1 and t.stride(2) != 1:
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and shape[2] > 1:
         raise ValueError(f"{where}: {name}: columns are not adjacent (strides {t.stride()})")
     used.append(t)
-    return _View(t.data_ptr(), t.stride(0), t.stride(1))
+    return t.data_ptr(), s0, s1
+
+
+_no_rows = (0, 0, 0)
 
 
 def _side(where, layout, name, tensor, x, dy, out, used):
@@ -896,29 +894,27 @@ def _side(where, layout, name, tensor, x, dy, out, used):
         if x is not None or dy is not None:
             raise ValueError(f"{where}: {name}: has no output")
         return None
-    if out.dim() != 3:
-        raise ValueError(f"{where}: {name}: needs (tokens, heads, columns)")
+    b16 = _types()[1]
+    shape = out.shape
     if tensor is not None:
         _numel(where, layout, tensor)
-    h = _Heads(-1 if tensor is None else tensor, out.shape[1], _no_view, _no_view,
-               _view(where, name + " output", out, out.shape, used))
-    if x is not None:
-        h.x = _view(where, name, x, out.shape, used)
-    if dy is not None:
-        h.dy = _view(where, name + " gradient", dy, out.shape, used)
-    return h
+    return _pack_heads(-1 if tensor is None else tensor, shape[1],
+                       *(_no_rows if x is None else _rows3(where, name, x, shape, b16, used)),
+                       *(_no_rows if dy is None else _rows3(where, name + " gradient", dy, shape, b16, used)),
+                       *_rows3(where, name + " output", out, shape, b16, used))
 
 
-def _shape3(where, q, k):
+def _tokens_columns(where, q, k):
+    """Those of the outputs q and k, of which one may be None."""
     t = q if q is not None else k
     if t is None:
         raise ValueError(f"{where}: neither queries nor keys")
-    if q is not None and k is not None and (q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0]
-                                            or q.shape[2] != k.shape[2]):
-        raise ValueError(f"{where}: queries {tuple(q.shape)} and keys {tuple(k.shape)} differ in tokens or columns")
-    if t.dim() != 3:
+    if t.dim() != 3 or (k is not None and k.dim() != 3):
         raise ValueError(f"{where}: needs (tokens, heads, columns)")
-    return t.shape[0], t.shape[2]
+    tokens, _, cols = t.shape
+    if k is not None and (k.shape[0] != tokens or k.shape[2] != cols):
+        raise ValueError(f"{where}: queries {tuple(t.shape)} and keys {tuple(k.shape)} differ in tokens or columns")
+    return tokens, cols
 
 
 def zero_head_norm_rotate(layout: Layout, q_tensor, k_tensor, params, q, k, eps: float, rotation,
@@ -928,20 +924,18 @@ def zero_head_norm_rotate(layout: Layout, q_tensor, k_tensor, params, q, k, eps:
     (None: none).  q, k (either may be None with its output): (tokens, heads,
     columns) bfloat16, any strides with adjacent columns."""
     me = "zero_head_norm_rotate"
-    _, b16, _, _, _, _ = _types()
-    tokens, cols = _shape3(me, q_out, k_out)
-    used = []
-    sides = [_side(me, layout, n, w, x, None, o, used)
-             for n, w, x, o in (("q", q_tensor, q, q_out), ("k", k_tensor, k, k_out))]
+    tokens, cols = _tokens_columns(me, q_out, k_out)
     if (q is None) != (q_out is None) or (k is None) != (k_out is None):
         raise ValueError(f"{me}: an input without its output, or an output without its input")
-    if any(s is not None and s.tensor >= 0 for s in sides):
-        _flat(me, "params", params, layout, b16)
+    used = []
+    hq = _side(me, layout, "q", q_tensor, q, None, q_out, used)
+    hk = _side(me, layout, "k", k_tensor, k, None, k_out, used)
+    if (q is not None and q_tensor is not None) or (k is not None and k_tensor is not None):
+        _flat(me, "params", params, layout, _types()[1])
         used.append(params)
     turn = _rotation(me, rotation, tokens, used)
-    sides = [None if s is None else C.byref(s) for s in sides]
     _enqueue(me, stream, used, lambda s, _: load().zero_head_norm_rotate(
-        layout.handle, _ptr(params), tokens, cols, eps, turn, *sides, s))
+        layout.handle, _ptr(params), tokens, cols, eps, turn, hq, hk, s))
 
 
 def zero_head_norm_rotate_grad(layout: Layout, q_tensor, k_tensor, params, dq, dk, q, k, eps: float,
@@ -951,28 +945,27 @@ def zero_head_norm_rotate_grad(layout: Layout, q_tensor, k_tensor, params, dq, d
     without a norm does not need) from dq and dk; the weights' gradients,
     scaled, into `acc` / `bf16_out` (added up where q_tensor is k_tensor)."""
     me = "zero_head_norm_rotate_grad"
-    _, b16, _, _, _, _ = _types()
-    tokens, cols = _shape3(me, q_dx, k_dx)
-    used = []
-    sides = []
+    tokens, cols = _tokens_columns(me, q_dx, k_dx)
+    used, sides, normed = [], [], False
     for n, w, x, dy, o in (("q", q_tensor, q, dq, q_dx), ("k", k_tensor, k, dk, k_dx)):
-        s = _side(me, layout, n, w, x if w is not None else None, dy, o, used)
-        if s is not None and (dy is None or (w is not None and x is None)):
-            raise ValueError(f"{me}: {n}: its gradient or its input is missing")
-        sides.append(s)
-    if any(s is not None and s.tensor >= 0 for s in sides):
-        _flat(me, "params", params, layout, b16)
+        if o is not None:
+            if dy is None or (w is not None and x is None):
+                raise ValueError(f"{me}: {n}: its gradient or its input is missing")
+            normed = normed or w is not None
+        sides.append(_side(me, layout, n, w, x if w is not None else None, dy, o, used))
+    hq, hk = sides
+    if normed:
+        _flat(me, "params", params, layout, _types()[1])
         used.append(params)
         used += _grad_args(me, layout, acc, flags, bf16_out)
     turn = _rotation(me, rotation, tokens, used)
-    sides = [None if s is None else C.byref(s) for s in sides]
     lib = load()
 
     def call(s, device):
         ws = _workspace(me, workspace, lib.zero_head_norm_rotate_grad_workspace(
-            layout.handle, tokens, cols, *sides), device)
+            layout.handle, tokens, cols, hq, hk), device)
         return lib.zero_head_norm_rotate_grad(
-            layout.handle, _ptr(params), tokens, cols, eps, turn, *sides, scale, flags, _ptr(acc),
+            layout.handle, _ptr(params), tokens, cols, eps, turn, hq, hk, scale, flags, _ptr(acc),
             _ptr(bf16_out), _ptr(ws), _size(ws), s)
     _enqueue(me, stream, used, call)
 

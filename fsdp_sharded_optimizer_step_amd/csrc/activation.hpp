@@ -62,6 +62,16 @@ __device__ __forceinline__ float slope(float x) {
   return 1.f;
 }
 
+template <bool SLOPE>
+__device__ __forceinline__ float apply1(int act, float x) {
+  switch (act) {
+    case ZERO_ACT_RELU: return SLOPE ? slope<ZERO_ACT_RELU>(x) : activate<ZERO_ACT_RELU>(x);
+    case ZERO_ACT_GELU: return SLOPE ? slope<ZERO_ACT_GELU>(x) : activate<ZERO_ACT_GELU>(x);
+    case ZERO_ACT_GELU_TANH: return SLOPE ? slope<ZERO_ACT_GELU_TANH>(x) : activate<ZERO_ACT_GELU_TANH>(x);
+    case ZERO_ACT_SILU: return SLOPE ? slope<ZERO_ACT_SILU>(x) : activate<ZERO_ACT_SILU>(x);
+    default: return SLOPE ? 1.f : x;
+  }
+}
 // Eight values; one branch for the wave.
 template <int ACT, bool SLOPE>
 __device__ __forceinline__ void apply8(float (&v)[8]) {

@@ -395,7 +395,11 @@ __device__ __forceinline__ int column_of(const SumArgs& S, int k) {
   if (j >= S.half || S.neighbours) return 2 * j + (second ? 1 : 0);
   return second ? S.half + j : j;
 }
-__global__ void __launch_bounds__(kSumCols* kSumWays) rotate_sum_kernel(const SumArgs S) {
+struct BothSums {
+  SumArgs side[2];
+};
+__global__ void __launch_bounds__(kSumCols* kSumWays) rotate_sum_kernel(const BothSums both) {
+  const SumArgs& S = both.side[blockIdx.y];
   __shared__ float part[kSumWays][kSumCols + 1];
   const int c = threadIdx.x % kSumCols, way = threadIdx.x / kSumCols;
   const int k = (int)blockIdx.x * kSumCols + c;
@@ -689,9 +693,11 @@ int run(const zero_layout* L, const uint16_t* params, int64_t tokens, int32_t d,
   const int width = p.nl * 16;
   const bool shared = normed[0] && normed[1] && side[0]->tensor == side[1]->tensor;
   const int64_t parts[2] = {work ? p.chunks[0] * p.along : 0, work ? p.chunks[1] * p.along : 0};
+  BothSums both;
+  unsigned sides = 0;
   for (int n = 0; n < 2; ++n) {
     if (!normed[n] || (shared && n == 1)) continue;
-    SumArgs S;
+    SumArgs& S = both.side[sides];
     S.parts = (int32_t)(shared ? parts[0] + parts[1] : parts[n]);
     if (S.parts == 0 && !(g->flags & (ZERO_ACC_OVERWRITE | ZERO_ACC_EMIT_BF16))) continue;
     S.partial = (const float*)g->workspace + (n == 1 ? parts[0] * width : 0);
@@ -701,12 +707,12 @@ int run(const zero_layout* L, const uint16_t* params, int64_t tokens, int32_t d,
     S.half = pairs;
     S.neighbours = neighbours;
     S.out = GradOut{g->acc, g->out, A.side[n].place, g->scale, g->flags};
-    hipLaunchKernelGGL(rotate_sum_kernel, dim3((unsigned)((width + kSumCols - 1) / kSumCols)),
-                       dim3(kSumCols * kSumWays), 0, stream, S);
-    rc = launched();
-    if (rc != ZERO_OK) return rc;
+    ++sides;
   }
-  return ZERO_OK;
+  if (sides == 0) return ZERO_OK;
+  hipLaunchKernelGGL(rotate_sum_kernel, dim3((unsigned)((width + kSumCols - 1) / kSumCols), sides),
+                     dim3(kSumCols * kSumWays), 0, stream, both);
+  return launched();
 }
 
 }  // namespace

@@ -26,7 +26,7 @@
 // buffer, padding inside it) is first copied to the workspace.
 #include <algorithm>
 
-#include "activation.hpp"
+#include "linear.hpp"
 #include "matrix.hpp"
 
 namespace {
@@ -37,19 +37,6 @@ using namespace zs;
 
 constexpr int kThreads = 256;
 constexpr int kStep = 64;  // k of an LDS buffer: 128 bytes of a row
-
-// What becomes of a sum.
-struct Epilogue {
-  const uint16_t* bias;  // flat parameters; null: none
-  Place bias_place;
-  const uint16_t* add;  // res, or the gradient's other part; null: none
-  int64_t add_stride;
-  const uint16_t* pre_in;  // input gradient: what the activation was taken of
-  uint16_t* pre_out;       // forward: kept for the backward pass
-  void* out;
-  int64_t out_stride;
-  int32_t act, f32, grad;
-};
 
 struct Args {
   const uint16_t *a, *b;
@@ -174,79 +161,6 @@ struct NRows {
   }
   static constexpr int kReads = 2;
 };
-
-// Eight columns of bias, from column c; `left` of them exist.
-__device__ __forceinline__ void bias_at(const Epilogue& e, int32_t c, int left, float (&v)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    v[j] = e.bias && j < left ? bf16_one(e.bias[place_at<true>(e.bias_place, c + j)]) : 0.f;
-}
-
-// What the epilogue reads beside the sums: 8 columns from column c of row r.
-// N: the matrix's columns (rows of pre lie densely).
-struct Beside {
-  u32x4 add, pre;
-};
-__device__ __forceinline__ Beside beside_at(const Epilogue& e, int32_t N, int64_t r, int32_t c, int left) {
-  Beside b{{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
-  if (e.add) {
-    const uint16_t* p = e.add + r * e.add_stride + c;
-    b.add = left >= 8 ? *(const u32x4_a2*)p : load_some(p, left);
-  }
-  if (e.pre_in) {
-    const uint16_t* p = e.pre_in + r * N + c;
-    b.pre = left >= 8 ? *(const u32x4_a2*)p : load_some(p, left);
-  }
-  return b;
-}
-
-// Eight sums of row r, columns c to c + 7, of which `left` exist.
-__device__ __forceinline__ void finish8(const Epilogue& e, int32_t N, int64_t r, int32_t c, int left, float (&v)[8],
-                                        const Beside& b, const float (&bias)[8]) {
-  float add[8];
-  widen8(b.add, add);
-  if (e.grad) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += add[j];
-    if (e.act != ZERO_ACT_NONE) {
-      float s[8];
-      widen8(b.pre, s);
-      apply8<true>(e.act, s);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= s[j];
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += bias[j];
-    if (e.pre_out) {
-      uint16_t* p = e.pre_out + r * N + c;
-      if (left >= 8)
-        *(u32x4_a2*)p = round8(v);
-      else
-        store_some(p, round8(v), left);
-    }
-    apply8<false>(e.act, v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += add[j];
-  }
-  if (e.f32) {
-    float* o = (float*)e.out + r * e.out_stride + c;
-    if (left >= 8) {
-      *(f32x4_a4*)o = f32x4{v[0], v[1], v[2], v[3]};
-      *(f32x4_a4*)(o + 4) = f32x4{v[4], v[5], v[6], v[7]};
-    } else {
-#pragma unroll
-      for (int j = 0; j < 7; ++j)
-        if (j < left) o[j] = v[j];
-    }
-  } else {
-    uint16_t* o = (uint16_t*)e.out + r * e.out_stride + c;
-    if (left >= 8)
-      *(u32x4_a2*)o = round8(v);
-    else
-      store_some(o, round8(v), left);
-  }
-}
 
 template <class S, bool NC>
 __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(const Args A) {
@@ -658,6 +572,7 @@ int64_t workspace_of(const zero_layout* L, int32_t tensor, int32_t transposed, c
   if (O == 0 || I == 0 || tokens == 0) return 0;
   const Sizes z = sizes_of(tokens, O, I, transposed != 0, grad);
   if (a_stride < z.K) return ZERO_EINVAL;
+  if (is_few(tokens, z.n_adjacent)) return 0;
   const Plan p = make_plan(L, tensor, z, params, a, a_stride);
   return plan_ok(p) == ZERO_OK ? p.bytes : ZERO_ERANGE;
 }
@@ -668,7 +583,8 @@ int64_t workspace_of(const zero_layout* L, int32_t tensor, int32_t transposed, c
 int run(const zero_layout* L, int32_t tensor, const uint16_t* params, const uint16_t* a, int64_t a_stride,
         const Sizes& z, const Epilogue& e, const Bytes (&out)[2], const Bytes (&in)[3], void* workspace,
         int64_t workspace_bytes, hipStream_t stream) {
-  const Plan p = make_plan(L, tensor, z, params, a, a_stride);
+  const bool few = is_few(z.M, z.n_adjacent);
+  const Plan p = few ? Plan{} : make_plan(L, tensor, z, params, a, a_stride);
   if (plan_ok(p) != ZERO_OK) return ZERO_ERANGE;
   if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes || ((uintptr_t)workspace & 15u))) return ZERO_EINVAL;
   int64_t lo, hi;
@@ -677,6 +593,9 @@ int run(const zero_layout* L, int32_t tensor, const uint16_t* params, const uint
   const Bytes ins[] = {in[0], in[1], in[2], Bytes{params + lo, 2 * (hi - lo)}, rows_of(a, z.M, z.K, a_stride, 2)};
   if (any_overlap(outs, ins)) return ZERO_EOVERLAP;
   if (hip_error_pending()) return ZERO_EHIP;
+  if (few)
+    return launch_few(Few{a, params, a_stride, place, (int32_t)z.M, (int32_t)z.N, (int32_t)z.K, e}, z.n_adjacent,
+                      stream);
   Args A{};
   A.M = (int32_t)z.M;
   A.N = (int32_t)z.N;

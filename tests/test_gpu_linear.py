@@ -120,6 +120,26 @@ def test_addresses(how, t, o, i, tr):
             assert (v.as_strided((t, cols + extra), (cols + extra, 1))[:-1, cols:] == 7).all()
 
 
+@pytest.mark.parametrize("tr", [False, True])
+@pytest.mark.parametrize("t", list(range(1, 10)) + [15, 16, 17])
+def test_few_tokens(t, tr):
+    """One pass over the weight up to 16 tokens (8 where the sums run down its
+    columns), at odd places, across padding, for lengths around a wave's."""
+    for o, i, lead, cap in ((1, 700, 17, 0), (65, 63, 17, 0), (200, 1024 + 9, 16, 0), (513, 64, 5, 4001), (16, 2000, 16, 0)):
+        w = Weights(o, i, tr, lead=lead, cap=cap, fill=lambda n: ints(n, n))
+        x, dy = strided(ints(1, t, i), 5, 3), strided(ints(2, t, o), 1, 0)
+        res, pre = ints(3, t, o, top=50), torch.zeros(t, o, dtype=BF16, device=DEV)
+        out = strided(torch.zeros(t, o, dtype=F32, device=DEV), 2, 1)
+        z.zero_linear(w.L, 1, w.params, x, out, bias=3, res=res, pre=pre, transposed=tr, activation="relu")
+        p = x.double() @ w.w.t() + w.b
+        assert torch.equal(out.double(), p.clamp(min=0) + res.double())
+        assert torch.equal(pre, p.float().bfloat16())
+        dx, add = strided(torch.zeros(t, i, dtype=BF16, device=DEV), 3, 1), ints(4, t, i, top=50)
+        z.zero_linear_input_grad(w.L, 1, w.params, dy, dx, activation="relu", pre=x.contiguous(), add=add, transposed=tr)
+        assert torch.equal(dx, torch.where(x > 0, dy.double() @ w.w + add.double(), 0.0).float().bfloat16())
+        assert (out.as_strided((t, o + 2), (o + 2, 1))[:-1, o:] == 7).all()
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("t,o,i,tr", [(1, 512, 300, False), (40, 260, 512, True), (300, 384, 256, False),
                                       (2100, 1024, 192, True)])

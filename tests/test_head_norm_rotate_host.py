@@ -6,10 +6,31 @@ import torch
 
 import fsdp_sharded_optimizer_step_amd as z
 from fsdp_sharded_optimizer_step_amd import binding
-from fsdp_sharded_optimizer_step_amd.binding import _Heads, _Rotation, _View
 
 EINVAL, ERANGE, EOVERLAP = binding.ZERO_EINVAL, binding.ZERO_ERANGE, binding.ZERO_EOVERLAP
 T, D = 10, 24
+
+
+class _View(C.Structure):
+    _fields_ = [("data_dev", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class _Heads(C.Structure):
+    _fields_ = [("tensor", C.c_int32), ("heads", C.c_int32), ("x", _View), ("dy", _View), ("out", _View)]
+
+
+class _Rotation(C.Structure):
+    _fields_ = [("positions_dev", C.c_void_p), ("freqs_dev", C.c_void_p), ("position_bytes", C.c_int32),
+                ("n_axes", C.c_int32), ("sections", C.c_int32 * 4), ("interleaved", C.c_int32)]
+
+
+def test_packed_structures():
+    """What the binding packs is what a C client fills in."""
+    h = _Heads(3, 7, _View(at(1), 11, 12), _View(at(2), 21, 22), _View(at(3), 31, 32))
+    assert binding._pack_heads(3, 7, at(1), 11, 12, at(2), 21, 22, at(3), 31, 32) == bytes(h)
+    r = _Rotation(at(4), at(5), 8, 3, (C.c_int32 * 4)(1, 2, 3, 0), 1)
+    packed = binding._pack_rotation(at(4), at(5), 8, 3, 1, 2, 3, 0, 1)
+    assert len(packed) == C.sizeof(r) and packed[:44] == bytes(r)[:44]
 
 
 def at(n, off=0):
