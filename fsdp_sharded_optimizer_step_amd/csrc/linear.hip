@@ -468,6 +468,7 @@ constexpr int64_t kCus = 256, kMinSteps = 4, kMaxSplits = 32;
 constexpr int64_t kMaxStride = (int64_t)1 << 22;  // a tile's rows lie within 32 bits
 
 struct Plan {
+  bool few;  // the kernels of few tokens
   int64_t side, row_tiles, col_tiles, whole, further, splits, per_split;
   int64_t w_bytes, a_bytes, bytes;  // copies, and everything
   double us;
@@ -528,11 +529,17 @@ Sizes sizes_of(int64_t tokens, int64_t out_f, int64_t in_f, bool transposed, boo
 
 Plan make_plan(const zero_layout* L, int32_t tensor, const Sizes& z, const uint16_t* params, const uint16_t* a,
                int64_t a_stride) {
-  const Plan x = plan_for<Large>(z.M, z.N, z.K), y = plan_for<Small>(z.M, z.N, z.K);
-  Plan p = x.us <= y.us ? x : y;
   int64_t lo, hi;
   const Place pl = make_place(L, tensor, &lo, &hi);
   const bool copy_w = pl.gap != 0 || z.w_cols % 8 || !aligned16(params + lo);
+  if (is_few(z.M, z.n_adjacent, copy_w)) {
+    Plan p{};
+    p.few = true;
+    p.bytes = few_bytes(z.M, z.N, z.K, z.n_adjacent);
+    return p;
+  }
+  const Plan x = plan_for<Large>(z.M, z.N, z.K), y = plan_for<Small>(z.M, z.N, z.K);
+  Plan p = x.us <= y.us ? x : y;
   const bool copy_a = z.K % 8 || a_stride % 8 || a_stride > kMaxStride || !aligned16(a);
   p.w_bytes = copy_w ? z.w_rows * ((z.w_cols + 7) / 8) * 16 : 0;
   p.a_bytes = copy_a ? z.M * ((z.K + 7) / 8) * 16 : 0;
@@ -572,7 +579,6 @@ int64_t workspace_of(const zero_layout* L, int32_t tensor, int32_t transposed, c
   if (O == 0 || I == 0 || tokens == 0) return 0;
   const Sizes z = sizes_of(tokens, O, I, transposed != 0, grad);
   if (a_stride < z.K) return ZERO_EINVAL;
-  if (is_few(tokens, z.n_adjacent)) return 0;
   const Plan p = make_plan(L, tensor, z, params, a, a_stride);
   return plan_ok(p) == ZERO_OK ? p.bytes : ZERO_ERANGE;
 }
@@ -583,8 +589,7 @@ int64_t workspace_of(const zero_layout* L, int32_t tensor, int32_t transposed, c
 int run(const zero_layout* L, int32_t tensor, const uint16_t* params, const uint16_t* a, int64_t a_stride,
         const Sizes& z, const Epilogue& e, const Bytes (&out)[2], const Bytes (&in)[3], void* workspace,
         int64_t workspace_bytes, hipStream_t stream) {
-  const bool few = is_few(z.M, z.n_adjacent);
-  const Plan p = few ? Plan{} : make_plan(L, tensor, z, params, a, a_stride);
+  const Plan p = make_plan(L, tensor, z, params, a, a_stride);
   if (plan_ok(p) != ZERO_OK) return ZERO_ERANGE;
   if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes || ((uintptr_t)workspace & 15u))) return ZERO_EINVAL;
   int64_t lo, hi;
@@ -593,9 +598,9 @@ int run(const zero_layout* L, int32_t tensor, const uint16_t* params, const uint
   const Bytes ins[] = {in[0], in[1], in[2], Bytes{params + lo, 2 * (hi - lo)}, rows_of(a, z.M, z.K, a_stride, 2)};
   if (any_overlap(outs, ins)) return ZERO_EOVERLAP;
   if (hip_error_pending()) return ZERO_EHIP;
-  if (few)
+  if (p.few)
     return launch_few(Few{a, params, a_stride, place, (int32_t)z.M, (int32_t)z.N, (int32_t)z.K, e}, z.n_adjacent,
-                      stream);
+                      workspace, stream);
   Args A{};
   A.M = (int32_t)z.M;
   A.N = (int32_t)z.N;

@@ -116,9 +116,14 @@ struct Few {
   int32_t M, N, K;
   Epilogue e;
 };
-// The most tokens that launch_few takes.
-constexpr int64_t kFewRows = 16, kFewColumns = 8;
-constexpr bool is_few(int64_t tokens, bool n_adjacent) { return tokens <= (n_adjacent ? kFewColumns : kFewRows); }
-int launch_few(const Few& f, bool n_adjacent, hipStream_t stream);
+// Whether launch_few is to take a product; copied: the other kernels would have
+// to copy the weight first.  Measured (us, 14336 x 4096; launch_few, the other
+// kernels, those with the copy): k adjacent, 16 tokens 38, 38, 73; n adjacent, 2
+// tokens 32, 41, 72; 4 tokens 40 to 50, 41, 72.
+constexpr bool is_few(int64_t tokens, bool n_adjacent, bool copied) {
+  return tokens <= (n_adjacent ? (copied ? 4 : 2) : 16);
+}
+int64_t few_bytes(int64_t M, int64_t N, int64_t K, bool n_adjacent);
+int launch_few(const Few& f, bool n_adjacent, void* workspace, hipStream_t stream);
 
 }  // namespace zs

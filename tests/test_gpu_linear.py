@@ -123,7 +123,7 @@ def test_addresses(how, t, o, i, tr):
 @pytest.mark.parametrize("tr", [False, True])
 @pytest.mark.parametrize("t", list(range(1, 10)) + [15, 16, 17])
 def test_few_tokens(t, tr):
-    """One pass over the weight up to 16 tokens (8 where the sums run down its
+    """One pass over the weight up to 16 tokens (4 where the sums run down its
     columns), at odd places, across padding, for lengths around a wave's."""
     for o, i, lead, cap in ((1, 700, 17, 0), (65, 63, 17, 0), (200, 1024 + 9, 16, 0), (513, 64, 5, 4001), (16, 2000, 16, 0)):
         w = Weights(o, i, tr, lead=lead, cap=cap, fill=lambda n: ints(n, n))
