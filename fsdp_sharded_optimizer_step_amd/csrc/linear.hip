@@ -459,12 +459,11 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const Copy w, const Copy
 }
 
 // ------------------------------------------------------------------ host
-// Tiles that fill the chip's 256 CUs are summed by one block each; the rest of
-// the tiles share the CUs, each tile's k being split over as many blocks as
-// there is room for, kMinSteps steps each at least.  The number of CUs is a
-// constant: the order of a sum and the workspace's size follow from the sizes
-// alone.
-constexpr int64_t kCus = 256, kMinSteps = 4, kMaxSplits = 32;
+// Tiles that fill the chip's 256 CUs are summed by one block each; the k of the
+// rest may be split over several blocks each, where an estimate of the time
+// says so.  The number of CUs is a constant: the order of a sum and the
+// workspace's size follow from the sizes alone.
+constexpr int64_t kCus = 256, kMaxSplits = 32;
 constexpr int64_t kMaxStride = (int64_t)1 << 22;  // a tile's rows lie within 32 bits
 
 struct Plan {
@@ -474,33 +473,55 @@ struct Plan {
   double us;
 };
 
+// What a block was measured to take (us): a step of 64 k, alone on its CU or
+// beside another; its beginning and end; a split's part of a tile, written and
+// read again; the launch that adds the parts up.
+template <class S>
+struct Cost;
+template <>
+struct Cost<Shape<4>> {
+  static constexpr double step[2] = {1.45, 1.45}, ends = 19, part = 0.054, sum = 2.7;
+};
+template <>
+struct Cost<Shape<2>> {
+  static constexpr double step[2] = {0.64, 0.95}, ends = 4.5, part = 0.0134, sum = 2.7;
+};
+
+// Measured (us) in splits of the smaller tile: 1000 x 2304 x 768 (tokens,
+// outputs, inputs) 1: 13.6, 3: 19.7; 1000 x 768 x 2304 1: 26.6, 3: 16.3, 9: 18.3; 333
+// x 8192 x 1024 1: 15.7, 2: 20.9; 300 x 300 x 8192 1: 73.9, 4: 24.6, 12: 15.8; 512 x
+// 4096 x 4096 1: 41.9, 4: 29.4.
 template <class S>
 Plan plan_for(int64_t M, int64_t N, int64_t K) {
+  using C = Cost<S>;
   Plan p{};
   p.side = S::kSide;
   p.row_tiles = (M + p.side - 1) / p.side;
   p.col_tiles = (N + p.side - 1) / p.side;
-  const int64_t tiles = p.row_tiles * p.col_tiles, steps = (K + kStep - 1) / kStep;
-  const int64_t at_once = kCus * (S::W == 4 ? 1 : 2);
+  const int64_t tiles = p.row_tiles * p.col_tiles, steps = std::max<int64_t>(1, (K + kStep - 1) / kStep);
+  const int64_t per_cu = S::W == 4 ? 1 : 2, at_once = kCus * per_cu;
   p.whole = tiles / at_once * at_once;
   p.further = tiles - p.whole;
   p.splits = 1;
-  p.per_split = std::max<int64_t>(steps, 1);
-  if (p.further > 0) {
-    const int64_t most = std::max<int64_t>(1, steps / kMinSteps);
-    p.splits = std::max<int64_t>(1, std::min({most, at_once / p.further, kMaxSplits}));
-    p.per_split = std::max<int64_t>(1, (steps + p.splits - 1) / p.splits);
-    p.splits = std::max<int64_t>(1, (steps + p.per_split - 1) / p.per_split);
-    if (p.splits == 1) {
-      p.whole = tiles;
-      p.further = 0;
+  p.per_split = steps;
+  p.us = (double)(p.whole / at_once) * ((double)steps * C::step[per_cu - 1] + C::ends);
+  if (p.further == 0) return p;
+  double best = 0;
+  for (int64_t n = 1; n <= std::min(kMaxSplits, steps) && (n == 1 || n * p.further <= at_once); ++n) {
+    const int64_t per = (steps + n - 1) / n, splits = (steps + per - 1) / per, blocks = splits * p.further;
+    double us = C::ends + (double)per * C::step[blocks > kCus ? 1 : 0];
+    if (splits > 1) us += C::sum + (double)blocks * C::part;
+    if (n == 1 || us < best) {
+      best = us;
+      p.splits = splits;
+      p.per_split = per;
     }
   }
-  const double step = S::W == 4 ? 1.1 : 0.55;
-  const double tile_io = (double)(p.side * p.side) * 8 / 4.7e6;
-  const double rounds = (double)((p.whole + at_once - 1) / at_once);
-  p.us = rounds * ((double)steps * step + 2);
-  if (p.further > 0) p.us += (double)p.per_split * step + (double)(p.further * (p.splits + 1)) * tile_io + 4;
+  p.us += best;
+  if (p.splits == 1) {
+    p.whole = tiles;
+    p.further = 0;
+  }
   return p;
 }
 
