@@ -376,7 +376,7 @@ unsigned grid_for(uint32_t units, int64_t blocks_per_cu) {
   return (unsigned)std::max<int64_t>(1, std::min(need, blocks_per_cu * kCus));
 }
 
-constexpr int64_t kStepBlocks = 4, kConvertBlocks = 8;
+constexpr int64_t kStepBlocks = 2, kConvertBlocks = 5;
 
 struct Call {
   const void* const* g;
