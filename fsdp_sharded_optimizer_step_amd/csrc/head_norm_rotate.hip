@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, GRAD ? 3 : 4) rotate_kernel(const Ar
       // by those that need them.
       for (int v = l; v < down * NL * 8; v += 64) {
         const int64_t u = t0 + v / (NL * 8);
-        if (u < A.tokens) table[v] = turn<NL, MODE>(A, u, v / 8 % NL, v % 8);
+        table[v] = u < A.tokens ? turn<NL, MODE>(A, u, v / 8 % NL, v % 8) : f32x2{1.f, 0.f};
       }
       lanes_meet_in_lds();
 #pragma unroll
@@ -333,7 +333,9 @@ __global__ void __launch_bounds__(kThreads, GRAD ? 3 : 4) rotate_kernel(const Ar
               ss += x[m] * x[m] + y[m] * y[m];
               sg += ox[m] * weight(wx, m) * x[m] + oy[m] * weight(wy, m) * y[m];
             }
-            const float r = 1.f / __builtin_sqrtf(lanes_sum<NL>(ss) * inv_d + A.eps);
+            // lanes without a row, whose values are zeros, count for nothing
+            const float rms = __builtin_sqrtf(lanes_sum<NL>(ss) * inv_d + A.eps);
+            const float r = here && h < h1 ? 1.f / rms : 0.f;
             const float mean = lanes_sum<NL>(sg) * inv_d * r;  // of g*n
 #pragma unroll
             for (int m = 0; m < 8; ++m) {

@@ -271,6 +271,33 @@ def test_gradient_against_differences():
     assert abs(got - slope) <= (bx * np.abs(vx)).sum() + ((bw + 2 * U * np.abs(f64(acc)).max()) * np.abs(vw)).sum() + own
 
 
+@pytest.mark.parametrize("t,hq,hk", [(1, 3, 1), (5, 1, 1), (7, 2, 0), (13, 9, 5)])
+def test_lanes_without_a_row_count_for_nothing(t, hq, hk):
+    """Tokens and heads that do not fill a wave: with eps = 0 a row of zeros has
+    no norm, and LDS may hold NaN from an earlier kernel."""
+    d = 64
+    L, pl = layout(d, False)
+    params, rot = randn(d, L.padded) + 1, rotation(t, 32)
+    w = f64(params)[positions(pl, d)]
+    n = 1024
+    W = z.Layout([n * n], 0, 1, 0)
+    nan = torch.full((16 * n, n), float("nan"), dtype=BF16, device=DEV)
+    z.zero_linear(W, 0, nan[:n].view(-1), nan, torch.empty_like(nan))
+    x = [randn(1 + k, t, h, d) for k, h in enumerate((hq, hk))]
+    dy = [randn(3 + k, t, h, d) for k, h in enumerate((hq, hk))]
+    dx = [torch.empty_like(a) for a in x]
+    use = lambda v: [a if h else None for a, h in zip(v, (hq, hk))]  # noqa: E731
+    flat = Flat(L, pl, d, DEV)
+    z.zero_head_norm_rotate_grad(L, 1, 1, params, *use(dy), *use(x), 0.0, rot, *use(dx), flat.acc)
+    dw, odw = np.zeros(d), np.zeros(d)
+    for a, b, o in zip(dy, x, dx):
+        if a.shape[1]:
+            g, bound, s, os_ = backward(f64(a), f64(b), w, rot, 0.0)
+            close(o, g, bound, "gradient")
+            dw, odw = dw + s, odw + os_
+    flat.check(dw, odw + U * np.abs(dw), 1.0, 0, "weight")
+
+
 @pytest.mark.parametrize("flags", [0, z.ACC_OVERWRITE, z.ACC_EMIT_BF16])
 def test_no_tokens(flags):
     L, pl = layout(64, False)
