@@ -46,11 +46,13 @@
  *   - Arithmetic is binary32 with every operation rounded to nearest-even,
  *     no fused multiply-add, subnormals kept, correctly rounded division
  *     and square root.  Results do not depend on the launch configuration.
- *     (The norm's forward pass is binary64 and the weight gradient's sums are
- *     those of the matrix cores: see there.)
+ *     (The norm's forward pass is binary64, the sums of products with a weight
+ *     are those of the matrix cores, and the heads' norms, the activations and
+ *     their gradients may use fused multiply-adds: see there.)
  *   - Any pointer alignment is accepted; 16-byte aligned buffers take the
  *     vector path, others a scalar path with the same results (the calls of
- *     "gradients of a micro-batch" take vectors at any alignment).
+ *     "gradients of a micro-batch" and those after them take vectors at any
+ *     alignment, or copy an operand first).
  *   - Entry points may be called from several host threads at once (no
  *     mutable global state apart from a per-device count of compute units);
  *     calls that write the same buffers must be ordered by the caller.
@@ -708,7 +710,9 @@ int zero_head_norm_rotate_grad(const zero_layout* layout, const uint16_t* params
  *
  * The workspace functions take the operands' addresses: one that does not
  * begin at 16 bytes, or whose rows are not whole multiples of 16 bytes, is
- * copied there first (the weight also where padding falls inside it).
+ * copied there first (the weight also where padding falls inside it; not with
+ * up to 16 tokens where the sum runs along the weight's rows, and up to 4, 2 of
+ * a weight that needs no copy, where it runs along its columns).
  * Common errors; ZERO_EINVAL also for a sum over no features, ZERO_ERANGE for
  * more than ZERO_MAX_FEATURES features, or more than 2^23 tiles of 128 x 128
  * outputs. */
