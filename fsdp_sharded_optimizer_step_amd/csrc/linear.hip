@@ -162,6 +162,20 @@ struct NRows {
   static constexpr int kReads = 2;
 };
 
+// A block's tile of the result, or its share of a split tile.  The matrix cores
+// bound the loop: a step's 64 products of 32 x 32 x 16 a wave take 1.45 us of the
+// larger tile, 1.48 PFLOP/s over the chip; beside each product stands its share
+// of the next fragments' reads and of the requests two steps on, so that no
+// wave waits for either.  Sides of 256 read LDS half as often a product as sides
+// of 128 and fill a CU alone, so nothing computes while a block begins and
+// ends (19 us; results and what the epilogue reads cross HBM then); sides of 128
+// stand two to a CU.  Measured (us): 8192 x 14336 x 4096 (tokens, sum, columns),
+// residual added, 790 to 811 (three cards), 1187 TFLOP/s and more; where it took
+// 790, 718 with every request a hit in L2 and 660 without requests.  16384 x 4096
+// x 14336 with n adjacent and the activation's gradient 1721, 1118 TFLOP/s.  Not
+// kept: a third place in LDS for A's steps (783 to 768, but 16384 x 14336 x 4096
+// 1593 to 1700); tiles in groups of 4 or 16 rows instead of 8 (up to 3 % better
+// in sums over 14336, 1.4 % worse in those over 4096).
 template <class S, bool NC>
 __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(const Args A) {
   constexpr int W = S::W, kSide = S::kSide;

@@ -267,6 +267,9 @@ __device__ __forceinline__ void step_unit(const Args& A, const Spot& x, const in
   }
 }
 
+// HBM bounds it: 262M elements of 30 bytes at N_d = 8 take 1.52 ms, 5.2 TB/s (a
+// copy reached 4.6 to 4.8); without the update or the hash, for timing, it took
+// the same.
 template <class T, int ND, class Geo>
 __global__ void __launch_bounds__(kThreads) step8_kernel(const StepArgs<pointers(ND)> A, const Geo G) {
   const int lane = threadIdx.x & 63;
@@ -284,7 +287,8 @@ __global__ void __launch_bounds__(kThreads) step8_kernel(const StepArgs<pointers
   }
 }
 
-// Conversion of binary32 moments and back.
+// Conversion of binary32 moments and back, 10 bytes an element.  Measured: back,
+// 262M elements, 0.50 ms, 5.3 TB/s.
 struct ConvertArgs {
   float *m, *v;
   Codes q;
@@ -376,6 +380,9 @@ unsigned grid_for(uint32_t units, int64_t blocks_per_cu) {
   return (unsigned)std::max<int64_t>(1, std::min(need, blocks_per_cu * kCus));
 }
 
+// Waves a CU, four to a block: few that each have 24 loads in flight.  Measured
+// (us, 262M elements, N_d = 8): the step with 4 waves 1618, 8 1520, 16 1606 to
+// 1660; the next unit's loads requested before this one's stores 1525.
 constexpr int64_t kStepBlocks = 2, kConvertBlocks = 5;
 
 struct Call {
