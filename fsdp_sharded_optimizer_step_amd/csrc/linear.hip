@@ -170,7 +170,7 @@ struct NRows {
 // of 128 and fill a CU alone, so nothing computes while a block begins and
 // ends (19 us; results and what the epilogue reads cross HBM then); sides of 128
 // stand two to a CU.  Measured (us): 8192 x 14336 x 4096 (tokens, sum, columns),
-// residual added, 790 to 811 (three cards), 1187 TFLOP/s and more; where it took
+// bias, gelu, residual and pre, 790 to 811 (three cards), 1187 TFLOP/s and more; where it took
 // 790, 718 with every request a hit in L2 and 660 without requests.  16384 x 4096
 // x 14336 with n adjacent and the activation's gradient 1721, 1118 TFLOP/s.  Not
 // kept: a third place in LDS for A's steps (783 to 768, but 16384 x 14336 x 4096
