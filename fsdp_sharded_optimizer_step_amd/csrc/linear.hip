@@ -226,21 +226,19 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
   const bool has_end = sz == all_steps;
   const auto at = [&](int32_t i) ZERO_INLINE { return has_end ? (i == 0 ? all_steps - 1 : sa + i - 1) : sa + i; };
   const uint32_t mine = lds_base + wave * S::kLoads * 1024;
-  // request j for step i; 0 to kLoads - 1 are A's
-  const auto fetch1 = [&](const char* a_at, const char* b_at, int buf, auto index) ZERO_INLINE {
+  // request j of A or B for the step at a_at or b_at
+  const auto fetch_a = [&](const char* a_at, int buf, auto index) ZERO_INLINE {
     constexpr int j = decltype(index)::value;
-    if constexpr (j < S::kLoads)
-      request(a_at, ra.off[j], mine + buf * S::kBuffer + j * 1024);
-    else
-      request(b_at, rb.off[j - S::kLoads], mine + buf * S::kBuffer + S::kOperand + (j - S::kLoads) * 1024);
+    request(a_at, ra.off[j], mine + buf * S::kBuffer + j * 1024);
+  };
+  const auto fetch_b = [&](const char* b_at, int buf, auto index) ZERO_INLINE {
+    constexpr int j = decltype(index)::value;
+    request(b_at, rb.off[j], mine + buf * S::kBuffer + S::kOperand + j * 1024);
   };
   const auto a_of = [&](int32_t i) ZERO_INLINE { return uniform(pa + (int64_t)at(i) * KRows<S>::step_bytes(A.a_stride)); };
   const auto b_of = [&](int32_t i) ZERO_INLINE { return uniform(pb + (int64_t)at(i) * BRows::step_bytes(A.b_stride)); };
-  const auto fetch = [&](int32_t i, int buf) ZERO_INLINE {
-    const char *a_at = a_of(i), *b_at = b_of(i);
-    unrolled<2 * S::kLoads>([&](auto j) ZERO_INLINE { fetch1(a_at, b_at, buf, j); });
-  };
-  // The first two steps, the first one's k from `left` on replaced by zeros.
+  // The first step, its k from `left` on replaced by zeros, and A's part of the
+  // second.
   const auto fetch_first = [&]() ZERO_INLINE {
     const char *a_at = a_of(0), *b_at = b_of(0);
     const int left_a = A.K - at(0) * kStep, left_b = (NC ? A.Kb : A.K) - at(0) * kStep;
@@ -250,8 +248,9 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
       request(b_at, rb.at(j, left_b), mine + S::kOperand + j * 1024);
     }
     if (steps > 1) {
-      fetch(1, 1);
-      requests_done<2 * S::kLoads>();
+      const char* a_1 = a_of(1);
+      unrolled<S::kLoads>([&](auto j) ZERO_INLINE { fetch_a(a_1, 1, j); });
+      requests_done<S::kLoads>();
     } else {
       requests_done();
     }
@@ -300,24 +299,35 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
     unrolled<next - first>([&](auto j) ZERO_INLINE { f(std::integral_constant<int, first + decltype(j)::value>{}); });
   };
   constexpr std::integral_constant<int, 2 * W> kReads;
-  constexpr std::integral_constant<int, 2 * S::kLoads> kRequests;
+  constexpr std::integral_constant<int, S::kLoads> kRequests;
   const auto with_reads = [&](auto from, auto to, int buf, int s) ZERO_INLINE {
     multiply(from, [&](auto index) ZERO_INLINE { share(index, kReads, [&](auto j) ZERO_INLINE { read1(to, buf, s, j); }); });
   };
-  // Step i, in buffer `buf`.  NEXT: steps that follow, two or more of which
-  // the first of those is requested.
+  // Step i, in buffer `buf`.  kNext: steps that follow (2: or more).  Its buffer
+  // is free once the last stretch is read.  A's part of step i + 2 is requested
+  // then, B's in the first stretch of step i + 1: all at once the requests
+  // would hold the products up (8192 x 14336 x 4096: 775 us against 724), and
+  // further apart they come too late (733).
   const auto step = [&](auto next, int32_t i, int buf) ZERO_INLINE {
     constexpr int kNext = decltype(next)::value;
-    with_reads(k0, k1, buf, 1);
+    if constexpr (kNext > 0) {
+      const char* b_at = b_of(i + 1);
+      multiply(k0, [&](auto index) ZERO_INLINE {
+        share(index, kReads, [&](auto j) ZERO_INLINE { read1(k1, buf, 1, j); });
+        share(index, kRequests, [&](auto j) ZERO_INLINE { fetch_b(b_at, buf ^ 1, j); });
+      });
+    } else {
+      with_reads(k0, k1, buf, 1);
+    }
     with_reads(k1, k0, buf, 2);
     with_reads(k0, k1, buf, 3);
     if (kNext > 0) requests_done();
     __syncthreads();
     if constexpr (kNext > 1) {
-      const char *a_at = a_of(i + 2), *b_at = b_of(i + 2);
+      const char* a_at = a_of(i + 2);
       multiply(k1, [&](auto index) ZERO_INLINE {
         share(index, kReads, [&](auto j) ZERO_INLINE { read1(k0, buf ^ 1, 0, j); });
-        share(index, kRequests, [&](auto j) ZERO_INLINE { fetch1(a_at, b_at, buf, j); });
+        share(index, kRequests, [&](auto j) ZERO_INLINE { fetch_a(a_at, buf, j); });
       });
     } else if constexpr (kNext > 0) {
       with_reads(k1, k0, buf ^ 1, 0);
