@@ -50,17 +50,16 @@ struct Args {
   Epilogue e;
 };
 
-// The shape of a block's tile: 64*W rows and columns, four waves two by two,
-// W panels of 32 along each side of a wave.
+// The shape of a block's tile: 64*W rows and columns, four waves two by two.
 template <int W_>
 struct Shape {
   static constexpr int W = W_, kSide = 64 * W;
   static constexpr int kOperand = kSide * 128, kBuffer = 2 * kOperand;
   static constexpr int kLoads = 2 * W;  // requests of a wave for an operand
-  // The way out: a strip of 32 rows of a wave's sums, its rows 32 bytes apart
-  // from each other's banks, and what the epilogue reads beside them, 16 bytes
-  // a lane and piece of 8 columns.
-  static constexpr int kCols = W * 32, kRow = kCols + 8;
+  // The way out: a strip of 32 rows of a wave's sums, of which 16 lanes write 16
+  // bytes to as many rows and meet all banks, and what the epilogue reads beside
+  // them, 16 bytes a lane and piece of 8 columns.
+  static constexpr int kCols = W * 32, kRow = kCols + 4;
   static constexpr int kAcross = kCols / 8, kDown = 64 / kAcross, kVecs = 32 / kDown;
   static constexpr int kStrip = 32 * kRow * 4, kWay = kStrip + 2 * kVecs * 1024;
   static constexpr int kLds = 2 * kBuffer > 4 * kWay ? 2 * kBuffer : 4 * kWay;
@@ -112,14 +111,18 @@ struct KRows {
   }
   static __device__ __forceinline__ bool missing(int j, int left) { return chunk(j) * 8 >= left; }
   static __device__ __forceinline__ int64_t step_bytes(int64_t) { return kStep * 2; }
-  // fragment: 32 rows x 16 k; lane l holds row l % 32, k 8 * (l / 32) to + 7
-  static __device__ __forceinline__ int frag_offset() { return (threadIdx.x & 31) * 128; }
-  static __device__ __forceinline__ bf16x8 frag(const lds_char* p, int panel, int s) {
-    const int c = (2 * s + (int)((threadIdx.x >> 5) & 1)) ^ (int)((threadIdx.x >> 1) & 7);
-    typedef __attribute__((address_space(3))) bf16x8 lds_t;
-    return *(const lds_t*)(p + panel * 4096 + c * 16);
+  // fragment s of a panel of ROWS (16 or 32): 512 / ROWS k; lane l holds row l %
+  // ROWS, k 8 * (l / ROWS) to + 7
+  template <int ROWS>
+  static __device__ __forceinline__ int frag_offset() {
+    return (threadIdx.x & (ROWS - 1)) * 128;
   }
-  static constexpr int kReads = 1;
+  template <int ROWS>
+  static __device__ __forceinline__ bf16x8 frag(const lds_char* p, int panel, int s) {
+    const int c = (64 / ROWS * s + (int)((threadIdx.x & 63) / ROWS)) ^ (int)((threadIdx.x >> 1) & 7);
+    typedef __attribute__((address_space(3))) bf16x8 lds_t;
+    return *(const lds_t*)(p + panel * (128 * ROWS) + c * 16);
+  }
 };
 
 // The same for an operand with n adjacent, in panels of 64 columns: request j
@@ -148,8 +151,13 @@ struct NRows {
   static __device__ __forceinline__ bool missing(int j, int left) { return row(j) >= left; }
   static __device__ __forceinline__ int64_t step_bytes(int64_t stride) { return kStep * stride * 2; }
   // 16 lanes read 4 rows of 16 columns and each gets a column's 4 rows
-  static __device__ __forceinline__ int frag_offset() { return 0; }
+  template <int COLS>
+  static __device__ __forceinline__ int frag_offset() {
+    return 0;
+  }
+  template <int COLS>
   static __device__ __forceinline__ bf16x8 frag(const lds_char* p, int panel, int s) {
+    static_assert(COLS == 32);
     typedef __attribute__((address_space(3))) s16x4 lds_t;
     const int l = threadIdx.x & 63, g = l >> 4, i = l & 15;
     const int k = i >> 2;  // row % 4 of both reads
@@ -159,7 +167,33 @@ struct NRows {
     const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(q + 512));
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
   }
-  static constexpr int kReads = 2;
+};
+
+// The matrix instructions: panels of 16 rows and columns and 32 k take less power
+// a product, since a sum is read and written half as often, and so run at a
+// higher clock (16384 x 4096 x 14336: 1490 us, of 32 rows and 16 k 1555).  With n
+// adjacent the compiler moves the sums of the smaller panels about (2190).
+template <bool NC>
+struct Panels {
+  static constexpr int kSide = 16, kQuads = 1;
+  typedef f32x4 Sums;
+  // lane l, value j: row l % 16 of a, row 4 * (l / 16) + j of b
+  static __device__ __forceinline__ Sums multiply(bf16x8 a, bf16x8 b, Sums c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x4 quad(const Sums& c, int) { return c; }
+};
+template <>
+struct Panels<true> {
+  static constexpr int kSide = 32, kQuads = 4;
+  typedef f32x16 Sums;
+  // lane l, value j: row l % 32 of a, row 8 * (j / 4) + 4 * (l / 32) + j % 4 of b
+  static __device__ __forceinline__ Sums multiply(bf16x8 a, bf16x8 b, Sums c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, a, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x4 quad(const Sums& c, int q) {
+    return f32x4{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+  }
 };
 
 // A block's tile of the result, or its share of a split tile.  The matrix cores
@@ -180,6 +214,9 @@ template <class S, bool NC>
 __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(const Args A) {
   constexpr int W = S::W, kSide = S::kSide;
   using BRows = std::conditional_t<NC, NRows<S>, KRows<S>>;
+  using Matrix = Panels<NC>;
+  constexpr int kPanel = Matrix::kSide, P = S::kCols / kPanel;  // panels of a wave's side
+  constexpr int kStretches = kStep * kPanel / 512;              // of a step, each of an instruction's k
   __shared__ __align__(1024) char shared[S::kLds];
   lds_char* lds = (lds_char*)shared;
   const uint32_t lds_base = (uint32_t)(uintptr_t)lds;
@@ -206,13 +243,11 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 1, wn = wave & 1;
   const int lane = threadIdx.x & 63;
-  f32x16 acc[W][W];
+  typename Matrix::Sums acc[P][P];
 #pragma unroll
-  for (int m = 0; m < W; ++m)
+  for (int m = 0; m < P; ++m)
 #pragma unroll
-    for (int n = 0; n < W; ++n)
-#pragma unroll
-      for (int k = 0; k < 16; ++k) acc[m][n][k] = 0.f;
+    for (int n = 0; n < P; ++n) acc[m][n] = typename Matrix::Sums{};
 
   KRows<S> ra;
   BRows rb;
@@ -237,8 +272,8 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
   };
   const auto a_of = [&](int32_t i) ZERO_INLINE { return uniform(pa + (int64_t)at(i) * KRows<S>::step_bytes(A.a_stride)); };
   const auto b_of = [&](int32_t i) ZERO_INLINE { return uniform(pb + (int64_t)at(i) * BRows::step_bytes(A.b_stride)); };
-  // The first step, its k from `left` on replaced by zeros, and A's part of the
-  // second.
+  // The first step, its k from `left` on replaced by zeros, and what step 0 does
+  // not request of the second.
   const auto fetch_first = [&]() ZERO_INLINE {
     const char *a_at = a_of(0), *b_at = b_of(0);
     const int left_a = A.K - at(0) * kStep, left_b = (NC ? A.Kb : A.K) - at(0) * kStep;
@@ -248,9 +283,10 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
       request(b_at, rb.at(j, left_b), mine + S::kOperand + j * 1024);
     }
     if (steps > 1) {
-      const char* a_1 = a_of(1);
+      const char *a_1 = a_of(1), *b_1 = b_of(1);
       unrolled<S::kLoads>([&](auto j) ZERO_INLINE { fetch_a(a_1, 1, j); });
-      requests_done<S::kLoads>();
+      if constexpr (kStretches == 2) unrolled<S::kLoads>([&](auto j) ZERO_INLINE { fetch_b(b_1, 1, j); });
+      requests_done<(kStretches == 2 ? 2 : 1) * S::kLoads>();
     } else {
       requests_done();
     }
@@ -264,81 +300,87 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
     }
   };
 
-  const lds_char* const fa = lds + wm * W * 4096 + KRows<S>::frag_offset();
-  const lds_char* const fb = lds + S::kOperand + wn * W * 4096 + BRows::frag_offset();
-  bf16x8 a[2][W], b[2][W];
+  const lds_char* const fa = lds + wm * W * 4096 + KRows<S>::template frag_offset<kPanel>();
+  const lds_char* const fb = lds + S::kOperand + wn * W * 4096 + BRows::template frag_offset<kPanel>();
+  bf16x8 a[2][P], b[2][P];  // two sets of fragments
   const auto read1 = [&](auto set, int buf, int s, auto index) ZERO_INLINE {
     constexpr int to = decltype(set)::value, j = decltype(index)::value;
-    if constexpr (j < W)
-      a[to][j] = KRows<S>::frag(fa + buf * S::kBuffer, j, s);
+    if constexpr (j < P)
+      a[to][j] = KRows<S>::template frag<kPanel>(fa + buf * S::kBuffer, j, s);
     else
-      b[to][j - W] = BRows::frag(fb + buf * S::kBuffer, j - W, s);
+      b[to][j - P] = BRows::template frag<kPanel>(fb + buf * S::kBuffer, j - P, s);
   };
-  constexpr std::integral_constant<int, 0> k0;  // the two sets of fragments
-  constexpr std::integral_constant<int, 1> k1;
-  const auto read = [&](auto set, int buf, int s) ZERO_INLINE {
-    unrolled<2 * W>([&](auto j) ZERO_INLINE { read1(set, buf, s, j); });
-  };
-  // The products of one stretch of 16 k; after each of them `beside` puts its
-  // share of other work.
-  constexpr int kM = W * W;
+  // The products of one stretch; after each of them `beside` puts its share of
+  // other work.
+  constexpr int kM = P * P;
   const auto multiply = [&](auto set, auto beside) ZERO_INLINE {
     constexpr int from = decltype(set)::value;
     unrolled<kM>([&](auto index) ZERO_INLINE {
       constexpr int i = decltype(index)::value;
-      acc[i / W][i % W] =
-          __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[from][i / W], b[from][i % W], acc[i / W][i % W], 0, 0, 0);
+      acc[i / P][i % P] = Matrix::multiply(a[from][i / P], b[from][i % P], acc[i / P][i % P]);
       beside(index);
       __builtin_amdgcn_sched_barrier(0);
     });
   };
-  // f(j) for those of N things that go beside product I
-  const auto share = [](auto index, auto count, auto f) ZERO_INLINE {
-    constexpr int i = decltype(index)::value, n = decltype(count)::value;
-    constexpr int first = (i * n + kM - 1) / kM, next = ((i + 1) * n + kM - 1) / kM;
-    unrolled<next - first>([&](auto j) ZERO_INLINE { f(std::integral_constant<int, first + decltype(j)::value>{}); });
+  // f(j) for those of N things, dealt to the products from FROM to TO - 1, that
+  // go beside product I
+  const auto share = [](auto index, auto from, auto to, auto count, auto f) ZERO_INLINE {
+    constexpr int len = decltype(to)::value - decltype(from)::value, n = decltype(count)::value;
+    constexpr int i = decltype(index)::value - decltype(from)::value;
+    if constexpr (i >= 0 && i < len) {
+      constexpr int first = (i * n + len - 1) / len, next = ((i + 1) * n + len - 1) / len;
+      unrolled<next - first>([&](auto j) ZERO_INLINE { f(std::integral_constant<int, first + decltype(j)::value>{}); });
+    }
   };
-  constexpr std::integral_constant<int, 2 * W> kReads;
+  constexpr std::integral_constant<int, 0> k0;
+  constexpr std::integral_constant<int, kM / 2> kHalf;
+  constexpr std::integral_constant<int, kM> kAll;
+  constexpr std::integral_constant<int, kStretches == 2 ? kM / 2 : kM> kRead;  // the products that reads go beside
+  constexpr std::integral_constant<int, 2 * P> kReads;
   constexpr std::integral_constant<int, S::kLoads> kRequests;
-  const auto with_reads = [&](auto from, auto to, int buf, int s) ZERO_INLINE {
-    multiply(from, [&](auto index) ZERO_INLINE { share(index, kReads, [&](auto j) ZERO_INLINE { read1(to, buf, s, j); }); });
-  };
   // Step i, in buffer `buf`.  kNext: steps that follow (2: or more).  Its buffer
-  // is free once the last stretch is read.  A's part of step i + 2 is requested
-  // then, B's in the first stretch of step i + 1: all at once the requests
-  // would hold the products up (8192 x 14336 x 4096: 775 us against 724), and
-  // further apart they come too late (733).
+  // is free once the last stretch is read.  The requests for step i + 2 go with
+  // the 32 k after that, A's first, B's, where the stretches have 16 k, with
+  // the first one of step i + 1: all within 16 k they would hold the products
+  // up (8192 x 14336 x 4096: 775 us against 724), and further apart they come
+  // too late (733).
   const auto step = [&](auto next, int32_t i, int buf) ZERO_INLINE {
     constexpr int kNext = decltype(next)::value;
-    if constexpr (kNext > 0) {
-      const char* b_at = b_of(i + 1);
-      multiply(k0, [&](auto index) ZERO_INLINE {
-        share(index, kReads, [&](auto j) ZERO_INLINE { read1(k1, buf, 1, j); });
-        share(index, kRequests, [&](auto j) ZERO_INLINE { fetch_b(b_at, buf ^ 1, j); });
+    unrolled<kStretches - 1>([&](auto stretch) ZERO_INLINE {
+      constexpr int s = decltype(stretch)::value;
+      const char* b_at = pb;
+      if constexpr (s == 0 && kNext > 0 && kStretches > 2) b_at = b_of(i + 1);
+      multiply(std::integral_constant<int, s % 2>{}, [&](auto index) ZERO_INLINE {
+        share(index, k0, kRead, kReads,
+              [&](auto j) ZERO_INLINE { read1(std::integral_constant<int, (s + 1) % 2>{}, buf, s + 1, j); });
+        if constexpr (s == 0 && kNext > 0 && kStretches > 2)
+          share(index, k0, kAll, kRequests, [&](auto j) ZERO_INLINE { fetch_b(b_at, buf ^ 1, j); });
       });
-    } else {
-      with_reads(k0, k1, buf, 1);
-    }
-    with_reads(k1, k0, buf, 2);
-    with_reads(k0, k1, buf, 3);
+    });
     if (kNext > 0) requests_done();
     __syncthreads();
-    if constexpr (kNext > 1) {
-      const char* a_at = a_of(i + 2);
-      multiply(k1, [&](auto index) ZERO_INLINE {
-        share(index, kReads, [&](auto j) ZERO_INLINE { read1(k0, buf ^ 1, 0, j); });
-        share(index, kRequests, [&](auto j) ZERO_INLINE { fetch_a(a_at, buf, j); });
+    constexpr std::integral_constant<int, (kStretches - 1) % 2> kLast;
+    if constexpr (kNext > 0) {
+      const char *a_at = pa, *b_at = pb;
+      if constexpr (kNext > 1) a_at = a_of(i + 2);
+      if constexpr (kNext > 1 && kStretches == 2) b_at = b_of(i + 2);
+      multiply(kLast, [&](auto index) ZERO_INLINE {
+        share(index, k0, kRead, kReads, [&](auto j) ZERO_INLINE { read1(k0, buf ^ 1, 0, j); });
+        if constexpr (kNext > 1 && kStretches == 2) {
+          share(index, k0, kHalf, kRequests, [&](auto j) ZERO_INLINE { fetch_a(a_at, buf, j); });
+          share(index, kHalf, kAll, kRequests, [&](auto j) ZERO_INLINE { fetch_b(b_at, buf, j); });
+        } else if constexpr (kNext > 1) {
+          share(index, k0, kAll, kRequests, [&](auto j) ZERO_INLINE { fetch_a(a_at, buf, j); });
+        }
       });
-    } else if constexpr (kNext > 0) {
-      with_reads(k1, k0, buf ^ 1, 0);
     } else {
-      multiply(k1, [](auto) ZERO_INLINE {});
+      multiply(kLast, [](auto) ZERO_INLINE {});
     }
   };
   if (steps > 0) {
     fetch_first();
     __syncthreads();
-    read(k0, 0, 0);
+    unrolled<2 * P>([&](auto j) ZERO_INLINE { read1(k0, 0, 0, j); });
     int32_t i = 0;
 #pragma unroll 1
     for (; i + 2 < steps; ++i) step(std::integral_constant<int, 2>{}, i, i & 1);
@@ -349,100 +391,108 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
     step(std::integral_constant<int, 0>{}, i, i & 1);
   }
 
-  // lane l, register k: row 8*(k/4) + 4*(l/32) + k%4, column l%32
-  if (tile < A.whole) {
-    // A wave's sums leave 32 rows at a time through LDS of its own, from where
-    // a lane gets 8 columns of a row.  What the epilogue reads of the next 32
-    // rows is on its way meanwhile; it waits in LDS too, so that the
-    // activations stand in a loop and not in every piece's code.
-    constexpr int kVecs = S::kVecs, kDown = S::kDown, kRow = S::kRow;
-    typedef __attribute__((address_space(3))) float lds_f32;
-    typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
-    lds_char* const way = lds + wave * S::kWay;
-    lds_f32* const strip = (lds_f32*)way;
-    lds_u32x4* const kept = (lds_u32x4*)(way + S::kStrip) + lane;
-    const int down = lane / S::kAcross, across = lane % S::kAcross * 8;
-    const int32_t c = c0 + wn * S::kCols + across;
-    const int left = A.N - c;
-    const bool reads = A.e.add || A.e.pre_in;
-    float bias[8];
-    bias_at(A.e, c, left, bias);
-    Beside b[kVecs];
-    const auto fetch_beside = [&](int m) ZERO_INLINE {
-      if (!reads) return;
+  if (tile >= A.whole) {
+    // to the workspace as they lie, for sum_kernel
+    float* const to = A.partial + (((int64_t)(tile - A.whole) * A.splits + split) * 4 + wave) * (kSide * kSide / 4) + lane * 4;
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        const int32_t r = r0 + (wm * W + m) * 32 + i * kDown + down;
-        b[i] = beside_at(A.e, A.N, r, c, r < A.M ? left : 0);
-      }
-    };
-    fetch_beside(0);
-    __syncthreads();
-    unrolled<W>([&](auto index) ZERO_INLINE {
-      constexpr int m = decltype(index)::value;
+    for (int m = 0; m < P; ++m)
 #pragma unroll
-      for (int n = 0; n < W; ++n)
+      for (int n = 0; n < P; ++n)
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-          strip[(8 * (k >> 2) + (k & 3) + 4 * (lane >> 5)) * kRow + n * 32 + (lane & 31)] = acc[m][n][k];
-      if (reads) {
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-          kept[i * 128] = b[i].add;
-          kept[i * 128 + 64] = b[i].pre;
-        }
-      }
-      lanes_meet_in_lds();
-      if constexpr (m + 1 < W) fetch_beside(m + 1);
-      const int32_t rb = r0 + (wm * W + m) * 32 + down;
-#pragma unroll 2
-      for (int i = 0; i < kVecs; ++i) {
-        const lds_f32x4* p = (const lds_f32x4*)(strip + (i * kDown + down) * kRow + across);
-        const f32x4 lo = p[0], hi = p[1];
-        float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        Beside x{{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
-        if (reads) x = Beside{kept[i * 128], kept[i * 128 + 64]};
-        const int32_t r = rb + i * kDown;
-        if (r < A.M && left > 0) finish8(A.e, A.N, r, c, left, v, x, bias);
-      }
-      lanes_meet_in_lds();
-    });
+        for (int q = 0; q < Matrix::kQuads; ++q)
+          *(f32x4*)(to + ((m * P + n) * Matrix::kQuads + q) * 256) = Matrix::quad(acc[m][n], q);
     return;
   }
-  // a tile of the workspace, rows of kSide columns
-  float* const to = A.partial + ((int64_t)(tile - A.whole) * A.splits + split) * kSide * kSide +
-                    4 * (lane >> 5) * kSide + (lane & 31);
+  // A wave's sums leave 32 rows at a time through LDS of its own, from where a
+  // lane gets 8 columns of a row.  What the epilogue reads of the next 32 rows is
+  // on its way meanwhile; it waits in LDS too, so that the activations stand in
+  // a loop and not in every piece's code.
+  constexpr int kVecs = S::kVecs, kDown = S::kDown, kRow = S::kRow;
+  typedef __attribute__((address_space(3))) float lds_f32;
+  typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+  lds_char* const way = lds + wave * S::kWay;
+  lds_f32* const strip = (lds_f32*)way;
+  lds_u32x4* const kept = (lds_u32x4*)(way + S::kStrip) + lane;
+  const int down = lane / S::kAcross, across = lane % S::kAcross * 8;
+  const int32_t c = c0 + wn * S::kCols + across;
+  const int left = A.N - c;
+  const bool reads = A.e.add || A.e.pre_in;
+  float bias[8];
+  bias_at(A.e, c, left, bias);
+  Beside beside[kVecs];
+  const auto fetch_beside = [&](int m) ZERO_INLINE {
+    if (!reads) return;
 #pragma unroll
-  for (int m = 0; m < W; ++m)
+    for (int i = 0; i < kVecs; ++i) {
+      const int32_t r = r0 + (wm * W + m) * 32 + i * kDown + down;
+      beside[i] = beside_at(A.e, A.N, r, c, r < A.M ? left : 0);
+    }
+  };
+  fetch_beside(0);
+  __syncthreads();
+  unrolled<W>([&](auto index) ZERO_INLINE {
+    constexpr int m = decltype(index)::value, kDeep = 32 / kPanel;
 #pragma unroll
-    for (int n = 0; n < W; ++n)
+    for (int h = 0; h < kDeep; ++h)
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-        to[((wm * W + m) * 32 + 8 * (k >> 2) + (k & 3)) * kSide + (wn * W + n) * 32] = acc[m][n][k];
+      for (int n = 0; n < P; ++n)
+#pragma unroll
+        for (int q = 0; q < Matrix::kQuads; ++q)
+          *(lds_f32x4*)(strip + (h * kPanel + lane % kPanel) * kRow + n * kPanel + 8 * q + lane / kPanel * 4) =
+              Matrix::quad(acc[m * kDeep + h][n], q);
+    if (reads) {
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        kept[i * 128] = beside[i].add;
+        kept[i * 128 + 64] = beside[i].pre;
+      }
+    }
+    lanes_meet_in_lds();
+    if constexpr (m + 1 < W) fetch_beside(m + 1);
+    const int32_t rb = r0 + (wm * W + m) * 32 + down;
+#pragma unroll 2
+    for (int i = 0; i < kVecs; ++i) {
+      const lds_f32x4* p = (const lds_f32x4*)(strip + (i * kDown + down) * kRow + across);
+      const f32x4 lo = p[0], hi = p[1];
+      float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      Beside x{{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
+      if (reads) x = Beside{kept[i * 128], kept[i * 128 + 64]};
+      const int32_t r = rb + i * kDown;
+      if (r < A.M && left > 0) finish8(A.e, A.N, r, c, left, v, x, bias);
+    }
+    lanes_meet_in_lds();
+  });
 }
 
 // Adds up a tile's splits, in order, and finishes the sums: `parts` blocks to
-// a tile.
-template <int SIDE>
+// a tile.  The 32 pieces of 8 columns in which 64 lanes hold 4 sums each are 32
+// neighbouring threads'.
+template <class S, bool NC>
 __global__ void __launch_bounds__(kThreads) sum_kernel(const Args A, int32_t parts) {
+  constexpr int SIDE = S::kSide, kWave = SIDE * SIDE / 4, kPanel = Panels<NC>::kSide, P = S::kCols / kPanel;
+  constexpr int kQuads = Panels<NC>::kQuads;
   const int32_t at = (int32_t)blockIdx.x / parts, part = (int32_t)blockIdx.x % parts;
   int32_t r0, c0;
   tile_place(A.whole + at, A.row_tiles, A.col_tiles, r0, c0);
   const float* from = A.partial + (int64_t)at * A.splits * SIDE * SIDE;
   const int per = SIDE * SIDE / 8 / parts;
   for (int g = part * per + threadIdx.x; g < (part + 1) * per; g += kThreads) {
-    const int32_t r = r0 * SIDE + g / (SIDE / 8), c = c0 * SIDE + (g % (SIDE / 8)) * 8;
+    const int wave = g / (kWave / 8), unit = g / 32 % (kWave / 256), x = g % 32;
+    const int m = unit / (P * kQuads), n = unit / kQuads % P, q = unit % kQuads;
+    const int row = x % kPanel, eight = kQuads * (x / kPanel) + q;  // of a panel
+    const int32_t r = r0 * SIDE + wave / 2 * S::kCols + m * kPanel + row;
+    const int32_t c = c0 * SIDE + wave % 2 * S::kCols + n * kPanel + 8 * eight;
     const int left = A.N - c;
     if (r >= A.M || left <= 0) continue;
     const Beside b = beside_at(A.e, A.N, r, c, left);
     float bias[8];
     bias_at(A.e, c, left, bias);
     f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = {0.f, 0.f, 0.f, 0.f};
+    const float* p = from + wave * kWave + unit * 256 + (row + 2 * kPanel * (x / kPanel)) * 4;
 #pragma unroll 8
-    for (int k = 0; k < A.splits; ++k) {
-      const f32x4* p = (const f32x4*)(from + (int64_t)k * SIDE * SIDE + g * 8);
-      lo += p[0];
-      hi += p[1];
+    for (int k = 0; k < A.splits; ++k, p += SIDE * SIDE) {
+      lo += *(const f32x4*)p;
+      hi += *(const f32x4*)(p + 4 * kPanel);
     }
     float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
     finish8(A.e, A.N, r, c, left, v, b, bias);
@@ -613,7 +663,11 @@ int launch(const Args& A, const Plan& p, bool n_adjacent, hipStream_t s) {
   if (rc != ZERO_OK || p.further == 0) return rc;
   int32_t parts = S::kSide * S::kSide / 2048;
   while (parts > 1 && parts * p.further > 2048) parts >>= 1;
-  hipLaunchKernelGGL(sum_kernel<S::kSide>, dim3((unsigned)(p.further * parts)), dim3(kThreads), 0, s, A, parts);
+  const dim3 sums((unsigned)(p.further * parts));
+  if (n_adjacent)
+    hipLaunchKernelGGL((sum_kernel<S, true>), sums, dim3(kThreads), 0, s, A, parts);
+  else
+    hipLaunchKernelGGL((sum_kernel<S, false>), sums, dim3(kThreads), 0, s, A, parts);
   return launched();
 }
 

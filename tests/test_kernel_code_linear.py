@@ -42,7 +42,7 @@ def test_lanes_exchange_sums_through_lds_in_order(linear):
         def step(open_, line):
             if line.startswith("fence "):
                 return frozenset()
-            if line.startswith("store float") and "addrspace(3)" in line:
+            if line.startswith("store <4 x float>") and "addrspace(3)" in line:
                 assert "read" not in open_, f"{name}: {line}"
                 seen.add("write")
                 return open_ | {"write"}
