@@ -13,8 +13,7 @@
 // and x is multiplied, or (in, out) and dy; n adjacent in the other two.
 //
 // A block's tiles of A and B go from memory straight to LDS, 16 bytes a lane,
-// two buffers of 64 k in turn: the next buffer but one is requested as soon as
-// every wave has read this one.  A request puts a wave's 1024 bytes next to
+// 64 k a step: the next step but one is requested as places become free.  A request puts a wave's 1024 bytes next to
 // each other in LDS, 8 rows of 128 bytes; which 16 bytes of its row a lane
 // fetches is permuted, so that the rows that a fragment read meets at a time
 // use all banks.  A fragment of k adjacent is one 16-byte read a lane, one
@@ -54,7 +53,8 @@ struct Args {
 template <int W_>
 struct Shape {
   static constexpr int W = W_, kSide = 64 * W;
-  static constexpr int kOperand = kSide * 128, kBuffer = 2 * kOperand;
+  static constexpr int kOperand = kSide * 128;  // bytes of a step
+  static constexpr int kB = 3 * kOperand;       // A has three places in LDS, behind them are B's two
   static constexpr int kLoads = 2 * W;  // requests of a wave for an operand
   // The way out: a strip of 32 rows of a wave's sums, of which 16 lanes write 16
   // bytes to as many rows and meet all banks, and what the epilogue reads beside
@@ -62,7 +62,8 @@ struct Shape {
   static constexpr int kCols = W * 32, kRow = kCols + 4;
   static constexpr int kAcross = kCols / 8, kDown = 64 / kAcross, kVecs = 32 / kDown;
   static constexpr int kStrip = 32 * kRow * 4, kWay = kStrip + 2 * kVecs * 1024;
-  static constexpr int kLds = 2 * kBuffer > 4 * kWay ? 2 * kBuffer : 4 * kWay;
+  static constexpr int kLds = 5 * kOperand;
+  static_assert(kLds >= 4 * kWay);
 };
 
 // An address that is the same in all lanes, in scalar registers.
@@ -261,32 +262,33 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
   const bool has_end = sz == all_steps;
   const auto at = [&](int32_t i) ZERO_INLINE { return has_end ? (i == 0 ? all_steps - 1 : sa + i - 1) : sa + i; };
   const uint32_t mine = lds_base + wave * S::kLoads * 1024;
-  // request j of A or B for the step at a_at or b_at
-  const auto fetch_a = [&](const char* a_at, int buf, auto index) ZERO_INLINE {
+  // request j of A or B for the step at a_at or b_at; `to`: its place
+  const auto fetch_a = [&](const char* a_at, int to, auto index) ZERO_INLINE {
     constexpr int j = decltype(index)::value;
-    request(a_at, ra.off[j], mine + buf * S::kBuffer + j * 1024);
+    request(a_at, ra.off[j], mine + to + j * 1024);
   };
-  const auto fetch_b = [&](const char* b_at, int buf, auto index) ZERO_INLINE {
+  const auto fetch_b = [&](const char* b_at, int to, auto index) ZERO_INLINE {
     constexpr int j = decltype(index)::value;
-    request(b_at, rb.off[j], mine + buf * S::kBuffer + S::kOperand + j * 1024);
+    request(b_at, rb.off[j], mine + S::kB + to + j * 1024);
   };
   const auto a_of = [&](int32_t i) ZERO_INLINE { return uniform(pa + (int64_t)at(i) * KRows<S>::step_bytes(A.a_stride)); };
   const auto b_of = [&](int32_t i) ZERO_INLINE { return uniform(pb + (int64_t)at(i) * BRows::step_bytes(A.b_stride)); };
   // The first step, its k from `left` on replaced by zeros, and what step 0 does
   // not request of the second.
+  constexpr int kEarly = kStretches > 2 ? S::kLoads / 2 : S::kLoads;  // of B's requests
   const auto fetch_first = [&]() ZERO_INLINE {
     const char *a_at = a_of(0), *b_at = b_of(0);
     const int left_a = A.K - at(0) * kStep, left_b = (NC ? A.Kb : A.K) - at(0) * kStep;
 #pragma unroll
     for (int j = 0; j < S::kLoads; ++j) {
       request(a_at, ra.at(j, left_a), mine + j * 1024);
-      request(b_at, rb.at(j, left_b), mine + S::kOperand + j * 1024);
+      request(b_at, rb.at(j, left_b), mine + S::kB + j * 1024);
     }
     if (steps > 1) {
       const char *a_1 = a_of(1), *b_1 = b_of(1);
-      unrolled<S::kLoads>([&](auto j) ZERO_INLINE { fetch_a(a_1, 1, j); });
-      if constexpr (kStretches == 2) unrolled<S::kLoads>([&](auto j) ZERO_INLINE { fetch_b(b_1, 1, j); });
-      requests_done<(kStretches == 2 ? 2 : 1) * S::kLoads>();
+      unrolled<S::kLoads>([&](auto j) ZERO_INLINE { fetch_a(a_1, S::kOperand, j); });
+      unrolled<kEarly>([&](auto j) ZERO_INLINE { fetch_b(b_1, S::kOperand, j); });
+      requests_done<S::kLoads + kEarly>();
     } else {
       requests_done();
     }
@@ -295,20 +297,20 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
 #pragma unroll 1
       for (int j = 0; j < S::kLoads; ++j) {
         if (KRows<S>::missing(j, left_a)) *(lds_u32x4*)(p + j * 1024) = u32x4{0u, 0u, 0u, 0u};
-        if (BRows::missing(j, left_b)) *(lds_u32x4*)(p + S::kOperand + j * 1024) = u32x4{0u, 0u, 0u, 0u};
+        if (BRows::missing(j, left_b)) *(lds_u32x4*)(p + S::kB + j * 1024) = u32x4{0u, 0u, 0u, 0u};
       }
     }
   };
 
   const lds_char* const fa = lds + wm * W * 4096 + KRows<S>::template frag_offset<kPanel>();
-  const lds_char* const fb = lds + S::kOperand + wn * W * 4096 + BRows::template frag_offset<kPanel>();
+  const lds_char* const fb = lds + S::kB + wn * W * 4096 + BRows::template frag_offset<kPanel>();
   bf16x8 a[2][P], b[2][P];  // two sets of fragments
-  const auto read1 = [&](auto set, int buf, int s, auto index) ZERO_INLINE {
+  const auto read1 = [&](auto set, int pa, int pb, int s, auto index) ZERO_INLINE {
     constexpr int to = decltype(set)::value, j = decltype(index)::value;
     if constexpr (j < P)
-      a[to][j] = KRows<S>::template frag<kPanel>(fa + buf * S::kBuffer, j, s);
+      a[to][j] = KRows<S>::template frag<kPanel>(fa + pa, j, s);
     else
-      b[to][j - P] = BRows::template frag<kPanel>(fb + buf * S::kBuffer, j - P, s);
+      b[to][j - P] = BRows::template frag<kPanel>(fb + pb, j - P, s);
   };
   // The products of one stretch; after each of them `beside` puts its share of
   // other work.
@@ -333,62 +335,74 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
     }
   };
   constexpr std::integral_constant<int, 0> k0;
-  constexpr std::integral_constant<int, kM / 2> kHalf;
   constexpr std::integral_constant<int, kM> kAll;
   constexpr std::integral_constant<int, kStretches == 2 ? kM / 2 : kM> kRead;  // the products that reads go beside
   constexpr std::integral_constant<int, 2 * P> kReads;
-  constexpr std::integral_constant<int, S::kLoads> kRequests;
-  // Step i, in buffer `buf`.  kNext: steps that follow (2: or more).  Its buffer
-  // is free once the last stretch is read.  The requests for step i + 2 go with
-  // the 32 k after that, A's first, B's, where the stretches have 16 k, with
-  // the first one of step i + 1: all within 16 k they would hold the products
-  // up (8192 x 14336 x 4096: 775 us against 724), and further apart they come
-  // too late (733).
-  const auto step = [&](auto next, int32_t i, int buf) ZERO_INLINE {
+  // Step i, in places p0 of A and q0 of B; p1: A's next place, p2: the free one.
+  // kNext: steps that follow (2: or more).  B's place is free once the last
+  // stretch is read, which is when the waves meet.  A CU takes 64 bytes a cycle, a
+  // request of a wave in 16, and one that has to wait holds its wave's
+  // products up: so the requests for step i + 2 are dealt over the whole step, A's
+  // before the waves meet, B's after that (and, where a step has four stretches,
+  // half of them with the next step's first).
+  const auto step = [&](auto next, int32_t i, int p0, int p1, int p2, int q0) ZERO_INLINE {
     constexpr int kNext = decltype(next)::value;
+    const int q1 = q0 ^ S::kOperand;
+    const char *a_at = pa, *b_at = pb;
+    if constexpr (kNext > 1) a_at = a_of(i + 2);
     unrolled<kStretches - 1>([&](auto stretch) ZERO_INLINE {
       constexpr int s = decltype(stretch)::value;
-      const char* b_at = pb;
       if constexpr (s == 0 && kNext > 0 && kStretches > 2) b_at = b_of(i + 1);
       multiply(std::integral_constant<int, s % 2>{}, [&](auto index) ZERO_INLINE {
         share(index, k0, kRead, kReads,
-              [&](auto j) ZERO_INLINE { read1(std::integral_constant<int, (s + 1) % 2>{}, buf, s + 1, j); });
-        if constexpr (s == 0 && kNext > 0 && kStretches > 2)
-          share(index, k0, kAll, kRequests, [&](auto j) ZERO_INLINE { fetch_b(b_at, buf ^ 1, j); });
-      });
-    });
-    if (kNext > 0) requests_done();
-    __syncthreads();
-    constexpr std::integral_constant<int, (kStretches - 1) % 2> kLast;
-    if constexpr (kNext > 0) {
-      const char *a_at = pa, *b_at = pb;
-      if constexpr (kNext > 1) a_at = a_of(i + 2);
-      if constexpr (kNext > 1 && kStretches == 2) b_at = b_of(i + 2);
-      multiply(kLast, [&](auto index) ZERO_INLINE {
-        share(index, k0, kRead, kReads, [&](auto j) ZERO_INLINE { read1(k0, buf ^ 1, 0, j); });
-        if constexpr (kNext > 1 && kStretches == 2) {
-          share(index, k0, kHalf, kRequests, [&](auto j) ZERO_INLINE { fetch_a(a_at, buf, j); });
-          share(index, kHalf, kAll, kRequests, [&](auto j) ZERO_INLINE { fetch_b(b_at, buf, j); });
+              [&](auto j) ZERO_INLINE { read1(std::integral_constant<int, (s + 1) % 2>{}, p0, q0, s + 1, j); });
+        if constexpr (kStretches == 2) {
+          if constexpr (kNext > 1)
+            share(index, k0, kAll, std::integral_constant<int, S::kLoads>{}, [&](auto j) ZERO_INLINE { fetch_a(a_at, p2, j); });
+        } else if constexpr (s == 0) {
+          if constexpr (kNext > 0)
+            share(index, k0, kAll, std::integral_constant<int, S::kLoads - kEarly>{}, [&](auto j) ZERO_INLINE {
+              fetch_b(b_at, q1, std::integral_constant<int, kEarly + decltype(j)::value>{});
+            });
         } else if constexpr (kNext > 1) {
-          share(index, k0, kAll, kRequests, [&](auto j) ZERO_INLINE { fetch_a(a_at, buf, j); });
+          share(index, k0, kAll, std::integral_constant<int, S::kLoads / 2>{}, [&](auto j) ZERO_INLINE {
+            fetch_a(a_at, p2, std::integral_constant<int, (s - 1) * (S::kLoads / 2) + decltype(j)::value>{});
+          });
         }
       });
-    } else {
-      multiply(kLast, [](auto) ZERO_INLINE {});
-    }
+    });
+    // all but A's of step i + 2
+    if constexpr (kNext > 0) requests_done<(kNext > 1 ? S::kLoads : 0)>();
+    __syncthreads();
+    constexpr std::integral_constant<int, (kStretches - 1) % 2> kLast;
+    if constexpr (kNext > 1) b_at = b_of(i + 2);
+    multiply(kLast, [&](auto index) ZERO_INLINE {
+      if constexpr (kNext > 0) share(index, k0, kRead, kReads, [&](auto j) ZERO_INLINE { read1(k0, p1, q1, 0, j); });
+      if constexpr (kNext > 1)
+        share(index, k0, kAll, std::integral_constant<int, kEarly>{}, [&](auto j) ZERO_INLINE { fetch_b(b_at, q0, j); });
+    });
   };
   if (steps > 0) {
     fetch_first();
     __syncthreads();
-    unrolled<2 * P>([&](auto j) ZERO_INLINE { read1(k0, 0, 0, j); });
+    unrolled<2 * P>([&](auto j) ZERO_INLINE { read1(k0, 0, 0, 0, j); });
     int32_t i = 0;
-#pragma unroll 1
-    for (; i + 2 < steps; ++i) step(std::integral_constant<int, 2>{}, i, i & 1);
-    if (i + 1 < steps) {
-      step(std::integral_constant<int, 1>{}, i, i & 1);
+    int p0 = 0, p1 = S::kOperand, p2 = 2 * S::kOperand, q0 = 0;
+    const auto turn = [&]() ZERO_INLINE {
+      const int p = p0;
+      p0 = p1;
+      p1 = p2;
+      p2 = p;
+      q0 ^= S::kOperand;
       ++i;
+    };
+#pragma unroll 1
+    for (; i + 2 < steps; turn()) step(std::integral_constant<int, 2>{}, i, p0, p1, p2, q0);
+    if (i + 1 < steps) {
+      step(std::integral_constant<int, 1>{}, i, p0, p1, p2, q0);
+      turn();
     }
-    step(std::integral_constant<int, 0>{}, i, i & 1);
+    step(std::integral_constant<int, 0>{}, i, p0, p1, p2, q0);
   }
 
   if (tile >= A.whole) {
