@@ -13,12 +13,12 @@
 // and x is multiplied, or (in, out) and dy; n adjacent in the other two.
 //
 // A block's tiles of A and B go from memory straight to LDS, 16 bytes a lane,
-// 64 k a step: the next step but one is requested as places become free.  A request puts a wave's 1024 bytes next to
-// each other in LDS, 8 rows of 128 bytes; which 16 bytes of its row a lane
-// fetches is permuted, so that the rows that a fragment read meets at a time
-// use all banks.  A fragment of k adjacent is one 16-byte read a lane, one
-// of n adjacent two transposing reads of 8 bytes.  Products of bf16 are exact
-// in binary32, sums are binary32.
+// 64 k a step: the next step but one is requested as places become free.  A
+// request puts a wave's 1024 bytes next to each other in LDS, 8 rows of 128
+// bytes; which 16 bytes of its row a lane fetches is permuted, so that the rows
+// that a fragment read meets at a time use all banks.  A fragment of k adjacent
+// is one 16-byte read a lane, one of n adjacent two transposing reads of 8
+// bytes.  Products of bf16 are exact in binary32, sums are binary32.
 //
 // Requests of 16 bytes need addresses of 16 bytes and rows of whole chunks.
 // An operand that has not (an odd width, a tensor at an odd place of the flat
@@ -198,19 +198,20 @@ struct Panels<true> {
 };
 
 // A block's tile of the result, or its share of a split tile.  The matrix cores
-// bound the loop: a step's 64 products of 32 x 32 x 16 a wave take 1.45 us of the
-// larger tile, 1.48 PFLOP/s over the chip; beside each product stands its share
-// of the next fragments' reads and of the requests two steps on, so that no
-// wave waits for either.  Sides of 256 read LDS half as often a product as sides
-// of 128 and fill a CU alone, so nothing computes while a block begins and
-// ends (19 us; results and what the epilogue reads cross HBM then); sides of 128
-// stand two to a CU.  Measured (us): 8192 x 14336 x 4096 (tokens, sum, columns),
-// bias, gelu, residual and pre, 790 to 811 (three cards), 1187 TFLOP/s and more; where it took
-// 790, 718 with every request a hit in L2 and 660 without requests.  16384 x 4096
-// x 14336 with n adjacent and the activation's gradient 1721, 1118 TFLOP/s.  Not
-// kept: a third place in LDS for A's steps (783 to 768, but 16384 x 14336 x 4096
-// 1593 to 1700); tiles in groups of 4 or 16 rows instead of 8 (up to 3 % better
-// in sums over 14336, 1.4 % worse in those over 4096).
+// bound the loop, at the clock that their power allows: beside each product
+// stands its share of the next fragments' reads and of the requests two steps
+// on, so that no wave waits for either.  Sides of 256 read LDS half as often a
+// product as sides of 128 and fill a CU alone, so nothing computes while a block
+// begins and ends (13 to 15 us; results and what the epilogue reads cross HBM
+// then); sides of 128 stand two to a CU.  Measured (us): 8192 x 14336 x 4096
+// (tokens, sum, columns) 623, 1545 TFLOP/s, with n adjacent 687; 16384 x 4096 x
+// 14336 1395, with n adjacent 1460; with everything in the epilogue 696 (K of
+// 14336), through the activation's gradient and with n adjacent 1659.  On the
+// way there: A's and B's steps in two places each, all requests beside a
+// quarter of a step's products 775 (1560 for sums over 4096), beside two quarters
+// 724 (1550), smaller panels of k adjacent 690 (1425); tiles in groups of 4 or 16 rows
+// instead of 8 within 3 % either way.  Without requests, for timing, 528 of the 690;
+// requests that always hit L2 611; without LDS reads 679.
 template <class S, bool NC>
 __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(const Args A) {
   constexpr int W = S::W, kSide = S::kSide;
@@ -358,7 +359,8 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
               [&](auto j) ZERO_INLINE { read1(std::integral_constant<int, (s + 1) % 2>{}, p0, q0, s + 1, j); });
         if constexpr (kStretches == 2) {
           if constexpr (kNext > 1)
-            share(index, k0, kAll, std::integral_constant<int, S::kLoads>{}, [&](auto j) ZERO_INLINE { fetch_a(a_at, p2, j); });
+            share(index, k0, kAll, std::integral_constant<int, S::kLoads>{},
+                  [&](auto j) ZERO_INLINE { fetch_a(a_at, p2, j); });
         } else if constexpr (s == 0) {
           if constexpr (kNext > 0)
             share(index, k0, kAll, std::integral_constant<int, S::kLoads - kEarly>{}, [&](auto j) ZERO_INLINE {
@@ -407,7 +409,8 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
 
   if (tile >= A.whole) {
     // to the workspace as they lie, for sum_kernel
-    float* const to = A.partial + (((int64_t)(tile - A.whole) * A.splits + split) * 4 + wave) * (kSide * kSide / 4) + lane * 4;
+    const int64_t part = (int64_t)(tile - A.whole) * A.splits + split;
+    float* const to = A.partial + (part * 4 + wave) * (kSide * kSide / 4) + lane * 4;
 #pragma unroll
     for (int m = 0; m < P; ++m)
 #pragma unroll
@@ -464,7 +467,10 @@ __global__ void __launch_bounds__(kThreads, S::W == 4 ? 1 : 2) product_kernel(co
     lanes_meet_in_lds();
     if constexpr (m + 1 < W) fetch_beside(m + 1);
     const int32_t rb = r0 + (wm * W + m) * 32 + down;
-#pragma unroll 2
+    // Not unrolled: a tile runs this code once, and the more of it there is the
+    // longer a CU waits for it (16384 x 4096 x 14336 with everything in the
+    // epilogue: 1580 us, by 2 1610, by 4 1710, by 8 1855).
+#pragma unroll 1
     for (int i = 0; i < kVecs; ++i) {
       const lds_f32x4* p = (const lds_f32x4*)(strip + (i * kDown + down) * kRow + across);
       const f32x4 lo = p[0], hi = p[1];
@@ -568,17 +574,17 @@ template <class S>
 struct Cost;
 template <>
 struct Cost<Shape<4>> {
-  static constexpr double step[2] = {1.45, 1.45}, ends = 19, part = 0.054, sum = 2.7;
+  static constexpr double step[2] = {1.42, 1.42}, ends = 13, part = 0.054, sum = 2.7;
 };
 template <>
 struct Cost<Shape<2>> {
-  static constexpr double step[2] = {0.64, 0.95}, ends = 4.5, part = 0.0134, sum = 2.7;
+  static constexpr double step[2] = {0.49, 0.80}, ends = 6, part = 0.0134, sum = 2.7;
 };
 
-// Measured (us) in splits of the smaller tile: 1000 x 2304 x 768 (tokens,
-// outputs, inputs) 1: 13.6, 3: 19.7; 1000 x 768 x 2304 1: 26.6, 3: 16.3, 9: 18.3; 333
-// x 8192 x 1024 1: 15.7, 2: 20.9; 300 x 300 x 8192 1: 73.9, 4: 24.6, 12: 15.8; 512 x
-// 4096 x 4096 1: 41.9, 4: 29.4.
+// Measured (us) in splits of the smaller tile, with a step of 0.64 us: 1000 x 2304
+// x 768 (tokens, outputs, inputs) 1: 13.6, 3: 19.7; 1000 x 768 x 2304 1: 26.6, 3: 16.3,
+// 9: 18.3; 333 x 8192 x 1024 1: 15.7, 2: 20.9; 300 x 300 x 8192 1: 73.9, 4: 24.6, 12: 15.8;
+// 512 x 4096 x 4096 1: 41.9, 4: 29.4.
 template <class S>
 Plan plan_for(int64_t M, int64_t N, int64_t K) {
   using C = Cost<S>;
