@@ -348,3 +348,22 @@ def test_the_same_bits_every_time():
         outs.append(torch.empty(333, 1000, device=DEV))
         z.zero_linear(w.L, 1, w.params, x, outs[-1], bias=3, activation="silu")
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+# Tiles of 256: of one block each, ragged; split over three blocks, with a sum of
+# odd length; whole ones and the split rest of them.
+LARGE = [(3000, 4160, 384), (3000, 384, 4160), (1000, 4160, 4100), (4100, 1000, 4104), (1000, 4104, 4160),
+         (4100, 5000, 4100)]
+
+
+@pytest.mark.parametrize("tr", [False, True])
+@pytest.mark.parametrize("t,o,i", LARGE)
+def test_large_tiles(t, o, i, tr):
+    test_whole_numbers(t, o, i, tr)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("t,o,i,tr", [(3000, 4160, 384, False), (3001, 4160, 384, True), (1000, 4160, 4100, False),
+                                      (1000, 4160, 4104, True)])
+def test_large_tiles_epilogues(act, t, o, i, tr):
+    test_epilogues(act, t, o, i, tr)
