@@ -19,6 +19,7 @@
 #include <algorithm>
 
 #include "act8.hpp"
+#include "activation.hpp"
 #include "matrix.hpp"
 
 namespace {
@@ -164,8 +165,9 @@ __device__ __forceinline__ void store_row(const Args& A, uint16_t* p, const Cols
     for (int m = 0; m < 8; ++m) {
       int i, j;
       pair_cols(A, pair_of<NL, MODE>(A, lane, m), i, j);
-      if (live && i < A.d) p[i] = (uint16_t)bf16_round(x[m]);
-      if (live && j < A.d) p[j] = (uint16_t)bf16_round(y[m]);
+      const uint32_t w = round2(x[m], y[m]);  // the instruction: fewer registers here than bf16_round
+      if (live && i < A.d) p[i] = (uint16_t)w;
+      if (live && j < A.d) p[j] = (uint16_t)(w >> 16);
     }
   } else {
     u32x4 a, b;
@@ -203,6 +205,13 @@ __device__ __forceinline__ f32x2 turn(const Args& A, int64_t t, int lane, int m)
   float si, co;
   sincospif(2.f * (float)(x - __builtin_rint(x)), &si, &co);
   return f32x2{co, si};
+}
+
+// What a column of pair m gives to the other one: nothing where the pair does
+// not turn, since an infinity or a NaN times a sine of zero would be a NaN.
+template <int NL, int MODE>
+__device__ __forceinline__ float crossing(const Args& A, int lane, int m, float x) {
+  return pair_of<NL, MODE>(A, lane, m) < A.half ? x : 0.f;
 }
 
 // A side's weights in LDS in the lanes' order: x's of a lane, then y's.
@@ -307,6 +316,11 @@ __global__ void __launch_bounds__(kThreads, GRAD ? 3 : 4) rotate_kernel(const Ar
         if (hb + k * across >= h1) break;
         const int h = hb + k * across + head_in;
         float x[8], y[8], ox[8], oy[8];
+        // Which pairs turn is found anew for each row: kept from row to row, in two
+        // scalar registers a pair, it makes the element-by-element kernels spill
+        // (16384 tokens, 32 + 8 heads of 96, 24 columns turning: 112 us against 104).
+        int own = lane;
+        if constexpr (MODE == kSingle) asm volatile("" : "+v"(own));
         if constexpr (!GRAD) {
           widen<MODE>(rx[k], x, y);
           if (normed) {
@@ -319,16 +333,16 @@ __global__ void __launch_bounds__(kThreads, GRAD ? 3 : 4) rotate_kernel(const Ar
           }
 #pragma unroll
           for (int m = 0; m < 8; ++m) {
-            ox[m] = x[m] * co[m] - y[m] * si[m];
-            oy[m] = x[m] * si[m] + y[m] * co[m];
+            ox[m] = x[m] * co[m] - crossing<NL, MODE>(A, own, m, y[m]) * si[m];
+            oy[m] = crossing<NL, MODE>(A, own, m, x[m]) * si[m] + y[m] * co[m];
           }
         } else {
           float gx[8], gy[8];
           widen<MODE>(ry[k], gx, gy);
 #pragma unroll
           for (int m = 0; m < 8; ++m) {
-            ox[m] = gx[m] * co[m] + gy[m] * si[m];
-            oy[m] = gy[m] * co[m] - gx[m] * si[m];
+            ox[m] = gx[m] * co[m] + crossing<NL, MODE>(A, own, m, gy[m]) * si[m];
+            oy[m] = gy[m] * co[m] - crossing<NL, MODE>(A, own, m, gx[m]) * si[m];
           }
           if (normed) {
             widen<MODE>(rx[k], x, y);

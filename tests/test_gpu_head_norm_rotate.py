@@ -249,6 +249,32 @@ def test_rows_of_infinities_leave_the_others_alone():
         assert torch.equal(a[~hit], b[~hit])
 
 
+@pytest.mark.parametrize("d,r,inter", [(128, 64, False), (128, 0, False), (128, 64, True), (64, 16, False),
+                                       (96, 24, False), (80, 20, True), (33, 32, False), (7, 0, False)])
+def test_columns_that_do_not_turn_leave_each_other_alone(d, r, inter):
+    """An infinity or a NaN in one of them reaches no other column: without a
+    norm they come out as they went in, in both directions."""
+    t, h = 6, 3
+    L, _ = layout(d, False)
+    rot = rotation(t, r // 2, inter=inter)
+    x = randn(1, t, h, d)
+    new = lambda: [torch.empty_like(x) for _ in range(2)]  # noqa: E731
+
+    def both(a, out):
+        z.zero_head_norm_rotate(L, None, None, None, a, None, 0.0, rot, out[0], None)
+        z.zero_head_norm_rotate_grad(L, None, None, None, a, None, None, None, 0.0, rot, out[1], None)
+    clean, got, bad = new(), new(), x.clone()
+    both(x, clean)
+    for k, c in enumerate(range(r, d)):                     # every column once, in a row of its own if there are enough
+        bad.view(t * h, d)[k % (t * h), c] = (float("inf"), float("nan"), float("-inf"))[k % 3]
+    both(bad, got)
+    hit = bad != x
+    for a, b in zip(clean, got):
+        assert torch.equal(a[~hit], b[~hit])
+        assert torch.equal(torch.nan_to_num(b[hit].float(), 5.0), torch.nan_to_num(bad[hit].float(), 5.0))
+        assert torch.equal(a[..., r:], x[..., r:])
+
+
 def test_gradient_against_differences():
     """Sums of dy * out change along a direction by the gradient's product with
     it: central differences in 64 bits of the reference's forward pass against
