@@ -273,6 +273,8 @@ __global__ void __launch_bounds__(kThreads, GRAD ? 3 : 4) rotate_kernel(const Ar
     for (int m = 0; m < 8; ++m) dwx[m] = dwy[m] = 0.f;
   }
   f32x2* const table = (f32x2*)shared + wave * kTable;
+  // Means are sums of what is divided by d first: where the mean of the squares
+  // is a binary32 number, their sum need not be.
   const float inv_d = 1.f / (float)A.d;
   // all lanes of a wave stay in the loops together: their rows' sums meet
   for (int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * down; t0 < A.tokens;
@@ -326,8 +328,8 @@ __global__ void __launch_bounds__(kThreads, GRAD ? 3 : 4) rotate_kernel(const Ar
           if (normed) {
             float ss = 0.f;
 #pragma unroll
-            for (int m = 0; m < 8; ++m) ss += x[m] * x[m] + y[m] * y[m];
-            const float r = 1.f / __builtin_sqrtf(lanes_sum<NL>(ss) * inv_d + A.eps);
+            for (int m = 0; m < 8; ++m) ss += x[m] * inv_d * x[m] + y[m] * inv_d * y[m];
+            const float r = 1.f / __builtin_sqrtf(lanes_sum<NL>(ss) + A.eps);
 #pragma unroll
             for (int m = 0; m < 8; ++m) x[m] = x[m] * r * weight(wx, m), y[m] = y[m] * r * weight(wy, m);
           }
@@ -349,13 +351,14 @@ __global__ void __launch_bounds__(kThreads, GRAD ? 3 : 4) rotate_kernel(const Ar
             float ss = 0.f, sg = 0.f;
 #pragma unroll
             for (int m = 0; m < 8; ++m) {
-              ss += x[m] * x[m] + y[m] * y[m];
-              sg += ox[m] * weight(wx, m) * x[m] + oy[m] * weight(wy, m) * y[m];
+              const float xd = x[m] * inv_d, yd = y[m] * inv_d;
+              ss += xd * x[m] + yd * y[m];
+              sg += ox[m] * weight(wx, m) * xd + oy[m] * weight(wy, m) * yd;
             }
             // lanes without a row, whose values are zeros, count for nothing
-            const float rms = __builtin_sqrtf(lanes_sum<NL>(ss) * inv_d + A.eps);
+            const float rms = __builtin_sqrtf(lanes_sum<NL>(ss) + A.eps);
             const float r = here && h < h1 ? 1.f / rms : 0.f;
-            const float mean = lanes_sum<NL>(sg) * inv_d * r;  // of g*n
+            const float mean = lanes_sum<NL>(sg) * r;  // of g*n
 #pragma unroll
             for (int m = 0; m < 8; ++m) {
               const float nx = x[m] * r, ny = y[m] * r;

@@ -249,6 +249,27 @@ def test_rows_of_infinities_leave_the_others_alone():
         assert torch.equal(a[~hit], b[~hit])
 
 
+@pytest.mark.parametrize("d,r,inter,top", [(128, 128, False, 1.5e19), (512, 512, True, 1.5e19), (100, 90, False, 1.5e19),
+                                           (64, 64, True, 1.5e19), (128, 64, False, 4e18), (16, 16, False, 1e19),
+                                           (512, 0, False, 1e-15)])
+def test_rows_up_to_the_largest_mean_square(d, r, inter, top):
+    """mean(x^2) up to 2.3e38: the sum of the squares would be infinite."""
+    t, h = 5, 3
+    L, pl = layout(d, False)
+    params, rot = randn(d, L.padded) + 1, rotation(t, r // 2, inter=inter)
+    w = f64(params)[positions(pl, d)]
+    x, dy = (randn(1, t, h, d).clamp(-1, 1) * top).to(BF16), randn(2, t, h, d)
+    x[0, 0] = top                                          # every column
+    out, dx, flat = torch.empty_like(x), torch.empty_like(x), Flat(L, pl, d, DEV)
+    z.zero_head_norm_rotate(L, 1, None, params, x, None, 0.0, rot, out, None)
+    close(out, *forward(f64(x), w, rot, 0.0), "out")
+    dy *= 1e18 if top > 1 else 1e-15                       # mean(|g x|) stays below 3e38
+    z.zero_head_norm_rotate_grad(L, 1, None, params, dy, None, x, None, 0.0, rot, dx, None, flat.acc, 2.0 ** -60)
+    g, bound, dw, odw = backward(f64(dy), f64(x), w, rot, 0.0)
+    close(dx, g, bound, "gradient")
+    flat.check(dw, odw + U * np.abs(dw), 2.0 ** -60, 0, "weight")
+
+
 @pytest.mark.parametrize("d,r,inter", [(128, 64, False), (128, 0, False), (128, 64, True), (64, 16, False),
                                        (96, 24, False), (80, 20, True), (33, 32, False), (7, 0, False)])
 def test_columns_that_do_not_turn_leave_each_other_alone(d, r, inter):
