@@ -17,6 +17,7 @@
 // for all the heads of a token that the lane works on.  The sums over a row go
 // through data-parallel moves between the lanes.
 #include <algorithm>
+#include <cfloat>
 
 #include "act8.hpp"
 #include "activation.hpp"
@@ -598,7 +599,7 @@ int run(const zero_layout* L, const uint16_t* params, int64_t tokens, int32_t d,
   const zero_heads* const side[2] = {q, k};
   int rc = shape_ok(L, tokens, d, side);
   if (rc != ZERO_OK) return rc;
-  if (!(eps >= 0.0) || !(eps - eps == 0.0)) return ZERO_EINVAL;
+  if (!(eps >= 0.0) || eps > (double)FLT_MAX) return ZERO_EINVAL;
   int32_t pairs;
   rc = rotation_ok(rot, tokens, d, &pairs);
   if (rc != ZERO_OK) return rc;
@@ -707,7 +708,8 @@ int run(const zero_layout* L, const uint16_t* params, int64_t tokens, int32_t d,
       }
     }
     A.chunks = p.chunks[0];
-    A.eps = (float)eps;
+    // one too small for binary32 still keeps rows of zeros from 0 / 0
+    A.eps = eps > 0.0 ? std::max((float)eps, FLT_TRUE_MIN) : 0.f;
     A.partial = sums ? (float*)g->workspace : nullptr;
     const dim3 grid((unsigned)p.along, (unsigned)(p.chunks[0] + p.chunks[1]));
     rc = g ? launch<true>(A, p.nl, mode, grid, stream) : launch<false>(A, p.nl, mode, grid, stream);

@@ -639,7 +639,8 @@ int zero_rms_norm_grad(const zero_layout* layout, int32_t tensor, const uint16_t
  *   positions_dev: n_axes x tokens signed numbers of position_bytes (4 or 8)
  *   bytes; freqs_dev: R/2 binary64 values, radians a position.  Angles are
  *   binary64; rows binary32 (so are the means: mean(x^2) up to 3e38, for the
- *   gradient mean(g*x), and its parts, too).
+ *   gradient mean(g*x), and its parts, too), and eps is rounded to binary32, a
+ *   positive one not to 0.
  * grad, for every row, out = dx from dy and the forward pass's x:
  *   u' = dy turned back; g = u'*w, n = x/rms: dx = bf16((g - n*mean(g*n))/rms);
  *   without a norm dx = bf16(u'), and x is not read.  The gradient of the
@@ -648,8 +649,9 @@ int zero_rms_norm_grad(const zero_layout* layout, int32_t tensor, const uint16_t
  *   The acc_flat_dev and bf16_flat_dev rules are those above; with no norm
  *   neither is used.
  * Common errors, and ZERO_EINVAL for a tensor of another size than head_dim,
- * more than head_dim / 2 pairs, an output whose rows meet; ZERO_ERANGE for more
- * than ZERO_MAX_HEADS heads or an operand over 2^50 elements. */
+ * more than head_dim / 2 pairs, an eps beyond binary32, an output whose rows
+ * meet; ZERO_ERANGE for more than ZERO_MAX_HEADS heads or an operand over 2^50
+ * elements. */
 #define ZERO_MAX_HEAD_DIM 512
 #define ZERO_MAX_HEADS (1 << 14)
 #define ZERO_MAX_AXES 4

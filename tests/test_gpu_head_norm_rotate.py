@@ -270,6 +270,18 @@ def test_rows_up_to_the_largest_mean_square(d, r, inter, top):
     flat.check(dw, odw + U * np.abs(dw), 2.0 ** -60, 0, "weight")
 
 
+def test_an_eps_too_small_for_binary32_keeps_rows_of_zeros():
+    t, d = 5, 64
+    L, _ = layout(d, False)
+    params, rot = randn(d, L.padded) + 1, rotation(t, 32)
+    x = randn(1, t, 2, d)
+    x[1] = 0
+    out = [torch.full_like(x, 9) for _ in range(3)]
+    for o, eps in zip(out, (1e-60, 2.0 ** -149, 1e-300)):
+        z.zero_head_norm_rotate(L, 1, None, params, x, None, eps, rot, o, None)
+    assert not out[0][1].any() and torch.equal(out[0], out[1]) and torch.equal(out[0], out[2])
+
+
 @pytest.mark.parametrize("d,r,inter", [(128, 64, False), (128, 0, False), (128, 64, True), (64, 16, False),
                                        (96, 24, False), (80, 20, True), (33, 32, False), (7, 0, False)])
 def test_columns_that_do_not_turn_leave_each_other_alone(d, r, inter):

@@ -103,6 +103,12 @@ GRAD = [
 
 
 @pytest.mark.parametrize("grad", [False, True])
+def test_an_eps_beyond_binary32_is_refused(L, grad):
+    assert call(L, grad, eps=3.5e38) == EINVAL and call(L, grad, eps=1e300) == EINVAL
+    assert call(L, grad, eps=3e38, tokens=0) == 0
+
+
+@pytest.mark.parametrize("grad", [False, True])
 def test_both_refuse(L, grad):
     for status, bad in BOTH:
         assert call(L, grad, **bad) == status, bad
