@@ -75,13 +75,20 @@ __device__ __forceinline__ const char* uniform(const char* p) {
 
 // 16 bytes a lane from base + off to LDS at `lds` + 16 * lane.  Written out:
 // the compiler does not know that the address is read at issue and would wait
-// for the data before the next LDS read.  No register is written; the wait is
-// requests_done().
+// for the data before the next LDS read.  No vector register is written; the wait
+// is requests_done().  m0 is a reserved register, of which the compiler warns: what
+// it keeps there itself it writes right before its use.  With memory declared it
+// keeps requests and LDS accesses in the order written, and the loop got faster
+// (8192 x 14336 x 4096: 660 us, 643 with it; 16384 x 4096 x 14336: 1400, 1373).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void request(const void* base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :
-               : "s"(lds), "v"(off), "s"(base));
+               : "s"(lds), "v"(off), "s"(base)
+               : "m0", "memory");
 }
+#pragma clang diagnostic pop
 // All but the last N of them.
 template <int N = 0>
 __device__ __forceinline__ void requests_done() {
