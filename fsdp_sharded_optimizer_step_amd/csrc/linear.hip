@@ -26,6 +26,7 @@
 #include <algorithm>
 
 #include "linear.hpp"
+#include "linear_plan.hpp"
 #include "matrix.hpp"
 
 namespace {
@@ -35,7 +36,7 @@ using namespace zs;
 #define ZERO_INLINE __attribute__((always_inline))
 
 constexpr int kThreads = 256;
-constexpr int kStep = 64;  // k of an LDS buffer: 128 bytes of a row
+constexpr int kStep = kTileStep;  // k of an LDS buffer: 128 bytes of a row
 
 struct Args {
   const uint16_t *a, *b;
@@ -52,7 +53,7 @@ struct Args {
 // The shape of a block's tile: 64*W rows and columns, four waves two by two.
 template <int W_>
 struct Shape {
-  static constexpr int W = W_, kSide = 64 * W;
+  static constexpr int W = W_, kSide = tile_side(W);
   static constexpr int kOperand = kSide * 128;  // bytes of a step
   static constexpr int kB = 3 * kOperand;       // A has three places in LDS, behind them are B's two
   static constexpr int kLoads = 2 * W;  // requests of a wave for an operand
@@ -560,71 +561,12 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const Copy w, const Copy
 }
 
 // ------------------------------------------------------------------ host
-// Tiles that fill the chip's 256 CUs are summed by one block each; the k of the
-// rest may be split over several blocks each, where an estimate of the time
-// says so.  The number of CUs is a constant: the order of a sum and the
-// workspace's size follow from the sizes alone.
-constexpr int64_t kCus = 256, kMaxSplits = 32;
 constexpr int64_t kMaxStride = (int64_t)1 << 22;  // a tile's rows lie within 32 bits
 
-struct Plan {
-  bool few;  // the kernels of few tokens
-  int64_t side, row_tiles, col_tiles, whole, further, splits, per_split;
+struct Plan : TilePlan {
+  bool few;                        // the kernels of few tokens
   int64_t w_bytes, a_bytes, bytes;  // copies, and everything
-  double us;
 };
-
-// What a block was measured to take (us): a step of 64 k, alone on its CU or
-// beside another; its beginning and end; a split's part of a tile, written and
-// read again; the launch that adds the parts up.
-template <class S>
-struct Cost;
-template <>
-struct Cost<Shape<4>> {
-  static constexpr double step[2] = {1.42, 1.42}, ends = 13, part = 0.054, sum = 2.7;
-};
-template <>
-struct Cost<Shape<2>> {
-  static constexpr double step[2] = {0.49, 0.80}, ends = 6, part = 0.0134, sum = 2.7;
-};
-
-// Measured (us) in splits of the smaller tile, with a step of 0.64 us: 1000 x 2304
-// x 768 (tokens, outputs, inputs) 1: 13.6, 3: 19.7; 1000 x 768 x 2304 1: 26.6, 3: 16.3,
-// 9: 18.3; 333 x 8192 x 1024 1: 15.7, 2: 20.9; 300 x 300 x 8192 1: 73.9, 4: 24.6, 12: 15.8;
-// 512 x 4096 x 4096 1: 41.9, 4: 29.4.
-template <class S>
-Plan plan_for(int64_t M, int64_t N, int64_t K) {
-  using C = Cost<S>;
-  Plan p{};
-  p.side = S::kSide;
-  p.row_tiles = (M + p.side - 1) / p.side;
-  p.col_tiles = (N + p.side - 1) / p.side;
-  const int64_t tiles = p.row_tiles * p.col_tiles, steps = std::max<int64_t>(1, (K + kStep - 1) / kStep);
-  const int64_t per_cu = S::W == 4 ? 1 : 2, at_once = kCus * per_cu;
-  p.whole = tiles / at_once * at_once;
-  p.further = tiles - p.whole;
-  p.splits = 1;
-  p.per_split = steps;
-  p.us = (double)(p.whole / at_once) * ((double)steps * C::step[per_cu - 1] + C::ends);
-  if (p.further == 0) return p;
-  double best = 0;
-  for (int64_t n = 1; n <= std::min(kMaxSplits, steps) && (n == 1 || n * p.further <= at_once); ++n) {
-    const int64_t per = (steps + n - 1) / n, splits = (steps + per - 1) / per, blocks = splits * p.further;
-    double us = C::ends + (double)per * C::step[blocks > kCus ? 1 : 0];
-    if (splits > 1) us += C::sum + (double)blocks * C::part;
-    if (n == 1 || us < best) {
-      best = us;
-      p.splits = splits;
-      p.per_split = per;
-    }
-  }
-  p.us += best;
-  if (p.splits == 1) {
-    p.whole = tiles;
-    p.further = 0;
-  }
-  return p;
-}
 
 typedef Shape<4> Large;
 typedef Shape<2> Small;
@@ -660,8 +602,7 @@ Plan make_plan(const zero_layout* L, int32_t tensor, const Sizes& z, const uint1
     p.bytes = few_bytes(z.M, z.N, z.K, z.n_adjacent);
     return p;
   }
-  const Plan x = plan_for<Large>(z.M, z.N, z.K), y = plan_for<Small>(z.M, z.N, z.K);
-  Plan p = x.us <= y.us ? x : y;
+  Plan p{plan_of(z.M, z.N, z.K)};
   const bool copy_a = z.K % 8 || a_stride % 8 || a_stride > kMaxStride || !aligned16(a);
   p.w_bytes = copy_w ? z.w_rows * ((z.w_cols + 7) / 8) * 16 : 0;
   p.a_bytes = copy_a ? z.M * ((z.K + 7) / 8) * 16 : 0;

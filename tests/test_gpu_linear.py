@@ -16,6 +16,7 @@ import torch
 
 import fsdp_sharded_optimizer_step_amd as z
 import oracle
+from linear_cases import LARGE_TILES
 from micrograd_ref import BF, FLAG_SETS, U, Flat, f64
 from micrograd_ref import layout as odd_layout
 from test_gpu_micrograd import randn, strided
@@ -367,3 +368,18 @@ def test_large_tiles(t, o, i, tr):
                                       (1000, 4160, 4104, True)])
 def test_large_tiles_epilogues(act, t, o, i, tr):
     test_epilogues(act, t, o, i, tr)
+
+
+@pytest.mark.parametrize("tr", [False, True])
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("m,n,k", LARGE_TILES)
+def test_sizes_of_large_tiles(m, n, k, grad, tr):
+    """Each of these products, forward and as an input gradient, both orders of the weight."""
+    test_whole_numbers(m, *((k, n) if grad else (n, k)), tr)
+
+
+@pytest.mark.parametrize("act,tr", [("gelu", False), ("silu", True)])
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("m,n,k", [s for s in LARGE_TILES if s[0] % 2])
+def test_epilogues_of_large_tiles(act, m, n, k, grad, tr):
+    test_epilogues(act, m, *((k, n) if grad else (n, k)), tr)
