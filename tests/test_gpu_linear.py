@@ -190,6 +190,43 @@ def test_activations_at_every_bf16_value(act):
     assert ((dx.double() - s).abs() <= 64 * U * (1 + torch.clamp(x.double().abs(), max=40)) + BF * s.abs()).all()
 
 
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+def test_activations_keep_their_digits_below_zero(act):
+    """Every finite bf16 number below zero, relative to the value itself.
+
+    e^a is off by the error of a, 2 U |a| for its product with log2(e), and 2 U.
+    gelu: a = q - z^2 by 4 U z^2 (z is off by 2 U of itself), a rounding, the fit's
+    1.5 U and q's 25 U (8 steps of magnitude 1.5, and t, which is off by 6 U of
+    itself, with Q's slope of 2): 3.5 U x^2 + 44 U with the factors' roundings.
+    gelu_tanh: a is off by 7 U of itself, silu: not at all; 1 / (1 + e^-a) adds 3
+    roundings and the product one.  Factors below 2^-126 may be 0.
+    The derivative of gelu adds x times the density, off by 1.5 U x^2 + 10 U of
+    itself; those of the others a product of the same p with 1 - p, off by another
+    U, and three roundings (of the polynomial in gelu_tanh another four)."""
+    x = torch.arange(32769, 65536, dtype=torch.int32).to(torch.uint16).view(BF16).to(DEV)
+    x = x[torch.isfinite(x)].view(-1, 1).contiguous()
+    w = Weights(1, 1, False, fill=lambda n: torch.ones(n, dtype=BF16, device=DEV))
+    out, dx = torch.empty(x.shape, dtype=F32, device=DEV), torch.empty_like(x)
+    z.zero_linear(w.L, 1, w.params, x, out, activation=act)
+    z.zero_linear_input_grad(w.L, 1, w.params, torch.ones_like(x), dx, activation=act, pre=x)
+    v = x.double().clamp(min=-1000.0)          # all further ones are 0 in 64 bits, too
+    a = {"gelu": v * v, "silu": v, "gelu_tanh": 2 * (2 / np.pi) ** 0.5 * (v + 0.044715 * v ** 3)}[act].abs()
+    if act == "gelu":                           # ndtr is made of 1 + erf, which has no digits there
+        low, dense = torch.special.erfc(-v * 0.5 ** 0.5) / 2, v * torch.exp(-v * v / 2) / (2 * np.pi) ** 0.5
+        y, s, parts = v * low, low + dense, low + dense.abs()
+        rel = (44 + 4 * a) * U
+        rel_s = rel + 2 * U
+    else:
+        y, s = act64(v, act), slope64(v, act)
+        rel = (12 + (10 if act == "gelu_tanh" else 3) * a) * U
+        slope = 2 * (2 / np.pi) ** 0.5 * (1 + 0.134145 * v * v) if act == "gelu_tanh" else 1.0
+        parts, rel_s = torch.sigmoid(-a) * (1 + v.abs() * slope), 2 * rel
+    least = 2.0 ** -126 * x.double().abs() + 2.0 ** -149    # the second: the result's own step
+    assert ((out.double() - y).abs() <= rel * y.abs() + least).all()
+    e = rel_s * parts + 2.0 ** -126 * (1 + v.abs()) ** 3
+    assert ((dx.double() - s).abs() <= e + BF * (s.abs() + e) + 2.0 ** -134).all()
+
+
 def test_values_outside_the_matrices_count_for_nothing():
     """Infinities and NaN behind a row's last column, behind the last row, and in
     the parameters around the weight."""
