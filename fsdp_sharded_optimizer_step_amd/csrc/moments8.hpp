@@ -14,9 +14,10 @@
 // A moment decays by (1 - beta) of itself a step, less than the distance of
 // two codes where beta is near 1: the nearest code would be the old one for
 // ever.  So the step rounds at random, up with the probability of the part
-// that is cut off: the expected value is the moment itself.  What is above
-// zero keeps the smallest code at least, since a second moment of zero would
-// leave the first one divided by eps.
+// that is cut off: the expected value is the moment itself.  But a second moment
+// above zero keeps the smallest code at least, since one of zero would leave the
+// first moment divided by eps: next to the smallest code, 2^-19 to 2^-18 of the
+// block's largest value, it is biased upwards and stops decaying.
 #pragma once
 
 #include "act8.hpp"

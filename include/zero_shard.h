@@ -374,9 +374,11 @@ int zero_shard_step_buckets(const zero_layout* layout, const zero_adamw* hp, int
  * |value| / 2^(e-127) in units of its code's lowest bit (units of the smallest
  * code for smaller ones, where u is first rounded to 20 fraction bits, 19 for
  * exp_avg_sq), the code is floor(u + (r + 0.5) / 65536), the largest code at
- * most.  A positive v' keeps a code of 1 at least.  Infinities and NaN become
- * NaN codes and do not count for the scale.  The expected value is the moment,
- * also where it changes by less than the distance of two codes.
+ * most.  Infinities and NaN become NaN codes and do not count for the scale.
+ * The expected value is the moment, also where it changes by less than the
+ * distance of two codes, with one exception: a positive v' keeps a code of 1 at
+ * least, so below one smallest code (2^-19 to 2^-18 of the block's largest
+ * v') it is held up there, and does not decay further while the scale stays.
  * r are 16 bits for each element: the lower (exp_avg) and upper half
  * (exp_avg_sq) of h, in 32-bit arithmetic, i the shard index,
  *   h = lo32(i) * 0x9E3779B1 + hi32(i) * 0x85EBCA77 + k0
@@ -403,7 +405,8 @@ int zero_shard_step_moments8(const zero_layout* layout, const zero_adamw* hp, in
                              hipStream_t stream);
 
 /* binary32 moments (S floats each) to 8 bits, rounded to the nearest code (ties
- * to even; a negative second moment counts as zero), and the values that codes
+ * to even; a negative second moment counts as zero, a positive one keeps a code
+ * of 1 at least), and the values that codes
  * stand for back to binary32, exactly: to start from a binary32 state, to save
  * one, or to re-cut it for another layout (unpack, zero_reshard, pack).
  * pack of what unpack gave restores values, except where a lowered scale

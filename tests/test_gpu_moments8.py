@@ -297,3 +297,33 @@ def test_moments_keep_their_expected_value():
     sigma = (n * k * (1 + 2.0 ** -10) ** k) ** 0.5 * one / 32
     assert abs(float(v.double().sum()) - exp) <= 5 * sigma
     assert 5 * sigma < 0.1 * exp and not bool(m.any())
+
+
+def test_small_moments_stay_at_the_smallest_code():
+    """Blocks of one large second moment, which a gradient of its root keeps where
+    it is, and small ones without gradients.  Those of one smallest code stay
+    there, those of three come down to it and no further; those of 1024 decay as
+    expected, with the bound of the test above."""
+    blocks, k, b2 = 512, 500, 0.999
+    n, unit = 128 * blocks, 2.0 ** -18
+    L = z.Layout([n], 0, 1, 0)
+    mom = z.Moments8.zeros(L, DEV)
+    v0 = torch.full((blocks, 128), 1024 * unit, dtype=torch.float32, device=DEV)
+    v0[:, 0], v0[:, 1:43], v0[:, 43:85] = 1.0, unit, 3 * unit
+    zero = torch.zeros(n, dtype=torch.float32, device=DEV)
+    z.zero_moments8_pack(L, zero, v0.view(-1), mom)
+    m, v = torch.empty_like(zero), torch.empty_like(v0)
+    grad = torch.zeros(blocks, 128, dtype=torch.bfloat16, device=DEV)
+    grad[:, 0] = 1.0
+    out, master = zero.bfloat16(), zero.clone()
+    for t in range(1, k + 1):
+        z.zero_shard_step_moments8(L, z.AdamW(beta2=b2), t, [grad.view(-1)], z.GRAD_COMPACT, master, mom, out,
+                                   z.OUT_SHARD, 19)
+    z.zero_moments8_unpack(L, mom, m, v.view(-1))
+    v = v.double()
+    assert (v[:, 1:43] == unit).all()
+    assert (v[:, 43:85] >= unit).all() and (v[:, 43:85] == unit).any()
+    exp, count = 1024 * unit * b2 ** k, blocks * 43
+    sigma = (count * k * (1 + 2.0 ** -10) ** k) ** 0.5 * 1024 * unit / 32
+    assert abs(float(v[:, 85:].sum()) - count * exp) <= 5 * sigma and 5 * sigma < 0.1 * count * exp
+    assert (v[:, 0] >= 1 - 2.0 ** -4).all()
