@@ -37,7 +37,7 @@ __device__ __forceinline__ u32x4 load8(const uint16_t* p, int n) {
 // library); 1000 x 2304 without one 3.8 + 3.0.
 template <int ACROSS, bool ACT>
 __global__ void __launch_bounds__(kThreads) bias_kernel(const Args A) {
-  constexpr int kDown = kThreads / ACROSS;
+  constexpr int kDown = kThreads / ACROSS;  // rows at a time
   const int across = threadIdx.x % ACROSS, down = threadIdx.x / ACROSS;
   const int32_t c = ((int32_t)blockIdx.x * ACROSS + across) * 8;
   const int n = min(8, A.cols - c);
@@ -76,27 +76,20 @@ __global__ void __launch_bounds__(kThreads) bias_kernel(const Args A) {
       for (int j = 0; j < 8; ++j) sum[j] += g[j];
     }
   }
-  if constexpr (kDown > 1) {
-    __shared__ alignas(16) f32x4 all[kThreads * 2];
-    all[threadIdx.x * 2] = f32x4{sum[0], sum[1], sum[2], sum[3]};
-    all[threadIdx.x * 2 + 1] = f32x4{sum[4], sum[5], sum[6], sum[7]};
-    __syncthreads();
-    // thread k sums 4 columns (k / 2, k % 2) over the rows of threads
-    if (threadIdx.x >= ACROSS * 2) return;
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  __shared__ alignas(16) f32x4 all[kThreads * 2];
+  all[threadIdx.x * 2] = f32x4{sum[0], sum[1], sum[2], sum[3]};
+  all[threadIdx.x * 2 + 1] = f32x4{sum[4], sum[5], sum[6], sum[7]};
+  __syncthreads();
+  // thread k sums 4 columns (k / 2, k % 2) over the rows of threads
+  if (threadIdx.x >= ACROSS * 2) return;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-    for (int d = 0; d < kDown; ++d) v = v + all[d * ACROSS * 2 + threadIdx.x];
-    const int32_t at = (int32_t)blockIdx.x * ACROSS * 8 + (int)threadIdx.x * 4;
-    float* p = A.partial + (int64_t)blockIdx.y * A.cols + at;
+  for (int d = 0; d < kDown; ++d) v = v + all[d * ACROSS * 2 + threadIdx.x];
+  const int32_t at = (int32_t)blockIdx.x * ACROSS * 8 + (int)threadIdx.x * 4;
+  float* p = A.partial + (int64_t)blockIdx.y * A.cols + at;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (at + j < A.cols) p[j] = v[j];
-  } else {
-    float* p = A.partial + (int64_t)blockIdx.y * A.cols + c;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < n) p[j] = sum[j];
-  }
+  for (int j = 0; j < 4; ++j)
+    if (at + j < A.cols) p[j] = v[j];
 }
 
 // Sum over the groups: 32 columns per block, 32 threads per column, each
@@ -123,8 +116,8 @@ __global__ void __launch_bounds__(kSumCols* kSumWays)
 }
 
 // ------------------------------------------------------------------ host
-// Lanes along a row: all of a block where the rows are long, fewer where they
-// are short; groups of rows so that about 2048 blocks have work.  A function
+// Threads along a row: 64 of a block's 256 where the rows are long, fewer where
+// they are short; groups of rows so that about 2048 blocks have work.  A function
 // of the shape alone, and so is the order of the sums.
 struct Plan {
   int across;
