@@ -83,7 +83,8 @@ __device__ __forceinline__ uint32_t v8_code(float x, float inv, const R& r) {
 }
 
 // 32 random bits for element i of the shard: products with odd numbers and
-// shifts, keyed by the step's two words.
+// shifts, keyed by the step's two words.  The numbers are four of the five
+// prime constants of the published hash xxHash32; the steps are not its own.
 struct Random {
   uint32_t k0, k1;
 };
@@ -97,7 +98,9 @@ __device__ __forceinline__ uint32_t random_bits(const Random& r, uint32_t seed) 
   return h ^ (h >> 16);
 }
 
-// The two words of step t.
+// The two words of step t, by a published mixer of 64 bits (degski's: two rounds
+// of a shift by half the word and this product); t is spread by 2^64 over the
+// golden ratio first.
 inline Random random_of(uint64_t seed, int64_t t) {
   uint64_t x = seed ^ ((uint64_t)t * 0x9E3779B97F4A7C15ull);
   for (int k = 0; k < 2; ++k) {

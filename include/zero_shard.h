@@ -387,6 +387,9 @@ int zero_shard_step_buckets(const zero_layout* layout, const zero_adamw* hp, int
  * with k0 and k1 the lower and upper half of x: x = seed ^ (t *
  * 0x9E3779B97F4A7C15), twice x = (x ^ (x >> 32)) * 0xD6E8FEB86659FD93, then
  * x = x ^ (x >> 32), in 64 bits.  The same arguments give the same bits.
+ * (The 32-bit factors are the primes of the published hash xxHash32; the 64-bit
+ * ones 2^64 divided by the golden ratio, and that of a published two-round
+ * mixer by degski.)
  *
  * grad_dtype: ZERO_DTYPE_BF16 or ZERO_DTYPE_F32, the contributions' type.
  * Buckets [bucket_begin, bucket_end) are stepped (zero_shard_step_buckets);
@@ -701,8 +704,10 @@ int zero_head_norm_rotate_grad(const zero_layout* layout, const uint16_t* params
  *
  * W[o, i]: the tensor holds (out_features, in_features), or with transposed =
  * 1 (in_features, out_features).  Activations are bf16, products exact, sums
- * binary32 in the matrix cores (their order depends on the sizes alone), and
- * so is everything up to the one rounding of each output.
+ * binary32 in the matrix cores, and so is everything up to the one rounding of
+ * each output.  A sum's order depends on the sizes alone, except that with 3 or
+ * 4 tokens and the sum along the weight's columns it also depends on whether the
+ * weight would have to be copied (see the workspace functions).
  *
  * zero_linear:  pre[t, o] = sum over i of x[t, i] * W[o, i] + b[o], b the
  *   out_features elements of bias_tensor (-1: none);
