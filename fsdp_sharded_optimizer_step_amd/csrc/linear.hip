@@ -596,7 +596,7 @@ Plan make_plan(const zero_layout* L, int32_t tensor, const Sizes& z, const uint1
   int64_t lo, hi;
   const Place pl = make_place(L, tensor, &lo, &hi);
   const bool copy_w = pl.gap != 0 || z.w_cols % 8 || !aligned16(params + lo);
-  if (is_few(z.M, z.n_adjacent, copy_w)) {
+  if (is_few(z.M, z.N, z.K, z.n_adjacent, copy_w)) {
     Plan p{};
     p.few = true;
     p.bytes = few_bytes(z.M, z.N, z.K, z.n_adjacent);

@@ -117,11 +117,23 @@ struct Few {
   Epilogue e;
 };
 // Whether launch_few is to take a product; copied: the other kernels would have
-// to copy the weight first.  Measured (us, 14336 x 4096; launch_few, the other
-// kernels, those with the copy): k adjacent, 16 tokens 38, 38, 73; n adjacent, 2
-// tokens 32, 41, 72; 4 tokens 40 to 50, 41, 72.
-constexpr bool is_few(int64_t tokens, bool n_adjacent, bool copied) {
-  return tokens <= (n_adjacent ? (copied ? 4 : 2) : 16);
+// to copy the weight first.  Measured (us; outputs x inputs; launch_few, the other
+// kernels), the weight from HBM:
+//   k adjacent: a block sums 16 outputs alone, 8192 k in 11 us for one token and
+//   17 for 16, so long sums for few outputs are split by the others: 2048 x 8192 1
+//   token 12.6, 14.9; 16 tokens 17.6, 15.0; 1024 x 16384 20.8, 16.2 and 30.9, 16.0.
+//   From 4096 outputs on all CUs have a block: 4096 x 14336 29.9, 39.6 and 41, 40;
+//   8192 x 8192 33, 49 and 44, 54.  Very many outputs: 32768 x 512 12.0, 10.0 and
+//   14.6, 10.1; 32768 x 4096 55, 69 and 81, 70.  With the copy (a weight at an odd
+//   place): 2048 x 4096 16.0, 20.8; 2048 x 8192 27.6, 26.8; 4096 x 32768 143, 181.
+//   n adjacent: 1 and 2 tokens, 2048 x 2048 9.2, 10.4 and 10.2, 10.5; 4096 x 4096
+//   16.7, 14.2 and 18.4, 14.2; 16384 x 512 8.3, 8.6 and 9.5, 8.4; 4096 x 14336 44,
+//   35.  With the copy, 4 tokens: 4096 x 4096 22, 27; 14336 x 4096 50, 68.
+constexpr bool is_few(int64_t tokens, int64_t N, int64_t K, bool n_adjacent, bool copied) {
+  if (n_adjacent) return copied ? tokens <= 4 : tokens <= 2 && N <= 8192 && N * K <= (int64_t)1 << 23;
+  if (tokens > 16) return false;
+  if (N < 4096) return (copied ? 40 : tokens + 24) * K <= 28 * 8192;
+  return copied || N <= 16384 || (tokens <= 8 && K >= 2048);
 }
 int64_t few_bytes(int64_t M, int64_t N, int64_t K, bool n_adjacent);
 int launch_few(const Few& f, bool n_adjacent, void* workspace, hipStream_t stream);

@@ -705,9 +705,9 @@ int zero_head_norm_rotate_grad(const zero_layout* layout, const uint16_t* params
  * W[o, i]: the tensor holds (out_features, in_features), or with transposed =
  * 1 (in_features, out_features).  Activations are bf16, products exact, sums
  * binary32 in the matrix cores, and so is everything up to the one rounding of
- * each output.  A sum's order depends on the sizes alone, except that with 3 or
- * 4 tokens and the sum along the weight's columns it also depends on whether the
- * weight would have to be copied (see the workspace functions).
+ * each output.  A sum's order depends on the sizes, and with up to 16 tokens
+ * also on whether the weight would have to be copied (see the workspace
+ * functions).
  *
  * zero_linear:  pre[t, o] = sum over i of x[t, i] * W[o, i] + b[o], b the
  *   out_features elements of bias_tensor (-1: none);
@@ -723,9 +723,8 @@ int zero_head_norm_rotate_grad(const zero_layout* layout, const uint16_t* params
  *
  * The workspace functions take the operands' addresses: one that does not
  * begin at 16 bytes, or whose rows are not whole multiples of 16 bytes, is
- * copied there first (the weight also where padding falls inside it; not with
- * up to 16 tokens where the sum runs along the weight's rows, and up to 4, 2 of
- * a weight that needs no copy, where it runs along its columns).
+ * copied there first (the weight also where padding falls inside it), except that
+ * some products of up to 16 tokens read the operands where they lie.
  * Common errors; ZERO_EINVAL also for a sum over no features, ZERO_ERANGE for
  * more than ZERO_MAX_FEATURES features, or more than 2^23 tiles of 128 x 128
  * outputs. */

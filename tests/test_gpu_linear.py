@@ -141,6 +141,24 @@ def test_few_tokens(t, tr):
         assert (out.as_strided((t, o + 2), (o + 2, 1))[:-1, o:] == 7).all()
 
 
+@pytest.mark.parametrize("lead", [16, 17])
+@pytest.mark.parametrize("tr", [False, True])
+@pytest.mark.parametrize("o,i", [(64, 9000), (2048, 8192), (4096, 8200), (500, 16384), (16400, 512), (20000, 2048),
+                                 (8200, 1024), (8192, 1024), (4096, 2056)])
+def test_few_tokens_on_both_sides_of_the_choice(o, i, tr, lead):
+    """Sizes next to where other kernels take few tokens' products, with and
+    without a copy of the weight, forward and as the gradient of the other order."""
+    w = Weights(o, i, tr, lead=lead, fill=lambda n: ints(n, n))
+    for t in (1, 2, 3, 5, 8, 9, 16):
+        x, dy = ints(t, t, i), ints(t + 1, t, o)
+        out = torch.zeros(t, o, dtype=F32, device=DEV)
+        z.zero_linear(w.L, 1, w.params, x, out, bias=3, transposed=tr)
+        assert torch.equal(out.double(), x.double() @ w.w.t() + w.b)
+        dx = torch.zeros(t, i, dtype=BF16, device=DEV)
+        z.zero_linear_input_grad(w.L, 1, w.params, dy, dx, transposed=tr)
+        assert torch.equal(dx, (dy.double() @ w.w).float().bfloat16())
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("t,o,i,tr", [(1, 512, 300, False), (40, 260, 512, True), (300, 384, 256, False),
                                       (2100, 1024, 192, True)])
