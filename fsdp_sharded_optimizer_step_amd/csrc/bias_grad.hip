@@ -34,7 +34,8 @@ __device__ __forceinline__ u32x4 load8(const uint16_t* p, int n) {
 // ACROSS lanes along a row (8 columns each), the rest of the block down.  Bound by
 // HBM: 16384 x 14336 through an activation takes 272 us and the sum's launch 5,
 // 5.1 TB/s (439 where the normal distribution's function came from the math
-// library); 1000 x 2304 without one 3.8 + 3.0.
+// library); 1000 x 2304 without one 3.8 + 3.0.  At an odd place 339; rows of 14337
+// columns 380, of 14335 568.
 template <int ACROSS, bool ACT>
 __global__ void __launch_bounds__(kThreads) bias_kernel(const Args A) {
   constexpr int kDown = kThreads / ACROSS;  // rows at a time

@@ -212,10 +212,10 @@ struct Panels<true> {
 // product as sides of 128 and fill a CU alone, so nothing computes while a block
 // begins and ends (13 to 15 us; results and what the epilogue reads cross HBM
 // then); sides of 128 stand two to a CU.  Measured (us): 8192 x 14336 x 4096
-// (tokens, sum, columns) 623, 1545 TFLOP/s, with n adjacent 687; 16384 x 4096 x
-// 14336 1395, with n adjacent 1460; with everything in the epilogue 696 (K of
-// 14336), through the activation's gradient and with n adjacent 1659.  On the
-// way there: A's and B's steps in two places each, all requests beside a
+// (tokens, sum, columns) 643, 1496 TFLOP/s, with n adjacent 717; 16384 x 4096 x
+// 14336 1373, with n adjacent 1497; with everything in the epilogue 674 (K of
+// 14336), through the activation's gradient and with n adjacent 1648.  On the
+// way there (cards differ by 4 %): A's and B's steps in two places each, all requests beside a
 // quarter of a step's products 775 (1560 for sums over 4096), beside two quarters
 // 724 (1550), smaller panels of k adjacent 690 (1425); tiles in groups of 4 or 16 rows
 // instead of 8 within 3 % either way.  Without requests, for timing, 528 of the 690;

@@ -22,7 +22,7 @@ using namespace zs;
 
 // 8 elements from p.  ODD: p may lie between two words of 4 bytes.  A load of 16
 // bytes from there takes more than twice the time (1 token, 14336 x 4096: 63 us
-// against 28; of words 40), so it is made of words, each of which holds an
+// against 28; of words 40, 50 of a weight that no cache holds), so it is made of words, each of which holds an
 // element that belongs to the operand: `inside` says that those next to the 8
 // do.
 template <bool ODD>
@@ -112,6 +112,8 @@ __global__ void __launch_bounds__(kRowWaves * 64) few_rows_kernel(const Few f) {
 // ---------------------------------------------------------------- n adjacent
 constexpr int kColWaves = 8, kAcross = 8, kDown = 64 / kAcross;  // a wave: 8 rows of 64 columns
 constexpr int kColAhead = 8;
+// Loads go to any address: 1 token, 14336 x 4096, 38.6 us at an odd place, 39.1 at
+// one of 16 bytes.
 constexpr int kColStep = kColWaves * kDown * kColAhead;          // k of a block at a time
 
 // per_split: k of a block of one split; partial: its sums (splits x tokens x

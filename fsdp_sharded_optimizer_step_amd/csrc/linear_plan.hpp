@@ -34,10 +34,11 @@ struct TileCost<2> {
   static constexpr double step[2] = {0.49, 0.80}, ends = 6, part = 0.0134, sum = 2.7;
 };
 
-// Measured (us) in splits of the smaller tile, with a step of 0.64 us: 1000 x 2304
-// x 768 (tokens, outputs, inputs) 1: 13.6, 3: 19.7; 1000 x 768 x 2304 1: 26.6, 3: 16.3,
-// 9: 18.3; 333 x 8192 x 1024 1: 15.7, 2: 20.9; 300 x 300 x 8192 1: 73.9, 4: 24.6, 12: 15.8;
-// 512 x 4096 x 4096 1: 41.9, 4: 29.4.
+// Measured (us) in splits of the smaller tile: 1000 x 2304 x 768 (tokens, outputs,
+// inputs) 1: 11.0, 2: 20.1; 1000 x 768 x 2304 1: 25.2, 3: 16.2, 4: 16.5, 8: 21.8; 333
+// x 8192 x 1024 1: 12.6, 2: 23.4; 300 x 300 x 8192 1: 57, 4: 17.8, 8: 12.8, 16: 12.8,
+// 26: 15.4; 512 x 4096 x 4096 1: 38, 2: 31.7, 3: 38.5.  The estimate takes 1, 4, 1, 26
+// and 2.  1000 x 4160 x 4100: the smaller tile in 2 83, the larger in 3 69.
 template <int W>
 TilePlan plan_for(int64_t M, int64_t N, int64_t K) {
   using C = TileCost<W>;

@@ -269,7 +269,11 @@ __device__ __forceinline__ void step_unit(const Args& A, const Spot& x, const in
 
 // HBM bounds it: 262M elements of 30 bytes at N_d = 8 take 1.52 ms, 5.2 TB/s (a
 // copy reached 4.6 to 4.8); without the update or the hash, for timing, it took
-// the same.
+// the same.  Other counts of ranks (TB/s; bf16, binary32 contributions): 2 4.8, 5.2;
+// 4 5.2, 4.8; 6, by the loop of any count, 4.1, 4.1; 16 5.0, 5.1; 32 5.1, 5.3; 64
+// 2.5, 5.4: the loads of 64 ranks move far ahead, 412 registers, so one wave a SIMD
+// (512 and 233 spilled of binary32).  Slices that begin anywhere, vectors at odd
+// addresses: 3.7 to 4.2 (bf16, 4 to 16 ranks).
 template <class T, int ND, class Geo>
 __global__ void __launch_bounds__(kThreads) step8_kernel(const StepArgs<pointers(ND)> A, const Geo G) {
   const int lane = threadIdx.x & 63;
@@ -287,8 +291,8 @@ __global__ void __launch_bounds__(kThreads) step8_kernel(const StepArgs<pointers
   }
 }
 
-// Conversion of binary32 moments and back, 10 bytes an element.  Measured: back,
-// 262M elements, 0.50 ms, 5.3 TB/s.
+// Conversion of binary32 moments and back, 10 bytes an element.  Measured (2^28
+// elements): to 8 bits 0.53 ms, 5.1 TB/s; back 0.50 ms, 5.3 TB/s.
 struct ConvertArgs {
   float *m, *v;
   Codes q;
