@@ -80,6 +80,11 @@ __device__ __forceinline__ float lanes_sum(float x) {
   return x;
 }
 
+// One rounding, and one instruction where a product and a sum are two: the columns'
+// parts of each other, chosen for every pair, and the division of what is summed
+// cost as many.
+__device__ __forceinline__ float plus_product(float s, float a, float b) { return __builtin_fmaf(a, b, s); }
+
 // A lane's place in a row.
 struct Cols {
   int32_t a, b;    // first columns of its two vectors, or its first pair
@@ -333,23 +338,23 @@ __global__ void __launch_bounds__(kThreads, GRAD ? 3 : 4) rotate_kernel(const Ar
           if (normed) {
             float ss = 0.f;
 #pragma unroll
-            for (int m = 0; m < 8; ++m) ss += x[m] * inv_d * x[m] + y[m] * inv_d * y[m];
+            for (int m = 0; m < 8; ++m) ss = plus_product(plus_product(ss, x[m] * inv_d, x[m]), y[m] * inv_d, y[m]);
             const float r = 1.f / __builtin_sqrtf(lanes_sum<NL>(ss) + A.eps);
 #pragma unroll
             for (int m = 0; m < 8; ++m) x[m] = x[m] * r * weight(wx, m), y[m] = y[m] * r * weight(wy, m);
           }
 #pragma unroll
           for (int m = 0; m < 8; ++m) {
-            ox[m] = x[m] * co[m] - crossing<NL, MODE>(A, own, m, y[m]) * si[m];
-            oy[m] = crossing<NL, MODE>(A, own, m, x[m]) * si[m] + y[m] * co[m];
+            ox[m] = plus_product(x[m] * co[m], -crossing<NL, MODE>(A, own, m, y[m]), si[m]);
+            oy[m] = plus_product(y[m] * co[m], crossing<NL, MODE>(A, own, m, x[m]), si[m]);
           }
         } else {
           float gx[8], gy[8];
           widen<MODE>(ry[k], gx, gy);
 #pragma unroll
           for (int m = 0; m < 8; ++m) {
-            ox[m] = gx[m] * co[m] + crossing<NL, MODE>(A, own, m, gy[m]) * si[m];
-            oy[m] = gy[m] * co[m] - crossing<NL, MODE>(A, own, m, gx[m]) * si[m];
+            ox[m] = plus_product(gx[m] * co[m], crossing<NL, MODE>(A, own, m, gy[m]), si[m]);
+            oy[m] = plus_product(gy[m] * co[m], -crossing<NL, MODE>(A, own, m, gx[m]), si[m]);
           }
           if (normed) {
             widen<MODE>(rx[k], x, y);
@@ -357,8 +362,8 @@ __global__ void __launch_bounds__(kThreads, GRAD ? 3 : 4) rotate_kernel(const Ar
 #pragma unroll
             for (int m = 0; m < 8; ++m) {
               const float xd = x[m] * inv_d, yd = y[m] * inv_d;
-              ss += xd * x[m] + yd * y[m];
-              sg += ox[m] * weight(wx, m) * xd + oy[m] * weight(wy, m) * yd;
+              ss = plus_product(plus_product(ss, xd, x[m]), yd, y[m]);
+              sg = plus_product(plus_product(sg, ox[m] * weight(wx, m), xd), oy[m] * weight(wy, m), yd);
             }
             // lanes without a row, whose values are zeros, count for nothing
             const float rms = __builtin_sqrtf(lanes_sum<NL>(ss) + A.eps);
