@@ -47,8 +47,8 @@
  *     no fused multiply-add, subnormals kept, correctly rounded division
  *     and square root.  Results do not depend on the launch configuration.
  *     (The norm's forward pass is binary64, the sums of products with a weight
- *     are those of the matrix cores, and the heads' norms, the activations and
- *     their gradients may use fused multiply-adds: see there.)
+ *     are those of the matrix cores, and the heads' norms and rotations, the
+ *     activations and their gradients may use fused multiply-adds: see there.)
  *   - Any pointer alignment is accepted; 16-byte aligned buffers take the
  *     vector path, others a scalar path with the same results (the calls of
  *     "gradients of a micro-batch" and those after them take vectors at any
