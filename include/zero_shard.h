@@ -530,7 +530,9 @@ int zero_step_scalars(const zero_adamw* hp, int64_t t, float out[8]);
  * Matrices are rows of consecutive columns; a stride is the distance of two
  * rows in elements (at least the number of columns); matrices without a
  * stride argument are dense.  Any alignment is accepted.  No outputs may
- * overlap each other or an input; in particular nothing works in place.
+ * overlap each other or an input; in particular nothing works in place.  For
+ * that, a matrix is everything from its first to its last element: one that
+ * lies between another's rows is refused, too.
  * A workspace (16-byte aligned, of the bytes that the call's _workspace
  * function gives for the same sizes; none where it gives 0) holds intermediate
  * sums: its contents before and after a call mean nothing, and two calls that
@@ -630,8 +632,9 @@ int zero_rms_norm_grad(const zero_layout* layout, int32_t tensor, const uint16_t
  * (at most ZERO_MAX_HEAD_DIM), one for each token and head, at
  * data_dev + t*token_stride + h*head_stride (bf16, strides in elements), so
  * that parts of one projection's output, or outputs with the heads in front,
- * need no copy.  The rows of an output must not meet; two outputs may take
- * turns in one buffer (equal token strides, or equal head strides).
+ * need no copy.  The rows of an output must not meet (a token's heads lie before
+ * the next token's, or a head's tokens before the next head's); two outputs may
+ * take turns in one buffer (equal token strides, or equal head strides).
  *
  * forward, for every row x, out from x (dy is not used):
  *   u = x * w / sqrt(mean(x^2) + eps), w the head_dim elements of `tensor`

@@ -74,6 +74,12 @@ def test_the_library_refuses(L, name, status, bads):
         assert call(L, name, **bad) == status, bad
 
 
+def test_a_matrix_between_anothers_rows_is_refused(L):
+    assert call(L, "zero_linear", xs=64, out=at(2, 2 * 32), os=64) == EOVERLAP
+    assert call(L, "zero_linear_input_grad", ys=64, dx=at(2, 2 * 24), xs=64) == EOVERLAP
+    assert call(L, "zero_bias_grad", ys=64, dpre=at(1, 2 * 24)) == EOVERLAP
+
+
 def test_nothing_to_do(L):
     assert call(L, "zero_linear", t=0, x=None, out=None, ws=None) == 0
     assert call(L, "zero_linear", tensor=4, o=0, i=I, bias=-1, out=None) == 0
