@@ -647,9 +647,9 @@ int zero_rms_norm_grad(const zero_layout* layout, int32_t tensor, const uint16_t
  *   so on (time, height, width).  rotation NULL, or without pairs: no rotation.
  *   positions_dev: n_axes x tokens signed numbers of position_bytes (4 or 8)
  *   bytes; freqs_dev: R/2 binary64 values, radians a position.  Angles are
- *   binary64; rows binary32 (so are the means: mean(x^2) up to 3e38, for the
- *   gradient mean(g*x), and its parts, too), and eps is rounded to binary32, a
- *   positive one not to 0.
+ *   binary64; rows binary32 (so are the means: mean(x^2) up to 3e38, and from
+ *   1e-36 where eps is 0; for the gradient mean(g*x), and its parts, too), and eps
+ *   is rounded to binary32, a positive one not to 0.
  * grad, for every row, out = dx from dy and the forward pass's x:
  *   u' = dy turned back; g = u'*w, n = x/rms: dx = bf16((g - n*mean(g*n))/rms);
  *   without a norm dx = bf16(u'), and x is not read.  The gradient of the

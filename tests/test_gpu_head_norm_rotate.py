@@ -251,9 +251,10 @@ def test_rows_of_infinities_leave_the_others_alone():
 
 @pytest.mark.parametrize("d,r,inter,top", [(128, 128, False, 1.5e19), (512, 512, True, 1.5e19), (100, 90, False, 1.5e19),
                                            (64, 64, True, 1.5e19), (128, 64, False, 4e18), (16, 16, False, 1e19),
-                                           (512, 0, False, 1e-15)])
+                                           (512, 0, False, 1e-15), (512, 0, False, 2e-18), (100, 90, True, 2e-18)])
 def test_rows_up_to_the_largest_mean_square(d, r, inter, top):
-    """mean(x^2) up to 2.3e38: the sum of the squares would be infinite."""
+    """mean(x^2) up to 2.3e38, where the sum of the squares would be infinite, and
+    down to 2e-36, where a part of the mean, 2^-127, is off by 2^-23 of itself."""
     t, h = 5, 3
     L, pl = layout(d, False)
     params, rot = randn(d, L.padded) + 1, rotation(t, r // 2, inter=inter)
