@@ -245,11 +245,12 @@ __device__ __forceinline__ void weights_to_lds(const Args& A, const Heads& s, ui
 // 128): 64 + 8 heads forward 111, 5.4 TB/s (without the non-temporal hints 125);
 // 32 + 8 heads backward 107 with the sum's launch (4 us), 4.9 TB/s (four rows in
 // flight instead of two 142; four waves a SIMD, at which all of them spill
-// 22 registers and more, 226).  Rows at an odd place, the same vectors: 177 for 125, backward 132 for 111 (calls
-// alone in a graph).  Element by element (kSingle), 32 + 8 heads of 96 with 24
-// columns turning: 104, 2.4 TB/s, backward 289, 1.3 TB/s; these kernels are bound
-// by their instructions and spill up to 8 registers.  One token takes 4.5 us: the
-// angles' chain of binary64 and the rows' trip to memory.
+// 22 registers and more, 226).  Rows at an odd place, the same vectors: 177 for
+// 125, backward 132 for 111 (calls alone in a graph).  Element by element
+// (kSingle), 32 + 8 heads of 96 with 24 columns turning: 104, 2.4 TB/s, backward
+// 289, 1.3 TB/s; these kernels are bound by their instructions and spill up to 8
+// registers.  One token takes 4.5 us: the angles' chain of binary64 and the rows'
+// trip to memory.
 template <int NL, int MODE, bool GRAD>
 __global__ void __launch_bounds__(kThreads, GRAD ? 3 : 4) rotate_kernel(const Args A) {
   constexpr int kAhead = GRAD ? 2 : 4;  // rows whose loads a lane has in flight
